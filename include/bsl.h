@@ -300,6 +300,109 @@ BSL_API bsl_status bsl_bsr24_forward(const void *X, int32_t M, const bsl_bsr *W,
  * *status_host (a bsl_status value) and resets it to BSL_OK. */
 BSL_API bsl_status bsl_semi24_get_status(const bsl_semi24 *W, int32_t *status_host, void *stream);
 
+/* ---------------------------------------------------------------- experts (grouped rows)
+ *
+ * A linear layer with one weight per expert: the rows of X are sorted by
+ * expert, rows offsets[e] .. offsets[e + 1] - 1 belong to expert e and are
+ * multiplied with its weight.  The dense counterpart of the block-sparse
+ * layer over a block-diagonal pattern whose row ranges change from call to
+ * call, so they stay on the device: offsets is a device int32 [E + 1],
+ * ascending, 4-byte aligned, with 0 <= offsets[0] and offsets[E] <= T.  An
+ * expert may have no row; rows before offsets[0] and from offsets[E] on
+ * belong to none.  Offsets that are not ascending or leave 0 .. T are
+ * clamped (every access stays inside the matrices) and reported as
+ * BSL_ERR_INVALID_ARG in the device status. */
+#define BSL_GROUPED_MAX_EXPERTS 1024
+
+typedef struct {
+    int32_t E, N, K;    /* experts (1 .. BSL_GROUPED_MAX_EXPERTS), output and input features;
+                         * N and K multiples of 8 */
+    void *weight;       /* bf16 [E][N][K] */
+    int32_t *status;    /* [1] device status word; must be zeroed once at allocation */
+} bsl_grouped;
+
+/* Y [T][N]: Y[t] = X[t] . W[e]^T (+ bias[e]) for the rows t of each expert e.
+ * X is bf16 [T][K], bias bf16 [E][N] or NULL.  Rows of no expert are left as
+ * they were, or set to zero when zero_rest is not 0.  T >= 0 (nothing is
+ * done for T = 0). */
+BSL_API bsl_status bsl_grouped_forward(const void *X, int32_t T, const int32_t *offsets, const bsl_grouped *W,
+                                       const void *bias, void *Y, int32_t zero_rest, void *stream);
+
+/* dX [T][K]: dX[t] = dY[t] . W[e], rows of no expert as for bsl_grouped_forward. */
+BSL_API bsl_status bsl_grouped_backward_input(const void *dY, int32_t T, const int32_t *offsets, const bsl_grouped *W,
+                                              void *dX, int32_t zero_rest, void *stream);
+
+/* dW [E][N][K]: dW[e] = sum over the rows t of e of dY[t]^T . X[t]; an expert
+ * without rows gets zeros.  W gives E, N, K and the status word (its weight
+ * is not read).  workspace: bsl_grouped_workspace_bytes(W) bytes of device
+ * scratch, 128-byte aligned, written before it is read (may be NULL when that
+ * size is 0); calls that use one workspace must not overlap on the GPU. */
+BSL_API bsl_status bsl_grouped_backward_weight(const void *dY, const void *X, int32_t T, const int32_t *offsets,
+                                               const bsl_grouped *W, void *dW, void *workspace,
+                                               size_t workspace_bytes, void *stream);
+
+/* Scratch bytes of bsl_grouped_backward_weight. */
+BSL_API size_t bsl_grouped_workspace_bytes(const bsl_grouped *W);
+
+/* db [E][N]: sums of each expert's rows of dY [T][N] (zeros for an expert
+ * without rows), fp32 sums in a fixed order, rounded once to bf16.  N must be
+ * a multiple of 8.  Needs no scratch and reports no device status: offsets
+ * are clamped as above. */
+BSL_API bsl_status bsl_grouped_bias_grad(const void *dY, int32_t T, const int32_t *offsets, int32_t E, int32_t N,
+                                         void *db, void *stream);
+
+/* SYNCHRONOUS: waits for the stream, copies the device status word of W to
+ * *status_host (a bsl_status value) and resets it to BSL_OK. */
+BSL_API bsl_status bsl_grouped_get_status(const bsl_grouped *W, int32_t *status_host, void *stream);
+
+/* ---------------------------------------------------------------- microscaled 4-bit
+ *
+ * Microscaled 4-bit floating point (OCP Microscaling Formats, MXFP4): 32
+ * neighbours along K share a scale, a power of two; each element is one of
+ * +-{0, 0.5, 1, 1.5, 2, 3, 4, 6} times it.
+ *   codes   uint8 [rows][K/2]: column 2i in the low half of byte i, column
+ *           2i + 1 in the high half; a code is its sign in bit 3 and the index
+ *           of its magnitude in the list above;
+ *   scales  uint8 [rows][K/32]: log2 of the scale + 127; 255 makes the block NaN.
+ * Both 16-byte aligned, K a multiple of 32. */
+
+/* X bf16 [rows][K] to codes and scales.  With a the largest magnitude of a
+ * block, its scale is 2^(max(floor(log2 a), -125) - 2) and its elements are
+ * rounded to the nearest value (ties to the even code), at most 6 times the
+ * scale.  A block holding an infinity or a NaN becomes NaN (scale byte 255,
+ * codes 0).  rows >= 0. */
+BSL_API bsl_status bsl_mx4_quantize(const void *X, int64_t rows, int32_t K, uint8_t *codes, uint8_t *scales,
+                                    void *stream);
+
+/* The values codes and scales stand for, as bf16 [rows][K]: exact, but for
+ * the scale bytes 253 and 254, whose largest values are infinite in bf16. */
+BSL_API bsl_status bsl_mx4_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t rows, int32_t K, void *X,
+                                      void *stream);
+
+/* A weight in that form: a linear layer's (E = 1) or one per expert. */
+typedef struct {
+    int32_t E, N, K;          /* experts (1 .. BSL_GROUPED_MAX_EXPERTS); N a multiple of 8, K of 32 */
+    const uint8_t *codes;     /* [E][N][K/2] */
+    const uint8_t *scales;    /* [E][N][K/32] */
+    int32_t *status;          /* [1] device status word; must be zeroed once at allocation */
+} bsl_mx4;
+
+/* Y [M][N] = X . W^T (+ bias) with X [M][K] in codes and scales and W of E = 1,
+ * fp32 accumulation; bias bf16 [N] added before the one rounding to bf16, or
+ * NULL.  M >= 0. */
+BSL_API bsl_status bsl_mx4_forward(const uint8_t *x_codes, const uint8_t *x_scales, int32_t M, const bsl_mx4 *W,
+                                   const void *bias, void *Y, void *stream);
+
+/* The same grouped by expert: offsets, bias [E][N] and zero_rest as for
+ * bsl_grouped_forward. */
+BSL_API bsl_status bsl_mx4_grouped_forward(const uint8_t *x_codes, const uint8_t *x_scales, int32_t T,
+                                           const int32_t *offsets, const bsl_mx4 *W, const void *bias, void *Y,
+                                           int32_t zero_rest, void *stream);
+
+/* SYNCHRONOUS: waits for the stream, copies the device status word of W to
+ * *status_host (a bsl_status value) and resets it to BSL_OK. */
+BSL_API bsl_status bsl_mx4_get_status(const bsl_mx4 *W, int32_t *status_host, void *stream);
+
 /* SYNCHRONOUS: waits for the stream, copies the device status word of W to
  * *status_host (a bsl_status value) and resets it to BSL_OK. */
 BSL_API bsl_status bsl_get_device_status(const bsl_bsr *W, int32_t *status_host, void *stream);

@@ -27,6 +27,10 @@ __all__ = [
     "BlockSparseLinearFunction", "BlockSparseLinear",
     "Semi24Weight", "compress24", "forward24", "semi24_status", "Semi24Linear",
     "Bsr24Weight", "compress_bsr24", "forward_bsr24",
+    "GroupedWeight", "grouped_forward", "grouped_backward_input", "grouped_backward_weight",
+    "grouped_bias_grad", "grouped_status", "GroupedLinearFunction", "GroupedLinear",
+    "Mx4Tensor", "quantize_mx4", "dequantize_mx4", "forward_mx4", "grouped_forward_mx4", "mx4_status",
+    "Mx4Linear", "GroupedMx4Linear",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -58,6 +62,19 @@ class _SEMI24(ctypes.Structure):
                 ("meta", ctypes.c_void_p), ("status", ctypes.c_void_p)]
 
 
+class _GROUPED(ctypes.Structure):
+    _fields_ = [("E", ctypes.c_int32), ("N", ctypes.c_int32), ("K", ctypes.c_int32),
+                ("weight", ctypes.c_void_p), ("status", ctypes.c_void_p)]
+
+
+class _MX4(ctypes.Structure):
+    _fields_ = [("E", ctypes.c_int32), ("N", ctypes.c_int32), ("K", ctypes.c_int32),
+                ("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("status", ctypes.c_void_p)]
+
+
+# experts of a grouped layer (BSL_GROUPED_MAX_EXPERTS in include/bsl.h)
+GROUPED_MAX_EXPERTS = 1024
+
 # int32 entries of bsl_bsr.sbounds (BSL_SBOUNDS_LEN in include/bsl.h)
 SBOUNDS_LEN = 1026
 
@@ -73,6 +90,7 @@ def library() -> ctypes.CDLL:
             raise RuntimeError(f"{LIB_PATH} is missing: build it with `python -m sparse_gemm_b200.build`")
         lib = ctypes.CDLL(LIB_PATH)
         P, I32, SZ, U64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t, ctypes.c_uint64
+        I64, GP, XP = ctypes.c_int64, ctypes.POINTER(_GROUPED), ctypes.POINTER(_MX4)
         BP = ctypes.POINTER(_BSR)
         SP = ctypes.POINTER(_SEMI24)
         sig = {
@@ -97,6 +115,17 @@ def library() -> ctypes.CDLL:
             "bsl_semi24_get_status": (ctypes.c_int, [SP, ctypes.POINTER(I32), P]),
             "bsl_bsr24_compress": (ctypes.c_int, [BP, P, P, P]),
             "bsl_bsr24_forward": (ctypes.c_int, [P, I32, BP, P, P, P, P, P]),
+            "bsl_grouped_forward": (ctypes.c_int, [P, I32, P, GP, P, P, I32, P]),
+            "bsl_grouped_backward_input": (ctypes.c_int, [P, I32, P, GP, P, I32, P]),
+            "bsl_grouped_backward_weight": (ctypes.c_int, [P, P, I32, P, GP, P, P, SZ, P]),
+            "bsl_grouped_workspace_bytes": (SZ, [GP]),
+            "bsl_grouped_bias_grad": (ctypes.c_int, [P, I32, P, I32, I32, P, P]),
+            "bsl_grouped_get_status": (ctypes.c_int, [GP, ctypes.POINTER(I32), P]),
+            "bsl_mx4_quantize": (ctypes.c_int, [P, I64, I32, P, P, P]),
+            "bsl_mx4_dequantize": (ctypes.c_int, [P, P, I64, I32, P, P]),
+            "bsl_mx4_forward": (ctypes.c_int, [P, P, I32, XP, P, P, P]),
+            "bsl_mx4_grouped_forward": (ctypes.c_int, [P, P, I32, P, XP, P, P, I32, P]),
+            "bsl_mx4_get_status": (ctypes.c_int, [XP, ctypes.POINTER(I32), P]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(lib, name)
@@ -578,3 +607,339 @@ def forward_bsr24(X: torch.Tensor, w: Bsr24Weight, bias: torch.Tensor | None = N
     _check(library().bsl_bsr24_forward(X.data_ptr(), M, Wp.cref(), w.values.data_ptr(), w.meta.data_ptr(),
                                        bptr, Y.data_ptr(), _stream(X)), "bsl_bsr24_forward")
     return Y
+
+
+# ---------------------------------------------------------------- experts (grouped rows)
+
+
+def _tensor_arg(t, name: str, shape, dtype, like: torch.Tensor | None = None) -> None:
+    """``t`` must be a contiguous CUDA tensor of this shape (None: any size) and dtype."""
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == dtype and t.dim() == len(shape)):
+        raise TypeError(f"{name} must be a {len(shape)}-D {str(dtype)[6:]} CUDA tensor")
+    if any(want is not None and have != want for have, want in zip(t.shape, shape)):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if like is not None and t.device != like.device:
+        raise ValueError(f"{name} must be on {like.device}")
+
+
+def _out_arg(out, shape, like: torch.Tensor) -> torch.Tensor:
+    if out is None:
+        return torch.empty(shape, dtype=torch.bfloat16, device=like.device)
+    _tensor_arg(out, "out", shape, torch.bfloat16, like)
+    return out
+
+
+def _expert_bias(bias, E: int, N: int, like: torch.Tensor):
+    if bias is None:
+        return None
+    _tensor_arg(bias, "bias", (E, N), torch.bfloat16, like)
+    return bias.data_ptr()
+
+
+class GroupedWeight:
+    """The weights of a linear layer's experts, a contiguous bf16 tensor
+    [E, N, K] (kept, not copied: in-place updates are seen by the next call),
+    with the device status word of the calls that use it.  N and K are
+    multiples of 8, E at most 1024."""
+
+    def __init__(self, weight: torch.Tensor):
+        _tensor_arg(weight, "weight", (None, None, None), torch.bfloat16)
+        E, N, K = weight.shape
+        if not 0 < E <= GROUPED_MAX_EXPERTS or N <= 0 or K <= 0 or N % 8 or K % 8:
+            raise ValueError("weight must be [E, N, K] with 1 <= E <= 1024 and N, K positive multiples of 8")
+        self.weight = weight.detach()
+        self.E, self.N, self.K = int(E), int(N), int(K)
+        self.status = torch.zeros(1, dtype=torch.int32, device=weight.device)
+        self._c = _GROUPED(self.E, self.N, self.K, self.weight.data_ptr(), self.status.data_ptr())
+
+    @property
+    def device(self):
+        return self.weight.device
+
+    def cref(self):
+        return ctypes.byref(self._c)
+
+
+def grouped_forward(X: torch.Tensor, Wg: GroupedWeight, offsets: torch.Tensor, bias: torch.Tensor | None = None,
+                    out: torch.Tensor | None = None) -> torch.Tensor:
+    """Y[t] = X[t] W[e]^T (+ bias[e]) for the rows t = offsets[e] .. offsets[e + 1] - 1 of each
+    expert e.  ``offsets`` is an int32 CUDA tensor [E + 1], ascending within 0 .. X.shape[0] (else
+    clamped, and reported by :func:`grouped_status`), ``bias`` bf16 [E, N].  Rows of no expert are
+    zero, or left as they are in ``out``."""
+    _tensor_arg(X, "X", (None, Wg.K), torch.bfloat16, Wg.weight)
+    _tensor_arg(offsets, "offsets", (Wg.E + 1,), torch.int32, X)
+    bptr = _expert_bias(bias, Wg.E, Wg.N, X)
+    Y = _out_arg(out, (X.shape[0], Wg.N), X)
+    _check(library().bsl_grouped_forward(X.data_ptr(), X.shape[0], offsets.data_ptr(), Wg.cref(), bptr, Y.data_ptr(),
+                                         out is None, _stream(X)), "bsl_grouped_forward")
+    return Y
+
+
+def grouped_backward_input(dY: torch.Tensor, Wg: GroupedWeight, offsets: torch.Tensor,
+                           out: torch.Tensor | None = None) -> torch.Tensor:
+    """dX[t] = dY[t] W[e]; rows of no expert as in :func:`grouped_forward`."""
+    _tensor_arg(dY, "dY", (None, Wg.N), torch.bfloat16, Wg.weight)
+    _tensor_arg(offsets, "offsets", (Wg.E + 1,), torch.int32, dY)
+    dX = _out_arg(out, (dY.shape[0], Wg.K), dY)
+    _check(library().bsl_grouped_backward_input(dY.data_ptr(), dY.shape[0], offsets.data_ptr(), Wg.cref(),
+                                                dX.data_ptr(), out is None, _stream(dY)),
+           "bsl_grouped_backward_input")
+    return dX
+
+
+def grouped_backward_weight(dY: torch.Tensor, X: torch.Tensor, Wg: GroupedWeight, offsets: torch.Tensor,
+                            out: torch.Tensor | None = None) -> torch.Tensor:
+    """dW[e] = sum over the rows t of e of dY[t]^T X[t], [E, N, K]; zeros for an expert without rows."""
+    _tensor_arg(dY, "dY", (None, Wg.N), torch.bfloat16, Wg.weight)
+    _tensor_arg(X, "X", (dY.shape[0], Wg.K), torch.bfloat16, Wg.weight)
+    _tensor_arg(offsets, "offsets", (Wg.E + 1,), torch.int32, X)
+    dW = _out_arg(out, (Wg.E, Wg.N, Wg.K), X)
+    nbytes = int(library().bsl_grouped_workspace_bytes(Wg.cref()))
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=X.device)
+    _check(library().bsl_grouped_backward_weight(dY.data_ptr(), X.data_ptr(), X.shape[0], offsets.data_ptr(),
+                                                 Wg.cref(), dW.data_ptr(), ws.data_ptr(), nbytes, _stream(X)),
+           "bsl_grouped_backward_weight")
+    return dW
+
+
+def grouped_bias_grad(dY: torch.Tensor, offsets: torch.Tensor, out: torch.Tensor | None = None) -> torch.Tensor:
+    """dbias[e] = sum of expert e's rows of dY [T, N], [E, N]; zeros for an expert without rows."""
+    _tensor_arg(dY, "dY", (None, None), torch.bfloat16)
+    _tensor_arg(offsets, "offsets", (None,), torch.int32, dY)
+    E, N = offsets.shape[0] - 1, dY.shape[1]
+    db = _out_arg(out, (E, N), dY)
+    _check(library().bsl_grouped_bias_grad(dY.data_ptr(), dY.shape[0], offsets.data_ptr(), E, N, db.data_ptr(),
+                                           _stream(dY)), "bsl_grouped_bias_grad")
+    return db
+
+
+def grouped_status(Wg: GroupedWeight) -> int:
+    """Read and clear the weight's device status word (synchronises the stream)."""
+    out = ctypes.c_int32(0)
+    _check(library().bsl_grouped_get_status(Wg.cref(), ctypes.byref(out), _stream(Wg.weight)),
+           "bsl_grouped_get_status")
+    return int(out.value)
+
+
+class GroupedLinearFunction(torch.autograd.Function):
+    """Autograd wrapper of the expert layer: forward as :func:`grouped_forward`; backward dX, dW and
+    dbias.  ``weight`` must be the tensor that ``Wg`` was built on."""
+
+    @staticmethod
+    def forward(ctx, X, weight, offsets, Wg, bias=None):
+        if weight.data_ptr() != Wg.weight.data_ptr() or weight.shape != Wg.weight.shape:
+            raise ValueError("weight must be the tensor Wg was built on")
+        X = X.contiguous()
+        ctx.save_for_backward(X, weight, offsets)
+        ctx.Wg = Wg
+        ctx.has_bias = bias is not None
+        return grouped_forward(X, Wg, offsets, bias=bias)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dY):
+        X, _, offsets = ctx.saved_tensors
+        Wg = ctx.Wg
+        dY = dY.contiguous()
+        dX = grouped_backward_input(dY, Wg, offsets) if ctx.needs_input_grad[0] else None
+        dW = grouped_backward_weight(dY, X, Wg, offsets) if ctx.needs_input_grad[1] else None
+        db = grouped_bias_grad(dY, offsets) if ctx.has_bias and ctx.needs_input_grad[4] else None
+        return dX, dW, None, None, db
+
+
+class GroupedLinear(torch.nn.Module):
+    """One linear layer per expert over rows sorted by expert, bf16 on an sm_100 GPU.  Parameters:
+    ``weight`` [E, out_features, in_features] and ``bias`` [E, out_features] or None.  The input's
+    leading dimensions are the rows; ``offsets`` as in :func:`grouped_forward`."""
+
+    def __init__(self, weight: torch.Tensor, bias: torch.Tensor | None = None):
+        super().__init__()
+        weight = weight.detach().to(torch.bfloat16).contiguous()
+        self._packed = GroupedWeight(weight)
+        self.experts, self.out_features, self.in_features = weight.shape
+        self.weight = torch.nn.Parameter(weight)
+        if bias is not None:
+            if bias.shape != weight.shape[:2]:
+                raise ValueError("bias must be [experts, out_features]")
+            bias = torch.nn.Parameter(bias.detach().to(device=weight.device, dtype=torch.bfloat16).contiguous())
+        self.bias = bias
+
+    @property
+    def packed(self) -> GroupedWeight:
+        """The weight's handle, made anew when the parameter's storage was replaced."""
+        if self._packed.weight.data_ptr() != self.weight.data_ptr():
+            self._packed = GroupedWeight(self.weight)
+        return self._packed
+
+    def forward(self, x: torch.Tensor, offsets: torch.Tensor) -> torch.Tensor:
+        lead = x.shape[:-1]
+        x2 = x.reshape(-1, self.in_features)
+        if x2.dtype != torch.bfloat16:
+            x2 = x2.to(torch.bfloat16)
+        y = GroupedLinearFunction.apply(x2, self.weight, offsets, self.packed, self.bias)
+        return y.reshape(*lead, self.out_features)
+
+    def extra_repr(self) -> str:
+        return (f"experts={self.experts}, in_features={self.in_features}, out_features={self.out_features}, "
+                f"bias={self.bias is not None}")
+
+
+# ---------------------------------------------------------------- microscaled 4-bit
+
+
+class Mx4Tensor:
+    """A matrix (or a stack of them) in microscaled 4-bit floating point (OCP MX, MXFP4): ``codes``
+    uint8 [..., K/2], two 4-bit codes a byte, and ``scales`` uint8 [..., K/32], one power of two for
+    32 neighbours along K; layout in include/bsl.h.  As a weight, [N, K] or [E, N, K], it carries
+    the device status word of the products that use it."""
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor):
+        if not (isinstance(codes, torch.Tensor) and codes.dim() >= 2):
+            raise TypeError("codes must be a uint8 CUDA tensor of at least two dimensions")
+        lead, K = tuple(codes.shape[:-1]), codes.shape[-1] * 2
+        if K <= 0 or K % 32:
+            raise ValueError("codes must hold a positive multiple of 32 columns (16 bytes) a row")
+        _tensor_arg(codes, "codes", codes.shape, torch.uint8)
+        _tensor_arg(scales, "scales", (*lead, K // 32), torch.uint8, codes)
+        self.codes, self.scales = codes, scales
+        self.shape = (*lead, K)
+        self._status = None
+
+    @property
+    def device(self):
+        return self.codes.device
+
+    @property
+    def K(self):
+        return self.shape[-1]
+
+    @property
+    def status(self) -> torch.Tensor:
+        if self._status is None:
+            self._status = torch.zeros(1, dtype=torch.int32, device=self.device)
+        return self._status
+
+    def cref(self):
+        """The weight's descriptor (one expert for a matrix)."""
+        E, N = (1, *self.shape[:-1]) if len(self.shape) == 2 else self.shape[:-1]
+        return ctypes.byref(_MX4(E, N, self.K, self.codes.data_ptr(), self.scales.data_ptr(),
+                                 self.status.data_ptr()))
+
+
+def quantize_mx4(X: torch.Tensor, out: Mx4Tensor | None = None) -> Mx4Tensor:
+    """A bf16 tensor [..., K], K a multiple of 32, in 4 bits: each block of 32 along K gets the scale
+    2^(floor(log2 max|x|) - 2) and is rounded to the nearest value (ties to the even code), at most
+    6 times the scale.  A block with an infinity or a NaN becomes NaN."""
+    if not (isinstance(X, torch.Tensor) and X.dim() >= 2):
+        raise TypeError("X must be a bfloat16 CUDA tensor of at least two dimensions")
+    _tensor_arg(X, "X", X.shape, torch.bfloat16)
+    K = X.shape[-1]
+    if K <= 0 or K % 32:
+        raise ValueError("X's last dimension must be a positive multiple of 32")
+    if out is None:
+        lead = tuple(X.shape[:-1])
+        out = Mx4Tensor(torch.empty((*lead, K // 2), dtype=torch.uint8, device=X.device),
+                        torch.empty((*lead, K // 32), dtype=torch.uint8, device=X.device))
+    elif out.shape != tuple(X.shape) or out.device != X.device:
+        raise ValueError(f"out holds {out.shape} on {out.device}, X is {tuple(X.shape)} on {X.device}")
+    _check(library().bsl_mx4_quantize(X.data_ptr(), X.numel() // K, K, out.codes.data_ptr(), out.scales.data_ptr(),
+                                      _stream(X)), "bsl_mx4_quantize")
+    return out
+
+
+def dequantize_mx4(q: Mx4Tensor, out: torch.Tensor | None = None) -> torch.Tensor:
+    """The values ``q`` stands for, as bf16 (exact)."""
+    X = _out_arg(out, q.shape, q.codes)
+    _check(library().bsl_mx4_dequantize(q.codes.data_ptr(), q.scales.data_ptr(), q.codes.numel() * 2 // q.K, q.K,
+                                        X.data_ptr(), _stream(q.codes)), "bsl_mx4_dequantize")
+    return X
+
+
+def _mx4_input(X, Wq: Mx4Tensor) -> Mx4Tensor:
+    if not isinstance(X, Mx4Tensor):
+        _tensor_arg(X, "X", (None, Wq.K), torch.bfloat16, Wq.codes)
+        return quantize_mx4(X)
+    if len(X.shape) != 2 or X.K != Wq.K:
+        raise ValueError(f"X holds {X.shape}, expected [rows, {Wq.K}]")
+    if X.device != Wq.device:
+        raise ValueError(f"X must be on {Wq.device}")
+    return X
+
+
+def forward_mx4(X, Wq: Mx4Tensor, bias: torch.Tensor | None = None, out: torch.Tensor | None = None) -> torch.Tensor:
+    """Y = Q(X) Q(W)^T (+ bias), bf16 [M, N], on the block-scaled tensor cores.  X is bf16 [M, K]
+    (quantised on the way) or an Mx4Tensor, ``Wq`` a weight [N, K] with N a multiple of 8."""
+    if len(Wq.shape) != 2:
+        raise ValueError("Wq must be a weight [N, K]")
+    N = Wq.shape[0]
+    Xq = _mx4_input(X, Wq)
+    bptr = _bias_ptr(bias, N, Xq.codes)
+    Y = _out_arg(out, (Xq.shape[0], N), Xq.codes)
+    _check(library().bsl_mx4_forward(Xq.codes.data_ptr(), Xq.scales.data_ptr(), Xq.shape[0], Wq.cref(), bptr,
+                                     Y.data_ptr(), _stream(Xq.codes)), "bsl_mx4_forward")
+    return Y
+
+
+def grouped_forward_mx4(X, Wq: Mx4Tensor, offsets: torch.Tensor, bias: torch.Tensor | None = None,
+                        out: torch.Tensor | None = None) -> torch.Tensor:
+    """:func:`grouped_forward` with the experts' weights [E, N, K] and the rows in 4 bits (X bf16, or
+    an Mx4Tensor [T, K]); bad offsets are reported by :func:`mx4_status`."""
+    if len(Wq.shape) != 3:
+        raise ValueError("Wq must be a weight [E, N, K]")
+    E, N, _ = Wq.shape
+    Xq = _mx4_input(X, Wq)
+    _tensor_arg(offsets, "offsets", (E + 1,), torch.int32, Xq.codes)
+    bptr = _expert_bias(bias, E, N, Xq.codes)
+    Y = _out_arg(out, (Xq.shape[0], N), Xq.codes)
+    _check(library().bsl_mx4_grouped_forward(Xq.codes.data_ptr(), Xq.scales.data_ptr(), Xq.shape[0],
+                                             offsets.data_ptr(), Wq.cref(), bptr, Y.data_ptr(), out is None,
+                                             _stream(Xq.codes)), "bsl_mx4_grouped_forward")
+    return Y
+
+
+def mx4_status(Wq: Mx4Tensor) -> int:
+    """Read and clear the weight's device status word (synchronises the stream)."""
+    out = ctypes.c_int32(0)
+    _check(library().bsl_mx4_get_status(Wq.cref(), ctypes.byref(out), _stream(Wq.codes)), "bsl_mx4_get_status")
+    return int(out.value)
+
+
+class Mx4Linear(torch.nn.Module):
+    """Inference ``nn.Linear`` with weight and activations in 4 bits.  Built with :meth:`from_dense`;
+    inputs may have any leading dimensions."""
+
+    def __init__(self, weight4: Mx4Tensor, bias: torch.Tensor | None = None):
+        super().__init__()
+        self.weight4 = weight4
+        self.in_features, self.out_features = weight4.K, weight4.shape[-2]
+        if bias is not None:
+            if tuple(bias.shape) != weight4.shape[:-1]:
+                raise ValueError(f"bias must have shape {weight4.shape[:-1]}")
+            bias = bias.detach().to(device=weight4.device, dtype=torch.bfloat16).contiguous()
+        self.register_buffer("bias", bias)
+
+    @classmethod
+    def from_dense(cls, weight: torch.Tensor, bias: torch.Tensor | None = None):
+        """Quantise a [out_features, in_features] weight (in_features a multiple of 32)."""
+        return cls(quantize_mx4(weight.detach().to(torch.bfloat16).contiguous()), bias)
+
+    def _rows(self, x: torch.Tensor) -> torch.Tensor:
+        x2 = x.reshape(-1, self.in_features)
+        return (x2 if x2.dtype == torch.bfloat16 else x2.to(torch.bfloat16)).contiguous()
+
+    @torch.no_grad()
+    def forward(self, x: torch.Tensor) -> torch.Tensor:
+        y = forward_mx4(self._rows(x), self.weight4, bias=self.bias)
+        return y.reshape(*x.shape[:-1], self.out_features)
+
+
+class GroupedMx4Linear(Mx4Linear):
+    """:class:`GroupedLinear` for inference with the experts' weights and the activations in 4 bits:
+    :meth:`from_dense` takes weights [E, out_features, in_features] and bias [E, out_features]."""
+
+    @torch.no_grad()
+    def forward(self, x: torch.Tensor, offsets: torch.Tensor) -> torch.Tensor:
+        y = grouped_forward_mx4(self._rows(x), self.weight4, offsets, bias=self.bias)
+        return y.reshape(*x.shape[:-1], self.out_features)

@@ -117,6 +117,39 @@ bsl_status check_semi24(const bsl_semi24 *W)
     return BSL_OK;
 }
 
+bsl_status check_grouped(const bsl_grouped *W)
+{
+    if (!W) return BSL_ERR_INVALID_ARG;
+    if (W->E <= 0 || W->N <= 0 || W->K <= 0 || W->N % 8 || W->K % 8) return BSL_ERR_INVALID_ARG;
+    if (W->E > BSL_GROUPED_MAX_EXPERTS) return BSL_ERR_UNSUPPORTED;
+    if (!W->weight || !aligned(W->weight, 16) || !W->status || !aligned(W->status, 4)) return BSL_ERR_INVALID_ARG;
+    return BSL_OK;
+}
+
+bsl_status check_mx4(const bsl_mx4 *W)
+{
+    if (!W) return BSL_ERR_INVALID_ARG;
+    if (W->E <= 0 || W->N <= 0 || W->K <= 0 || W->N % 8 || W->K % 32) return BSL_ERR_INVALID_ARG;
+    if (W->E > BSL_GROUPED_MAX_EXPERTS) return BSL_ERR_UNSUPPORTED;
+    if (!W->codes || !aligned(W->codes, 16) || !W->scales || !aligned(W->scales, 16) || !W->status ||
+        !aligned(W->status, 4))
+        return BSL_ERR_INVALID_ARG;
+    return BSL_OK;
+}
+
+namespace {
+// Device status word -> host, cleared (synchronous).
+bsl_status read_status(int32_t *status, int32_t *status_host, void *stream)
+{
+    DeviceGuard guard;
+    BSL_TRY(guard.bind(status));
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    BSL_TRY(cuda_status(cudaMemcpyAsync(status_host, status, sizeof(int32_t), cudaMemcpyDeviceToHost, s)));
+    BSL_TRY(cuda_status(cudaMemsetAsync(status, 0, sizeof(int32_t), s)));
+    return cuda_status(cudaStreamSynchronize(s));
+}
+}  // namespace
+
 namespace {
 thread_local int g_last_cuda_error = 0;  // last CUDA error seen by this host thread
 }
@@ -449,6 +482,136 @@ bsl_status bsl_bsr24_forward(const void *X, int32_t M, const bsl_bsr *W, const v
     BSL_TRY(guard.bind(X));
     BSL_TRY(check_device());
     return launch_bsr24_fwd(X, M, W, values24, meta24, bias, Y, static_cast<cudaStream_t>(stream));
+}
+
+bsl_status bsl_grouped_forward(const void *X, int32_t T, const int32_t *offsets, const bsl_grouped *W, const void *bias,
+                               void *Y, int32_t zero_rest, void *stream)
+{
+    BSL_TRY(check_grouped(W));
+    if (T < 0 || !offsets || !aligned(offsets, 4)) return BSL_ERR_INVALID_ARG;
+    if (check_matrix(X, T) != BSL_OK || check_matrix(Y, T) != BSL_OK) return BSL_ERR_INVALID_ARG;
+    if (bias && !aligned(bias, 16)) return BSL_ERR_INVALID_ARG;
+    if (T == 0) return BSL_OK;
+    DeviceGuard guard;
+    BSL_TRY(guard.bind(X));
+    BSL_TRY(check_device());
+    return launch_grouped_rows(X, T, offsets, W, false, bias, Y, zero_rest, static_cast<cudaStream_t>(stream));
+}
+
+bsl_status bsl_grouped_backward_input(const void *dY, int32_t T, const int32_t *offsets, const bsl_grouped *W,
+                                      void *dX, int32_t zero_rest, void *stream)
+{
+    BSL_TRY(check_grouped(W));
+    if (T < 0 || !offsets || !aligned(offsets, 4)) return BSL_ERR_INVALID_ARG;
+    if (check_matrix(dY, T) != BSL_OK || check_matrix(dX, T) != BSL_OK) return BSL_ERR_INVALID_ARG;
+    if (T == 0) return BSL_OK;
+    DeviceGuard guard;
+    BSL_TRY(guard.bind(dY));
+    BSL_TRY(check_device());
+    return launch_grouped_rows(dY, T, offsets, W, true, nullptr, dX, zero_rest, static_cast<cudaStream_t>(stream));
+}
+
+size_t bsl_grouped_workspace_bytes(const bsl_grouped *W)
+{
+    return check_grouped(W) == BSL_OK ? grouped_workspace_bytes(W) : 0;
+}
+
+bsl_status bsl_grouped_backward_weight(const void *dY, const void *X, int32_t T, const int32_t *offsets,
+                                       const bsl_grouped *W, void *dW, void *workspace, size_t workspace_bytes,
+                                       void *stream)
+{
+    BSL_TRY(check_grouped(W));
+    if (T < 0 || !offsets || !aligned(offsets, 4)) return BSL_ERR_INVALID_ARG;
+    if (check_matrix(dY, T) != BSL_OK || check_matrix(X, T) != BSL_OK || check_matrix(dW, 1) != BSL_OK)
+        return BSL_ERR_INVALID_ARG;
+    const size_t need = grouped_workspace_bytes(W);
+    if (need && (!workspace || !aligned(workspace, 128) || workspace_bytes < need)) return BSL_ERR_INVALID_ARG;
+    DeviceGuard guard;
+    BSL_TRY(guard.bind(dW));
+    BSL_TRY(check_device());
+    if (T == 0)
+        return cuda_status(cudaMemsetAsync(dW, 0, static_cast<size_t>(W->E) * W->N * W->K * 2,
+                                           static_cast<cudaStream_t>(stream)));
+    return launch_grouped_dw(dY, X, T, offsets, W, dW, workspace, static_cast<cudaStream_t>(stream));
+}
+
+bsl_status bsl_grouped_bias_grad(const void *dY, int32_t T, const int32_t *offsets, int32_t E, int32_t N, void *db,
+                                 void *stream)
+{
+    if (T < 0 || E <= 0 || N <= 0 || N % 8 || !offsets || !aligned(offsets, 4)) return BSL_ERR_INVALID_ARG;
+    if (check_matrix(dY, T) != BSL_OK || check_matrix(db, 1) != BSL_OK) return BSL_ERR_INVALID_ARG;
+    if (E > BSL_GROUPED_MAX_EXPERTS) return BSL_ERR_UNSUPPORTED;
+    DeviceGuard guard;
+    BSL_TRY(guard.bind(db));
+    BSL_TRY(check_device());
+    return launch_grouped_bias_grad(dY, T, offsets, E, N, db, static_cast<cudaStream_t>(stream));
+}
+
+bsl_status bsl_grouped_get_status(const bsl_grouped *W, int32_t *status_host, void *stream)
+{
+    if (!W || !W->status || !status_host) return BSL_ERR_INVALID_ARG;
+    return read_status(W->status, status_host, stream);
+}
+
+bsl_status bsl_mx4_quantize(const void *X, int64_t rows, int32_t K, uint8_t *codes, uint8_t *scales, void *stream)
+{
+    if (rows < 0 || K <= 0 || K % 32) return BSL_ERR_INVALID_ARG;
+    if (check_matrix(X, rows) != BSL_OK || check_matrix(codes, rows) != BSL_OK || check_matrix(scales, rows) != BSL_OK)
+        return BSL_ERR_INVALID_ARG;
+    if (rows == 0) return BSL_OK;
+    if (rows > INT64_MAX / K) return BSL_ERR_UNSUPPORTED;
+    DeviceGuard guard;
+    BSL_TRY(guard.bind(X));
+    BSL_TRY(check_device());
+    return launch_mx4_quantize(X, rows * K, codes, scales, static_cast<cudaStream_t>(stream));
+}
+
+bsl_status bsl_mx4_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t rows, int32_t K, void *X,
+                              void *stream)
+{
+    if (rows < 0 || K <= 0 || K % 32) return BSL_ERR_INVALID_ARG;
+    if (check_matrix(X, rows) != BSL_OK || check_matrix(codes, rows) != BSL_OK || check_matrix(scales, rows) != BSL_OK)
+        return BSL_ERR_INVALID_ARG;
+    if (rows == 0) return BSL_OK;
+    if (rows > INT64_MAX / K) return BSL_ERR_UNSUPPORTED;
+    DeviceGuard guard;
+    BSL_TRY(guard.bind(X));
+    BSL_TRY(check_device());
+    return launch_mx4_dequantize(codes, scales, rows * K, X, static_cast<cudaStream_t>(stream));
+}
+
+bsl_status bsl_mx4_forward(const uint8_t *x_codes, const uint8_t *x_scales, int32_t M, const bsl_mx4 *W,
+                           const void *bias, void *Y, void *stream)
+{
+    BSL_TRY(check_mx4(W));
+    if (M < 0 || W->E != 1 || (bias && !aligned(bias, 16))) return BSL_ERR_INVALID_ARG;
+    if (check_matrix(x_codes, M) != BSL_OK || check_matrix(x_scales, M) != BSL_OK || check_matrix(Y, M) != BSL_OK)
+        return BSL_ERR_INVALID_ARG;
+    if (M == 0) return BSL_OK;
+    DeviceGuard guard;
+    BSL_TRY(guard.bind(x_codes));
+    BSL_TRY(check_device());
+    return launch_mx4_fwd(x_codes, x_scales, M, nullptr, W, bias, Y, 0, static_cast<cudaStream_t>(stream));
+}
+
+bsl_status bsl_mx4_grouped_forward(const uint8_t *x_codes, const uint8_t *x_scales, int32_t T, const int32_t *offsets,
+                                   const bsl_mx4 *W, const void *bias, void *Y, int32_t zero_rest, void *stream)
+{
+    BSL_TRY(check_mx4(W));
+    if (T < 0 || !offsets || !aligned(offsets, 4) || (bias && !aligned(bias, 16))) return BSL_ERR_INVALID_ARG;
+    if (check_matrix(x_codes, T) != BSL_OK || check_matrix(x_scales, T) != BSL_OK || check_matrix(Y, T) != BSL_OK)
+        return BSL_ERR_INVALID_ARG;
+    if (T == 0) return BSL_OK;
+    DeviceGuard guard;
+    BSL_TRY(guard.bind(x_codes));
+    BSL_TRY(check_device());
+    return launch_mx4_fwd(x_codes, x_scales, T, offsets, W, bias, Y, zero_rest, static_cast<cudaStream_t>(stream));
+}
+
+bsl_status bsl_mx4_get_status(const bsl_mx4 *W, int32_t *status_host, void *stream)
+{
+    if (!W || !W->status || !status_host) return BSL_ERR_INVALID_ARG;
+    return read_status(W->status, status_host, stream);
 }
 
 bsl_status bsl_semi24_get_status(const bsl_semi24 *W, int32_t *status_host, void *stream)

@@ -77,6 +77,8 @@ bsl_status set_smem_once(const void *func, int bytes);
 bsl_status check_device();              // current device is sm_100
 bsl_status check_bsr(const bsl_bsr *W);
 bsl_status check_semi24(const bsl_semi24 *W);
+bsl_status check_grouped(const bsl_grouped *W);
+bsl_status check_mx4(const bsl_mx4 *W);
 uint64_t wait_timeout_ns();
 bsl_status cuda_status(cudaError_t e);
 void note_driver_error(int code);
@@ -109,6 +111,22 @@ bsl_status launch_semi24_fwd(const void *X, int32_t M, const bsl_semi24 *W, cons
 bsl_status launch_bsr24_compress(const bsl_bsr *W, void *values24, uint16_t *meta24, cudaStream_t s);
 bsl_status launch_bsr24_fwd(const void *X, int32_t M, const bsl_bsr *W, const void *values24,
                             const uint16_t *meta24, const void *bias, void *Y, cudaStream_t s);
+
+// Expert (grouped) layer.  launch_grouped_rows: forward (A = X, out = Y) or,
+// transposed, the input gradient (A = dY, out = dX).
+size_t grouped_workspace_bytes(const bsl_grouped *W);
+bsl_status launch_grouped_rows(const void *A, int32_t T, const int32_t *offsets, const bsl_grouped *W, bool transposed,
+                               const void *bias, void *out, int32_t zero_rest, cudaStream_t s);
+bsl_status launch_grouped_dw(const void *dY, const void *X, int32_t T, const int32_t *offsets, const bsl_grouped *W,
+                             void *dW, void *workspace, cudaStream_t s);
+bsl_status launch_grouped_bias_grad(const void *dY, int32_t T, const int32_t *offsets, int32_t E, int32_t N, void *db,
+                                    cudaStream_t s);
+
+// Microscaled 4-bit: conversion, and the product (offsets null: one group of all rows).
+bsl_status launch_mx4_quantize(const void *X, int64_t elems, uint8_t *codes, uint8_t *scales, cudaStream_t s);
+bsl_status launch_mx4_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t elems, void *X, cudaStream_t s);
+bsl_status launch_mx4_fwd(const uint8_t *xc, const uint8_t *xs, int32_t T, const int32_t *offsets, const bsl_mx4 *W,
+                          const void *bias, void *Y, int32_t zero_rest, cudaStream_t s);
 
 bsl_status launch_debug_wait(int32_t *status, uint64_t timeout_ns, cudaStream_t s);
 

@@ -1,0 +1,115 @@
+// mx4_quant.cu -- microscaled 4-bit floating point (OCP MX, "MXFP4"): bf16 to
+// 4-bit codes with one power-of-two scale for 32 neighbours along K, and back.
+//
+// For a block of 32 with largest magnitude a (finite):
+//     s = 2^(max(floor(log2 a), -125) - 2)        scale byte = log2 s + 127
+//     q = x / s to the nearest of 0 .5 1 1.5 2 3 4 6 (ties to the even code), 6 at most
+// floor(log2 a) is the exponent field f of a's bf16 bits less 127, so the
+// scale byte is max(f - 2, 0); x / s is a product with a power of two, exact
+// in fp32, so the one rounding is the conversion to 4 bits.  f = 255 (an
+// infinity or NaN in the block) gives the scale byte 255, which stands for
+// NaN, and zero codes.
+//
+// Bound by bytes: 2 read and 17/32 written an element (the reverse back).
+// Four lanes share a block: 16-byte loads, 4-byte code stores, whole lines a
+// warp; the largest magnitude takes two shuffles.
+#include "common.cuh"
+#include "internal.h"
+
+namespace bsl {
+namespace {
+
+constexpr int kThreads = 256;
+
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+// Two values to two 4-bit codes, `lo` in the low half.
+__device__ __forceinline__ uint32_t to_e2m1x2(float lo, float hi)
+{
+    uint32_t r;
+    asm("{\n\t.reg .b8 b;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b, %2, %1;\n\t"
+        "cvt.u32.u8 %0, b;\n\t}"
+        : "=r"(r)
+        : "f"(lo), "f"(hi));
+    return r;
+}
+
+// Chunk i covers elements 8i .. 8i+7; n is the number of chunks, a multiple of 4.
+__global__ void __launch_bounds__(kThreads)
+    k_mx4_quantize(const uint4 *__restrict__ X, int64_t n, uint32_t *__restrict__ codes, uint8_t *__restrict__ scales)
+{
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
+    const bool live = i < n;  // whole blocks of four lanes
+    const uint4 x = live ? X[i] : make_uint4(0, 0, 0, 0);
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    uint32_t top = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) top = __vmaxu2(top, w[j] & 0x7FFF7FFFu);
+    top = max(top & 0xFFFFu, top >> 16);
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    const uint32_t f = top >> 7;
+    const uint32_t scale = f == 255 ? 255 : f > 2 ? f - 2 : 0;
+    // 1 / s = 2^(127 - scale); 0 where the block stands for NaN
+    const float inv = f == 255 ? 0.f : __uint_as_float((254 - scale) << 23);
+    uint32_t code = 0;
+    if (f != 255) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) code |= to_e2m1x2(bf16_lo(w[j]) * inv, bf16_hi(w[j]) * inv) << (8 * j);
+    }
+    if (!live) return;
+    codes[i] = code;
+    if ((i & 3) == 0) scales[i >> 2] = static_cast<uint8_t>(scale);
+}
+
+// One 4-bit code's value under the scale: 4 bits to fp32 by bits (no table).
+__device__ __forceinline__ float from_e2m1(uint32_t c, float scale)
+{
+    const uint32_t m = c & 7u;
+    // 0 .5 1 1.5 2 3 4 6: exponent and mantissa bits above the subnormal .5
+    const float v = m < 2 ? 0.5f * static_cast<float>(m)
+                          : __uint_as_float(((m >> 1) + 126u) << 23 | (m & 1u) << 22);
+    return (c & 8u ? -v : v) * scale;
+}
+
+__global__ void __launch_bounds__(kThreads)
+    k_mx4_dequantize(const uint32_t *__restrict__ codes, const uint8_t *__restrict__ scales, int64_t n,
+                     uint4 *__restrict__ X)
+{
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
+    if (i >= n) return;
+    const uint32_t c = codes[i], b = scales[i >> 2];
+    // 2^(b - 127); 2^-127 is below the normal range, 255 stands for NaN
+    const float scale = __uint_as_float(b == 255 ? 0x7FC00000u : b == 0 ? 0x00400000u : b << 23);
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        w[j] = pack_bf16x2(from_e2m1(c >> (8 * j), scale), from_e2m1(c >> (8 * j + 4), scale));
+    X[i] = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+}  // namespace
+
+bsl_status launch_mx4_quantize(const void *X, int64_t elems, uint8_t *codes, uint8_t *scales, cudaStream_t s)
+{
+    const int64_t n = elems / 8, blocks = (n + kThreads - 1) / kThreads;
+    if (blocks > 0x7FFFFFFF) return BSL_ERR_UNSUPPORTED;
+    if (blocks == 0) return BSL_OK;
+    k_mx4_quantize<<<static_cast<unsigned>(blocks), kThreads, 0, s>>>(
+        static_cast<const uint4 *>(X), n, reinterpret_cast<uint32_t *>(codes), scales);
+    return cuda_status(cudaGetLastError());
+}
+
+bsl_status launch_mx4_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t elems, void *X, cudaStream_t s)
+{
+    const int64_t n = elems / 8, blocks = (n + kThreads - 1) / kThreads;
+    if (blocks > 0x7FFFFFFF) return BSL_ERR_UNSUPPORTED;
+    if (blocks == 0) return BSL_OK;
+    k_mx4_dequantize<<<static_cast<unsigned>(blocks), kThreads, 0, s>>>(
+        reinterpret_cast<const uint32_t *>(codes), scales, n, static_cast<uint4 *>(X));
+    return cuda_status(cudaGetLastError());
+}
+
+}  // namespace bsl
