@@ -72,6 +72,28 @@ cudaError_t launch_dependent(void (*kern)(KArgs...), unsigned grid, unsigned blo
     return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
 }
 
+// The same with the grid cut into clusters of `cluster` CTAs (grid is a multiple of it).
+template <typename... KArgs, typename... Args>
+cudaError_t launch_dependent_cluster(void (*kern)(KArgs...), unsigned grid, unsigned cluster, unsigned block,
+                                     size_t smem, cudaStream_t s, Args &&...args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
+}
+
 // cudaFuncSetAttribute(MaxDynamicSharedMemorySize) once per kernel and device.
 bsl_status set_smem_once(const void *func, int bytes);
 bsl_status check_device();              // current device is sm_100
