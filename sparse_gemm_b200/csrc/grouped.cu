@@ -24,9 +24,9 @@
 // must not meet a zero).
 //
 // Persistent kernels, programmatic dependents, 8 warps a CTA:
-//   warp 0     TMA producer (ring of stages of 64 k);
+//   warps 0, 2 TMA producers of A and of B (a ring of stages of 64 k);
 //   warp 1     MMA issuer and TMEM owner;
-//   warps 2-3  zeros for the rows of no expert, on request;
+//   warp 3     zeros for the rows of no expert, on request;
 //   warps 4-7  epilogue: TMEM -> registers (+ bias) -> bf16, transposed
 //              through 2 KB of shared memory, TMA store of 32 x 32 chunks;
 //              chunks that end inside an expert's rows with plain stores.
@@ -74,7 +74,8 @@ struct Cfg {
 };
 
 struct Maps {
-    CUtensorMap a[3];  // A: boxes of 128 (pair, or h = 128), 64, 32 features
+    CUtensorMap a[3];  // A: K-major boxes of 128 (pair, or h = 128), 64, 32 features;
+                       // M-major boxes of one strip of 64 features, of two strips
     CUtensorMap b[2];  // B: boxes of 128 rows and of Cfg::BOX rows
     CUtensorMap out;
 };
@@ -83,7 +84,7 @@ struct Args {
     const int32_t *offsets;
     const __nv_bfloat16 *bias;
     __nv_bfloat16 *out;
-    const CUtensorMap *expert_maps;  // weight gradient: [E][2], dY and X
+    const CUtensorMap *expert_maps;  // weight gradient: [E][4], see k_expert_maps
     int32_t *status;
     int32_t T, E;
     int32_t cols, rows, depth;       // of the product; the ragged one is unused
@@ -115,12 +116,14 @@ struct Tiles {
         x.e = expert_of(start, E, t);
         const int first = off[x.e], own = off[x.e + 1] - first;
         const int r = kMode == kWeightGrad ? rows : own;
-        x.n = even_rows(r, most(), Cfg<kPair>::STEP);
+        // dW's rows come in whole strips: tiles of `most` rows, a shorter last one
+        const int each = kMode == kWeightGrad ? most() : even_rows(r, most(), Cfg<kPair>::STEP);
         int ri, ci;
-        tile_place(t - start[x.e], (r + x.n - 1) / x.n, (cols + features() - 1) / features(), ri, ci);
+        tile_place(t - start[x.e], (r + each - 1) / each, (cols + features() - 1) / features(), ri, ci);
         x.c0 = ci * features();
-        x.r0 = static_cast<int64_t>(ri) * x.n;
-        x.valid = r - ri * x.n < x.n ? r - ri * x.n : x.n;
+        x.r0 = static_cast<int64_t>(ri) * each;
+        x.valid = r - ri * each < each ? r - ri * each : each;
+        x.n = kMode == kWeightGrad ? (x.valid + Cfg<kPair>::STEP - 1) / Cfg<kPair>::STEP * Cfg<kPair>::STEP : each;
         if (kMode != kWeightGrad) x.r0 += first;
         const int k = kMode == kWeightGrad ? own : depth;
         x.kb = (k + stage_k() - 1) / stage_k();
@@ -233,22 +236,23 @@ __global__ void __launch_bounds__(256, 1) k_grouped(const __grid_constant__ Maps
     const int first = blockIdx.x / C::CG, stride = gridDim.x / C::CG;
     const int J = kPair ? 1 : 128 / tiles.h;  // 64-k blocks per stage
 
-    if (warp == 0) {
-        // ------------------------------------------------------------ producer
+    if (warp == 0 || warp == 2) {
+        // ------------------------------------------------------------ producers: warp 0 copies A, warp 2 B
         if (lane == 0) {
+            const bool is_a = warp == 0;
             bool ok = true;
             int g = 0;  // stages issued
             int mapped = -1;
-            const CUtensorMap *ma = &maps.a[kPair ? 0 : tiles.h == 128 ? 0 : tiles.h == 64 ? 1 : 2];
-            const CUtensorMap *mdy = nullptr;
+            const CUtensorMap *strips = &maps.a[1];  // two strips a copy
+            const CUtensorMap *map = is_a ? &maps.a[kPair ? 0 : tiles.h == 128 ? 0 : tiles.h == 64 ? 1 : 2] : &maps.b[1];
             for (int t = first; ok && t < count; t += stride) {
                 const Tile x = tiles.at(t);
                 if (kBm && x.kb > 0 && x.e != mapped) {
                     mapped = x.e;
-                    mdy = args.expert_maps + 2 * static_cast<size_t>(x.e);
-                    ma = mdy + 1;
-                    asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(mdy) : "memory");
-                    asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(ma) : "memory");
+                    map = args.expert_maps + 4 * static_cast<size_t>(x.e) + is_a;
+                    strips = map + 2;
+                    asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(map) : "memory");
+                    asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(strips) : "memory");
                 }
                 const int half = x.n / C::CG;                    // rows of B in this CTA
                 const bool big = !kBm && kPair && half > 64;
@@ -257,6 +261,12 @@ __global__ void __launch_bounds__(256, 1) k_grouped(const __grid_constant__ Maps
                 const uint32_t bytes = C::CG * (C::A_BYTES + J * boxes * box_rows * 128);
                 const int ca = x.c0 + static_cast<int>(rank) * 128;
                 const int rb = static_cast<int>(x.r0) + static_cast<int>(rank) * half;
+                if (!is_a && !kBm) map = &maps.b[big ? 0 : 1];
+                // Two strips in one copy where they start on a strip and are whole (or lie
+                // behind the last): of the 128-row tile's copies, two instead of one per
+                // strip and operand took the weight gradient from 1770 to 1320 us.
+                const int at = is_a ? ca : rb, wide = is_a ? args.cols : args.rows;
+                const bool both = (is_a ? kAm : kBm && boxes == 2) && at % 64 == 0 && (wide % 64 == 0 || at + 128 <= wide);
                 for (int k = 0; k < x.kb; ++k, ++g) {
                     const int slot = g % C::S;
                     if (g >= C::S && !mbar_wait(&empty[slot], ((g / C::S) - 1) & 1, tmo, abort_flag)) {
@@ -264,39 +274,39 @@ __global__ void __launch_bounds__(256, 1) k_grouped(const __grid_constant__ Maps
                         break;
                     }
                     uint8_t *sa = stages + slot * C::STAGE, *sb = sa + C::A_BYTES;
+                    if (is_a && rank == 0) mbar_arrive_expect_tx(&full[slot], bytes);
                     if (kPair) {
-                        if (rank == 0) mbar_arrive_expect_tx(&full[slot], bytes);
                         const uint32_t bar = cluster_addr(&full[slot], 0);
-                        if (kAm) {
+                        if (kAm && both) {
+                            tma_load_4d_pair(is_a ? sa : sb, strips, bar, 0, k * 64, at / 64, kBm ? 0 : x.e);
+                        } else if (is_a && kAm) {
 #pragma unroll
                             for (int i = 0; i < 2; ++i)
-                                tma_load_3d_pair(sa + i * 8192, ma, bar, ca + 64 * i, k * 64, kBm ? 0 : x.e);
-                        } else {
-                            tma_load_3d_pair(sa, ma, bar, k * 64, ca, x.e);
-                        }
-                        if (kBm) {
+                                tma_load_3d_pair(sa + i * 8192, map, bar, ca + 64 * i, k * 64, kBm ? 0 : x.e);
+                        } else if (is_a) {
+                            tma_load_3d_pair(sa, map, bar, k * 64, ca, x.e);
+                        } else if (kBm) {
                             for (int i = 0; i < boxes; ++i)
-                                tma_load_3d_pair(sb + i * 8192, mdy, bar, rb + 64 * i, k * 64, 0);
+                                tma_load_3d_pair(sb + i * 8192, map, bar, rb + 64 * i, k * 64, 0);
                         } else {
                             for (int i = 0; i < boxes; ++i)
-                                tma_load_3d_pair(sb + i * box_rows * 128, &maps.b[big ? 0 : 1], bar, k * 64,
-                                                 rb + i * box_rows, 0);
+                                tma_load_3d_pair(sb + i * box_rows * 128, map, bar, k * 64, rb + i * box_rows, 0);
                         }
+                    } else if (is_a) {
+                        for (int j = 0; j < J; ++j)
+                            tma_load_3d(sa + j * tiles.h * 128, map, &full[slot], (k * J + j) * 64, ca, x.e);
                     } else {
-                        mbar_arrive_expect_tx(&full[slot], bytes);
-                        for (int j = 0; j < J; ++j)
-                            tma_load_3d(sa + j * tiles.h * 128, ma, &full[slot], (k * J + j) * 64, ca, x.e);
                         for (int j = 0; j < J; ++j)
                             for (int i = 0; i < boxes; ++i)
-                                tma_load_3d(sb + (j * boxes + i) * C::BOX * 128, &maps.b[1], &full[slot],
-                                            (k * J + j) * 64, rb + i * C::BOX, 0);
+                                tma_load_3d(sb + (j * boxes + i) * C::BOX * 128, map, &full[slot], (k * J + j) * 64,
+                                            rb + i * C::BOX, 0);
                     }
                 }
             }
             if (!ok) {
                 *abort_flag = 1;
                 set_status(args.status, BSL_ERR_TIMEOUT);
-            } else {  // the MMAs' arrivals on this CTA's barriers are in
+            } else if (is_a) {  // the MMAs' arrivals on this CTA's barriers are in
                 for (int s = 0; s < C::S && s < g; ++s) {
                     const int fills = (g - s + C::S - 1) / C::S;
                     if (!mbar_wait(&empty[s], (fills - 1) & 1, tmo, abort_flag))
@@ -305,7 +315,7 @@ __global__ void __launch_bounds__(256, 1) k_grouped(const __grid_constant__ Maps
             }
             // every copy lands before shared memory is released: the last fill of
             // each slot is the newest phase of its barrier, which the leader holds
-            if (rank == 0)
+            if (is_a && rank == 0)
                 for (int s = 0; s < C::S && s < g; ++s) {
                     const int fills = (g - s + C::S - 1) / C::S;
                     if (!mbar_wait(&full[s], (fills - 1) & 1, tmo, nullptr)) set_status(args.status, BSL_ERR_TIMEOUT);
@@ -376,13 +386,12 @@ __global__ void __launch_bounds__(256, 1) k_grouped(const __grid_constant__ Maps
             if (lane == 0 && !mbar_wait(drain, 0, tmo, nullptr)) set_status(args.status, BSL_ERR_TIMEOUT);
         }
         __syncwarp();
-    } else if (warp < 4) {
+    } else if (warp == 3) {
         // ------------------------------------------------------------ rows of no expert
         if (kMode != kWeightGrad && args.zero_rest) {
-            const int thread = threadIdx.x - 64;
-            zero_range(args.out, 0, static_cast<int64_t>(off[0]) * args.cols, thread);
+            zero_range(args.out, 0, static_cast<int64_t>(off[0]) * args.cols, lane);
             zero_range(args.out, static_cast<int64_t>(off[args.E]) * args.cols,
-                       static_cast<int64_t>(args.T) * args.cols, thread);
+                       static_cast<int64_t>(args.T) * args.cols, lane);
         }
         __syncwarp();
     } else {
@@ -470,42 +479,46 @@ __global__ void __launch_bounds__(256, 1) k_grouped(const __grid_constant__ Maps
 
 // ------------------------------------------------------------ per-expert maps
 
-// maps[e] = {dY, X} tensor maps that begin at the expert's first row and end
-// with its last (an expert without rows keeps one row, never read).  One warp
-// per expert: the template's copy in shared memory gets the address and the
-// row count, then goes to global memory with the fence that TMA needs.
+// maps[e] = tensor maps of dY, X (one strip a copy), dY, X (two strips) that
+// begin at the expert's first row and end with its last (an expert without
+// rows keeps one row, never read).  One warp per expert: the template's copy
+// in shared memory gets the address and the row count, then goes to global
+// memory with the fence that TMA needs.
+struct ExpertMaps {
+    CUtensorMap m[4];
+};
+
 __global__ void __launch_bounds__(32)
-    k_expert_maps(const __grid_constant__ CUtensorMap dy, const __grid_constant__ CUtensorMap x, const void *dY,
-                  const void *X, int32_t N, int32_t K, const int32_t *offsets, int32_t E, int32_t T, CUtensorMap *maps,
-                  int32_t *status)
+    k_expert_maps(const __grid_constant__ ExpertMaps base, const void *dY, const void *X, int32_t N, int32_t K,
+                  const int32_t *offsets, int32_t E, int32_t T, CUtensorMap *maps, int32_t *status)
 {
     __shared__ int32_t off[kMaxExperts + 1];
-    __shared__ alignas(128) CUtensorMap m[2];
+    __shared__ alignas(128) CUtensorMap m[4];
     dependents_may_launch();
     wait_for_prior_grid();
     load_offsets(offsets, E, T, off, blockIdx.x == 0 ? status : nullptr);
     const int lane = threadIdx.x, e = blockIdx.x;
     const int rows = off[e + 1] - off[e];
     uint32_t *w = reinterpret_cast<uint32_t *>(m);
-    w[lane] = reinterpret_cast<const uint32_t *>(&dy)[lane];
-    w[32 + lane] = reinterpret_cast<const uint32_t *>(&x)[lane];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[32 * i + lane] = reinterpret_cast<const uint32_t *>(&base.m[i])[lane];
     __syncwarp();
-    if (lane < 2) {
+    if (lane < 4) {
         const uint32_t a = smem_u32(&m[lane]);
         const int64_t first = rows ? off[e] : 0;
-        const char *base = lane ? static_cast<const char *>(X) + first * K * 2 : static_cast<const char *>(dY) + first * N * 2;
+        const char *p = lane & 1 ? static_cast<const char *>(X) + first * K * 2 : static_cast<const char *>(dY) + first * N * 2;
         asm volatile("tensormap.replace.tile.global_address.shared::cta.b1024.b64 [%0], %1;" ::"r"(a),
-                     "l"(__cvta_generic_to_global(base))
+                     "l"(__cvta_generic_to_global(p))
                      : "memory");
         asm volatile("tensormap.replace.tile.global_dim.shared::cta.b1024.b32 [%0], 1, %1;" ::"r"(a), "r"(rows ? rows : 1)
                      : "memory");
     }
     __syncwarp();
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < 4; ++i)
         asm volatile(
             "tensormap.cp_fenceproxy.global.shared::cta.tensormap::generic.release.gpu.sync.aligned [%0], [%1], 128;" ::"l"(
-                __cvta_generic_to_global(maps + 2 * static_cast<size_t>(e) + i)),
+                __cvta_generic_to_global(maps + 4 * static_cast<size_t>(e) + i)),
             "r"(smem_u32(&m[i]))
             : "memory");
 }
@@ -531,7 +544,7 @@ bsl_status run(const Maps &maps, const Args &args, cudaStream_t s)
 
 }  // namespace
 
-size_t grouped_workspace_bytes(const bsl_grouped *W) { return static_cast<size_t>(W->E) * 2 * sizeof(CUtensorMap); }
+size_t grouped_workspace_bytes(const bsl_grouped *W) { return static_cast<size_t>(W->E) * 4 * sizeof(CUtensorMap); }
 
 bsl_status launch_grouped_rows(const void *A, int32_t T, const int32_t *offsets, const bsl_grouped *W, bool transposed,
                                const void *bias, void *out, int32_t zero_rest, cudaStream_t s)
@@ -554,7 +567,8 @@ bsl_status launch_grouped_rows(const void *A, int32_t T, const int32_t *offsets,
     Maps m;
     bool good = true;
     if (transposed) {
-        good = make_map_3d(&m.a[0], W->weight, K, N, W->E, K * 2, K * 2 * N, 64, 64, 128);
+        good = make_map_3d(&m.a[0], W->weight, K, N, W->E, K * 2, K * 2 * N, 64, 64, 128) &&
+               make_strip_map(&m.a[1], W->weight, K, N, W->E);
     } else {
         for (int i = 0; i < (pair ? 1 : 3); ++i)
             good = good && make_map_3d(&m.a[i], W->weight, K, N, W->E, K * 2, K * 2 * N, 64, 128 >> i, 128);
@@ -572,12 +586,16 @@ bsl_status launch_grouped_dw(const void *dY, const void *X, int32_t T, const int
 {
     const int64_t N = W->N, K = W->K;
     Maps m;
-    if (!map_rows(&m.b[0], dY, N, T, 64, 64, 128) || !map_rows(&m.a[0], X, K, T, 64, 64, 128) ||
+    ExpertMaps base;
+    if (!map_rows(&base.m[0], dY, N, T, 64, 64, 128) || !map_rows(&base.m[1], X, K, T, 64, 64, 128) ||
+        !make_strip_map(&base.m[2], dY, N, T, 1) || !make_strip_map(&base.m[3], X, K, T, 1) ||
         !make_map_3d(&m.out, dW, K, N, W->E, K * 2, K * 2 * N, 32, 32, 0))
         return BSL_ERR_CUDA;
+    m.a[0] = base.m[0];  // (prefetched by every kernel)
+    m.b[0] = base.m[0];
     CUtensorMap *maps = static_cast<CUtensorMap *>(workspace);
-    const bsl_status st = cuda_status(launch_dependent(k_expert_maps, W->E, 32, 0, s, m.b[0], m.a[0], dY, X, W->N, W->K,
-                                                       offsets, W->E, T, maps, W->status));
+    const bsl_status st = cuda_status(launch_dependent(k_expert_maps, W->E, 32, 0, s, base, dY, X, W->N, W->K, offsets,
+                                                       W->E, T, maps, W->status));
     if (st != BSL_OK) return st;
     Args args = {};
     args.offsets = offsets;

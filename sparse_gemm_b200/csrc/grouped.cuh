@@ -102,12 +102,12 @@ __device__ __forceinline__ void tile_place(int i, int nr, int nc, int &r, int &c
     r = first + in - c * width;
 }
 
-// Zero out[a .. b) (elements, multiples of 8) with the 64 threads of two warps of every CTA.
-__device__ __forceinline__ void zero_range(__nv_bfloat16 *out, int64_t a, int64_t b, int thread)
+// Zero out[a .. b) (elements, multiples of 8) with one warp of every CTA.
+__device__ __forceinline__ void zero_range(__nv_bfloat16 *out, int64_t a, int64_t b, int lane)
 {
     uint4 *p = reinterpret_cast<uint4 *>(out);
-    for (int64_t i = a / 8 + static_cast<int64_t>(blockIdx.x) * 64 + thread; i < b / 8;
-         i += static_cast<int64_t>(gridDim.x) * 64)
+    for (int64_t i = a / 8 + static_cast<int64_t>(blockIdx.x) * 32 + lane; i < b / 8;
+         i += static_cast<int64_t>(gridDim.x) * 32)
         p[i] = make_uint4(0, 0, 0, 0);
 }
 
