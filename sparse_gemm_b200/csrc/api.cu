@@ -257,7 +257,8 @@ bool make_map_3d(CUtensorMap *map, const void *base, uint64_t d0, uint64_t d1, u
     return r == CUDA_SUCCESS;
 }
 
-bool make_strip_map(CUtensorMap *map, const void *base, uint64_t cols, uint64_t rows, uint64_t planes)
+bool make_strip_map(CUtensorMap *map, const void *base, uint64_t cols, uint64_t rows, uint64_t planes,
+                    uint32_t box_rows, uint32_t box_strips)
 {
     EncodeTiledFn fn = encode_fn();
     if (!fn) {
@@ -266,7 +267,7 @@ bool make_strip_map(CUtensorMap *map, const void *base, uint64_t cols, uint64_t 
     }
     const cuuint64_t dims[4] = {64, rows, cols >= 64 ? cols / 64 : 1, planes};
     const cuuint64_t strides[3] = {cols * 2, 128, rows * cols * 2};
-    const cuuint32_t box[4] = {64, 64, 2, 1};
+    const cuuint32_t box[4] = {64, box_rows, box_strips, 1};
     const cuuint32_t estr[4] = {1, 1, 1, 1};
     const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims, strides, box,
                           estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,

@@ -24,7 +24,7 @@
 // must not meet a zero).
 //
 // Persistent kernels, programmatic dependents, 8 warps a CTA:
-//   warps 0, 2 TMA producers of A and of B (a ring of stages of 64 k);
+//   warps 0, 2 TMA producers of A and of B (a ring of stages);
 //   warp 1     MMA issuer and TMEM owner;
 //   warp 3     zeros for the rows of no expert, on request;
 //   warps 4-7  epilogue: TMEM -> registers (+ bias) -> bf16, transposed
@@ -35,7 +35,14 @@
 // and every output is one sum in a fixed order.
 //
 // kPair: clusters of two CTAs on tiles of 256 features x 256 rows
-// (cta_group::2, M = 256; each CTA holds its 128 rows of A and half of B).
+// (cta_group::2, M = 256; each CTA holds its 128 rows of A and half of B),
+// three stages of 128 k.  Bound by the tensor pipe only while the copies keep
+// up (32 KB per 64 k and SM, 64 bytes a clock), and those go by their number:
+// an operand's stage is one copy of 32 KB, two strips of 128-byte rows.  At
+// 16384 x 4096 x 14336, 8 experts, kernels back to back (clock held by power
+// at 1.1-1.3 GHz): one 32 KB copy 1412 / 1459 / 1460 us for the three, copies
+// of 16 KB and stages of 64 k 1460 / 1575 / 1540, of 8 KB (gradients) 1775.
+//
 // Otherwise (forward with few rows, which reads each weight once): one CTA on
 // `h` = 128, 64 or 32 features x 64, 32 or 16 rows; a stage always holds
 // 16 KB of the weight, i.e. 64, 128 or 256 k, so small h only spreads the same
@@ -58,12 +65,12 @@ struct Cfg {
     static constexpr int CG = kPair ? 2 : 1;
     static constexpr int BR = kPair ? 256 : 64;          // rows per tile, at most (h = 128)
     static constexpr int STEP = 16 * CG;                 // granularity of the rows (MMA N)
-    static constexpr int BOX = kPair ? 32 : 16;          // rows of B's small copy box
-    static constexpr int BK = 64;
+    static constexpr int BOX = kPair ? 32 : 16;          // rows of B's smallest copy box
+    static constexpr int BK = kPair ? 128 : 64;          // k per stage (h = 128)
     static constexpr int A_BYTES = 128 * BK * 2;
     static constexpr int B_BYTES = BR / CG * BK * 2;
     static constexpr int STAGE = A_BYTES + B_BYTES;
-    static constexpr int S = 196608 / STAGE;             // 6 (pair) or 8 stages
+    static constexpr int S = 196608 / STAGE;             // 3 (pair) or 8 stages
     static constexpr int TMEM = 2 * BR;                  // two accumulators
     static constexpr int CHUNK = 32 * 32 * 2;
     static constexpr int OUT = 4 * 2 * CHUNK;            // two chunks per epilogue warp
@@ -74,10 +81,9 @@ struct Cfg {
 };
 
 struct Maps {
-    CUtensorMap a[3];  // A: K-major boxes of 128 (pair, or h = 128), 64, 32 features;
-                       // M-major boxes of one strip of 64 features, of two strips
-    CUtensorMap b[2];  // B: boxes of 128 rows and of Cfg::BOX rows
-    CUtensorMap out;
+    // pair: a[0] two strips a copy, a[1] one strip; b[0..2] two strips of 128, 64, 32 rows, b[3] one of 32 rows
+    // otherwise: a[0..2] K-major boxes of 128, 64, 32 features; b[3] of Cfg::BOX rows
+    CUtensorMap a[3], b[4], out;
 };
 
 struct Args {
@@ -96,7 +102,7 @@ struct Tile {
     int e, c0;        // expert, first column
     int64_t r0;       // first row: of the matrix, or of the expert's dW
     int n, valid;     // MMA N, rows that exist
-    int kb;           // stages
+    int k, kb;        // length of the sums, stages
 };
 
 // The tile list of a launch, the same in every CTA.
@@ -107,7 +113,7 @@ struct Tiles {
 
     __device__ __forceinline__ int features() const { return kPair ? 256 : h; }
     __device__ __forceinline__ int most() const { return kPair ? 256 : h / 2; }
-    __device__ __forceinline__ int stage_k() const { return kPair ? 64 : 64 * (128 / h); }
+    __device__ __forceinline__ int stage_k() const { return kPair ? 128 : 64 * (128 / h); }
     __device__ __forceinline__ int count() const { return start[E]; }
 
     __device__ __forceinline__ Tile at(int t) const
@@ -125,8 +131,8 @@ struct Tiles {
         x.valid = r - ri * each < each ? r - ri * each : each;
         x.n = kMode == kWeightGrad ? (x.valid + Cfg<kPair>::STEP - 1) / Cfg<kPair>::STEP * Cfg<kPair>::STEP : each;
         if (kMode != kWeightGrad) x.r0 += first;
-        const int k = kMode == kWeightGrad ? own : depth;
-        x.kb = (k + stage_k() - 1) / stage_k();
+        x.k = kMode == kWeightGrad ? own : depth;
+        x.kb = (x.k + stage_k() - 1) / stage_k();
         return x;
     }
 };
@@ -203,7 +209,7 @@ __global__ void __launch_bounds__(256, 1) k_grouped(const __grid_constant__ Maps
         *abort_flag = 0;
         fence_barrier_init();
         tma_prefetch_map(&maps.a[0]);
-        tma_prefetch_map(&maps.b[0]);
+        tma_prefetch_map(&maps.b[3]);
         tma_prefetch_map(&maps.out);
     }
     if (warp == 1) {
@@ -243,63 +249,75 @@ __global__ void __launch_bounds__(256, 1) k_grouped(const __grid_constant__ Maps
             bool ok = true;
             int g = 0;  // stages issued
             int mapped = -1;
-            const CUtensorMap *strips = &maps.a[1];  // two strips a copy
-            const CUtensorMap *map = is_a ? &maps.a[kPair ? 0 : tiles.h == 128 ? 0 : tiles.h == 64 ? 1 : 2] : &maps.b[1];
+            // one strip a copy, two strips a copy
+            const CUtensorMap *one = is_a ? &maps.a[kPair ? 1 : tiles.h == 128 ? 0 : tiles.h == 64 ? 1 : 2] : &maps.b[3];
+            const CUtensorMap *two = &maps.a[0];
             for (int t = first; ok && t < count; t += stride) {
                 const Tile x = tiles.at(t);
                 if (kBm && x.kb > 0 && x.e != mapped) {
                     mapped = x.e;
-                    map = args.expert_maps + 4 * static_cast<size_t>(x.e) + is_a;
-                    strips = map + 2;
-                    asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(map) : "memory");
-                    asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(strips) : "memory");
+                    one = args.expert_maps + 4 * static_cast<size_t>(x.e) + is_a;
+                    two = one + 2;
+                    asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(one) : "memory");
+                    asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(two) : "memory");
                 }
-                const int half = x.n / C::CG;                    // rows of B in this CTA
-                const bool big = !kBm && kPair && half > 64;
-                const int boxes = kBm ? (half + 63) / 64 : big ? 1 : (half + C::BOX - 1) / C::BOX;
-                const int box_rows = kBm ? 64 : big ? 128 : C::BOX;
-                const uint32_t bytes = C::CG * (C::A_BYTES + J * boxes * box_rows * 128);
-                const int ca = x.c0 + static_cast<int>(rank) * 128;
-                const int rb = static_cast<int>(x.r0) + static_cast<int>(rank) * half;
-                if (!is_a && !kBm) map = &maps.b[big ? 0 : 1];
-                // Two strips in one copy where they start on a strip and are whole (or lie
-                // behind the last): of the 128-row tile's copies, two instead of one per
-                // strip and operand took the weight gradient from 1770 to 1320 us.
-                const int at = is_a ? ca : rb, wide = is_a ? args.cols : args.rows;
-                const bool both = (is_a ? kAm : kBm && boxes == 2) && at % 64 == 0 && (wide % 64 == 0 || at + 128 <= wide);
-                for (int k = 0; k < x.kb; ++k, ++g) {
-                    const int slot = g % C::S;
-                    if (g >= C::S && !mbar_wait(&empty[slot], ((g / C::S) - 1) & 1, tmo, abort_flag)) {
-                        ok = false;
-                        break;
-                    }
-                    uint8_t *sa = stages + slot * C::STAGE, *sb = sa + C::A_BYTES;
-                    if (is_a && rank == 0) mbar_arrive_expect_tx(&full[slot], bytes);
-                    if (kPair) {
-                        const uint32_t bar = cluster_addr(&full[slot], 0);
-                        if (kAm && both) {
-                            tma_load_4d_pair(is_a ? sa : sb, strips, bar, 0, k * 64, at / 64, kBm ? 0 : x.e);
-                        } else if (is_a && kAm) {
-#pragma unroll
-                            for (int i = 0; i < 2; ++i)
-                                tma_load_3d_pair(sa + i * 8192, map, bar, ca + 64 * i, k * 64, kBm ? 0 : x.e);
-                        } else if (is_a) {
-                            tma_load_3d_pair(sa, map, bar, k * 64, ca, x.e);
-                        } else if (kBm) {
-                            for (int i = 0; i < boxes; ++i)
-                                tma_load_3d_pair(sb + i * 8192, map, bar, rb + 64 * i, k * 64, 0);
-                        } else {
-                            for (int i = 0; i < boxes; ++i)
-                                tma_load_3d_pair(sb + i * box_rows * 128, map, bar, k * 64, rb + i * box_rows, 0);
+                const int half = x.n / C::CG;  // rows of B in this CTA
+                const int at = is_a ? x.c0 + static_cast<int>(rank) * 128
+                                    : static_cast<int>(x.r0) + static_cast<int>(rank) * half;
+                if (kPair) {
+                    const bool mn = is_a ? kAm : kBm;                  // M- or N-major
+                    const int plane = is_a && !kBm ? x.e : 0;
+                    const int nb = half > 64 ? 0 : half > 32 ? 1 : 2;  // B K-major: box of 128, 64, 32 rows
+                    const int rows = is_a ? 128 : 128 >> nb;
+                    const int strips = kBm && !is_a ? (half + 63) / 64 : 2;
+                    const uint32_t bytes = 2 * (32768 + (kBm ? (half + 63) / 64 * 16384 : 256 * (128 >> nb)));
+                    // M-/N-major strips are whole along the features, K-major ones along k
+                    const int wide = is_a ? args.cols : args.rows;
+                    const bool aligned = mn && strips == 2 && at % 64 == 0 && (wide % 64 == 0 || at + 128 <= wide);
+                    if (!is_a && !kBm) two = &maps.b[nb];
+                    for (int k = 0; k < x.kb; ++k, ++g) {
+                        const int slot = g % C::S;
+                        if (g >= C::S && !mbar_wait(&empty[slot], ((g / C::S) - 1) & 1, tmo, abort_flag)) {
+                            ok = false;
+                            break;
                         }
-                    } else if (is_a) {
-                        for (int j = 0; j < J; ++j)
-                            tma_load_3d(sa + j * tiles.h * 128, map, &full[slot], (k * J + j) * 64, ca, x.e);
-                    } else {
-                        for (int j = 0; j < J; ++j)
-                            for (int i = 0; i < boxes; ++i)
-                                tma_load_3d(sb + (j * boxes + i) * C::BOX * 128, map, &full[slot], (k * J + j) * 64,
-                                            rb + i * C::BOX, 0);
+                        uint8_t *dst = stages + slot * C::STAGE + (is_a ? 0 : C::A_BYTES);
+                        if (is_a && rank == 0) mbar_arrive_expect_tx(&full[slot], bytes);
+                        const uint32_t bar = cluster_addr(&full[slot], 0);
+                        if (mn) {
+                            if (aligned)
+                                tma_load_4d_pair(dst, two, bar, 0, k * 128, at / 64, plane);
+                            else
+                                for (int i = 0; i < strips; ++i)
+                                    tma_load_3d_pair(dst + i * 16384, one, bar, at + 64 * i, k * 128, plane);
+                        } else if (x.k % 64 == 0 || k * 128 + 128 <= x.k) {
+                            tma_load_4d_pair(dst, two, bar, 0, at, k * 2, plane);
+                        } else {  // the last stage of a k that ends inside a strip
+                            for (int i = 0; i < 2; ++i)
+                                for (int r = 0; r < rows; r += is_a ? 128 : C::BOX)
+                                    tma_load_3d_pair(dst + (i * rows + r) * 128, one, bar, k * 128 + 64 * i, at + r, plane);
+                        }
+                    }
+                } else {
+                    const int boxes = (half + C::BOX - 1) / C::BOX;
+                    const uint32_t bytes = C::A_BYTES + J * boxes * C::BOX * 128;
+                    for (int k = 0; k < x.kb; ++k, ++g) {
+                        const int slot = g % C::S;
+                        if (g >= C::S && !mbar_wait(&empty[slot], ((g / C::S) - 1) & 1, tmo, abort_flag)) {
+                            ok = false;
+                            break;
+                        }
+                        uint8_t *sa = stages + slot * C::STAGE, *sb = sa + C::A_BYTES;
+                        if (is_a) {
+                            mbar_arrive_expect_tx(&full[slot], bytes);
+                            for (int j = 0; j < J; ++j)
+                                tma_load_3d(sa + j * tiles.h * 128, one, &full[slot], (k * J + j) * 64, at, x.e);
+                        } else {
+                            for (int j = 0; j < J; ++j)
+                                for (int i = 0; i < boxes; ++i)
+                                    tma_load_3d(sb + (j * boxes + i) * C::BOX * 128, one, &full[slot],
+                                                (k * J + j) * 64, at + i * C::BOX, 0);
+                        }
                     }
                 }
             }
@@ -347,17 +365,27 @@ __global__ void __launch_bounds__(256, 1) k_grouped(const __grid_constant__ Maps
                     }
                     tc_fence_after();
                     const uint32_t a0 = smem_u32(stages + slot * C::STAGE), b0 = a0 + C::A_BYTES;
-                    // K-major: 8-row atoms 1024 bytes apart, a K step of 16 is 32 bytes along the row;
-                    // M-major: 64-wide strips 8192 bytes apart, a K step is 16 rows of 128 bytes
-                    const uint64_t ad = kAm ? make_sdesc(a0, 8192, 1024, kLayoutSw128) : make_sdesc(a0, 16, 1024, kLayoutSw128);
-                    const uint64_t bd = kBm ? make_sdesc(b0, 8192, 1024, kLayoutSw128) : make_sdesc(b0, 16, 1024, kLayoutSw128);
+                    // K-major: 8-row atoms 1024 bytes apart, a K step of 16 is 32 bytes along the row, a strip
+                    // its rows x 128 bytes; M-major: strips 16384 bytes apart, a K step is 16 rows of 128 bytes
+                    const uint64_t ad = make_sdesc(a0, kAm ? 16384 : 16, 1024, kLayoutSw128);
+                    const uint64_t bd = make_sdesc(b0, kBm ? 16384 : 16, 1024, kLayoutSw128);
                     const uint32_t alo = static_cast<uint32_t>(ad), ahi = static_cast<uint32_t>(ad >> 32);
                     const uint32_t blo = static_cast<uint32_t>(bd), bhi = static_cast<uint32_t>(bd >> 32);
                     if (kPair) {
+                        const int half = x.n / 2;
+                        const uint32_t bs = half > 64 ? 1024 : half > 32 ? 512 : 256;  // K-major B: a strip, 16-byte units
+                        auto mma = [&](int i) {
+                            umma_bf16_lo_lead_pair(lead, d, alo + (kAm ? i * 128 : (i >> 2) * 1024 + (i & 3) * 2), ahi,
+                                                   blo + (kBm ? i * 128 : (i >> 2) * bs + (i & 3) * 2), bhi, idesc,
+                                                   (k | i) != 0);
+                        };
+                        const int left = x.k - k * 128;
+                        if (left >= 128) {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            umma_bf16_lo_lead_pair(lead, d, alo + i * (kAm ? 128 : 2), ahi, blo + i * (kBm ? 128 : 2),
-                                                   bhi, idesc, (k | i) != 0);
+                            for (int i = 0; i < 8; ++i) mma(i);
+                        } else {  // the copies filled the rest with zeros
+                            for (int i = 0; 16 * i < left; ++i) mma(i);
+                        }
                         umma_commit_lead_pair(lead, &empty[slot]);
                     } else {
                         const uint32_t aj = tiles.h * 8, bj = (x.n + C::BOX - 1) / C::BOX * C::BOX * 8;
@@ -566,15 +594,16 @@ bsl_status launch_grouped_rows(const void *A, int32_t T, const int32_t *offsets,
     const int64_t N = W->N, K = W->K;
     Maps m;
     bool good = true;
-    if (transposed) {
-        good = make_map_3d(&m.a[0], W->weight, K, N, W->E, K * 2, K * 2 * N, 64, 64, 128) &&
-               make_strip_map(&m.a[1], W->weight, K, N, W->E);
+    if (pair) {
+        // one strip: 64 columns (features, or k) x 128 rows of the weight
+        good = make_strip_map(&m.a[0], W->weight, K, N, W->E, 128, 2) &&
+               make_map_3d(&m.a[1], W->weight, K, N, W->E, K * 2, K * 2 * N, 64, 128, 128);
+        for (int i = 0; i < 3; ++i) good = good && make_strip_map(&m.b[i], A, args.depth, T, 1, 128 >> i, 2);
     } else {
-        for (int i = 0; i < (pair ? 1 : 3); ++i)
+        for (int i = 0; i < 3; ++i)
             good = good && make_map_3d(&m.a[i], W->weight, K, N, W->E, K * 2, K * 2 * N, 64, 128 >> i, 128);
     }
-    good = good && map_rows(&m.b[0], A, args.depth, T, 64, 128, 128) &&
-           map_rows(&m.b[1], A, args.depth, T, 64, pair ? Cfg<true>::BOX : Cfg<false>::BOX, 128) &&
+    good = good && map_rows(&m.b[3], A, args.depth, T, 64, pair ? Cfg<true>::BOX : Cfg<false>::BOX, 128) &&
            map_rows(&m.out, out, args.cols, T, 32, 32, 0);
     if (!good) return BSL_ERR_CUDA;
     if (transposed) return run<kInputGrad, true>(m, args, s);
@@ -587,12 +616,12 @@ bsl_status launch_grouped_dw(const void *dY, const void *X, int32_t T, const int
     const int64_t N = W->N, K = W->K;
     Maps m;
     ExpertMaps base;
-    if (!map_rows(&base.m[0], dY, N, T, 64, 64, 128) || !map_rows(&base.m[1], X, K, T, 64, 64, 128) ||
-        !make_strip_map(&base.m[2], dY, N, T, 1) || !make_strip_map(&base.m[3], X, K, T, 1) ||
+    if (!map_rows(&base.m[0], dY, N, T, 64, 128, 128) || !map_rows(&base.m[1], X, K, T, 64, 128, 128) ||
+        !make_strip_map(&base.m[2], dY, N, T, 1, 128, 2) || !make_strip_map(&base.m[3], X, K, T, 1, 128, 2) ||
         !make_map_3d(&m.out, dW, K, N, W->E, K * 2, K * 2 * N, 32, 32, 0))
         return BSL_ERR_CUDA;
     m.a[0] = base.m[0];  // (prefetched by every kernel)
-    m.b[0] = base.m[0];
+    m.b[3] = base.m[0];
     CUtensorMap *maps = static_cast<CUtensorMap *>(workspace);
     const bsl_status st = cuda_status(launch_dependent(k_expert_maps, W->E, 32, 0, s, base, dY, X, W->N, W->K, offsets,
                                                        W->E, T, maps, W->status));

@@ -23,10 +23,12 @@ bool make_map_2d(CUtensorMap *map, const void *base, uint64_t inner, uint64_t ou
 bool make_map_3d(CUtensorMap *map, const void *base, uint64_t d0, uint64_t d1, uint64_t d2, uint64_t stride1,
                  uint64_t stride2, uint32_t box0, uint32_t box1, int swizzle_bytes);
 
-// Encode the strips of bf16 planes [d2][rows][cols] as a 4-D tensor map (x = column inside a strip of 64,
-// y = row, z = strip, w = plane) with a box of 64 columns x 64 rows x 2 strips, 128-byte swizzle: one copy
-// brings 64 rows of 128 columns as two strips of 128-byte rows.  Whole strips only (cols / 64 of them).
-bool make_strip_map(CUtensorMap *map, const void *base, uint64_t cols, uint64_t rows, uint64_t planes);
+// Encode the strips of bf16 planes [planes][rows][cols] as a 4-D tensor map (x = column inside a strip of 64,
+// y = row, z = strip, w = plane) with a box of 64 columns x box_rows rows x box_strips strips, 128-byte swizzle:
+// one copy brings box_rows rows of 64 * box_strips columns, strip after strip of 128-byte rows.  Whole strips
+// only (cols / 64 of them).
+bool make_strip_map(CUtensorMap *map, const void *base, uint64_t cols, uint64_t rows, uint64_t planes,
+                    uint32_t box_rows, uint32_t box_strips);
 
 // Encode the packed weight values bf16 [nblocks][b][b] as a 3-D tensor map
 // (x = column inside a block, y = row inside a block, z = block) with a
