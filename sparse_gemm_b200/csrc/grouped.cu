@@ -16,7 +16,7 @@
 //     input gradient   W[e]^T M-major      dY    K-major     r
 //     weight gradient  X^T    M-major      dY^T  N-major     k
 // The MMA's N may be any multiple of 16, so a tile with few rows costs few
-// rows: an expert's rows are cut into equal tiles of at most 256.  Rows of
+// rows: an expert's rows are spread evenly over the fewest tiles of 256.  Rows of
 // the next expert that a copy brings along only reach accumulator columns
 // that are never stored.  For the weight gradient, whose ragged index is
 // summed over, k_expert_maps first writes a tensor map for each expert's rows,
@@ -100,7 +100,7 @@ struct Args {
 
 struct Tile {
     int e, c0;        // expert, first column
-    int64_t r0;       // first row: of the matrix, or of the expert's dW
+    int r0;           // first row: of the matrix, or of the expert's dW
     int n, valid;     // MMA N, rows that exist
     int k, kb;        // length of the sums, stages
 };
@@ -122,15 +122,18 @@ struct Tiles {
         x.e = expert_of(start, E, t);
         const int first = off[x.e], own = off[x.e + 1] - first;
         const int r = kMode == kWeightGrad ? rows : own;
-        // dW's rows come in whole strips: tiles of `most` rows, a shorter last one
-        const int each = kMode == kWeightGrad ? most() : even_rows(r, most(), Cfg<kPair>::STEP);
-        int ri, ci;
-        tile_place(t - start[x.e], (r + each - 1) / each, (cols + features() - 1) / features(), ri, ci);
+        constexpr int step = Cfg<kPair>::STEP;
+        int ri, ci, r0;
+        tile_place(t - start[x.e], (r + most() - 1) / most(), (cols + features() - 1) / features(), ri, ci);
         x.c0 = ci * features();
-        x.r0 = static_cast<int64_t>(ri) * each;
-        x.valid = r - ri * each < each ? r - ri * each : each;
-        x.n = kMode == kWeightGrad ? (x.valid + Cfg<kPair>::STEP - 1) / Cfg<kPair>::STEP * Cfg<kPair>::STEP : each;
-        if (kMode != kWeightGrad) x.r0 += first;
+        if (kMode == kWeightGrad) {  // whole strips: full tiles and a shorter last one
+            r0 = ri * most();
+            x.n = r - r0 < most() ? (r - r0 + step - 1) / step * step : most();
+        } else {
+            row_tile(r, most(), step, ri, r0, x.n);
+        }
+        x.valid = r - r0 < x.n ? r - r0 : x.n;
+        x.r0 = kMode == kWeightGrad ? r0 : first + r0;
         x.k = kMode == kWeightGrad ? own : depth;
         x.kb = (x.k + stage_k() - 1) / stage_k();
         return x;
@@ -263,7 +266,7 @@ __global__ void __launch_bounds__(256, 1) k_grouped(const __grid_constant__ Maps
                 }
                 const int half = x.n / C::CG;  // rows of B in this CTA
                 const int at = is_a ? x.c0 + static_cast<int>(rank) * 128
-                                    : static_cast<int>(x.r0) + static_cast<int>(rank) * half;
+                                    : x.r0 + static_cast<int>(rank) * half;
                 if (kPair) {
                     const bool mn = is_a ? kAm : kBm;                  // M- or N-major
                     const int plane = is_a && !kBm ? x.e : 0;
@@ -461,10 +464,10 @@ __global__ void __launch_bounds__(256, 1) k_grouped(const __grid_constant__ Maps
                     fence_async_smem();
                     __syncwarp();
                     if (lane == 0)
-                        tma_store_3d(&maps.out, dst, c, static_cast<int>(x.r0) + 32 * i, kMode == kWeightGrad ? x.e : 0);
+                        tma_store_3d(&maps.out, dst, c, x.r0 + 32 * i, kMode == kWeightGrad ? x.e : 0);
                 } else {
                     __syncwarp();
-                    store_rows(args.out + (x.r0 + 32 * i) * args.cols + c, args.cols, dst, left, args.cols - c, lane);
+                    store_rows(args.out + static_cast<int64_t>(x.r0 + 32 * i) * args.cols + c, args.cols, dst, left, args.cols - c, lane);
                 }
                 if (lane == 0) bulk_commit_group();  // one group a chunk, an empty one for plain stores
                 ob ^= 1;

@@ -44,15 +44,16 @@ __device__ __forceinline__ void load_offsets(const int32_t *offsets, int32_t E, 
     __syncwarp();
 }
 
-// Rows of one tile when `rows` rows are cut into the fewest tiles of at most
-// `most` rows: equal tiles, rounded up to `step` (most is a multiple of step).
-// The last tile is never empty: rows > most * (tiles - 1).
-__device__ __forceinline__ int even_rows(int rows, int most, int step)
+// Row tile i when `rows` rows are cut into the fewest tiles of at most `most`
+// rows: their units of `step` rows (most is a multiple of step) are spread
+// evenly, so tiles differ by one unit and only the last one holds rows that do
+// not exist, fewer than a unit.
+__device__ __forceinline__ void row_tile(int rows, int most, int step, int i, int &first, int &n)
 {
-    const int tiles = (rows + most - 1) / most;
-    if (tiles == 0) return step;
-    const int each = (rows + tiles - 1) / tiles;
-    return (each + step - 1) / step * step;
+    const int tiles = (rows + most - 1) / most, units = (rows + step - 1) / step;
+    const int q = units / tiles, more = units - q * tiles;
+    first = (i * q + (i < more ? i : more)) * step;
+    n = (q + (i < more)) * step;
 }
 
 // Prefix sums by the calling warp: start[i] = sum of count(j) over j < i, i = 0 .. E.
