@@ -65,7 +65,7 @@ struct Cfg {
     static constexpr int CG = kPair ? 2 : 1;
     static constexpr int BR = kPair ? 256 : 64;          // rows per tile, at most (h = 128)
     static constexpr int STEP = 16 * CG;                 // granularity of the rows (MMA N)
-    static constexpr int BOX = kPair ? 32 : 16;          // rows of B's smallest copy box
+    static constexpr int BOX = 16;                       // rows of B's smallest copy box
     static constexpr int BK = kPair ? 128 : 64;          // k per stage (h = 128)
     static constexpr int A_BYTES = 128 * BK * 2;
     static constexpr int B_BYTES = BR / CG * BK * 2;
@@ -81,9 +81,9 @@ struct Cfg {
 };
 
 struct Maps {
-    // pair: a[0] two strips a copy, a[1] one strip; b[0..2] two strips of 128, 64, 32 rows, b[3] one of 32 rows
-    // otherwise: a[0..2] K-major boxes of 128, 64, 32 features; b[3] of Cfg::BOX rows
-    CUtensorMap a[3], b[4], out;
+    // pair: a[0] two strips a copy, a[1] one strip; b[i] two strips of 16 (i + 1) rows, b[8] one of 16 rows
+    // otherwise: a[0..2] K-major boxes of 128, 64, 32 features; b[8] of 16 rows
+    CUtensorMap a[3], b[9], out;
 };
 
 struct Args {
@@ -212,7 +212,7 @@ __global__ void __launch_bounds__(256, 1) k_grouped(const __grid_constant__ Maps
         *abort_flag = 0;
         fence_barrier_init();
         tma_prefetch_map(&maps.a[0]);
-        tma_prefetch_map(&maps.b[3]);
+        tma_prefetch_map(&maps.b[8]);
         tma_prefetch_map(&maps.out);
     }
     if (warp == 1) {
@@ -253,7 +253,7 @@ __global__ void __launch_bounds__(256, 1) k_grouped(const __grid_constant__ Maps
             int g = 0;  // stages issued
             int mapped = -1;
             // one strip a copy, two strips a copy
-            const CUtensorMap *one = is_a ? &maps.a[kPair ? 1 : tiles.h == 128 ? 0 : tiles.h == 64 ? 1 : 2] : &maps.b[3];
+            const CUtensorMap *one = is_a ? &maps.a[kPair ? 1 : tiles.h == 128 ? 0 : tiles.h == 64 ? 1 : 2] : &maps.b[8];
             const CUtensorMap *two = &maps.a[0];
             for (int t = first; ok && t < count; t += stride) {
                 const Tile x = tiles.at(t);
@@ -268,16 +268,15 @@ __global__ void __launch_bounds__(256, 1) k_grouped(const __grid_constant__ Maps
                 const int at = is_a ? x.c0 + static_cast<int>(rank) * 128
                                     : x.r0 + static_cast<int>(rank) * half;
                 if (kPair) {
-                    const bool mn = is_a ? kAm : kBm;                  // M- or N-major
+                    const bool mn = is_a ? kAm : kBm;  // M- or N-major
                     const int plane = is_a && !kBm ? x.e : 0;
-                    const int nb = half > 64 ? 0 : half > 32 ? 1 : 2;  // B K-major: box of 128, 64, 32 rows
-                    const int rows = is_a ? 128 : 128 >> nb;
+                    const int rows = is_a ? 128 : half;
                     const int strips = kBm && !is_a ? (half + 63) / 64 : 2;
-                    const uint32_t bytes = 2 * (32768 + (kBm ? (half + 63) / 64 * 16384 : 256 * (128 >> nb)));
+                    const uint32_t bytes = 2 * (32768 + (kBm ? (half + 63) / 64 * 16384 : 256 * half));
                     // M-/N-major strips are whole along the features, K-major ones along k
                     const int wide = is_a ? args.cols : args.rows;
                     const bool aligned = mn && strips == 2 && at % 64 == 0 && (wide % 64 == 0 || at + 128 <= wide);
-                    if (!is_a && !kBm) two = &maps.b[nb];
+                    if (!is_a && !kBm) two = &maps.b[half / 16 - 1];  // exactly the tile's rows
                     for (int k = 0; k < x.kb; ++k, ++g) {
                         const int slot = g % C::S;
                         if (g >= C::S && !mbar_wait(&empty[slot], ((g / C::S) - 1) & 1, tmo, abort_flag)) {
@@ -375,8 +374,7 @@ __global__ void __launch_bounds__(256, 1) k_grouped(const __grid_constant__ Maps
                     const uint32_t alo = static_cast<uint32_t>(ad), ahi = static_cast<uint32_t>(ad >> 32);
                     const uint32_t blo = static_cast<uint32_t>(bd), bhi = static_cast<uint32_t>(bd >> 32);
                     if (kPair) {
-                        const int half = x.n / 2;
-                        const uint32_t bs = half > 64 ? 1024 : half > 32 ? 512 : 256;  // K-major B: a strip, 16-byte units
+                        const uint32_t bs = x.n / 2 * 8;  // K-major B: a strip of half the rows, in 16-byte units
                         auto mma = [&](int i) {
                             umma_bf16_lo_lead_pair(lead, d, alo + (kAm ? i * 128 : (i >> 2) * 1024 + (i & 3) * 2), ahi,
                                                    blo + (kBm ? i * 128 : (i >> 2) * bs + (i & 3) * 2), bhi, idesc,
@@ -601,12 +599,12 @@ bsl_status launch_grouped_rows(const void *A, int32_t T, const int32_t *offsets,
         // one strip: 64 columns (features, or k) x 128 rows of the weight
         good = make_strip_map(&m.a[0], W->weight, K, N, W->E, 128, 2) &&
                make_map_3d(&m.a[1], W->weight, K, N, W->E, K * 2, K * 2 * N, 64, 128, 128);
-        for (int i = 0; i < 3; ++i) good = good && make_strip_map(&m.b[i], A, args.depth, T, 1, 128 >> i, 2);
+        for (int i = 0; i < 8; ++i) good = good && make_strip_map(&m.b[i], A, args.depth, T, 1, 16 * (i + 1), 2);
     } else {
         for (int i = 0; i < 3; ++i)
             good = good && make_map_3d(&m.a[i], W->weight, K, N, W->E, K * 2, K * 2 * N, 64, 128 >> i, 128);
     }
-    good = good && map_rows(&m.b[3], A, args.depth, T, 64, pair ? Cfg<true>::BOX : Cfg<false>::BOX, 128) &&
+    good = good && map_rows(&m.b[8], A, args.depth, T, 64, 16, 128) &&
            map_rows(&m.out, out, args.cols, T, 32, 32, 0);
     if (!good) return BSL_ERR_CUDA;
     if (transposed) return run<kInputGrad, true>(m, args, s);
@@ -624,7 +622,7 @@ bsl_status launch_grouped_dw(const void *dY, const void *X, int32_t T, const int
         !make_map_3d(&m.out, dW, K, N, W->E, K * 2, K * 2 * N, 32, 32, 0))
         return BSL_ERR_CUDA;
     m.a[0] = base.m[0];  // (prefetched by every kernel)
-    m.b[3] = base.m[0];
+    m.b[8] = base.m[0];
     CUtensorMap *maps = static_cast<CUtensorMap *>(workspace);
     const bsl_status st = cuda_status(launch_dependent(k_expert_maps, W->E, 32, 0, s, base, dY, X, W->N, W->K, offsets,
                                                        W->E, T, maps, W->status));
