@@ -142,7 +142,8 @@ def _check(st: int, where: str):
 
 
 def _stream(t: torch.Tensor):
-    return ctypes.c_void_p(torch.cuda.current_stream(t.device).cuda_stream)
+    """The raw handle of the current stream of t's device."""
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
 
 
 def _cuda_bf16_2d(t: torch.Tensor, name: str, cols: int | None = None):
@@ -613,7 +614,12 @@ def forward_bsr24(X: torch.Tensor, w: Bsr24Weight, bias: torch.Tensor | None = N
 
 
 def _tensor_arg(t, name: str, shape, dtype, like: torch.Tensor | None = None) -> None:
-    """``t`` must be a contiguous CUDA tensor of this shape (None: any size) and dtype."""
+    """``t`` must be a contiguous CUDA tensor of this shape (None: any size) and dtype, on like's device."""
+    if (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.is_contiguous()
+            and (like is None or t.get_device() == like.get_device())):
+        have = t.shape
+        if have == shape or (len(have) == len(shape) == 2 and shape[0] is None and have[1] == shape[1]):
+            return
     if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == dtype and t.dim() == len(shape)):
         raise TypeError(f"{name} must be a {len(shape)}-D {str(dtype)[6:]} CUDA tensor")
     if any(want is not None and have != want for have, want in zip(t.shape, shape)):
@@ -626,7 +632,7 @@ def _tensor_arg(t, name: str, shape, dtype, like: torch.Tensor | None = None) ->
 
 def _out_arg(out, shape, like: torch.Tensor) -> torch.Tensor:
     if out is None:
-        return torch.empty(shape, dtype=torch.bfloat16, device=like.device)
+        return like.new_empty(shape, dtype=torch.bfloat16)
     _tensor_arg(out, "out", shape, torch.bfloat16, like)
     return out
 
@@ -653,6 +659,7 @@ class GroupedWeight:
         self.E, self.N, self.K = int(E), int(N), int(K)
         self.status = torch.zeros(1, dtype=torch.int32, device=weight.device)
         self._c = _GROUPED(self.E, self.N, self.K, self.weight.data_ptr(), self.status.data_ptr())
+        self._workspace_bytes = int(library().bsl_grouped_workspace_bytes(self.cref()))
 
     @property
     def device(self):
@@ -696,8 +703,8 @@ def grouped_backward_weight(dY: torch.Tensor, X: torch.Tensor, Wg: GroupedWeight
     _tensor_arg(X, "X", (dY.shape[0], Wg.K), torch.bfloat16, Wg.weight)
     _tensor_arg(offsets, "offsets", (Wg.E + 1,), torch.int32, X)
     dW = _out_arg(out, (Wg.E, Wg.N, Wg.K), X)
-    nbytes = int(library().bsl_grouped_workspace_bytes(Wg.cref()))
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=X.device)
+    nbytes = Wg._workspace_bytes
+    ws = X.new_empty(nbytes, dtype=torch.uint8)
     _check(library().bsl_grouped_backward_weight(dY.data_ptr(), X.data_ptr(), X.shape[0], offsets.data_ptr(),
                                                  Wg.cref(), dW.data_ptr(), ws.data_ptr(), nbytes, _stream(X)),
            "bsl_grouped_backward_weight")
@@ -803,17 +810,22 @@ class Mx4Tensor:
             raise ValueError("codes must hold a positive multiple of 32 columns (16 bytes) a row")
         _tensor_arg(codes, "codes", codes.shape, torch.uint8)
         _tensor_arg(scales, "scales", (*lead, K // 32), torch.uint8, codes)
-        self.codes, self.scales = codes, scales
-        self.shape = (*lead, K)
-        self._status = None
+        self._set(codes, scales, (*lead, K))
+
+    def _set(self, codes, scales, shape):
+        self.codes, self.scales, self.shape, self.K = codes, scales, shape, shape[-1]
+        self._status = self._c = None
+
+    @classmethod
+    def _of(cls, codes, scales, shape):
+        """Tensors that were made for each other (no checks)."""
+        self = cls.__new__(cls)
+        self._set(codes, scales, shape)
+        return self
 
     @property
     def device(self):
         return self.codes.device
-
-    @property
-    def K(self):
-        return self.shape[-1]
 
     @property
     def status(self) -> torch.Tensor:
@@ -823,9 +835,10 @@ class Mx4Tensor:
 
     def cref(self):
         """The weight's descriptor (one expert for a matrix)."""
-        E, N = (1, *self.shape[:-1]) if len(self.shape) == 2 else self.shape[:-1]
-        return ctypes.byref(_MX4(E, N, self.K, self.codes.data_ptr(), self.scales.data_ptr(),
-                                 self.status.data_ptr()))
+        if self._c is None:
+            E, N = (1, *self.shape[:-1]) if len(self.shape) == 2 else self.shape[:-1]
+            self._c = _MX4(E, N, self.K, self.codes.data_ptr(), self.scales.data_ptr(), self.status.data_ptr())
+        return ctypes.byref(self._c)
 
 
 def quantize_mx4(X: torch.Tensor, out: Mx4Tensor | None = None) -> Mx4Tensor:
@@ -834,16 +847,16 @@ def quantize_mx4(X: torch.Tensor, out: Mx4Tensor | None = None) -> Mx4Tensor:
     6 times the scale.  A block with an infinity or a NaN becomes NaN."""
     if not (isinstance(X, torch.Tensor) and X.dim() >= 2):
         raise TypeError("X must be a bfloat16 CUDA tensor of at least two dimensions")
-    _tensor_arg(X, "X", X.shape, torch.bfloat16)
-    K = X.shape[-1]
+    shape = tuple(X.shape)
+    _tensor_arg(X, "X", shape, torch.bfloat16)
+    *lead, K = shape
     if K <= 0 or K % 32:
         raise ValueError("X's last dimension must be a positive multiple of 32")
     if out is None:
-        lead = tuple(X.shape[:-1])
-        out = Mx4Tensor(torch.empty((*lead, K // 2), dtype=torch.uint8, device=X.device),
-                        torch.empty((*lead, K // 32), dtype=torch.uint8, device=X.device))
-    elif out.shape != tuple(X.shape) or out.device != X.device:
-        raise ValueError(f"out holds {out.shape} on {out.device}, X is {tuple(X.shape)} on {X.device}")
+        out = Mx4Tensor._of(X.new_empty((*lead, K // 2), dtype=torch.uint8),
+                            X.new_empty((*lead, K // 32), dtype=torch.uint8), shape)
+    elif out.shape != shape or out.device != X.device:
+        raise ValueError(f"out holds {out.shape} on {out.device}, X is {shape} on {X.device}")
     _check(library().bsl_mx4_quantize(X.data_ptr(), X.numel() // K, K, out.codes.data_ptr(), out.scales.data_ptr(),
                                       _stream(X)), "bsl_mx4_quantize")
     return out
