@@ -60,11 +60,12 @@
 namespace bsl {
 namespace {
 
-enum Mode { kForward = 0, kInputGrad = 1, kWeightGrad = 2, kForward4 = 3 };
+enum Mode { kForward = 0, kInputGrad = 1, kWeightGrad = 2, kForward4 = 3, kForward4Any = 4 };
+// kForward4: rows of scales in whole 16-byte units (K a multiple of 512); kForward4Any: any K
 
 template <int kMode, bool kPair>
 struct Cfg {
-    static constexpr bool F4 = kMode == kForward4;
+    static constexpr bool F4 = kMode == kForward4 || kMode == kForward4Any;
     static constexpr int CG = kPair ? 2 : 1;
     static constexpr int BR = kPair ? (F4 ? 224 : 256) : 64;  // rows per tile, at most (h = 128)
     static constexpr int STEP = 16 * CG;                 // granularity of the rows (MMA N)
@@ -197,69 +198,112 @@ __device__ __forceinline__ int pick_h(const int32_t *off, int E, int cols)
 // scales lie in plain rows in global memory, wherever an expert's rows begin,
 // so warps load each row's bytes (ahead, in registers) and write the chunks.
 
-// W words of a row's scale bytes from byte0 on, zeros past the row's end (a
-// scale of 2^-127 on zero codes; a NaN byte of the next row must not count)
-// and for rows that do not exist.  base holds `total` bytes.
+// Loads must not wait for one another, so nothing is computed on what was
+// loaded before it is stored.  Bytes past the row's end count as zeros (a
+// scale of 2^-127 on zero codes; a NaN byte of the next row must not reach
+// them), and so do rows that do not exist.
+
+// Whole rows of 16-byte units: W words of a row from byte0 on.
 template <int W>
-__device__ __forceinline__ void scale_words(const uint8_t *base, int64_t total, int32_t stride, int64_t row, bool exists,
-                                            int32_t byte0, uint32_t *w)
+__device__ __forceinline__ void load_words(const uint8_t *base, int32_t stride, int64_t row, bool exists, int32_t byte0,
+                                           uint32_t *w)
 {
     constexpr int V = W < 4 ? W : 4;
-    const int32_t left = exists ? stride - byte0 : 0;
-    const int64_t at = row * stride + byte0;
-    if (stride % (4 * V) == 0 && left >= 4 * W) {
+    const uint8_t *at = base + row * stride + byte0;
 #pragma unroll
-        for (int i = 0; i < W; i += V) {
-            if constexpr (V == 4) {
-                const uint4 v = __ldg(reinterpret_cast<const uint4 *>(base + at + 4 * i));
-                w[i] = v.x, w[i + 1] = v.y, w[i + 2] = v.z, w[i + 3] = v.w;
-            } else {
-                const uint2 v = __ldg(reinterpret_cast<const uint2 *>(base + at + 4 * i));
-                w[i] = v.x, w[i + 1] = v.y;
-            }
+    for (int i = 0; i < W; i += V) {
+        const bool in = exists && byte0 + 4 * i < stride;
+        if constexpr (V == 4) {
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (in) v = __ldg(reinterpret_cast<const uint4 *>(at + 4 * i));
+            w[i] = v.x, w[i + 1] = v.y, w[i + 2] = v.z, w[i + 3] = v.w;
+        } else {
+            uint2 v = make_uint2(0, 0);
+            if (in) v = __ldg(reinterpret_cast<const uint2 *>(at + 4 * i));
+            w[i] = v.x, w[i + 1] = v.y;
         }
-        return;
     }
-    // rows that start anywhere: two aligned words around each, never past the last byte
-    auto word = [&](int64_t a) -> uint32_t {
-        if (a + 4 <= total) return __ldg(reinterpret_cast<const uint32_t *>(base + a));
-        uint32_t v = 0;
-        for (int b = 0; a + b < total; ++b) v |= static_cast<uint32_t>(base[a + b]) << (8 * b);
-        return v;
-    };
+}
+
+// Rows that start at any byte: the W + 1 aligned words around them, as far as
+// they lie inside the `total` bytes ...
+template <int W>
+__device__ __forceinline__ void load_words_any(const uint8_t *base, int64_t total, int32_t stride, int64_t row, bool exists,
+                                               int32_t byte0, uint32_t *w)
+{
+    const int64_t at = (row * stride + byte0) & ~int64_t(3);
+#pragma unroll
+    for (int i = 0; i <= W; ++i) {
+        w[i] = 0;
+        if (exists && at + 4 * i + 4 <= total) w[i] = __ldg(reinterpret_cast<const uint32_t *>(base + at + 4 * i));
+    }
+}
+
+// ... and, when they are stored, shifted into place and cut at the row's end.
+// The last bytes of the array may fill no whole word: they are read here.
+template <int W>
+__device__ __forceinline__ void shift_words(const uint8_t *base, int64_t total, int32_t stride, int64_t row, bool exists,
+                                            int32_t byte0, const uint32_t *raw, uint32_t *w)
+{
+    const int64_t at = row * stride + byte0, low = at & ~int64_t(3);
+    const int32_t left = exists ? stride - byte0 : 0;
+    const uint32_t shift = static_cast<uint32_t>(at & 3) * 8;
+    uint32_t r[W + 1];
+#pragma unroll
+    for (int i = 0; i <= W; ++i) {
+        r[i] = raw[i];
+        const int64_t a = low + 4 * i;
+        if (exists && a < total && a + 4 > total)
+            for (int b = 0; a + b < total; ++b) r[i] |= static_cast<uint32_t>(base[a + b]) << (8 * b);
+    }
 #pragma unroll
     for (int i = 0; i < W; ++i) {
         const int32_t bytes = left - 4 * i;
-        uint32_t v = 0;
-        if (bytes > 0) {
-            const int64_t a = at + 4 * i;
-            const uint32_t shift = static_cast<uint32_t>(a & 3) * 8;
-            v = word(a & ~int64_t(3));
-            if (shift) v = __funnelshift_r(v, word((a & ~int64_t(3)) + 4), shift);
-            if (bytes < 4) v &= (1u << (8 * bytes)) - 1u;
-        }
-        w[i] = v;
+        const uint32_t v = __funnelshift_r(r[i], r[i + 1], shift);
+        w[i] = bytes >= 4 ? v : bytes <= 0 ? 0 : v & ((1u << (8 * bytes)) - 1u);
     }
 }
 
-// One warp's part of a stage: R rows a lane (row, row + 32, ...), W words each.
-template <int R, int W>
-__device__ __forceinline__ void load_scales(const uint8_t *base, int64_t total, int32_t stride, int64_t row, int32_t live,
-                                            int32_t byte0, uint32_t *w)
+// Where a lane finds its rows of a stage: row, row + 32, ... of which `live` exist from `row` on.
+struct ScaleRows {
+    const uint8_t *base;
+    int64_t total, row;
+    int32_t stride, live, byte0;
+};
+
+// One warp's part of a stage: R rows a lane, W words each (W + 1 as loaded, for any K).
+template <bool kAny, int R, int W>
+__device__ __forceinline__ void load_scales(const ScaleRows &s, uint32_t *w)
 {
 #pragma unroll
-    for (int c = 0; c < R; ++c)
-        scale_words<W>(base, total, stride, row + 32 * c, 32 * c < live, byte0, w + c * W);
+    for (int c = 0; c < R; ++c) {
+        if constexpr (kAny)
+            load_words_any<W>(s.base, s.total, s.stride, s.row + 32 * c, 32 * c < s.live, s.byte0, w + c * (W + 1));
+        else
+            load_words<W>(s.base, s.stride, s.row + 32 * c, 32 * c < s.live, s.byte0, w + c * W);
+    }
 }
 
 // Chunk j of the stage holds word j of every row: 16 bytes a lane.
-template <int R, int W>
-__device__ __forceinline__ void store_scales(uint8_t *dst, int step, int lane, const uint32_t *w)
+template <bool kAny, int R, int W>
+__device__ __forceinline__ void store_scales(uint8_t *dst, int step, int lane, const ScaleRows &s, const uint32_t *raw)
 {
+    uint32_t w[4][W];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        if (c >= R) {
+#pragma unroll
+            for (int j = 0; j < W; ++j) w[c][j] = 0;
+        } else if constexpr (kAny) {
+            shift_words<W>(s.base, s.total, s.stride, s.row + 32 * c, 32 * c < s.live, s.byte0, raw + c * (W + 1), w[c]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < W; ++j) w[c][j] = raw[c * W + j];
+        }
+    }
 #pragma unroll
     for (int j = 0; j < W; ++j)
-        *reinterpret_cast<uint4 *>(dst + j * step + lane * 16) =
-            make_uint4(w[j], R > 1 ? w[W + j] : 0, R > 2 ? w[(R > 2 ? 2 : 0) * W + j] : 0, R > 3 ? w[(R > 3 ? 3 : 0) * W + j] : 0);
+        *reinterpret_cast<uint4 *>(dst + j * step + lane * 16) = make_uint4(w[0][j], w[1][j], w[2][j], w[3][j]);
 }
 
 // A walk over this CTA's stages, tile after tile.
@@ -286,43 +330,48 @@ struct Walk {
 
 // Pair: warp 8 copies the scales of A, 9 and 10 those of B's rows 0 .. 127 and
 // 128 .. 223 (both CTAs hold all of B's).  Otherwise warp 8 A, warp 9 B.
-template <bool kPair>
-__device__ __forceinline__ void copy_scales(const Tiles<kForward4, kPair> &tiles, const Args &args, uint8_t *stages,
-                                            uint64_t *full, uint64_t *empty, const volatile int *abort_flag, int first,
+template <int kMode, bool kPair>
+__device__ __forceinline__ void copy_scales(const Tiles<kMode, kPair> &tiles, const Args &args, uint8_t *stages,
+                                            uint64_t *full, uint64_t *empty, volatile int *abort_flag, int first,
                                             int stride, int count, uint32_t rank)
 {
-    using C = Cfg<kForward4, kPair>;
-    constexpr int P = 4;                  // stages ahead
-    constexpr int WORDS = kPair ? 16 : 8; // a lane's words of a stage
+    using C = Cfg<kMode, kPair>;
+    constexpr bool kAny = kMode == kForward4Any;
+    constexpr int P = 4;  // stages ahead
+    constexpr int WORDS = (kPair ? 16 : 8) + (kAny ? 4 : 0);  // a lane's words of a stage
     const int part = (threadIdx.x >> 5) - 8, lane = threadIdx.x & 31;
-    const uint8_t *base = part ? args.b_scales : args.a_scales;
-    const int64_t rows = part ? args.T : static_cast<int64_t>(args.E) * args.cols;
-    const int64_t total = rows * args.scale_bytes;
     const int J = kPair ? 2 : 128 / tiles.h;
-    Walk<kForward4, kPair> ahead(tiles, first, stride, count), now(tiles, first, stride, count);
+    Walk<kMode, kPair> ahead(tiles, first, stride, count), now(tiles, first, stride, count);
     uint32_t w[P][WORDS];
 
+    auto rows = [&](const Walk<kMode, kPair> &at) {
+        ScaleRows s;
+        s.stride = args.scale_bytes;
+        s.byte0 = at.k * J * 8;
+        if (part == 0) {
+            const int c = at.x.c0 + static_cast<int>(rank) * 128 + lane;
+            s.base = args.a_scales;
+            s.total = static_cast<int64_t>(args.E) * args.cols * s.stride;
+            s.row = static_cast<int64_t>(at.x.e) * args.cols + c;
+            s.live = args.cols - c;
+        } else {
+            const int r = 128 * (part - 1) + lane;
+            s.base = args.b_scales;
+            s.total = static_cast<int64_t>(args.T) * s.stride;
+            s.row = at.x.r0 + r;
+            s.live = at.x.valid - r;
+        }
+        return s;
+    };
     auto load = [&](uint32_t *v) {
         if (!ahead.live()) return;
-        const Tile &x = ahead.x;
-        const int byte0 = ahead.k * J * 8;
-        // this lane's first row, and the rows that exist from it on
-        int64_t row;
-        int live;
-        if (part == 0) {
-            const int c = x.c0 + static_cast<int>(rank) * 128 + lane;
-            row = static_cast<int64_t>(x.e) * args.cols + c;
-            live = args.cols - c;
-        } else {
-            row = x.r0 + 128 * (part - 1) + lane;
-            live = x.valid - 128 * (part - 1) - lane;
-        }
-        if (kPair) load_scales<4, 4>(base, total, args.scale_bytes, row, live, byte0, v);
-        else if (J == 1 && part == 0) load_scales<4, 2>(base, total, args.scale_bytes, row, live, byte0, v);
-        else if (J == 1) load_scales<2, 2>(base, total, args.scale_bytes, row, live, byte0, v);
-        else if (J == 2 && part == 0) load_scales<2, 4>(base, total, args.scale_bytes, row, live, byte0, v);
-        else if (J == 2) load_scales<1, 4>(base, total, args.scale_bytes, row, live, byte0, v);
-        else load_scales<1, 8>(base, total, args.scale_bytes, row, live, byte0, v);
+        const ScaleRows s = rows(ahead);
+        if (kPair) load_scales<kAny, 4, 4>(s, v);
+        else if (J == 1 && part == 0) load_scales<kAny, 4, 2>(s, v);
+        else if (J == 1) load_scales<kAny, 2, 2>(s, v);
+        else if (J == 2 && part == 0) load_scales<kAny, 2, 4>(s, v);
+        else if (J == 2) load_scales<kAny, 1, 4>(s, v);
+        else load_scales<kAny, 1, 8>(s, v);
         ahead.next();
     };
 #pragma unroll
@@ -339,12 +388,13 @@ __device__ __forceinline__ void copy_scales(const Tiles<kForward4, kPair> &tiles
                 break;
             }
             uint8_t *dst = stages + slot * C::STAGE + C::A_BYTES + C::B_BYTES + (part ? C::SA_BYTES : 0);
-            if (kPair) store_scales<4, 4>(part == 2 ? dst + 512 : dst, part ? 1024 : 512, lane, w[p]);
-            else if (J == 1 && part == 0) store_scales<4, 2>(dst, 512, lane, w[p]);
-            else if (J == 1) store_scales<2, 2>(dst, 512, lane, w[p]);
-            else if (J == 2 && part == 0) store_scales<2, 4>(dst, 512, lane, w[p]);
-            else if (J == 2) store_scales<1, 4>(dst, 512, lane, w[p]);
-            else store_scales<1, 8>(dst, 512, lane, w[p]);
+            const ScaleRows r = rows(now);
+            if (kPair) store_scales<kAny, 4, 4>(part == 2 ? dst + 512 : dst, part ? 1024 : 512, lane, r, w[p]);
+            else if (J == 1 && part == 0) store_scales<kAny, 4, 2>(dst, 512, lane, r, w[p]);
+            else if (J == 1) store_scales<kAny, 2, 2>(dst, 512, lane, r, w[p]);
+            else if (J == 2 && part == 0) store_scales<kAny, 2, 4>(dst, 512, lane, r, w[p]);
+            else if (J == 2) store_scales<kAny, 1, 4>(dst, 512, lane, r, w[p]);
+            else store_scales<kAny, 1, 8>(dst, 512, lane, r, w[p]);
             fence_async_smem();
             __syncwarp();
             if (lane == 0) {
@@ -356,7 +406,7 @@ __device__ __forceinline__ void copy_scales(const Tiles<kForward4, kPair> &tiles
         }
     }
     if (lane == 0 && !ok) {
-        *const_cast<volatile int *>(abort_flag) = 1;
+        *abort_flag = 1;
         set_status(args.status, BSL_ERR_TIMEOUT);
     }
     __syncwarp();
@@ -638,7 +688,7 @@ __global__ void __launch_bounds__(Cfg<kMode, kPair>::THREADS, 1)
         }
         __syncwarp();
     } else if (C::F4 && warp >= 8) {
-        if constexpr (C::F4) copy_scales<kPair>(tiles, args, stages, full, empty, abort_flag, first, stride, count, rank);
+        if constexpr (C::F4) copy_scales<kMode, kPair>(tiles, args, stages, full, empty, abort_flag, first, stride, count, rank);
     } else {
         // ------------------------------------------------------------ epilogue
         // Warp q reads TMEM lanes 32q .. 32q+31: features c0 + 32q + lane of its CTA.

@@ -30,7 +30,8 @@ bsl_status launch_mx4_fwd(const uint8_t *xc, const uint8_t *xs, int32_t T, const
     const bool pair = T > static_cast<int64_t>(W->E) * 32;
     Maps m;
     if (!forward_maps(m, W->codes, N, depth, W->E, xc, T, Y, pair)) return BSL_ERR_CUDA;
-    return pair ? run<kForward4, true>(m, args, s) : run<kForward4, false>(m, args, s);
+    if (W->K % 512 == 0) return pair ? run<kForward4, true>(m, args, s) : run<kForward4, false>(m, args, s);
+    return pair ? run<kForward4Any, true>(m, args, s) : run<kForward4Any, false>(m, args, s);
 }
 
 }  // namespace bsl
