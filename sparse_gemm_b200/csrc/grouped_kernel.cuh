@@ -85,8 +85,9 @@ struct Cfg {
     static constexpr int OUT = 4 * 2 * CHUNK;            // two chunks per epilogue warp
     static constexpr int BARS = (2 * S + 5) * 8 + 16;
     static constexpr int SMEM = 1024 + S * STAGE + OUT + BARS + 2 * (kMaxExperts + 1) * 4;
-    static constexpr int SCALE_WARPS = !F4 ? 0 : kPair ? 3 : 2;
-    static constexpr int THREADS = 256 + 32 * SCALE_WARPS;
+    static constexpr int SCALE_WARPS = !F4 ? 0 : kPair ? 3 : 2;  // of a stage
+    static constexpr int SCALE_SETS = 2;                         // taking stages in turn
+    static constexpr int THREADS = 256 + 32 * SCALE_WARPS * SCALE_SETS;
     static_assert(SMEM <= 227 * 1024, "shared memory");
     static_assert(STAGE % 1024 == 0, "swizzle atoms");
     static_assert(!F4 || SB_COL + SB_BYTES / 128 <= TMEM, "TMEM columns");
@@ -319,17 +320,20 @@ struct Walk {
         if (t < count) x = tiles.at(t);
     }
     __device__ __forceinline__ bool live() const { return t < count; }
-    __device__ __forceinline__ void next()
+    __device__ __forceinline__ void skip(int n)
     {
-        if (++k < x.kb) return;
-        k = 0;
-        t += stride;
-        if (t < count) x = tiles.at(t);
+        for (k += n; live() && k >= x.kb;) {
+            k -= x.kb;
+            t += stride;
+            if (t < count) x = tiles.at(t);
+        }
     }
 };
 
-// Pair: warp 8 copies the scales of A, 9 and 10 those of B's rows 0 .. 127 and
-// 128 .. 223 (both CTAs hold all of B's).  Otherwise warp 8 A, warp 9 B.
+// Pair: one warp copies the scales of A, two those of B's rows 0 .. 127 and
+// 128 .. 223 (both CTAs hold all of B's).  Otherwise one A, one B.  The fence
+// that hands a stage to the tensor core waits for the warp's loads under way,
+// so two sets of warps take the stages in turn: each has two stages' time.
 template <int kMode, bool kPair>
 __device__ __forceinline__ void copy_scales(const Tiles<kMode, kPair> &tiles, const Args &args, uint8_t *stages,
                                             uint64_t *full, uint64_t *empty, volatile int *abort_flag, int first,
@@ -337,11 +341,14 @@ __device__ __forceinline__ void copy_scales(const Tiles<kMode, kPair> &tiles, co
 {
     using C = Cfg<kMode, kPair>;
     constexpr bool kAny = kMode == kForward4Any;
-    constexpr int P = 4;  // stages ahead
+    constexpr int P = 2;  // a set's stages ahead
     constexpr int WORDS = (kPair ? 16 : 8) + (kAny ? 4 : 0);  // a lane's words of a stage
-    const int part = (threadIdx.x >> 5) - 8, lane = threadIdx.x & 31;
+    const int part = ((threadIdx.x >> 5) - 8) % C::SCALE_WARPS, set = ((threadIdx.x >> 5) - 8) / C::SCALE_WARPS;
+    const int lane = threadIdx.x & 31;
     const int J = kPair ? 2 : 128 / tiles.h;
-    Walk<kMode, kPair> ahead(tiles, first, stride, count), now(tiles, first, stride, count);
+    Walk<kMode, kPair> now(tiles, first, stride, count);
+    now.skip(set);
+    Walk<kMode, kPair> ahead = now;
     uint32_t w[P][WORDS];
 
     auto rows = [&](const Walk<kMode, kPair> &at) {
@@ -372,16 +379,16 @@ __device__ __forceinline__ void copy_scales(const Tiles<kMode, kPair> &tiles, co
         else if (J == 2 && part == 0) load_scales<kAny, 2, 4>(s, v);
         else if (J == 2) load_scales<kAny, 1, 4>(s, v);
         else load_scales<kAny, 1, 8>(s, v);
-        ahead.next();
+        ahead.skip(C::SCALE_SETS);
     };
 #pragma unroll
     for (int p = 0; p < P; ++p) load(w[p]);
     bool ok = true;
-    for (int g0 = 0; ok && now.live(); g0 += P) {
+    for (int g0 = set; ok && now.live(); g0 += P * C::SCALE_SETS) {
 #pragma unroll
         for (int p = 0; p < P; ++p) {
             if (!ok || !now.live()) break;
-            const int g = g0 + p, slot = g % C::S;
+            const int g = g0 + p * C::SCALE_SETS, slot = g % C::S;
             if (g >= C::S &&
                 __any_sync(0xffffffffu, !mbar_wait(&empty[slot], ((g / C::S) - 1) & 1, args.timeout_ns, abort_flag))) {
                 ok = false;
@@ -401,7 +408,7 @@ __device__ __forceinline__ void copy_scales(const Tiles<kMode, kPair> &tiles, co
                 if (kPair) mbar_arrive_cluster(cluster_addr(&full[slot], 0));
                 else mbar_arrive(&full[slot]);
             }
-            now.next();
+            now.skip(C::SCALE_SETS);
             load(w[p]);
         }
     }
