@@ -25,7 +25,9 @@ __global__ void __launch_bounds__(32)
     __shared__ alignas(128) CUtensorMap m[4];
     dependents_may_launch();
     wait_for_prior_grid();
-    load_offsets(offsets, E, T, off, blockIdx.x == 0 ? status : nullptr);
+    fetch_offsets(offsets, E, T, off);
+    __syncwarp();
+    clamp_offsets(E, T, off, blockIdx.x == 0 ? status : nullptr);
     const int lane = threadIdx.x, e = blockIdx.x;
     const int rows = off[e + 1] - off[e];
     uint32_t *w = reinterpret_cast<uint32_t *>(m);
@@ -70,22 +72,9 @@ bsl_status launch_grouped_rows(const void *A, int32_t T, const int32_t *offsets,
     args.depth = transposed ? W->N : W->K;
     args.zero_rest = zero_rest;
     args.timeout_ns = wait_timeout_ns();
-    // few rows an expert: the weight's bytes bound the call, and the unpaired
-    // kernel spreads them over the SMs
-    const bool pair = transposed || T > static_cast<int64_t>(W->E) * 32;
-    const int64_t N = W->N, K = W->K;
     Maps m;
-    if (!transposed) {
-        if (!forward_maps(m, W->weight, N, K, W->E, A, T, out, pair)) return BSL_ERR_CUDA;
-    } else {
-        bool good = make_strip_map(&m.a[0], W->weight, K, N, W->E, 128, 2) &&
-                    make_map_3d(&m.a[1], W->weight, K, N, W->E, K * 2, K * 2 * N, 64, 128, 128) &&
-                    map_rows(&m.b[8], A, N, T, 64, 16, 128) && map_rows(&m.out, out, K, T, 32, 32, 0);
-        for (int i = 0; i < 8; ++i) good = good && make_strip_map(&m.b[i], A, N, T, 1, 16 * (i + 1), 2);
-        if (!good) return BSL_ERR_CUDA;
-        return run<kInputGrad, true>(m, args, s);
-    }
-    return pair ? run<kForward, true>(m, args, s) : run<kForward, false>(m, args, s);
+    if (!row_maps(m, W->weight, W->E, W->N, W->K, A, T, args.depth, out, args.cols)) return BSL_ERR_CUDA;
+    return transposed ? run<kInputGrad>(m, args, s) : run<kForward>(m, args, s);
 }
 
 bsl_status launch_grouped_dw(const void *dY, const void *X, int32_t T, const int32_t *offsets, const bsl_grouped *W,
@@ -98,8 +87,7 @@ bsl_status launch_grouped_dw(const void *dY, const void *X, int32_t T, const int
         !make_strip_map(&base.m[2], dY, N, T, 1, 128, 2) || !make_strip_map(&base.m[3], X, K, T, 1, 128, 2) ||
         !make_map_3d(&m.out, dW, K, N, W->E, K * 2, K * 2 * N, 32, 32, 0))
         return BSL_ERR_CUDA;
-    m.a[0] = base.m[0];  // (prefetched by every kernel)
-    m.b[8] = base.m[0];
+    m.a[0] = base.m[2];  // (prefetched by every kernel)
     CUtensorMap *maps = static_cast<CUtensorMap *>(workspace);
     const bsl_status st = cuda_status(launch_dependent(k_expert_maps, W->E, 32, 0, s, base, dY, X, W->N, W->K, offsets,
                                                        W->E, T, maps, W->status));
@@ -113,7 +101,7 @@ bsl_status launch_grouped_dw(const void *dY, const void *X, int32_t T, const int
     args.rows = W->N;
     args.status = W->status;
     args.timeout_ns = wait_timeout_ns();
-    return run<kWeightGrad, true>(m, args, s);
+    return run<kWeightGrad>(m, args, s);
 }
 
 }  // namespace bsl

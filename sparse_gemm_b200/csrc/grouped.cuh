@@ -9,24 +9,25 @@ namespace bsl {
 
 constexpr int kMaxExperts = BSL_GROUPED_MAX_EXPERTS;
 
-// Copy offsets[0..E] into shared memory, made safe by the calling warp: every
-// entry is clamped to [previous entry, T], so no value on the device can lead
-// outside the matrices; one that had to be clamped is reported in `status`.
-// offsets null: one expert (E = 1) owns all rows.
-__device__ __forceinline__ void load_offsets(const int32_t *offsets, int32_t E, int32_t T, int32_t *off,
-                                             int32_t *status)
+// The experts' offsets[0..E] into shared memory, by the whole block (which
+// synchronises before clamp_offsets).  offsets null: one expert (E = 1) owns
+// all rows.
+__device__ __forceinline__ void fetch_offsets(const int32_t *offsets, int32_t E, int32_t T, int32_t *off)
+{
+    for (int i = threadIdx.x; i <= E; i += blockDim.x) off[i] = offsets ? offsets[i] : i ? T : 0;
+}
+
+// Make them safe, by one warp: every entry is clamped to [previous entry, T],
+// so no value on the device can lead outside the matrices; one that had to be
+// clamped is reported in `status`.  The block synchronises before it uses them.
+__device__ __forceinline__ void clamp_offsets(int32_t E, int32_t T, int32_t *off, int32_t *status)
 {
     const int lane = threadIdx.x & 31;
-    if (!offsets) {
-        if (lane < 2) off[lane] = lane ? T : 0;
-        __syncwarp();
-        return;
-    }
     int carry = 0;
     bool bad = false;
     for (int i0 = 0; i0 <= E; i0 += 32) {
         const int i = i0 + lane;
-        const int raw = i <= E ? offsets[i] : 0;
+        const int raw = i <= E ? off[i] : 0;
         int v = raw < 0 ? 0 : raw > T ? T : raw;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {

@@ -45,7 +45,9 @@ __global__ void __launch_bounds__(kWarps * 32)
     const int col = (cols - e * tiles) * kCols + 8 * lane;  // N is a multiple of 8
     dependents_may_launch();
     wait_for_prior_grid();
-    if (warp == 0) load_offsets(offsets, E, T, off, nullptr);
+    fetch_offsets(offsets, E, T, off);
+    __syncthreads();
+    if (warp == 0) clamp_offsets(E, T, off, nullptr);
     __syncthreads();
     float acc[8] = {};
     if (col < N) {

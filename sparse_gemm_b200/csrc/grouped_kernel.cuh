@@ -34,20 +34,19 @@
 // are dealt round robin; no counters and no workspace are shared by calls,
 // and every output is one sum in a fixed order.
 //
-// kPair: clusters of two CTAs on tiles of 256 features x 256 rows
-// (cta_group::2, M = 256; each CTA holds its 128 rows of A and half of B),
-// three stages of 128 k.  Bound by the tensor pipe only while the copies keep
-// up (32 KB per 64 k and SM, 64 bytes a clock), and those go by their number:
-// an operand's stage is one copy of 32 KB, two strips of 128-byte rows.  At
-// 16384 x 4096 x 14336, 8 experts, kernels back to back (clock held by power
-// at 1.1-1.3 GHz): one 32 KB copy 1412 / 1459 / 1460 us for the three, copies
-// of 16 KB and stages of 64 k 1460 / 1575 / 1540, of 8 KB (gradients) 1775.
-//
-// Otherwise (forward with few rows, which reads each weight once): one CTA on
-// `h` = 128, 64 or 32 features x 64, 32 or 16 rows; a stage always holds
-// 16 KB of the weight, i.e. 64, 128 or 256 k, so small h only spreads the same
-// stream over more SMs.  The MMA still takes 128 rows of A; those past h are
-// other bytes of the ring and reach lanes that are never stored.
+// Clusters of two CTAs work on tiles of 256 features x up to 256 rows
+// (cta_group::2, M = 256; each CTA holds its 128 rows of A and half of B) with
+// three stages of 128 k.  With many rows the tensor pipe bounds it, as long as
+// the copies keep up (32 KB per 64 k and SM, 64 bytes a clock), and those go
+// by their number: an operand's stage is one copy of 32 KB, two strips of
+// 128-byte rows.  At 16384 x 4096 x 14336, 8 experts, kernels back to back
+// (clock held by power at 1.1-1.3 GHz): one 32 KB copy 1412 / 1459 / 1460 us
+// for the three, copies of 16 KB and stages of 64 k 1460 / 1575 / 1540, of 8
+// KB (gradients) 1775.  With few rows the weight's bytes bound it: 64 rows of
+// 16 experts of 11008 x 4096 take 237 us (6.1 TB/s).  There, too, the pair is
+// ahead of one CTA on tiles of 128 features (240 us; 93 against 110 us with
+// 4-bit operands): a dependent MMA takes about 90 clocks however few rows it
+// has, and the pair's covers twice the weight.
 //
 // Every wait is bounded (BSL_ERR_TIMEOUT in the status word, then all roles
 // leave through an abort flag).
@@ -60,97 +59,92 @@
 namespace bsl {
 namespace {
 
+// kForward4: 4-bit operands, rows of scales in whole 16-byte units (K a multiple of 512); kForward4Any: any K
 enum Mode { kForward = 0, kInputGrad = 1, kWeightGrad = 2, kForward4 = 3, kForward4Any = 4 };
-// kForward4: rows of scales in whole 16-byte units (K a multiple of 512); kForward4Any: any K
 
-template <int kMode, bool kPair>
+template <int kMode>
 struct Cfg {
     static constexpr bool F4 = kMode == kForward4 || kMode == kForward4Any;
-    static constexpr int CG = kPair ? 2 : 1;
-    static constexpr int BR = kPair ? (F4 ? 224 : 256) : 64;  // rows per tile, at most (h = 128)
-    static constexpr int STEP = 16 * CG;                 // granularity of the rows (MMA N)
-    static constexpr int BOX = 16;                       // rows of B's smallest copy box
-    static constexpr int BK = kPair ? 128 : 64;          // k per stage (h = 128)
+    static constexpr bool AM = kMode == kInputGrad || kMode == kWeightGrad;  // A is M-major
+    static constexpr bool BN = kMode == kWeightGrad;                         // B is N-major
+    static constexpr int BC = 256;                   // features per tile
+    static constexpr int BR = F4 ? 224 : 256;        // rows per tile, at most (4 bits: TMEM holds scales too)
+    static constexpr int STEP = 32;                  // granularity of the rows (MMA N)
+    static constexpr int BK = 128;                   // k per stage (two-byte columns)
     static constexpr int A_BYTES = 128 * BK * 2;
-    static constexpr int B_BYTES = BR / CG * BK * 2;
+    static constexpr int B_BYTES = BR / 2 * BK * 2;
     // scales of a stage: chunks of 512 bytes for 128 rows x 128 elements
-    static constexpr int SA_BYTES = !F4 ? 0 : kPair ? 4 * 512 : 8 * 512;
-    static constexpr int SB_BYTES = !F4 ? 0 : 8 * 512;
+    static constexpr int SA_BYTES = F4 ? 4 * 512 : 0;
+    static constexpr int SB_BYTES = F4 ? 8 * 512 : 0;
     static constexpr int STAGE = A_BYTES + B_BYTES + SA_BYTES + SB_BYTES;
-    static constexpr int S = kPair ? 3 : 196608 / STAGE; // otherwise 8 stages, 6 with scales
-    // two accumulators, then the scales of the stage at work (A 4, B 4 or 8 columns a chunk)
+    static constexpr int S = 3;
+    // two accumulators, then the scales of the stage at work (A 4, B 8 columns a chunk)
     static constexpr int SA_COL = 2 * BR, SB_COL = SA_COL + SA_BYTES / 128;
-    static constexpr int TMEM = !F4 ? 2 * BR : kPair ? 512 : 256;
+    static constexpr int TMEM = 512;
     static constexpr int CHUNK = 32 * 32 * 2;
-    static constexpr int OUT = 4 * 2 * CHUNK;            // two chunks per epilogue warp
-    static constexpr int BARS = (2 * S + 5) * 8 + 16;
+    static constexpr int OUT = 4 * 2 * CHUNK;        // two chunks per epilogue warp
+    static constexpr int BARS = (2 * S + 5) * 8 + 8;
     static constexpr int SMEM = 1024 + S * STAGE + OUT + BARS + 2 * (kMaxExperts + 1) * 4;
-    static constexpr int SCALE_WARPS = !F4 ? 0 : kPair ? 3 : 2;  // of a stage
-    static constexpr int SCALE_SETS = 2;                         // taking stages in turn
-    static constexpr int THREADS = 256 + 32 * SCALE_WARPS * SCALE_SETS;
+    static constexpr int SCALE_WARPS = F4 ? 3 : 0;   // of a stage
+    static constexpr int THREADS = 256 + 2 * 32 * SCALE_WARPS;
     static_assert(SMEM <= 227 * 1024, "shared memory");
     static_assert(STAGE % 1024 == 0, "swizzle atoms");
-    static_assert(!F4 || SB_COL + SB_BYTES / 128 <= TMEM, "TMEM columns");
+    static_assert(SB_COL + SB_BYTES / 128 <= TMEM, "TMEM columns");
 };
 
 struct Maps {
-    // pair: a[0] two strips a copy, a[1] one strip; b[i] two strips of 16 (i + 1) rows, b[8] one of 16 rows
-    // otherwise: a[0..2] K-major boxes of 128, 64, 32 features; b[8] of 16 rows
-    CUtensorMap a[3], b[9], out;
+    CUtensorMap a[2];  // A: two strips a copy, one strip (128 rows of K, or of features, each)
+    CUtensorMap b[9];  // K-major B: b[i] two strips of 16 (i + 1) rows, b[8] one of 16 rows
+    CUtensorMap out;
 };
 
 struct Args {
     const int32_t *offsets;
     const __nv_bfloat16 *bias;
     __nv_bfloat16 *out;
-    const CUtensorMap *expert_maps;  // weight gradient: [E][4], see k_expert_maps
+    const CUtensorMap *expert_maps;      // weight gradient: [E][4], see k_expert_maps
     int32_t *status;
     int32_t T, E;
-    int32_t cols, rows, depth;       // of the product; the ragged one is unused
+    int32_t cols, rows, depth;           // of the product; the ragged one is unused
     int32_t zero_rest;
-    const uint8_t *a_scales, *b_scales;  // 4-bit forward: [E][cols][scale_bytes], [T][scale_bytes]
+    const uint8_t *a_scales, *b_scales;  // 4 bits: [E][cols][scale_bytes], [T][scale_bytes]
     int32_t scale_bytes;
     uint64_t timeout_ns;
 };
 
 struct Tile {
-    int e, c0;        // expert, first column
-    int r0;           // first row: of the matrix, or of the expert's dW
-    int n, valid;     // MMA N, rows that exist
-    int k, kb;        // length of the sums, stages
+    int e, c0;     // expert, first feature
+    int r0;        // first row: of the matrix, or of the expert's dW
+    int n, valid;  // MMA N, rows that exist
+    int k, kb;     // length of the sums, stages
 };
 
 // The tile list of a launch, the same in every CTA.
-template <int kMode, bool kPair>
+template <int kMode>
 struct Tiles {
     const int32_t *off, *start;
-    int E, h, cols, rows, depth;
-
-    __device__ __forceinline__ int features() const { return kPair ? 256 : h; }
-    __device__ __forceinline__ int most() const { return kPair ? Cfg<kMode, kPair>::BR : h / 2; }
-    __device__ __forceinline__ int stage_k() const { return kPair ? 128 : 64 * (128 / h); }
-    __device__ __forceinline__ int count() const { return start[E]; }
+    int E, cols, rows, depth;
 
     __device__ __forceinline__ Tile at(int t) const
     {
+        using C = Cfg<kMode>;
         Tile x;
         x.e = expert_of(start, E, t);
         const int first = off[x.e], own = off[x.e + 1] - first;
         const int r = kMode == kWeightGrad ? rows : own;
-        constexpr int step = Cfg<kMode, kPair>::STEP;
         int ri, ci, r0;
-        tile_place(t - start[x.e], (r + most() - 1) / most(), (cols + features() - 1) / features(), ri, ci);
-        x.c0 = ci * features();
+        tile_place(t - start[x.e], (r + C::BR - 1) / C::BR, (cols + C::BC - 1) / C::BC, ri, ci);
+        x.c0 = ci * C::BC;
         if (kMode == kWeightGrad) {  // whole strips: full tiles and a shorter last one
-            r0 = ri * most();
-            x.n = r - r0 < most() ? (r - r0 + step - 1) / step * step : most();
+            r0 = ri * C::BR;
+            x.n = r - r0 < C::BR ? (r - r0 + C::STEP - 1) / C::STEP * C::STEP : C::BR;
         } else {
-            row_tile(r, most(), step, ri, r0, x.n);
+            row_tile(r, C::BR, C::STEP, ri, r0, x.n);
         }
         x.valid = r - r0 < x.n ? r - r0 : x.n;
         x.r0 = kMode == kWeightGrad ? r0 : first + r0;
         x.k = kMode == kWeightGrad ? own : depth;
-        x.kb = (x.k + stage_k() - 1) / stage_k();
+        x.kb = (x.k + C::BK - 1) / C::BK;
         return x;
     }
 };
@@ -160,36 +154,6 @@ __device__ __forceinline__ uint8_t *align1024(uint8_t *p)
     return reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(p) + 1023) & ~uintptr_t(1023));
 }
 
-// Features of a tile of the unpaired kernel.  Halving h keeps the SMs evenly
-// loaded when there are few tiles, as long as no expert's rows need a second
-// tile (which would read the weight twice).  Cost: rounds of tiles times the
-// weight rows of one, plus 16 for what a tile costs besides.
-__device__ __forceinline__ int pick_h(const int32_t *off, int E, int cols)
-{
-    const int lane = threadIdx.x & 31;
-    int live[3] = {0, 0, 0}, top = 0;
-    for (int e = lane; e < E; e += 32) {
-        const int r = off[e + 1] - off[e];
-        top = max(top, r);
-#pragma unroll
-        for (int i = 0; i < 3; ++i) live[i] += (r + (64 >> i) - 1) / (64 >> i);
-    }
-    top = __reduce_max_sync(0xffffffffu, top);
-    int best = 128;
-    int64_t cost = 0;
-#pragma unroll
-    for (int i = 0; i < 3; ++i) {
-        const int h = 128 >> i;
-        const int64_t tiles = static_cast<int64_t>(__reduce_add_sync(0xffffffffu, live[i])) * ((cols + h - 1) / h);
-        const int64_t c = (tiles + gridDim.x - 1) / gridDim.x * (h + 16);
-        if (i == 0 || (top <= (64 >> i) && c < cost)) {
-            best = h;
-            cost = c;
-        }
-    }
-    return best;
-}
-
 // ------------------------------------------------------------ scales (4-bit forward)
 //
 // The block-scaled MMA takes its scales from TMEM: row r of 128 has, for 128
@@ -197,12 +161,18 @@ __device__ __forceinline__ int pick_h(const int32_t *off, int E, int cols)
 // the same in all four quarters of the lanes.  A chunk in shared memory is
 // that arrangement as 32 rows of 16 bytes, which one tcgen05.cp spreads.  The
 // scales lie in plain rows in global memory, wherever an expert's rows begin,
-// so warps load each row's bytes (ahead, in registers) and write the chunks.
-
-// Loads must not wait for one another, so nothing is computed on what was
-// loaded before it is stored.  Bytes past the row's end count as zeros (a
-// scale of 2^-127 on zero codes; a NaN byte of the next row must not reach
-// them), and so do rows that do not exist.
+// so warps load each row's bytes into registers and write the chunks.
+//
+// The fence that hands a chunk to the tensor core waits for the warp's loads
+// under way, so a warp loads four stages at a time (64 bytes of a row a lane)
+// and two sets of warps take these blocks in turn: one loads while the other
+// hands out (8192 x 4096 x 14336: loads before every stage's fence, one set
+// 295 us; two sets 269; blocks of four stages 2xx).
+//
+// Nothing is computed on what was loaded before it is handed out, so the loads
+// of a block do not wait for one another.  Bytes past the row's end count as
+// zeros (a scale of 2^-127 on zero codes; a NaN byte of the next row must not
+// reach them), and so do rows that do not exist.
 
 // Whole rows of 16-byte units: W words of a row from byte0 on.
 template <int W>
@@ -265,152 +235,108 @@ __device__ __forceinline__ void shift_words(const uint8_t *base, int64_t total, 
     }
 }
 
-// Where a lane finds its rows of a stage: row, row + 32, ... of which `live` exist from `row` on.
-struct ScaleRows {
-    const uint8_t *base;
-    int64_t total, row;
-    int32_t stride, live, byte0;
-};
+constexpr int kBlock = 4;  // stages a warp loads at a time
 
-// One warp's part of a stage: R rows a lane, W words each (W + 1 as loaded, for any K).
-template <bool kAny, int R, int W>
-__device__ __forceinline__ void load_scales(const ScaleRows &s, uint32_t *w)
-{
-#pragma unroll
-    for (int c = 0; c < R; ++c) {
-        if constexpr (kAny)
-            load_words_any<W>(s.base, s.total, s.stride, s.row + 32 * c, 32 * c < s.live, s.byte0, w + c * (W + 1));
-        else
-            load_words<W>(s.base, s.stride, s.row + 32 * c, 32 * c < s.live, s.byte0, w + c * W);
-    }
-}
-
-// Chunk j of the stage holds word j of every row: 16 bytes a lane.
-template <bool kAny, int R, int W>
-__device__ __forceinline__ void store_scales(uint8_t *dst, int step, int lane, const ScaleRows &s, const uint32_t *raw)
-{
-    uint32_t w[4][W];
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        if (c >= R) {
-#pragma unroll
-            for (int j = 0; j < W; ++j) w[c][j] = 0;
-        } else if constexpr (kAny) {
-            shift_words<W>(s.base, s.total, s.stride, s.row + 32 * c, 32 * c < s.live, s.byte0, raw + c * (W + 1), w[c]);
-        } else {
-#pragma unroll
-            for (int j = 0; j < W; ++j) w[c][j] = raw[c * W + j];
-        }
-    }
-#pragma unroll
-    for (int j = 0; j < W; ++j)
-        *reinterpret_cast<uint4 *>(dst + j * step + lane * 16) = make_uint4(w[0][j], w[1][j], w[2][j], w[3][j]);
-}
-
-// A walk over this CTA's stages, tile after tile.
-template <int kMode, bool kPair>
+// A walk over this CTA's blocks of stages, tile after tile: `len` stages from
+// stage k of tile t on, the g-th of the launch.
+template <int kMode>
 struct Walk {
-    const Tiles<kMode, kPair> &tiles;
-    int t, stride, count, k;
+    const Tiles<kMode> &tiles;
+    int t, stride, count, k, g, len;
     Tile x;
 
-    __device__ __forceinline__ Walk(const Tiles<kMode, kPair> &l, int first, int step, int n)
-        : tiles(l), t(first), stride(step), count(n), k(0)
+    __device__ __forceinline__ Walk(const Tiles<kMode> &l, int first, int step, int n)
+        : tiles(l), t(first), stride(step), count(n), k(0), g(0)
     {
-        if (t < count) x = tiles.at(t);
+        if (live()) x = tiles.at(t);
+        measure();
     }
     __device__ __forceinline__ bool live() const { return t < count; }
-    __device__ __forceinline__ void skip(int n)
+    __device__ __forceinline__ void measure() { len = !live() ? 0 : x.kb - k < kBlock ? x.kb - k : kBlock; }
+    __device__ __forceinline__ void next()
     {
-        for (k += n; live() && k >= x.kb;) {
-            k -= x.kb;
+        if (!live()) return;
+        k += len;
+        g += len;
+        if (k == x.kb) {
+            k = 0;
             t += stride;
-            if (t < count) x = tiles.at(t);
+            if (live()) x = tiles.at(t);
         }
+        measure();
     }
 };
 
-// Pair: one warp copies the scales of A, two those of B's rows 0 .. 127 and
-// 128 .. 223 (both CTAs hold all of B's).  Otherwise one A, one B.  The fence
-// that hands a stage to the tensor core waits for the warp's loads under way,
-// so two sets of warps take the stages in turn: each has two stages' time.
-template <int kMode, bool kPair>
-__device__ __forceinline__ void copy_scales(const Tiles<kMode, kPair> &tiles, const Args &args, uint8_t *stages,
-                                            uint64_t *full, uint64_t *empty, volatile int *abort_flag, int first,
-                                            int stride, int count, uint32_t rank)
+// The warps' parts of a stage: 0 the scales of A, 1 and 2 those of B's rows
+// 0 .. 127 and 128 .. 223 (both CTAs hold all of B's).  A lane has the rows
+// lane, lane + 32, ... of its part.
+template <int kMode>
+__device__ __forceinline__ void copy_scales(const Tiles<kMode> &tiles, const Args &args, uint8_t *stages, uint64_t *full,
+                                            uint64_t *empty, volatile int *abort_flag, int first, int stride, int count,
+                                            uint32_t rank)
 {
-    using C = Cfg<kMode, kPair>;
+    using C = Cfg<kMode>;
     constexpr bool kAny = kMode == kForward4Any;
-    constexpr int P = 2;  // a set's stages ahead
-    constexpr int WORDS = (kPair ? 16 : 8) + (kAny ? 4 : 0);  // a lane's words of a stage
+    constexpr int W = 4 * kBlock, R = W + kAny;  // a row's words of a block, and as loaded
     const int part = ((threadIdx.x >> 5) - 8) % C::SCALE_WARPS, set = ((threadIdx.x >> 5) - 8) / C::SCALE_WARPS;
     const int lane = threadIdx.x & 31;
-    const int J = kPair ? 2 : 128 / tiles.h;
-    Walk<kMode, kPair> now(tiles, first, stride, count);
-    now.skip(set);
-    Walk<kMode, kPair> ahead = now;
-    uint32_t w[P][WORDS];
-
-    auto rows = [&](const Walk<kMode, kPair> &at) {
-        ScaleRows s;
-        s.stride = args.scale_bytes;
-        s.byte0 = at.k * J * 8;
-        if (part == 0) {
-            const int c = at.x.c0 + static_cast<int>(rank) * 128 + lane;
-            s.base = args.a_scales;
-            s.total = static_cast<int64_t>(args.E) * args.cols * s.stride;
-            s.row = static_cast<int64_t>(at.x.e) * args.cols + c;
-            s.live = args.cols - c;
-        } else {
-            const int r = 128 * (part - 1) + lane;
-            s.base = args.b_scales;
-            s.total = static_cast<int64_t>(args.T) * s.stride;
-            s.row = at.x.r0 + r;
-            s.live = at.x.valid - r;
-        }
-        return s;
-    };
-    auto load = [&](uint32_t *v) {
-        if (!ahead.live()) return;
-        const ScaleRows s = rows(ahead);
-        if (kPair) load_scales<kAny, 4, 4>(s, v);
-        else if (J == 1 && part == 0) load_scales<kAny, 4, 2>(s, v);
-        else if (J == 1) load_scales<kAny, 2, 2>(s, v);
-        else if (J == 2 && part == 0) load_scales<kAny, 2, 4>(s, v);
-        else if (J == 2) load_scales<kAny, 1, 4>(s, v);
-        else load_scales<kAny, 1, 8>(s, v);
-        ahead.skip(C::SCALE_SETS);
-    };
-#pragma unroll
-    for (int p = 0; p < P; ++p) load(w[p]);
+    const int32_t bytes = args.scale_bytes;
+    const uint8_t *base = part ? args.b_scales : args.a_scales;
+    const int64_t total = (part ? args.T : static_cast<int64_t>(args.E) * args.cols) * bytes;
+    Walk<kMode> at(tiles, first, stride, count);
+    if (set) at.next();
     bool ok = true;
-    for (int g0 = set; ok && now.live(); g0 += P * C::SCALE_SETS) {
+    for (bool turn = set; at.live(); turn = true) {
+        const int r = part ? 128 * (part - 1) + lane : at.x.c0 + static_cast<int>(rank) * 128 + lane;
+        const int64_t row = part ? at.x.r0 + r : static_cast<int64_t>(at.x.e) * args.cols + r;
+        const int live = (part ? at.x.valid : args.cols) - r;  // rows that exist from the lane's first on
+        const int byte0 = at.k * 16;
+        uint32_t w[4][R];
 #pragma unroll
-        for (int p = 0; p < P; ++p) {
-            if (!ok || !now.live()) break;
-            const int g = g0 + p * C::SCALE_SETS, slot = g % C::S;
+        for (int c = 0; c < 4; ++c) {
+            if constexpr (kAny) load_words_any<W>(base, total, bytes, row + 32 * c, 32 * c < live, byte0, w[c]);
+            else load_words<W>(base, bytes, row + 32 * c, 32 * c < live, byte0, w[c]);
+        }
+        // The block's turn comes when the other set has handed out the one before
+        // it (always waited for and passed on, so that neither set is left
+        // waiting).  A slot's barrier tells neighbouring phases apart and no more:
+        // the other set saw stage g - 1 free, hence g - 4 and g - 6 finished, when
+        // this one waits for g - 3; and g - 3 cannot be overtaken by g, which
+        // needs this warp.
+        if (turn) named_bar_sync(1 + 2 * part + (set ^ 1), 64);
+#pragma unroll
+        for (int i = 0; i < kBlock; ++i) {
+            if (i >= at.len || !ok) break;
+            const int g = at.g + i, slot = g % C::S;
             if (g >= C::S &&
                 __any_sync(0xffffffffu, !mbar_wait(&empty[slot], ((g / C::S) - 1) & 1, args.timeout_ns, abort_flag))) {
                 ok = false;
                 break;
             }
-            uint8_t *dst = stages + slot * C::STAGE + C::A_BYTES + C::B_BYTES + (part ? C::SA_BYTES : 0);
-            const ScaleRows r = rows(now);
-            if (kPair) store_scales<kAny, 4, 4>(part == 2 ? dst + 512 : dst, part ? 1024 : 512, lane, r, w[p]);
-            else if (J == 1 && part == 0) store_scales<kAny, 4, 2>(dst, 512, lane, r, w[p]);
-            else if (J == 1) store_scales<kAny, 2, 2>(dst, 512, lane, r, w[p]);
-            else if (J == 2 && part == 0) store_scales<kAny, 2, 4>(dst, 512, lane, r, w[p]);
-            else if (J == 2) store_scales<kAny, 1, 4>(dst, 512, lane, r, w[p]);
-            else store_scales<kAny, 1, 8>(dst, 512, lane, r, w[p]);
+            uint8_t *dst = stages + slot * C::STAGE + C::A_BYTES + C::B_BYTES + lane * 16 +
+                           (part ? C::SA_BYTES + 512 * (part - 1) : 0);
+            const int step = part ? 1024 : 512;  // from chunk to chunk
+            uint32_t v[4][4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                if constexpr (kAny) {
+                    shift_words<4>(base, total, bytes, row + 32 * c, 32 * c < live, byte0 + 16 * i, &w[c][4 * i], v[c]);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) v[c][j] = w[c][4 * i + j];
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)  // chunk j: word j of every row
+                *reinterpret_cast<uint4 *>(dst + j * step) = make_uint4(v[0][j], v[1][j], v[2][j], v[3][j]);
             fence_async_smem();
             __syncwarp();
-            if (lane == 0) {
-                if (kPair) mbar_arrive_cluster(cluster_addr(&full[slot], 0));
-                else mbar_arrive(&full[slot]);
-            }
-            now.skip(C::SCALE_SETS);
-            load(w[p]);
+            if (lane == 0) mbar_arrive_cluster(cluster_addr(&full[slot], 0));
         }
+        at.next();
+        __syncwarp();
+        if (at.live()) named_bar_arrive(1 + 2 * part + set, 64);
+        at.next();
     }
     if (lane == 0 && !ok) {
         *abort_flag = 1;
@@ -419,12 +345,11 @@ __device__ __forceinline__ void copy_scales(const Tiles<kMode, kPair> &tiles, co
     __syncwarp();
 }
 
-template <int kMode, bool kPair>
-__global__ void __launch_bounds__(Cfg<kMode, kPair>::THREADS, 1)
+template <int kMode>
+__global__ void __launch_bounds__(Cfg<kMode>::THREADS, 1)
     k_grouped(const __grid_constant__ Maps maps, const Args args)
 {
-    using C = Cfg<kMode, kPair>;
-    constexpr bool kAm = kMode == kInputGrad || kMode == kWeightGrad, kBm = kMode == kWeightGrad;  // M- / N-major operands
+    using C = Cfg<kMode>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *stages = align1024(smem_raw);
     uint8_t *outbuf = stages + C::S * C::STAGE;
@@ -435,136 +360,105 @@ __global__ void __launch_bounds__(Cfg<kMode, kPair>::THREADS, 1)
     uint64_t *drain = aempty + 2;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-    int *h_slot = reinterpret_cast<int *>(tmem_slot + 2);
-    int32_t *off = reinterpret_cast<int32_t *>(tmem_slot + 4);
+    int32_t *off = reinterpret_cast<int32_t *>(tmem_slot + 2);
     int32_t *start = off + kMaxExperts + 1;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t rank = kPair ? cluster_rank() : 0;
+    const uint32_t rank = cluster_rank();
     const uint64_t tmo = args.timeout_ns;
     dependents_may_launch();
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::S; ++s) {
-            mbar_init(&full[s], 1 + C::CG * C::SCALE_WARPS);
+            mbar_init(&full[s], 1 + 2 * C::SCALE_WARPS);
             mbar_init(&empty[s], 1);
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(&afull[a], 1);
-            mbar_init(&aempty[a], 4 * C::CG);
+            mbar_init(&aempty[a], 8);
         }
         mbar_init(drain, 1);
         *abort_flag = 0;
         fence_barrier_init();
         tma_prefetch_map(&maps.a[0]);
-        tma_prefetch_map(&maps.b[8]);
         tma_prefetch_map(&maps.out);
     }
     if (warp == 1) {
-        if (kPair) {
-            tmem_alloc_pair(tmem_slot, C::TMEM);
-            tmem_relinquish_pair();
-        } else {
-            tmem_alloc(tmem_slot, C::TMEM);
-            tmem_relinquish();
-        }
+        tmem_alloc_pair(tmem_slot, C::TMEM);
+        tmem_relinquish_pair();
     }
     wait_for_prior_grid();  // nothing above touched global memory
-    if (warp == 0) {
-        load_offsets(args.offsets, args.E, args.T, off, args.status);
-        const int h = kPair ? 256 : pick_h(off, args.E, args.cols);
-        const int nc = (args.cols + h - 1) / h, most = kPair ? C::BR : h / 2;
-        tile_starts(args.E, start, [&](int e) {
-            const int r = kMode == kWeightGrad ? args.rows : off[e + 1] - off[e];
-            return (r + most - 1) / most * nc;
-        });
-        if (lane == 0) *h_slot = h;
-    }
+    fetch_offsets(args.offsets, args.E, args.T, off);
     tc_fence_before();
     __syncthreads();
-    if (kPair) cluster_sync_all();  // the peer's barriers are initialised
+    if (warp == 0) {
+        clamp_offsets(args.E, args.T, off, args.status);
+        const int nc = (args.cols + C::BC - 1) / C::BC;
+        tile_starts(args.E, start, [&](int e) {
+            const int r = kMode == kWeightGrad ? args.rows : off[e + 1] - off[e];
+            return (r + C::BR - 1) / C::BR * nc;
+        });
+    }
+    __syncthreads();
+    cluster_sync_all();  // the peer's barriers are initialised
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    const Tiles<kMode, kPair> tiles = {off, start, args.E, *h_slot, args.cols, args.rows, args.depth};
-    const int count = tiles.count();
-    const int first = blockIdx.x / C::CG, stride = gridDim.x / C::CG;
-    const int J = kPair ? 1 : 128 / tiles.h;  // 64-k blocks per stage
+    const Tiles<kMode> tiles = {off, start, args.E, args.cols, args.rows, args.depth};
+    const int count = start[args.E];
+    const int first = blockIdx.x / 2, stride = gridDim.x / 2;
 
     if (warp == 0 || warp == 2) {
         // ------------------------------------------------------------ producers: warp 0 copies A, warp 2 B
         if (lane == 0) {
             const bool is_a = warp == 0;
+            const bool mn = is_a ? C::AM : C::BN;  // M- or N-major
             bool ok = true;
             int g = 0;  // stages issued
             int mapped = -1;
-            // one strip a copy, two strips a copy
-            const CUtensorMap *one = is_a ? &maps.a[kPair ? 1 : tiles.h == 128 ? 0 : tiles.h == 64 ? 1 : 2] : &maps.b[8];
-            const CUtensorMap *two = &maps.a[0];
+            const CUtensorMap *one = is_a ? &maps.a[1] : &maps.b[8], *two = &maps.a[0];  // one, two strips a copy
+            Tile x, next;
+            if (first < count) next = tiles.at(first);
             for (int t = first; ok && t < count; t += stride) {
-                const Tile x = tiles.at(t);
-                if (kBm && x.kb > 0 && x.e != mapped) {
+                x = next;
+                if (t + stride < count) next = tiles.at(t + stride);
+                if (kMode == kWeightGrad && x.kb > 0 && x.e != mapped) {
                     mapped = x.e;
                     one = args.expert_maps + 4 * static_cast<size_t>(x.e) + is_a;
                     two = one + 2;
                     asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(one) : "memory");
                     asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(two) : "memory");
                 }
-                const int half = x.n / C::CG;  // rows of B in this CTA
-                const int at = is_a ? x.c0 + static_cast<int>(rank) * 128
-                                    : x.r0 + static_cast<int>(rank) * half;
-                if (kPair) {
-                    const bool mn = is_a ? kAm : kBm;  // M- or N-major
-                    const int plane = is_a && !kBm ? x.e : 0;
-                    const int rows = is_a ? 128 : half;
-                    const int strips = kBm && !is_a ? (half + 63) / 64 : 2;
-                    const uint32_t bytes = 2 * (32768 + (kBm ? (half + 63) / 64 * 16384 : 256 * half));
-                    // M-/N-major strips are whole along the features, K-major ones along k
-                    const int wide = is_a ? args.cols : args.rows;
-                    const bool aligned = mn && strips == 2 && at % 64 == 0 && (wide % 64 == 0 || at + 128 <= wide);
-                    if (!is_a && !kBm) two = &maps.b[half / 16 - 1];  // exactly the tile's rows
-                    for (int k = 0; k < x.kb; ++k, ++g) {
-                        const int slot = g % C::S;
-                        if (g >= C::S && !mbar_wait(&empty[slot], ((g / C::S) - 1) & 1, tmo, abort_flag)) {
-                            ok = false;
-                            break;
-                        }
-                        uint8_t *dst = stages + slot * C::STAGE + (is_a ? 0 : C::A_BYTES);
-                        if (is_a && rank == 0) mbar_arrive_expect_tx(&full[slot], bytes);
-                        const uint32_t bar = cluster_addr(&full[slot], 0);
-                        if (mn) {
-                            if (aligned)
-                                tma_load_4d_pair(dst, two, bar, 0, k * 128, at / 64, plane);
-                            else
-                                for (int i = 0; i < strips; ++i)
-                                    tma_load_3d_pair(dst + i * 16384, one, bar, at + 64 * i, k * 128, plane);
-                        } else if (x.k % 64 == 0 || k * 128 + 128 <= x.k) {
-                            tma_load_4d_pair(dst, two, bar, 0, at, k * 2, plane);
-                        } else {  // the last stage of a k that ends inside a strip
-                            for (int i = 0; i < 2; ++i)
-                                for (int r = 0; r < rows; r += is_a ? 128 : C::BOX)
-                                    tma_load_3d_pair(dst + (i * rows + r) * 128, one, bar, k * 128 + 64 * i, at + r, plane);
-                        }
+                const int half = x.n / 2;  // rows of B in this CTA
+                const int at = is_a ? x.c0 + static_cast<int>(rank) * 128 : x.r0 + static_cast<int>(rank) * half;
+                const int plane = is_a && kMode != kWeightGrad ? x.e : 0;
+                const int rows = is_a ? 128 : half;
+                const int strips = C::BN && !is_a ? (half + 63) / 64 : 2;
+                const uint32_t bytes = 2 * (C::A_BYTES + (C::BN ? (half + 63) / 64 * 16384 : 256 * half));
+                // M- and N-major strips are whole along the features, K-major ones along k
+                const int wide = is_a ? args.cols : args.rows;
+                const bool aligned = mn && strips == 2 && at % 64 == 0 && (wide % 64 == 0 || at + 128 <= wide);
+                if (!is_a && !C::BN) two = &maps.b[half / 16 - 1];  // exactly the tile's rows
+                for (int k = 0; k < x.kb; ++k, ++g) {
+                    const int slot = g % C::S;
+                    if (g >= C::S && !mbar_wait(&empty[slot], ((g / C::S) - 1) & 1, tmo, abort_flag)) {
+                        ok = false;
+                        break;
                     }
-                } else {
-                    const int boxes = (half + C::BOX - 1) / C::BOX;
-                    const uint32_t bytes = C::A_BYTES + J * boxes * C::BOX * 128;
-                    for (int k = 0; k < x.kb; ++k, ++g) {
-                        const int slot = g % C::S;
-                        if (g >= C::S && !mbar_wait(&empty[slot], ((g / C::S) - 1) & 1, tmo, abort_flag)) {
-                            ok = false;
-                            break;
-                        }
-                        uint8_t *sa = stages + slot * C::STAGE, *sb = sa + C::A_BYTES;
-                        if (is_a) {
-                            mbar_arrive_expect_tx(&full[slot], bytes);
-                            for (int j = 0; j < J; ++j)
-                                tma_load_3d(sa + j * tiles.h * 128, one, &full[slot], (k * J + j) * 64, at, x.e);
-                        } else {
-                            for (int j = 0; j < J; ++j)
-                                for (int i = 0; i < boxes; ++i)
-                                    tma_load_3d(sb + (j * boxes + i) * C::BOX * 128, one, &full[slot],
-                                                (k * J + j) * 64, at + i * C::BOX, 0);
-                        }
+                    uint8_t *dst = stages + slot * C::STAGE + (is_a ? 0 : C::A_BYTES);
+                    if (is_a && rank == 0) mbar_arrive_expect_tx(&full[slot], bytes);
+                    const uint32_t bar = cluster_addr(&full[slot], 0);
+                    if (mn) {
+                        if (aligned)
+                            tma_load_4d_pair(dst, two, bar, 0, k * 128, at / 64, plane);
+                        else
+                            for (int i = 0; i < strips; ++i)
+                                tma_load_3d_pair(dst + i * 16384, one, bar, at + 64 * i, k * 128, plane);
+                    } else if (x.k % 64 == 0 || k * 128 + 128 <= x.k) {
+                        tma_load_4d_pair(dst, two, bar, 0, at, k * 2, plane);
+                    } else {  // the last stage of a k that ends inside a strip
+                        for (int i = 0; i < 2; ++i)
+                            for (int r = 0; r < rows; r += is_a ? 128 : 16)
+                                tma_load_3d_pair(dst + (i * rows + r) * 128, one, bar, k * 128 + 64 * i, at + r, plane);
                     }
                 }
             }
@@ -588,7 +482,7 @@ __global__ void __launch_bounds__(Cfg<kMode, kPair>::THREADS, 1)
         }
         __syncwarp();
     } else if (warp == 1) {
-        // ------------------------------------------------------------ MMA issuer
+        // ------------------------------------------------------------ MMA issuer (the leader's)
         if (rank == 0) {
             const uint32_t lead = lane == 0;
             bool ok = true;
@@ -602,8 +496,10 @@ __global__ void __launch_bounds__(Cfg<kMode, kPair>::THREADS, 1)
                     break;
                 }
                 tc_fence_after();
-                const uint32_t idesc = C::F4 ? make_idesc_mx4(128 * C::CG, x.n) : make_idesc_bf16(128 * C::CG, x.n, kAm, kBm);
+                const uint32_t idesc = C::F4 ? make_idesc_mx4(256, x.n) : make_idesc_bf16(256, x.n, C::AM, C::BN);
                 const uint32_t d = tmem + acc * C::BR;
+                const uint32_t bs = x.n / 2 * 8;  // K-major B: a strip of half the rows, in 16-byte units
+                const uint32_t sa_t = tmem + C::SA_COL, sb_t = tmem + C::SB_COL;
                 for (int k = 0; k < x.kb; ++k, ++g) {
                     const int slot = g % C::S;
                     if (__any_sync(0xffffffffu, !mbar_wait(&full[slot], (g / C::S) & 1, tmo, abort_flag))) {
@@ -612,67 +508,48 @@ __global__ void __launch_bounds__(Cfg<kMode, kPair>::THREADS, 1)
                     }
                     tc_fence_after();
                     const uint32_t a0 = smem_u32(stages + slot * C::STAGE), b0 = a0 + C::A_BYTES;
-                    // K-major: 8-row atoms 1024 bytes apart, a K step of 16 is 32 bytes along the row, a strip
-                    // its rows x 128 bytes; M-major: strips 16384 bytes apart, a K step is 16 rows of 128 bytes
-                    const uint64_t ad = make_sdesc(a0, kAm ? 16384 : 16, 1024, kLayoutSw128);
-                    const uint64_t bd = make_sdesc(b0, kBm ? 16384 : 16, 1024, kLayoutSw128);
+                    // K-major: 8-row atoms 1024 bytes apart, a K step of 32 bytes along the row, a strip its
+                    // rows x 128 bytes; M- and N-major: strips 16384 bytes apart, a K step of 16 rows of 128 bytes
+                    const uint64_t ad = make_sdesc(a0, C::AM ? 16384 : 16, 1024, kLayoutSw128);
+                    const uint64_t bd = make_sdesc(b0, C::BN ? 16384 : 16, 1024, kLayoutSw128);
+                    const uint64_t sd = make_sdesc(b0 + C::B_BYTES, 0, 128, 0);  // scales: rows of 16 bytes, no swizzle
                     const uint32_t alo = static_cast<uint32_t>(ad), ahi = static_cast<uint32_t>(ad >> 32);
                     const uint32_t blo = static_cast<uint32_t>(bd), bhi = static_cast<uint32_t>(bd >> 32);
-                    const uint32_t sa_t = tmem + C::SA_COL, sb_t = tmem + C::SB_COL;
-                    if (C::F4) {  // the stage's scales to TMEM, in order with the MMAs around them
-                        const uint64_t sc = make_sdesc(b0 + C::B_BYTES, 0, 128, 0);
-                        const uint32_t lo = static_cast<uint32_t>(sc), hi = static_cast<uint32_t>(sc >> 32);
-                        const int left = (x.k - k * 128 + 31) / 32;  // chunks of 128 elements
-                        const int chunks = !kPair ? 2 * J : left < 4 ? left : 4;
-                        for (int i = 0; i < chunks; ++i) {
-                            scales_to_tmem<kPair>(lead, sa_t + 4 * i, lo + 32 * i, hi);
-                            if (kPair) {
-                                scales_to_tmem<kPair>(lead, sb_t + 8 * i, lo + C::SA_BYTES / 16 + 64 * i, hi);
-                                if (x.n > 128) scales_to_tmem<kPair>(lead, sb_t + 8 * i + 4, lo + C::SA_BYTES / 16 + 64 * i + 32, hi);
-                            } else {
-                                scales_to_tmem<kPair>(lead, sb_t + 4 * i, lo + C::SA_BYTES / 16 + 32 * i, hi);
-                            }
-                        }
-                    }
-                    if (kPair) {
-                        const uint32_t bs = x.n / 2 * 8;  // K-major B: a strip of half the rows, in 16-byte units
-                        auto mma = [&](int i) {
-                            if (C::F4)
-                                umma_mx4<true>(lead, d, alo + (i >> 2) * 1024 + (i & 3) * 2, ahi,
-                                               blo + (i >> 2) * bs + (i & 3) * 2, bhi, idesc | (i & 1) * kSecondScales,
+                    const uint32_t slo = static_cast<uint32_t>(sd), shi = static_cast<uint32_t>(sd >> 32);
+                    auto scales = [&](int j) {  // chunk j: its scales to TMEM, in order with the MMAs around it
+                        if (!C::F4) return;
+                        scales_to_tmem(lead, sa_t + 4 * j, slo + 32 * j, shi);
+                        scales_to_tmem(lead, sb_t + 8 * j, slo + C::SA_BYTES / 16 + 64 * j, shi);
+                        if (x.n > 128) scales_to_tmem(lead, sb_t + 8 * j + 4, slo + C::SA_BYTES / 16 + 64 * j + 32, shi);
+                    };
+                    auto mma = [&](int i) {
+                        const uint32_t al = alo + (C::AM ? i * 128 : (i >> 2) * 1024 + (i & 3) * 2);
+                        const uint32_t bl = blo + (C::BN ? i * 128 : (i >> 2) * bs + (i & 3) * 2);
+                        if (C::F4)
+                            umma_mx4_lead_pair(lead, d, al, ahi, bl, bhi, idesc | (i & 1) * kSecondScales,
                                                sa_t + (i >> 1) * 4, sb_t + (i >> 1) * 8, (k | i) != 0);
-                            else
-                                umma_bf16_lo_lead_pair(lead, d, alo + (kAm ? i * 128 : (i >> 2) * 1024 + (i & 3) * 2), ahi,
-                                                       blo + (kBm ? i * 128 : (i >> 2) * bs + (i & 3) * 2), bhi, idesc,
-                                                       (k | i) != 0);
-                        };
-                        const int left = x.k - k * 128;
-                        if (left >= 128) {
+                        else
+                            umma_bf16_lo_lead_pair(lead, d, al, ahi, bl, bhi, idesc, (k | i) != 0);
+                    };
+                    const int left = x.k - k * 128;
+                    if (left >= 128) {
+                        scales(0);
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) mma(i);
-                        } else {  // the copies filled the rest with zeros
-                            for (int i = 0; 16 * i < left; ++i) mma(i);
+                        for (int i = 0; i < 8; ++i) {
+                            if (i % 2 == 0 && i < 6) scales(i / 2 + 1);  // one chunk ahead: 255 us against 269
+                            mma(i);
                         }
-                        umma_commit_lead_pair(lead, &empty[slot]);
-                    } else {
-                        const uint32_t aj = tiles.h * 8, bj = (x.n + C::BOX - 1) / C::BOX * C::BOX * 8;
-                        for (int j = 0; j < J; ++j)
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                if (C::F4)
-                                    umma_mx4<false>(lead, d, alo + j * aj + i * 2, ahi, blo + j * bj + i * 2, bhi,
-                                                    idesc | (i & 1) * kSecondScales, sa_t + (2 * j + (i >> 1)) * 4,
-                                                    sb_t + (2 * j + (i >> 1)) * 4, (k | j | i) != 0);
-                                else
-                                    umma_bf16_lo_lead(lead, d, alo + j * aj + i * 2, ahi, blo + j * bj + i * 2, bhi, idesc,
-                                                  (k | j | i) != 0);
-                        umma_commit_lead(lead, &empty[slot]);
+                    } else {  // the copies filled the rest with zeros
+                        for (int i = 0; 16 * i < left; ++i) {
+                            if (i % 2 == 0) scales(i / 2);
+                            mma(i);
+                        }
                     }
+                    umma_commit_lead_pair(lead, &empty[slot]);
                     __syncwarp();
                 }
                 if (!ok) break;
-                if (kPair) umma_commit_lead_pair(lead, &afull[acc]);
-                else umma_commit_lead(lead, &afull[acc]);
+                umma_commit_lead_pair(lead, &afull[acc]);
                 __syncwarp();
                 ++it;
             }
@@ -681,8 +558,7 @@ __global__ void __launch_bounds__(Cfg<kMode, kPair>::THREADS, 1)
                 set_status(args.status, BSL_ERR_TIMEOUT);
             }
             // every MMA is complete before TMEM and shared memory are released
-            if (kPair) umma_commit_lead_pair(lead, drain);
-            else umma_commit_lead(lead, drain);
+            umma_commit_lead_pair(lead, drain);
             if (lane == 0 && !mbar_wait(drain, 0, tmo, nullptr)) set_status(args.status, BSL_ERR_TIMEOUT);
         }
         __syncwarp();
@@ -695,7 +571,7 @@ __global__ void __launch_bounds__(Cfg<kMode, kPair>::THREADS, 1)
         }
         __syncwarp();
     } else if (C::F4 && warp >= 8) {
-        if constexpr (C::F4) copy_scales<kMode, kPair>(tiles, args, stages, full, empty, abort_flag, first, stride, count, rank);
+        if constexpr (C::F4) copy_scales<kMode>(tiles, args, stages, full, empty, abort_flag, first, stride, count, rank);
     } else {
         // ------------------------------------------------------------ epilogue
         // Warp q reads TMEM lanes 32q .. 32q+31: features c0 + 32q + lane of its CTA.
@@ -707,8 +583,7 @@ __global__ void __launch_bounds__(Cfg<kMode, kPair>::THREADS, 1)
         for (int t = first; ok && t < count; t += stride) {
             const Tile x = tiles.at(t);
             const int c = x.c0 + static_cast<int>(rank) * 128 + 32 * q;
-            const bool mine = c < args.cols && (kPair || 32 * q < tiles.h);
-            const float bv = args.bias && mine && c + lane < args.cols
+            const float bv = args.bias && c + lane < args.cols
                                  ? __bfloat162float(args.bias[static_cast<int64_t>(x.e) * args.cols + c + lane]) : 0.f;
             const int acc = it & 1;
             if (x.kb > 0 && __any_sync(0xffffffffu, !mbar_wait(&afull[acc], (it >> 1) & 1, tmo, abort_flag))) {
@@ -716,7 +591,7 @@ __global__ void __launch_bounds__(Cfg<kMode, kPair>::THREADS, 1)
                 break;
             }
             tc_fence_after();
-            const int chunks = mine ? (x.valid + 31) / 32 : 0;
+            const int chunks = c < args.cols ? (x.valid + 31) / 32 : 0;
             for (int i = 0; i < chunks; ++i) {
                 uint32_t v[32];
                 if (x.kb > 0) {
@@ -738,7 +613,8 @@ __global__ void __launch_bounds__(Cfg<kMode, kPair>::THREADS, 1)
                         tma_store_3d(&maps.out, dst, c, x.r0 + 32 * i, kMode == kWeightGrad ? x.e : 0);
                 } else {
                     __syncwarp();
-                    store_rows(args.out + static_cast<int64_t>(x.r0 + 32 * i) * args.cols + c, args.cols, dst, left, args.cols - c, lane);
+                    store_rows(args.out + static_cast<int64_t>(x.r0 + 32 * i) * args.cols + c, args.cols, dst, left,
+                               args.cols - c, lane);
                 }
                 if (lane == 0) bulk_commit_group();  // one group a chunk, an empty one for plain stores
                 ob ^= 1;
@@ -746,10 +622,7 @@ __global__ void __launch_bounds__(Cfg<kMode, kPair>::THREADS, 1)
             if (x.kb > 0) {
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) {
-                    if (kPair) mbar_arrive_cluster(cluster_addr(&aempty[acc], 0));
-                    else mbar_arrive(&aempty[acc]);
-                }
+                if (lane == 0) mbar_arrive_cluster(cluster_addr(&aempty[acc], 0));
                 ++it;
             }
         }
@@ -765,53 +638,45 @@ __global__ void __launch_bounds__(Cfg<kMode, kPair>::THREADS, 1)
 
     tc_fence_before();
     __syncthreads();
-    if (kPair) {
-        // the leader's last arrival on this CTA is in before the CTA may end
-        if (rank != 0 && threadIdx.x == 0 && !mbar_wait(drain, 0, tmo, nullptr))
-            set_status(args.status, BSL_ERR_TIMEOUT);
-        __syncthreads();
-        cluster_sync_all();  // no MMA, copy or arrival of the pair is left
-    }
+    // the leader's last arrival on this CTA is in before the CTA may end
+    if (rank != 0 && threadIdx.x == 0 && !mbar_wait(drain, 0, tmo, nullptr)) set_status(args.status, BSL_ERR_TIMEOUT);
+    __syncthreads();
+    cluster_sync_all();  // no MMA, copy or arrival of the pair is left
     if (warp == 1) {
         tc_fence_after();
-        if (kPair) tmem_dealloc_pair(tmem, C::TMEM);
-        else tmem_dealloc(tmem, C::TMEM);
+        tmem_dealloc_pair(tmem, C::TMEM);
     }
 }
 
 // ------------------------------------------------------------ host
 
-inline bool map_rows(CUtensorMap *m, const void *p, int64_t cols, int64_t rows, uint32_t box_cols, uint32_t box_rows, int swizzle)
+// Rows [rows][cols] of two-byte columns, boxes of box_cols x box_rows.
+inline bool map_rows(CUtensorMap *m, const void *p, int64_t cols, int64_t rows, uint32_t box_cols, uint32_t box_rows,
+                     int swizzle)
 {
     return make_map_3d(m, p, cols, rows, 1, cols * 2, cols * 2 * rows, box_cols, box_rows, swizzle);
 }
 
-// Maps of a forward pass: the weight [E][N][depth], the rows [T][depth] and the output [T][N], two-byte columns.
-inline bool forward_maps(Maps &m, const void *weight, int64_t N, int64_t depth, int64_t E, const void *X, int64_t T,
-                         void *Y, bool pair)
+// Maps of a pass over rows: the weight [E][N][K], the rows [T][depth] and the output [T][cols], two-byte columns.
+inline bool row_maps(Maps &m, const void *weight, int64_t E, int64_t N, int64_t K, const void *A, int64_t T, int64_t depth,
+                     void *out, int64_t cols)
 {
-    bool good = map_rows(&m.b[8], X, depth, T, 64, 16, 128) && map_rows(&m.out, Y, N, T, 32, 32, 0);
-    if (pair) {
-        good = good && make_strip_map(&m.a[0], weight, depth, N, E, 128, 2) &&
-               make_map_3d(&m.a[1], weight, depth, N, E, depth * 2, depth * 2 * N, 64, 128, 128);
-        for (int i = 0; i < 8; ++i) good = good && make_strip_map(&m.b[i], X, depth, T, 1, 16 * (i + 1), 2);
-    } else {
-        for (int i = 0; i < 3; ++i)
-            good = good && make_map_3d(&m.a[i], weight, depth, N, E, depth * 2, depth * 2 * N, 64, 128 >> i, 128);
-    }
+    bool good = make_strip_map(&m.a[0], weight, K, N, E, 128, 2) &&
+                make_map_3d(&m.a[1], weight, K, N, E, K * 2, K * 2 * N, 64, 128, 128) &&
+                map_rows(&m.b[8], A, depth, T, 64, 16, 128) && map_rows(&m.out, out, cols, T, 32, 32, 0);
+    for (int i = 0; i < 8; ++i) good = good && make_strip_map(&m.b[i], A, depth, T, 1, 16 * (i + 1), 2);
     return good;
 }
 
-template <int kMode, bool kPair>
+template <int kMode>
 bsl_status run(const Maps &maps, const Args &args, cudaStream_t s)
 {
-    using C = Cfg<kMode, kPair>;
-    auto kern = k_grouped<kMode, kPair>;
+    using C = Cfg<kMode>;
+    auto kern = k_grouped<kMode>;
     const bsl_status sa = set_smem_once(reinterpret_cast<const void *>(kern), C::SMEM);
     if (sa != BSL_OK) return sa;
-    const int grid = num_sms() / C::CG * C::CG;
-    return cuda_status(kPair ? launch_dependent_cluster(kern, grid, 2, C::THREADS, C::SMEM, s, maps, args)
-                             : launch_dependent(kern, grid, C::THREADS, C::SMEM, s, maps, args));
+    const int grid = num_sms() / 2 * 2;
+    return cuda_status(launch_dependent_cluster(kern, grid, 2, C::THREADS, C::SMEM, s, maps, args));
 }
 
 }  // namespace

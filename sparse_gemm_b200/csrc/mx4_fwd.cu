@@ -12,7 +12,6 @@ namespace bsl {
 bsl_status launch_mx4_fwd(const uint8_t *xc, const uint8_t *xs, int32_t T, const int32_t *offsets, const bsl_mx4 *W,
                           const void *bias, void *Y, int32_t zero_rest, cudaStream_t s)
 {
-    const int64_t N = W->N, depth = W->K / 4;
     Args args = {};
     args.offsets = offsets;
     args.bias = static_cast<const __nv_bfloat16 *>(bias);
@@ -27,11 +26,9 @@ bsl_status launch_mx4_fwd(const uint8_t *xc, const uint8_t *xs, int32_t T, const
     args.b_scales = xs;
     args.scale_bytes = W->K / 32;
     args.timeout_ns = wait_timeout_ns();
-    const bool pair = T > static_cast<int64_t>(W->E) * 32;
     Maps m;
-    if (!forward_maps(m, W->codes, N, depth, W->E, xc, T, Y, pair)) return BSL_ERR_CUDA;
-    if (W->K % 512 == 0) return pair ? run<kForward4, true>(m, args, s) : run<kForward4, false>(m, args, s);
-    return pair ? run<kForward4Any, true>(m, args, s) : run<kForward4Any, false>(m, args, s);
+    if (!row_maps(m, W->codes, W->E, W->N, args.depth, xc, T, args.depth, Y, W->N)) return BSL_ERR_CUDA;
+    return W->K % 512 == 0 ? run<kForward4>(m, args, s) : run<kForward4Any>(m, args, s);
 }
 
 }  // namespace bsl

@@ -10,6 +10,12 @@ namespace bsl {
 // Two CTAs of a cluster working on one tile (cta_group::2).  Rank 0 leads: it
 // issues the MMAs, and both CTAs' copies complete on its barriers.
 
+// Arrive on a named barrier of `count` threads without waiting (see named_bar_sync).
+__device__ __forceinline__ void named_bar_arrive(uint32_t id, uint32_t count)
+{
+    asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(count) : "memory");
+}
+
 __device__ __forceinline__ uint32_t cluster_rank()
 {
     uint32_t r;
@@ -122,59 +128,34 @@ __host__ __device__ constexpr uint32_t make_idesc_mx4(int M, int N)
 // Added to it: the scales are bytes 2 and 3 of each 32-bit cell instead of 0 and 1 (both operands).
 constexpr uint32_t kSecondScales = (2u << 29) | (2u << 4);
 
-template <bool kPair>
-__device__ __forceinline__ void umma_mx4(uint32_t leader, uint32_t d_tmem, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo,
-                                         uint32_t b_hi, uint32_t idesc, uint32_t sa_tmem, uint32_t sb_tmem,
-                                         uint32_t accumulate)
+__device__ __forceinline__ void umma_mx4_lead_pair(uint32_t leader, uint32_t d_tmem, uint32_t a_lo, uint32_t a_hi,
+                                                   uint32_t b_lo, uint32_t b_hi, uint32_t idesc, uint32_t sa_tmem,
+                                                   uint32_t sb_tmem, uint32_t accumulate)
 {
-    if (kPair)
-        asm volatile(
-            "{\n\t.reg .pred p, e;\n\t.reg .b64 ad, bd;\n\t"
-            "setp.ne.b32 e, %9, 0;\n\t"
-            "mov.b64 ad, {%1, %2};\n\t"
-            "mov.b64 bd, {%3, %4};\n\t"
-            "setp.ne.b32 p, %8, 0;\n\t"
-            "@e tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], ad, bd, %5, [%6], [%7], p;\n\t}" ::"r"(
-                d_tmem),
-            "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(sa_tmem), "r"(sb_tmem), "r"(accumulate),
-            "r"(leader)
-            : "memory");
-    else
-        asm volatile(
-            "{\n\t.reg .pred p, e;\n\t.reg .b64 ad, bd;\n\t"
-            "setp.ne.b32 e, %9, 0;\n\t"
-            "mov.b64 ad, {%1, %2};\n\t"
-            "mov.b64 bd, {%3, %4};\n\t"
-            "setp.ne.b32 p, %8, 0;\n\t"
-            "@e tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], ad, bd, %5, [%6], [%7], p;\n\t}" ::"r"(
-                d_tmem),
-            "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(sa_tmem), "r"(sb_tmem), "r"(accumulate),
-            "r"(leader)
-            : "memory");
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t.reg .b64 ad, bd;\n\t"
+        "setp.ne.b32 e, %9, 0;\n\t"
+        "mov.b64 ad, {%1, %2};\n\t"
+        "mov.b64 bd, {%3, %4};\n\t"
+        "setp.ne.b32 p, %8, 0;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], ad, bd, %5, [%6], [%7], p;\n\t}" ::"r"(
+            d_tmem),
+        "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(sa_tmem), "r"(sb_tmem), "r"(accumulate), "r"(leader)
+        : "memory");
 }
 
 // 32 rows of 16 bytes from shared memory (descriptor halves lo, hi) to 4 TMEM
-// columns of 32 lanes, the same in all four quarters of the lanes (in both CTAs
-// of a pair, each from its own shared memory).
-template <bool kPair>
+// columns of 32 lanes, the same in all four quarters of the lanes, in both
+// CTAs of a pair, each from its own shared memory.
 __device__ __forceinline__ void scales_to_tmem(uint32_t leader, uint32_t taddr, uint32_t lo, uint32_t hi)
 {
-    if (kPair)
-        asm volatile(
-            "{\n\t.reg .pred e;\n\t.reg .b64 sd;\n\t"
-            "setp.ne.b32 e, %3, 0;\n\t"
-            "mov.b64 sd, {%1, %2};\n\t"
-            "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], sd;\n\t}" ::"r"(taddr),
-            "r"(lo), "r"(hi), "r"(leader)
-            : "memory");
-    else
-        asm volatile(
-            "{\n\t.reg .pred e;\n\t.reg .b64 sd;\n\t"
-            "setp.ne.b32 e, %3, 0;\n\t"
-            "mov.b64 sd, {%1, %2};\n\t"
-            "@e tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], sd;\n\t}" ::"r"(taddr),
-            "r"(lo), "r"(hi), "r"(leader)
-            : "memory");
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t.reg .b64 sd;\n\t"
+        "setp.ne.b32 e, %3, 0;\n\t"
+        "mov.b64 sd, {%1, %2};\n\t"
+        "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], sd;\n\t}" ::"r"(taddr),
+        "r"(lo), "r"(hi), "r"(leader)
+        : "memory");
 }
 
 // 3-D tiled store from shared memory (bulk-group completion).

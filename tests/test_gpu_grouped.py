@@ -213,6 +213,17 @@ def test_repeatable_and_replayed_with_new_offsets(rows):
     assert sg.grouped_status(Wg) == 0
 
 
+@pytest.mark.parametrize("rows,N,K", [([900, 2100, 0, 40], 4104, 1032), ([4000, 1], 1032, 3000),
+                                      ([257] * 12, 2056, 640)])
+def test_many_tiles(rows, N, K):
+    """Every CTA walks several tiles and its rings wrap many times; a second run has the same bits."""
+    first = run_all(rows, N, K, 21)
+    for got, ref, S, depth, what in first:
+        check(got, ref, S, depth, what)
+    for (a, *_), (b, *_) in zip(first, run_all(rows, N, K, 21)):
+        assert torch.equal(a, b)
+
+
 def test_offsets_past_32_bits():
     """Row starts whose element index passes 2^31."""
     K, N, T = 8192, 16, 270000

@@ -75,6 +75,7 @@ def test_dequantise_every_scale():
 
 
 def weights(rng, *shape):
+    """Quantised normal weights and their values (the conversion has its own tests)."""
     W, _ = normal(rng, shape, shape[-1] ** -0.5)
     q = sg.quantize_mx4(W)
     return q, experts.mx4_values(*host(q))
@@ -132,6 +133,24 @@ def test_grouped_parity(rows, N, K, first, spare):
     sg.grouped_forward_mx4(X, Wq, off, bias=b, out=frame[1:T + 1])
     assert torch.equal(frame[1 + first:1 + int(o[-1])], Y[first:int(o[-1])])
     assert (frame[:1 + first] == 7.0).all() and (frame[1 + int(o[-1]):] == 7.0).all()
+
+
+@pytest.mark.parametrize("M,N,K", [(3000, 4104, 4096), (1500, 9000, 1312), (9000, 1032, 2560), (2000, 5000, 96)])
+def test_many_tiles(M, N, K):
+    """Every CTA walks several tiles and its rings wrap many times; all rows of a band of features and
+    all features of some rows are compared, and a second run has the same bits."""
+    rng = np.random.default_rng(M)
+    Wq, Wf = weights(rng, N, K)
+    X = rows_of(rng, M, K)
+    Xq = sg.quantize_mx4(X)
+    Y = sg.forward_mx4(Xq, Wq)
+    assert torch.equal(Y, sg.forward_mx4(Xq, Wq))
+    assert sg.mx4_status(Wq) == 0
+    Xf = experts.mx4_values(*host(Xq))
+    cols = slice(N - 300, N)
+    check(Y[:, cols], Xf @ Wf[cols].T, np.abs(Xf) @ np.abs(Wf[cols]).T, K, "features")
+    rows = sorted({0, 223, 224, M // 2, M - 33, M - 1})
+    check(Y[rows], Xf[rows] @ Wf.T, np.abs(Xf[rows]) @ np.abs(Wf).T, K, "rows")
 
 
 def test_many_experts():
