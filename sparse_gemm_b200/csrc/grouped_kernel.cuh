@@ -68,28 +68,25 @@ struct Cfg {
     static constexpr bool AM = kMode == kInputGrad || kMode == kWeightGrad;  // A is M-major
     static constexpr bool BN = kMode == kWeightGrad;                         // B is N-major
     static constexpr int BC = 256;                   // features per tile
-    static constexpr int BR = F4 ? 224 : 256;        // rows per tile, at most (4 bits: TMEM holds scales too)
+    static constexpr int BR = F4 ? 192 : 256;        // rows per tile, at most (4 bits: TMEM holds scales too)
     static constexpr int STEP = 32;                  // granularity of the rows (MMA N)
     static constexpr int BK = 128;                   // k per stage (two-byte columns)
     static constexpr int A_BYTES = 128 * BK * 2;
     static constexpr int B_BYTES = BR / 2 * BK * 2;
-    // scales of a stage: chunks of 512 bytes for 128 rows x 128 elements
-    static constexpr int SA_BYTES = F4 ? 4 * 512 : 0;
-    static constexpr int SB_BYTES = F4 ? 8 * 512 : 0;
-    static constexpr int STAGE = A_BYTES + B_BYTES + SA_BYTES + SB_BYTES;
+    static constexpr int STAGE = A_BYTES + B_BYTES;
     static constexpr int S = 3;
-    // two accumulators, then the scales of the stage at work (A 4, B 8 columns a chunk)
-    static constexpr int SA_COL = 2 * BR, SB_COL = SA_COL + SA_BYTES / 128;
+    // two accumulators, then a ring of scales: half a stage (256 elements of k), 8 columns of A's and 16 of B's
+    static constexpr int SR = F4 ? 5 : 0, SC_COL = 2 * BR, SC_COLS = 24;
     static constexpr int TMEM = 512;
     static constexpr int CHUNK = 32 * 32 * 2;
     static constexpr int OUT = 4 * 2 * CHUNK;        // two chunks per epilogue warp
-    static constexpr int BARS = (2 * S + 5) * 8 + 8;
-    static constexpr int SMEM = 1024 + S * STAGE + OUT + BARS + 2 * (kMaxExperts + 1) * 4;
-    static constexpr int SCALE_WARPS = F4 ? 3 : 0;   // of a stage
-    static constexpr int THREADS = 256 + 2 * 32 * SCALE_WARPS;
+    static constexpr int RAW = F4 ? 2 * (128 + BR) * 16 : 0;  // two stages' scales, 16 bytes a row
+    static constexpr int BARS = (2 * S + 2 * SR + 5) * 8 + 8;
+    static constexpr int SMEM = 1024 + S * STAGE + OUT + RAW + BARS + 2 * (kMaxExperts + 1) * 4;
+    static constexpr int THREADS = F4 ? 384 : 256;
     static_assert(SMEM <= 227 * 1024, "shared memory");
     static_assert(STAGE % 1024 == 0, "swizzle atoms");
-    static_assert(SB_COL + SB_BYTES / 128 <= TMEM, "TMEM columns");
+    static_assert(SC_COL + SR * SC_COLS <= TMEM, "TMEM columns");
 };
 
 struct Maps {
@@ -158,21 +155,21 @@ __device__ __forceinline__ uint8_t *align1024(uint8_t *p)
 //
 // The block-scaled MMA takes its scales from TMEM: row r of 128 has, for 128
 // elements of k (four blocks of 32), four bytes at lane r % 32, column r / 32,
-// the same in all four quarters of the lanes.  A chunk in shared memory is
-// that arrangement as 32 rows of 16 bytes, which one tcgen05.cp spreads.  The
-// scales lie in plain rows in global memory, wherever an expert's rows begin,
-// so warps load each row's bytes into registers and write the chunks.
+// the same in all four quarters of the lanes.  The scales lie in plain rows in
+// global memory, wherever an expert's rows begin.  Warps 8-11, one per quarter
+// of the lanes, bring them there: each loads a part of the rows (16 bytes of
+// a row a lane and stage, some stages ahead), the four share them through
+// shared memory, and each writes all of them to its lanes with tcgen05.st, half
+// a stage at a time into a ring of five.
 //
-// The fence that hands a chunk to the tensor core waits for the warp's loads
-// under way, so a warp loads four stages at a time (64 bytes of a row a lane)
-// and two sets of warps take these blocks in turn: one loads while the other
-// hands out (8192 x 4096 x 14336: loads before every stage's fence, one set
-// 295 us; two sets 269; blocks of four stages 2xx).
+// Measured at 8192 x 4096 x 14336, tiles of 224 rows: copying them with
+// tcgen05.cp (12 of 512 bytes a stage, in order with the MMAs, some 55 clocks
+// each) 260 us, without those copies 162, so they leave the MMAs' queue.
 //
-// Nothing is computed on what was loaded before it is handed out, so the loads
-// of a block do not wait for one another.  Bytes past the row's end count as
-// zeros (a scale of 2^-127 on zero codes; a NaN byte of the next row must not
-// reach them), and so do rows that do not exist.
+// Nothing is computed on what was loaded before its turn comes, so loads do
+// not wait for one another.  Bytes past the row's end count as zeros (a scale
+// of 2^-127 on zero codes; a NaN byte of the next row must not reach them),
+// and so do rows that do not exist.
 
 // Whole rows of 16-byte units: W words of a row from byte0 on.
 template <int W>
@@ -235,109 +232,150 @@ __device__ __forceinline__ void shift_words(const uint8_t *base, int64_t total, 
     }
 }
 
-constexpr int kBlock = 4;  // stages a warp loads at a time
-
-// A walk over this CTA's blocks of stages, tile after tile: `len` stages from
-// stage k of tile t on, the g-th of the launch.
+// A walk over this CTA's stages, tile after tile.
 template <int kMode>
 struct Walk {
     const Tiles<kMode> &tiles;
-    int t, stride, count, k, g, len;
+    int t, stride, count, k;
     Tile x;
 
     __device__ __forceinline__ Walk(const Tiles<kMode> &l, int first, int step, int n)
-        : tiles(l), t(first), stride(step), count(n), k(0), g(0)
+        : tiles(l), t(first), stride(step), count(n), k(0)
     {
         if (live()) x = tiles.at(t);
-        measure();
     }
     __device__ __forceinline__ bool live() const { return t < count; }
-    __device__ __forceinline__ void measure() { len = !live() ? 0 : x.kb - k < kBlock ? x.kb - k : kBlock; }
     __device__ __forceinline__ void next()
     {
-        if (!live()) return;
-        k += len;
-        g += len;
-        if (k == x.kb) {
-            k = 0;
-            t += stride;
-            if (live()) x = tiles.at(t);
-        }
-        measure();
+        if (++k < x.kb) return;
+        k = 0;
+        t += stride;
+        if (live()) x = tiles.at(t);
     }
 };
 
-// The warps' parts of a stage: 0 the scales of A, 1 and 2 those of B's rows
-// 0 .. 127 and 128 .. 223 (both CTAs hold all of B's).  A lane has the rows
-// lane, lane + 32, ... of its part.
+// Halves of a stage that hold elements.
+__device__ __forceinline__ int halves(const Tile &x, int k) { return x.k - k * 128 > 64 ? 2 : 1; }
+
 template <int kMode>
-__device__ __forceinline__ void copy_scales(const Tiles<kMode> &tiles, const Args &args, uint8_t *stages, uint64_t *full,
-                                            uint64_t *empty, volatile int *abort_flag, int first, int stride, int count,
-                                            uint32_t rank)
+__device__ __forceinline__ void copy_scales(const Tiles<kMode> &tiles, const Args &args, uint8_t *raw, uint64_t *sfull,
+                                            uint64_t *sempty, volatile int *abort_flag, int first, int stride, int count,
+                                            uint32_t rank, uint32_t tmem)
 {
     using C = Cfg<kMode>;
     constexpr bool kAny = kMode == kForward4Any;
-    constexpr int W = 4 * kBlock, R = W + kAny;  // a row's words of a block, and as loaded
-    const int part = ((threadIdx.x >> 5) - 8) % C::SCALE_WARPS, set = ((threadIdx.x >> 5) - 8) / C::SCALE_WARPS;
-    const int lane = threadIdx.x & 31;
+    constexpr int W = 4, R = W + kAny;  // a row's words of a stage, and as loaded
+    constexpr int P = 3;                // stages ahead
+    constexpr int G = C::BR / 32;       // groups of 32 rows of B
+    const int q = threadIdx.x / 32 - 8, lane = threadIdx.x & 31;
     const int32_t bytes = args.scale_bytes;
-    const uint8_t *base = part ? args.b_scales : args.a_scales;
-    const int64_t total = (part ? args.T : static_cast<int64_t>(args.E) * args.cols) * bytes;
-    Walk<kMode> at(tiles, first, stride, count);
-    if (set) at.next();
-    bool ok = true;
-    for (bool turn = set; at.live(); turn = true) {
-        const int r = part ? 128 * (part - 1) + lane : at.x.c0 + static_cast<int>(rank) * 128 + lane;
-        const int64_t row = part ? at.x.r0 + r : static_cast<int64_t>(at.x.e) * args.cols + r;
-        const int live = (part ? at.x.valid : args.cols) - r;  // rows that exist from the lane's first on
-        const int byte0 = at.k * 16;
-        uint32_t w[4][R];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            if constexpr (kAny) load_words_any<W>(base, total, bytes, row + 32 * c, 32 * c < live, byte0, w[c]);
-            else load_words<W>(base, bytes, row + 32 * c, 32 * c < live, byte0, w[c]);
+    const int64_t a_total = static_cast<int64_t>(args.E) * args.cols * bytes, b_total = static_cast<int64_t>(args.T) * bytes;
+    Walk<kMode> ahead(tiles, first, stride, count), now(tiles, first, stride, count);
+    uint32_t w[P][3][R];
+
+    // This warp's rows: 32q + lane of A, of B, and 128 + 32q + lane of B.
+    struct Row {
+        const uint8_t *base;
+        int64_t total, row;
+        bool exists;
+    };
+    auto rows = [&](const Walk<kMode> &at, int i) {
+        Row r;
+        if (i == 0) {
+            const int c = at.x.c0 + static_cast<int>(rank) * 128 + 32 * q + lane;
+            r.base = args.a_scales;
+            r.total = a_total;
+            r.row = static_cast<int64_t>(at.x.e) * args.cols + c;
+            r.exists = c < args.cols;
+        } else {
+            const int b = 128 * (i - 1) + 32 * q + lane;
+            r.base = args.b_scales;
+            r.total = b_total;
+            r.row = at.x.r0 + b;
+            r.exists = b < at.x.valid;
         }
-        // The block's turn comes when the other set has handed out the one before
-        // it (always waited for and passed on, so that neither set is left
-        // waiting).  A slot's barrier tells neighbouring phases apart and no more:
-        // the other set saw stage g - 1 free, hence g - 4 and g - 6 finished, when
-        // this one waits for g - 3; and g - 3 cannot be overtaken by g, which
-        // needs this warp.
-        if (turn) named_bar_sync(1 + 2 * part + (set ^ 1), 64);
+        return r;
+    };
+    auto load = [&](uint32_t(&v)[3][R]) {
+        if (!ahead.live()) return;
 #pragma unroll
-        for (int i = 0; i < kBlock; ++i) {
-            if (i >= at.len || !ok) break;
-            const int g = at.g + i, slot = g % C::S;
-            if (g >= C::S &&
-                __any_sync(0xffffffffu, !mbar_wait(&empty[slot], ((g / C::S) - 1) & 1, args.timeout_ns, abort_flag))) {
-                ok = false;
-                break;
-            }
-            uint8_t *dst = stages + slot * C::STAGE + C::A_BYTES + C::B_BYTES + lane * 16 +
-                           (part ? C::SA_BYTES + 512 * (part - 1) : 0);
-            const int step = part ? 1024 : 512;  // from chunk to chunk
-            uint32_t v[4][4];
+        for (int i = 0; i < 3; ++i) {
+            const Row r = rows(ahead, i);
+            if constexpr (kAny) load_words_any<W>(r.base, r.total, bytes, r.row, r.exists, 16 * ahead.k, v[i]);
+            else load_words<W>(r.base, bytes, r.row, r.exists, 16 * ahead.k, v[i]);
+        }
+        ahead.next();
+    };
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
+    for (int p = 0; p < P; ++p) load(w[p]);
+    bool ok = true;
+    int g = 0, h = 0;  // stages, halves of stages so far
+    while (now.live()) {
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+            if (!now.live()) break;
+            uint4 *buf = reinterpret_cast<uint4 *>(raw) + (g & 1) * (128 + C::BR);
+#pragma unroll
+            for (int i = 0; i < 3; ++i) {
+                const int at = 32 * q + lane + 128 * i;
+                if (at >= 128 + C::BR) break;
                 if constexpr (kAny) {
-                    shift_words<4>(base, total, bytes, row + 32 * c, 32 * c < live, byte0 + 16 * i, &w[c][4 * i], v[c]);
+                    const Row r = rows(now, i);
+                    uint32_t v[W];
+                    shift_words<W>(r.base, r.total, bytes, r.row, r.exists, 16 * now.k, w[p][i], v);
+                    buf[at] = make_uint4(v[0], v[1], v[2], v[3]);
                 } else {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) v[c][j] = w[c][4 * i + j];
+                    buf[at] = make_uint4(w[p][i][0], w[p][i][1], w[p][i][2], w[p][i][3]);
                 }
             }
+            // all four warps reach every one of these barriers, an aborted run's too;
+            // behind the next one, this buffer has been read
+            named_bar_sync(1, 128);
+            uint32_t a[4][4], b[8][4];  // [rows lane + 32 i][chunk of 128 elements]
 #pragma unroll
-            for (int j = 0; j < 4; ++j)  // chunk j: word j of every row
-                *reinterpret_cast<uint4 *>(dst + j * step) = make_uint4(v[0][j], v[1][j], v[2][j], v[3][j]);
-            fence_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(cluster_addr(&full[slot], 0));
+            for (int i = 0; i < 4; ++i) {
+                const uint4 v = buf[32 * i + lane];
+                a[i][0] = v.x, a[i][1] = v.y, a[i][2] = v.z, a[i][3] = v.w;
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint4 v = i < G ? buf[128 + 32 * i + lane] : make_uint4(0, 0, 0, 0);
+                b[i][0] = v.x, b[i][1] = v.y, b[i][2] = v.z, b[i][3] = v.w;
+            }
+            const int n = halves(now.x, now.k);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                if (i >= n) break;
+                const int slot = h % C::SR;
+                if (ok && h >= C::SR &&
+                    __any_sync(0xffffffffu, !mbar_wait(&sempty[slot], ((h / C::SR) - 1) & 1, args.timeout_ns, abort_flag)))
+                    ok = false;
+                if (ok) {
+                    tc_fence_after();
+                    uint32_t va[8], vb[16];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) va[c] = a[c][2 * i], va[4 + c] = a[c][2 * i + 1];
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) vb[c] = b[c][2 * i], vb[8 + c] = b[c][2 * i + 1];
+                    const uint32_t at = tmem + (static_cast<uint32_t>(32 * q) << 16) + C::SC_COL + slot * C::SC_COLS;
+                    tmem_st8(at, va);
+                    tmem_st16(at + 8, vb);
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster(cluster_addr(&sfull[slot], 0));
+                }
+                ++h;
+            }
+            ++g;
+            now.next();
+            load(w[p]);
         }
-        at.next();
-        __syncwarp();
-        if (at.live()) named_bar_arrive(1 + 2 * part + set, 64);
-        at.next();
     }
+    // the MMAs' last arrivals on this CTA's barriers are in before it may end
+    for (int s = 0; ok && s < C::SR && s < h; ++s)
+        if (__any_sync(0xffffffffu, !mbar_wait(&sempty[s], ((h - s + C::SR - 1) / C::SR - 1) & 1, args.timeout_ns, abort_flag)))
+            ok = false;
     if (lane == 0 && !ok) {
         *abort_flag = 1;
         set_status(args.status, BSL_ERR_TIMEOUT);
@@ -353,11 +391,14 @@ __global__ void __launch_bounds__(Cfg<kMode>::THREADS, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t *stages = align1024(smem_raw);
     uint8_t *outbuf = stages + C::S * C::STAGE;
-    uint64_t *full = reinterpret_cast<uint64_t *>(outbuf + C::OUT);  // copies of a stage landed (leader)
+    uint8_t *raw = outbuf + C::OUT;
+    uint64_t *full = reinterpret_cast<uint64_t *>(raw + C::RAW);     // copies of a stage landed (leader)
     uint64_t *empty = full + C::S;                                   // MMAs of a stage finished (each CTA)
     uint64_t *afull = empty + C::S;                                  // accumulator complete (each CTA)
     uint64_t *aempty = afull + 2;                                    // accumulator read out (leader)
-    uint64_t *drain = aempty + 2;
+    uint64_t *sfull = aempty + 2;                                    // half a stage's scales in TMEM (leader)
+    uint64_t *sempty = sfull + C::SR;                                // ... used (each CTA)
+    uint64_t *drain = sempty + C::SR;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     int32_t *off = reinterpret_cast<int32_t *>(tmem_slot + 2);
@@ -370,8 +411,12 @@ __global__ void __launch_bounds__(Cfg<kMode>::THREADS, 1)
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::S; ++s) {
-            mbar_init(&full[s], 1 + 2 * C::SCALE_WARPS);
+            mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
+        }
+        for (int s = 0; s < C::SR; ++s) {
+            mbar_init(&sfull[s], 8);
+            mbar_init(&sempty[s], 1);
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(&afull[a], 1);
@@ -486,7 +531,7 @@ __global__ void __launch_bounds__(Cfg<kMode>::THREADS, 1)
         if (rank == 0) {
             const uint32_t lead = lane == 0;
             bool ok = true;
-            int g = 0, it = 0;
+            int g = 0, h = 0, it = 0;
             for (int t = first; ok && t < count; t += stride) {
                 const Tile x = tiles.at(t);
                 if (x.kb == 0) continue;  // a sum over no rows: the epilogue writes zeros
@@ -499,7 +544,6 @@ __global__ void __launch_bounds__(Cfg<kMode>::THREADS, 1)
                 const uint32_t idesc = C::F4 ? make_idesc_mx4(256, x.n) : make_idesc_bf16(256, x.n, C::AM, C::BN);
                 const uint32_t d = tmem + acc * C::BR;
                 const uint32_t bs = x.n / 2 * 8;  // K-major B: a strip of half the rows, in 16-byte units
-                const uint32_t sa_t = tmem + C::SA_COL, sb_t = tmem + C::SB_COL;
                 for (int k = 0; k < x.kb; ++k, ++g) {
                     const int slot = g % C::S;
                     if (__any_sync(0xffffffffu, !mbar_wait(&full[slot], (g / C::S) & 1, tmo, abort_flag))) {
@@ -512,38 +556,41 @@ __global__ void __launch_bounds__(Cfg<kMode>::THREADS, 1)
                     // rows x 128 bytes; M- and N-major: strips 16384 bytes apart, a K step of 16 rows of 128 bytes
                     const uint64_t ad = make_sdesc(a0, C::AM ? 16384 : 16, 1024, kLayoutSw128);
                     const uint64_t bd = make_sdesc(b0, C::BN ? 16384 : 16, 1024, kLayoutSw128);
-                    const uint64_t sd = make_sdesc(b0 + C::B_BYTES, 0, 128, 0);  // scales: rows of 16 bytes, no swizzle
                     const uint32_t alo = static_cast<uint32_t>(ad), ahi = static_cast<uint32_t>(ad >> 32);
                     const uint32_t blo = static_cast<uint32_t>(bd), bhi = static_cast<uint32_t>(bd >> 32);
-                    const uint32_t slo = static_cast<uint32_t>(sd), shi = static_cast<uint32_t>(sd >> 32);
-                    auto scales = [&](int j) {  // chunk j: its scales to TMEM, in order with the MMAs around it
-                        if (!C::F4) return;
-                        scales_to_tmem(lead, sa_t + 4 * j, slo + 32 * j, shi);
-                        scales_to_tmem(lead, sb_t + 8 * j, slo + C::SA_BYTES / 16 + 64 * j, shi);
-                        if (x.n > 128) scales_to_tmem(lead, sb_t + 8 * j + 4, slo + C::SA_BYTES / 16 + 64 * j + 32, shi);
-                    };
-                    auto mma = [&](int i) {
+                    auto mma = [&](int i, uint32_t sc) {
                         const uint32_t al = alo + (C::AM ? i * 128 : (i >> 2) * 1024 + (i & 3) * 2);
                         const uint32_t bl = blo + (C::BN ? i * 128 : (i >> 2) * bs + (i & 3) * 2);
                         if (C::F4)
                             umma_mx4_lead_pair(lead, d, al, ahi, bl, bhi, idesc | (i & 1) * kSecondScales,
-                                               sa_t + (i >> 1) * 4, sb_t + (i >> 1) * 8, (k | i) != 0);
+                                               sc + (i >> 1 & 1) * 4, sc + 8 + (i >> 1 & 1) * 8, (k | i) != 0);
                         else
                             umma_bf16_lo_lead_pair(lead, d, al, ahi, bl, bhi, idesc, (k | i) != 0);
                     };
-                    const int left = x.k - k * 128;
-                    if (left >= 128) {
-                        scales(0);
+                    const int left = x.k - k * 128;  // the copies filled the rest of the stage with zeros
+                    if constexpr (C::F4) {
+                        const int n = halves(x, k);
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            if (i % 2 == 0 && i < 6) scales(i / 2 + 1);  // one chunk ahead: 255 us against 269
-                            mma(i);
+                        for (int j = 0; j < 2; ++j) {
+                            if (j >= n) break;
+                            const int sl = h % C::SR;
+                            if (__any_sync(0xffffffffu, !mbar_wait(&sfull[sl], (h / C::SR) & 1, tmo, abort_flag))) {
+                                ok = false;
+                                break;
+                            }
+                            tc_fence_after();
+                            const uint32_t sc = tmem + C::SC_COL + sl * C::SC_COLS;
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) mma(4 * j + i, sc);
+                            umma_commit_lead_pair(lead, &sempty[sl]);
+                            ++h;
                         }
-                    } else {  // the copies filled the rest with zeros
-                        for (int i = 0; 16 * i < left; ++i) {
-                            if (i % 2 == 0) scales(i / 2);
-                            mma(i);
-                        }
+                        if (!ok) break;
+                    } else if (left >= 128) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) mma(i, 0);
+                    } else {
+                        for (int i = 0; 16 * i < left; ++i) mma(i, 0);
                     }
                     umma_commit_lead_pair(lead, &empty[slot]);
                     __syncwarp();
@@ -571,7 +618,7 @@ __global__ void __launch_bounds__(Cfg<kMode>::THREADS, 1)
         }
         __syncwarp();
     } else if (C::F4 && warp >= 8) {
-        if constexpr (C::F4) copy_scales<kMode>(tiles, args, stages, full, empty, abort_flag, first, stride, count, rank);
+        if constexpr (C::F4) copy_scales<kMode>(tiles, args, raw, sfull, sempty, abort_flag, first, stride, count, rank, tmem);
     } else {
         // ------------------------------------------------------------ epilogue
         // Warp q reads TMEM lanes 32q .. 32q+31: features c0 + 32q + lane of its CTA.

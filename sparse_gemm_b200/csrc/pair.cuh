@@ -10,12 +10,6 @@ namespace bsl {
 // Two CTAs of a cluster working on one tile (cta_group::2).  Rank 0 leads: it
 // issues the MMAs, and both CTAs' copies complete on its barriers.
 
-// Arrive on a named barrier of `count` threads without waiting (see named_bar_sync).
-__device__ __forceinline__ void named_bar_arrive(uint32_t id, uint32_t count)
-{
-    asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(count) : "memory");
-}
-
 __device__ __forceinline__ uint32_t cluster_rank()
 {
     uint32_t r;
@@ -36,9 +30,13 @@ __device__ __forceinline__ uint32_t cluster_addr(const void *p, uint32_t rank)
     return r;
 }
 
+// Arrive on a barrier at a cluster address after TMEM accesses that were waited
+// for (tcgen05.wait), before which stands tc_fence_before.  Relaxed: no memory
+// access has to be ordered before it, and a release would wait for the warp's
+// loads under way.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar)
 {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 // 3-D tiled load into this CTA's own shared memory, completing on the
@@ -144,20 +142,6 @@ __device__ __forceinline__ void umma_mx4_lead_pair(uint32_t leader, uint32_t d_t
         : "memory");
 }
 
-// 32 rows of 16 bytes from shared memory (descriptor halves lo, hi) to 4 TMEM
-// columns of 32 lanes, the same in all four quarters of the lanes, in both
-// CTAs of a pair, each from its own shared memory.
-__device__ __forceinline__ void scales_to_tmem(uint32_t leader, uint32_t taddr, uint32_t lo, uint32_t hi)
-{
-    asm volatile(
-        "{\n\t.reg .pred e;\n\t.reg .b64 sd;\n\t"
-        "setp.ne.b32 e, %3, 0;\n\t"
-        "mov.b64 sd, {%1, %2};\n\t"
-        "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], sd;\n\t}" ::"r"(taddr),
-        "r"(lo), "r"(hi), "r"(leader)
-        : "memory");
-}
-
 // 3-D tiled store from shared memory (bulk-group completion).
 __device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, const void *src, int32_t x, int32_t y, int32_t z)
 {
@@ -166,6 +150,26 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, const void 
                  "r"(smem_u32(src)), "r"(x), "r"(y), "r"(z)
                  : "memory");
 }
+
+// 32 lanes x 32 bit to TMEM, 8 or 16 consecutive columns per thread.
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 "
+        "[%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // 32 lanes x 32 bit from TMEM, 32 consecutive columns per thread.
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32])
