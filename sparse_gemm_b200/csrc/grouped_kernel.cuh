@@ -80,10 +80,11 @@ struct Cfg {
     static constexpr int TMEM = 512;
     static constexpr int CHUNK = 32 * 32 * 2;
     static constexpr int OUT = 4 * 2 * CHUNK;        // two chunks per epilogue warp
-    static constexpr int RAW = F4 ? 2 * (128 + BR) * 16 : 0;  // two stages' scales, 16 bytes a row
+    static constexpr int SETS = 2;                   // of four warps that bring the scales of stages in turn
+    static constexpr int RAW = F4 ? SETS * 2 * (128 + BR) * 16 : 0;  // two stages' scales a set, 16 bytes a row
     static constexpr int BARS = (2 * S + 2 * SR + 5) * 8 + 8;
     static constexpr int SMEM = 1024 + S * STAGE + OUT + RAW + BARS + 2 * (kMaxExperts + 1) * 4;
-    static constexpr int THREADS = F4 ? 384 : 256;
+    static constexpr int THREADS = F4 ? 256 + SETS * 128 : 256;
     static_assert(SMEM <= 227 * 1024, "shared memory");
     static_assert(STAGE % 1024 == 0, "swizzle atoms");
     static_assert(SC_COL + SR * SC_COLS <= TMEM, "TMEM columns");
@@ -156,11 +157,12 @@ __device__ __forceinline__ uint8_t *align1024(uint8_t *p)
 // The block-scaled MMA takes its scales from TMEM: row r of 128 has, for 128
 // elements of k (four blocks of 32), four bytes at lane r % 32, column r / 32,
 // the same in all four quarters of the lanes.  The scales lie in plain rows in
-// global memory, wherever an expert's rows begin.  Warps 8-11, one per quarter
-// of the lanes, bring them there: each loads a part of the rows (16 bytes of
-// a row a lane and stage, some stages ahead), the four share them through
-// shared memory, and each writes all of them to its lanes with tcgen05.st, half
-// a stage at a time into a ring of five.
+// global memory, wherever an expert's rows begin.  Two sets of four warps, a
+// warp per quarter of the lanes, bring the scales of stages there in turn: each
+// warp loads a part of the rows (16 bytes of a row a lane and stage, some
+// stages ahead), the four share them through shared memory, and each writes
+// all of them to its lanes with tcgen05.st, half a stage at a time into a ring
+// of five.
 //
 // Measured at 8192 x 4096 x 14336, tiles of 224 rows: copying them with
 // tcgen05.cp (12 of 512 bytes a stage, in order with the MMAs, some 55 clocks
@@ -232,6 +234,9 @@ __device__ __forceinline__ void shift_words(const uint8_t *base, int64_t total, 
     }
 }
 
+// Halves of a stage that hold elements.
+__device__ __forceinline__ int halves(const Tile &x, int k) { return x.k - k * 128 > 64 ? 2 : 1; }
+
 // A walk over this CTA's stages, tile after tile.
 template <int kMode>
 struct Walk {
@@ -247,15 +252,12 @@ struct Walk {
     __device__ __forceinline__ bool live() const { return t < count; }
     __device__ __forceinline__ void next()
     {
-        if (++k < x.kb) return;
+        if (!live() || ++k < x.kb) return;
         k = 0;
         t += stride;
         if (live()) x = tiles.at(t);
     }
 };
-
-// Halves of a stage that hold elements.
-__device__ __forceinline__ int halves(const Tile &x, int k) { return x.k - k * 128 > 64 ? 2 : 1; }
 
 template <int kMode>
 __device__ __forceinline__ void copy_scales(const Tiles<kMode> &tiles, const Args &args, uint8_t *raw, uint64_t *sfull,
@@ -265,12 +267,18 @@ __device__ __forceinline__ void copy_scales(const Tiles<kMode> &tiles, const Arg
     using C = Cfg<kMode>;
     constexpr bool kAny = kMode == kForward4Any;
     constexpr int W = 4, R = W + kAny;  // a row's words of a stage, and as loaded
-    constexpr int P = 3;                // stages ahead
+    constexpr int P = 2;                // stages of its own that a set loads ahead
     constexpr int G = C::BR / 32;       // groups of 32 rows of B
-    const int q = threadIdx.x / 32 - 8, lane = threadIdx.x & 31;
+    const int q = threadIdx.x / 32 & 3, set = threadIdx.x / 128 - 2, lane = threadIdx.x & 31;
     const int32_t bytes = args.scale_bytes;
     const int64_t a_total = static_cast<int64_t>(args.E) * args.cols * bytes, b_total = static_cast<int64_t>(args.T) * bytes;
-    Walk<kMode> ahead(tiles, first, stride, count), now(tiles, first, stride, count);
+    Walk<kMode> now(tiles, first, stride, count);
+    int h = 0;  // halves of stages so far, the other set's too
+    if (set && now.live()) {
+        h = halves(now.x, now.k);
+        now.next();
+    }
+    Walk<kMode> ahead = now;
     uint32_t w[P][3][R];
 
     // This warp's rows: 32q + lane of A, of B, and 128 + 32q + lane of B.
@@ -305,16 +313,16 @@ __device__ __forceinline__ void copy_scales(const Tiles<kMode> &tiles, const Arg
             else load_words<W>(r.base, bytes, r.row, r.exists, 16 * ahead.k, v[i]);
         }
         ahead.next();
+        ahead.next();
     };
 #pragma unroll
     for (int p = 0; p < P; ++p) load(w[p]);
     bool ok = true;
-    int g = 0, h = 0;  // stages, halves of stages so far
     while (now.live()) {
 #pragma unroll
         for (int p = 0; p < P; ++p) {
             if (!now.live()) break;
-            uint4 *buf = reinterpret_cast<uint4 *>(raw) + (g & 1) * (128 + C::BR);
+            uint4 *buf = reinterpret_cast<uint4 *>(raw) + (2 * set + p) * (128 + C::BR);
 #pragma unroll
             for (int i = 0; i < 3; ++i) {
                 const int at = 32 * q + lane + 128 * i;
@@ -330,7 +338,7 @@ __device__ __forceinline__ void copy_scales(const Tiles<kMode> &tiles, const Arg
             }
             // all four warps reach every one of these barriers, an aborted run's too;
             // behind the next one, this buffer has been read
-            named_bar_sync(1, 128);
+            named_bar_sync(1 + set, 128);
             uint32_t a[4][4], b[8][4];  // [rows lane + 32 i][chunk of 128 elements]
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -346,6 +354,9 @@ __device__ __forceinline__ void copy_scales(const Tiles<kMode> &tiles, const Arg
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 if (i >= n) break;
+                // A barrier tells neighbouring phases apart and no more: this set's last
+                // wait was for half h - 3 - SR or a later one, and half h cannot be
+                // finished without this warp
                 const int slot = h % C::SR;
                 if (ok && h >= C::SR &&
                     __any_sync(0xffffffffu, !mbar_wait(&sempty[slot], ((h / C::SR) - 1) & 1, args.timeout_ns, abort_flag)))
@@ -367,7 +378,8 @@ __device__ __forceinline__ void copy_scales(const Tiles<kMode> &tiles, const Arg
                 }
                 ++h;
             }
-            ++g;
+            now.next();
+            if (now.live()) h += halves(now.x, now.k);
             now.next();
             load(w[p]);
         }
