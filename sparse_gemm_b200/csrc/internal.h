@@ -151,6 +151,14 @@ bsl_status launch_grouped_dw(const void *dY, const void *X, int32_t T, const int
 bsl_status launch_grouped_bias_grad(const void *dY, int32_t T, const int32_t *offsets, int32_t E, int32_t N, void *db,
                                     cudaStream_t s);
 
+// The forwards of both layers for calls of few rows, where these are true.
+bool few_rows(int32_t T);
+bool few_rows4(int32_t T, const bsl_mx4 *W);
+bsl_status launch_few_rows(const void *X, int32_t T, const int32_t *offsets, const bsl_grouped *W, const void *bias,
+                           void *Y, int32_t zero_rest, cudaStream_t s);
+bsl_status launch_few_rows4(const uint8_t *xc, const uint8_t *xs, int32_t T, const int32_t *offsets, const bsl_mx4 *W,
+                            const void *bias, void *Y, int32_t zero_rest, cudaStream_t s);
+
 // Microscaled 4-bit: conversion, and the product (offsets null: one group of all rows).
 bsl_status launch_mx4_quantize(const void *X, int64_t elems, uint8_t *codes, uint8_t *scales, cudaStream_t s);
 bsl_status launch_mx4_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t elems, void *X, cudaStream_t s);

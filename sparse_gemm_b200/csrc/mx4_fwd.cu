@@ -12,6 +12,7 @@ namespace bsl {
 bsl_status launch_mx4_fwd(const uint8_t *xc, const uint8_t *xs, int32_t T, const int32_t *offsets, const bsl_mx4 *W,
                           const void *bias, void *Y, int32_t zero_rest, cudaStream_t s)
 {
+    if (few_rows4(T, W)) return launch_few_rows4(xc, xs, T, offsets, W, bias, Y, zero_rest, s);
     Args args = {};
     args.offsets = offsets;
     args.bias = static_cast<const __nv_bfloat16 *>(bias);

@@ -12,14 +12,17 @@
 //
 // Bound by bytes: 2 read and 17/32 written an element (the reverse back).
 // Four lanes share a block: 16-byte loads, 4-byte code stores, whole lines a
-// warp; the largest magnitude takes two shuffles.
+// warp; the largest magnitude takes two shuffles.  A thread has kChunks such
+// loads in flight, a block's width apart.
 #include "common.cuh"
 #include "internal.h"
+#include "mx4.cuh"
 
 namespace bsl {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kChunks = 4;  // a thread's chunks of 8 elements
 
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
@@ -40,76 +43,81 @@ __device__ __forceinline__ uint32_t to_e2m1x2(float lo, float hi)
 __global__ void __launch_bounds__(kThreads)
     k_mx4_quantize(const uint4 *__restrict__ X, int64_t n, uint32_t *__restrict__ codes, uint8_t *__restrict__ scales)
 {
-    const int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-    const bool live = i < n;  // whole blocks of four lanes
-    const uint4 x = live ? X[i] : make_uint4(0, 0, 0, 0);
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-    uint32_t top = 0;
+    const int64_t i0 = static_cast<int64_t>(blockIdx.x) * kThreads * kChunks + threadIdx.x;
+    dependents_may_launch();
+    wait_for_prior_grid();
+    uint4 x[kChunks];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) top = __vmaxu2(top, w[j] & 0x7FFF7FFFu);
-    top = max(top & 0xFFFFu, top >> 16);
-    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-    const uint32_t f = top >> 7;
-    const uint32_t scale = f == 255 ? 255 : f > 2 ? f - 2 : 0;
-    // 1 / s = 2^(127 - scale); 0 where the block stands for NaN
-    const float inv = f == 255 ? 0.f : __uint_as_float((254 - scale) << 23);
-    uint32_t code = 0;
-    if (f != 255) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) code |= to_e2m1x2(bf16_lo(w[j]) * inv, bf16_hi(w[j]) * inv) << (8 * j);
+    for (int u = 0; u < kChunks; ++u) {
+        const int64_t i = i0 + u * kThreads;
+        x[u] = i < n ? X[i] : make_uint4(0, 0, 0, 0);  // a block's four lanes are in or out together
     }
-    if (!live) return;
-    codes[i] = code;
-    if ((i & 3) == 0) scales[i >> 2] = static_cast<uint8_t>(scale);
-}
-
-// One 4-bit code's value under the scale: 4 bits to fp32 by bits (no table).
-__device__ __forceinline__ float from_e2m1(uint32_t c, float scale)
-{
-    const uint32_t m = c & 7u;
-    // 0 .5 1 1.5 2 3 4 6: exponent and mantissa bits above the subnormal .5
-    const float v = m < 2 ? 0.5f * static_cast<float>(m)
-                          : __uint_as_float(((m >> 1) + 126u) << 23 | (m & 1u) << 22);
-    return (c & 8u ? -v : v) * scale;
+#pragma unroll
+    for (int u = 0; u < kChunks; ++u) {
+        const int64_t i = i0 + u * kThreads;
+        const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+        uint32_t top = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) top = __vmaxu2(top, w[j] & 0x7FFF7FFFu);
+        top = max(top & 0xFFFFu, top >> 16);
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const uint32_t f = top >> 7;
+        const uint32_t scale = f == 255 ? 255 : f > 2 ? f - 2 : 0;
+        // 1 / s = 2^(127 - scale)
+        const float inv = __uint_as_float((254 - scale) << 23);
+        uint32_t code = 0;
+        if (f != 255) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) code |= to_e2m1x2(bf16_lo(w[j]) * inv, bf16_hi(w[j]) * inv) << (8 * j);
+        }
+        if (i >= n) continue;
+        codes[i] = code;
+        if ((i & 3) == 0) scales[i >> 2] = static_cast<uint8_t>(scale);
+    }
 }
 
 __global__ void __launch_bounds__(kThreads)
     k_mx4_dequantize(const uint32_t *__restrict__ codes, const uint8_t *__restrict__ scales, int64_t n,
                      uint4 *__restrict__ X)
 {
-    const int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-    if (i >= n) return;
-    const uint32_t c = codes[i], b = scales[i >> 2];
-    // 2^(b - 127); 2^-127 is below the normal range, 255 stands for NaN
-    const float scale = __uint_as_float(b == 255 ? 0x7FC00000u : b == 0 ? 0x00400000u : b << 23);
-    uint32_t w[4];
+    const int64_t i0 = static_cast<int64_t>(blockIdx.x) * kThreads * kChunks + threadIdx.x;
+    dependents_may_launch();
+    wait_for_prior_grid();
+    uint32_t c[kChunks], b[kChunks];
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-        w[j] = pack_bf16x2(from_e2m1(c >> (8 * j), scale), from_e2m1(c >> (8 * j + 4), scale));
-    X[i] = make_uint4(w[0], w[1], w[2], w[3]);
+    for (int u = 0; u < kChunks; ++u) {
+        const int64_t i = i0 + u * kThreads;
+        c[u] = i < n ? codes[i] : 0;
+        b[u] = i < n ? scales[i >> 2] : 0;
+    }
+#pragma unroll
+    for (int u = 0; u < kChunks; ++u) {
+        const int64_t i = i0 + u * kThreads;
+        uint32_t v[4];  // codes j and j + 4
+        decode8<true>(c[u], b[u], 0, v);
+        if (i < n)
+            X[i] = make_uint4(__byte_perm(v[0], v[1], 0x5410), __byte_perm(v[2], v[3], 0x5410),
+                              __byte_perm(v[0], v[1], 0x7632), __byte_perm(v[2], v[3], 0x7632));
+    }
 }
 
 }  // namespace
 
 bsl_status launch_mx4_quantize(const void *X, int64_t elems, uint8_t *codes, uint8_t *scales, cudaStream_t s)
 {
-    const int64_t n = elems / 8, blocks = (n + kThreads - 1) / kThreads;
+    const int64_t n = elems / 8, blocks = (n + kThreads * kChunks - 1) / (kThreads * kChunks);
     if (blocks > 0x7FFFFFFF) return BSL_ERR_UNSUPPORTED;
-    if (blocks == 0) return BSL_OK;
-    k_mx4_quantize<<<static_cast<unsigned>(blocks), kThreads, 0, s>>>(
-        static_cast<const uint4 *>(X), n, reinterpret_cast<uint32_t *>(codes), scales);
-    return cuda_status(cudaGetLastError());
+    return cuda_status(launch_dependent(k_mx4_quantize, static_cast<unsigned>(blocks), kThreads, 0, s,
+                                        static_cast<const uint4 *>(X), n, reinterpret_cast<uint32_t *>(codes), scales));
 }
 
 bsl_status launch_mx4_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t elems, void *X, cudaStream_t s)
 {
-    const int64_t n = elems / 8, blocks = (n + kThreads - 1) / kThreads;
+    const int64_t n = elems / 8, blocks = (n + kThreads * kChunks - 1) / (kThreads * kChunks);
     if (blocks > 0x7FFFFFFF) return BSL_ERR_UNSUPPORTED;
-    if (blocks == 0) return BSL_OK;
-    k_mx4_dequantize<<<static_cast<unsigned>(blocks), kThreads, 0, s>>>(
-        reinterpret_cast<const uint32_t *>(codes), scales, n, static_cast<uint4 *>(X));
-    return cuda_status(cudaGetLastError());
+    return cuda_status(launch_dependent(k_mx4_dequantize, static_cast<unsigned>(blocks), kThreads, 0, s,
+                                        reinterpret_cast<const uint32_t *>(codes), scales, n, static_cast<uint4 *>(X)));
 }
 
 }  // namespace bsl

@@ -71,6 +71,17 @@ def test_many_experts(E, N, K):
         check(got, ref, S, depth, what)
 
 
+FEW = [([8], 1032, 4096, 0, 0), ([7], 24, 1000, 0, 0), ([0, 3, 0, 0, 1, 0, 2], 520, 2056, 1, 1), ([1] * 8, 264, 40, 0, 0),
+       ([0] * 31 + [2] + [0] * 200 + [1, 0, 3], 72, 136, 0, 2), ([0] * 1000 + [5], 16, 264, 2, 1), ([9], 136, 1000, 0, 0)]
+
+
+@pytest.mark.parametrize("rows,N,K,first,spare", FEW)
+def test_few_rows(rows, N, K, first, spare):
+    """Up to eight rows in all, and one more: any expert, long and odd K."""
+    for got, ref, S, depth, what in run_all(rows, N, K, 20, first=first, spare=spare):
+        check(got, ref, S, depth, what)
+
+
 @pytest.mark.parametrize("rows,N,K", [([130, 0, 70, 1], 264, 520), ([2, 3], 72, 264), ([600, 20], 40, 1032)])
 def test_exact_on_integers(rows, N, K):
     """Sums of small integers are exact in fp32: one rounding to bf16 remains."""

@@ -153,6 +153,45 @@ def test_many_tiles(M, N, K):
     check(Y[rows], Xf[rows] @ Wf.T, np.abs(Xf[rows]) @ np.abs(Wf).T, K, "rows")
 
 
+@pytest.mark.parametrize("rows,N,K,first,spare", [
+    ([8], 1032, 4096, 0, 0), ([1], 11008, 4096, 0, 0), ([0, 3, 0, 0, 1, 0, 2], 520, 2080, 1, 1),
+    ([0] * 31 + [2] + [0] * 200 + [1, 0, 3], 72, 160, 0, 2), ([0] * 1000 + [5], 16, 32, 2, 1), ([9], 136, 992, 0, 0)])
+def test_few_rows(rows, N, K, first, spare):
+    rng = np.random.default_rng(N + K + first)
+    off, o = offsets_of(rows, first)
+    Wq, Wf = weights(rng, len(rows), N, K)
+    X = rows_of(rng, int(o[-1]) + spare, K)
+    b, bf = normal(rng, (len(rows), N))
+    Xf = experts.mx4_values(*host(sg.quantize_mx4(X)))
+    Y = sg.grouped_forward_mx4(X, Wq, off, bias=b)
+    check(Y, *experts.grouped_forward(Xf, Wf, o, bf), K, "few rows")
+    assert not Y[:first].any() and not Y[int(o[-1]):].any()
+    assert sg.mx4_status(Wq) == 0
+
+
+@pytest.mark.parametrize("M", [3, 40])
+def test_every_scale_byte(M):
+    """Weight rows and activation rows under every scale byte whose products stay in the fp32 range."""
+    rng = np.random.default_rng(M)
+    N, K = 256, 64
+    codes = lambda r: torch.from_numpy(rng.integers(0, 256, (r, K // 2), dtype=np.uint8)).cuda()
+    for xs in (0, 1, 60, 127, 128, 129, 180, 250):
+        byte = np.arange(N)
+        ok = (byte + xs > 20) & (byte + xs < 360) & (byte < 255)      # 2^-234 .. 2^106
+        ws = np.where(ok, byte, 127).astype(np.uint8)
+        Wq = sg.Mx4Tensor(codes(N), torch.from_numpy(np.repeat(ws[:, None], 2, axis=1)).cuda())
+        Xq = sg.Mx4Tensor(codes(M), torch.full((M, 2), xs, dtype=torch.uint8, device="cuda"))
+        Xf, Wf = experts.mx4_values(*host(Xq)), experts.mx4_values(*host(Wq))
+        ref, S = Xf @ Wf.T, np.abs(Xf) @ np.abs(Wf).T
+        Y = sg.forward_mx4(Xq, Wq)
+        unit = ws.astype(int) + xs - 254
+        fits = (unit > -110) & (unit < 110)          # far above the subnormal numbers, below the fp32 range
+        check(Y[:, fits], ref[:, fits], S[:, fits], K, f"scale {xs}")
+        assert (Y[:, unit <= -110].double().abs().cpu().numpy() <= 2.0 ** -100).all()
+        # past the fp32 range: not finite (an infinity has the sign of the partial sum that passed it)
+        assert not np.isfinite(Y.double().cpu().numpy()[np.abs(ref) > 2.0 ** 129]).any()
+
+
 def test_many_experts():
     rng = np.random.default_rng(7)
     rows = rng.integers(0, 3, 1024).tolist()
