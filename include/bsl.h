@@ -399,6 +399,17 @@ BSL_API bsl_status bsl_mx4_grouped_forward(const uint8_t *x_codes, const uint8_t
                                            const int32_t *offsets, const bsl_mx4 *W, const void *bias, void *Y,
                                            int32_t zero_rest, void *stream);
 
+/* The same from bf16 rows X [T][K], quantised as by bsl_mx4_quantize on the way
+ * (into the workspace).  offsets NULL: W has E = 1 and owns all rows.
+ * workspace: bsl_mx4_workspace_bytes(T, W) bytes of device scratch, 16-byte
+ * aligned, written before it is read; calls that use one workspace must not
+ * overlap on the GPU. */
+BSL_API bsl_status bsl_mx4_linear(const void *X, int32_t T, const int32_t *offsets, const bsl_mx4 *W, const void *bias,
+                                  void *Y, int32_t zero_rest, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Scratch bytes of bsl_mx4_linear for T rows (0 for T <= 0). */
+BSL_API size_t bsl_mx4_workspace_bytes(int32_t T, const bsl_mx4 *W);
+
 /* SYNCHRONOUS: waits for the stream, copies the device status word of W to
  * *status_host (a bsl_status value) and resets it to BSL_OK. */
 BSL_API bsl_status bsl_mx4_get_status(const bsl_mx4 *W, int32_t *status_host, void *stream);

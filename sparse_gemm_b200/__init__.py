@@ -125,6 +125,8 @@ def library() -> ctypes.CDLL:
             "bsl_mx4_dequantize": (ctypes.c_int, [P, P, I64, I32, P, P]),
             "bsl_mx4_forward": (ctypes.c_int, [P, P, I32, XP, P, P, P]),
             "bsl_mx4_grouped_forward": (ctypes.c_int, [P, P, I32, P, XP, P, P, I32, P]),
+            "bsl_mx4_linear": (ctypes.c_int, [P, I32, P, XP, P, P, I32, P, SZ, P]),
+            "bsl_mx4_workspace_bytes": (SZ, [I32, XP]),
             "bsl_mx4_get_status": (ctypes.c_int, [XP, ctypes.POINTER(I32), P]),
         }
         for name, (res, args) in sig.items():
@@ -870,15 +872,31 @@ def dequantize_mx4(q: Mx4Tensor, out: torch.Tensor | None = None) -> torch.Tenso
     return X
 
 
-def _mx4_input(X, Wq: Mx4Tensor) -> Mx4Tensor:
-    if not isinstance(X, Mx4Tensor):
+def _mx4_product(X, Wq: Mx4Tensor, offsets, bias_ptr, N: int, out) -> torch.Tensor:
+    if isinstance(X, Mx4Tensor):
+        if len(X.shape) != 2 or X.K != Wq.K:
+            raise ValueError(f"X holds {X.shape}, expected [rows, {Wq.K}]")
+        if X.device != Wq.device:
+            raise ValueError(f"X must be on {Wq.device}")
+        rows, like = X.shape[0], X.codes
+    else:
         _tensor_arg(X, "X", (None, Wq.K), torch.bfloat16, Wq.codes)
-        return quantize_mx4(X)
-    if len(X.shape) != 2 or X.K != Wq.K:
-        raise ValueError(f"X holds {X.shape}, expected [rows, {Wq.K}]")
-    if X.device != Wq.device:
-        raise ValueError(f"X must be on {Wq.device}")
-    return X
+        rows, like = X.shape[0], X
+    Y = _out_arg(out, (rows, N), like)
+    lib, off = library(), None if offsets is None else offsets.data_ptr()
+    if like is X:
+        nbytes = rows * (Wq.K // 2 + Wq.K // 32)   # bsl_mx4_workspace_bytes
+        ws = X.new_empty(nbytes, dtype=torch.uint8)
+        st = lib.bsl_mx4_linear(X.data_ptr(), rows, off, Wq.cref(), bias_ptr, Y.data_ptr(), out is None, ws.data_ptr(),
+                                nbytes, _stream(X))
+    elif offsets is None:
+        st = lib.bsl_mx4_forward(X.codes.data_ptr(), X.scales.data_ptr(), rows, Wq.cref(), bias_ptr, Y.data_ptr(),
+                                 _stream(like))
+    else:
+        st = lib.bsl_mx4_grouped_forward(X.codes.data_ptr(), X.scales.data_ptr(), rows, off, Wq.cref(), bias_ptr,
+                                         Y.data_ptr(), out is None, _stream(like))
+    _check(st, "bsl_mx4_linear" if like is X else "bsl_mx4_forward" if offsets is None else "bsl_mx4_grouped_forward")
+    return Y
 
 
 def forward_mx4(X, Wq: Mx4Tensor, bias: torch.Tensor | None = None, out: torch.Tensor | None = None) -> torch.Tensor:
@@ -887,12 +905,7 @@ def forward_mx4(X, Wq: Mx4Tensor, bias: torch.Tensor | None = None, out: torch.T
     if len(Wq.shape) != 2:
         raise ValueError("Wq must be a weight [N, K]")
     N = Wq.shape[0]
-    Xq = _mx4_input(X, Wq)
-    bptr = _bias_ptr(bias, N, Xq.codes)
-    Y = _out_arg(out, (Xq.shape[0], N), Xq.codes)
-    _check(library().bsl_mx4_forward(Xq.codes.data_ptr(), Xq.scales.data_ptr(), Xq.shape[0], Wq.cref(), bptr,
-                                     Y.data_ptr(), _stream(Xq.codes)), "bsl_mx4_forward")
-    return Y
+    return _mx4_product(X, Wq, None, _bias_ptr(bias, N, Wq.codes), N, out)
 
 
 def grouped_forward_mx4(X, Wq: Mx4Tensor, offsets: torch.Tensor, bias: torch.Tensor | None = None,
@@ -902,14 +915,8 @@ def grouped_forward_mx4(X, Wq: Mx4Tensor, offsets: torch.Tensor, bias: torch.Ten
     if len(Wq.shape) != 3:
         raise ValueError("Wq must be a weight [E, N, K]")
     E, N, _ = Wq.shape
-    Xq = _mx4_input(X, Wq)
-    _tensor_arg(offsets, "offsets", (E + 1,), torch.int32, Xq.codes)
-    bptr = _expert_bias(bias, E, N, Xq.codes)
-    Y = _out_arg(out, (Xq.shape[0], N), Xq.codes)
-    _check(library().bsl_mx4_grouped_forward(Xq.codes.data_ptr(), Xq.scales.data_ptr(), Xq.shape[0],
-                                             offsets.data_ptr(), Wq.cref(), bptr, Y.data_ptr(), out is None,
-                                             _stream(Xq.codes)), "bsl_mx4_grouped_forward")
-    return Y
+    _tensor_arg(offsets, "offsets", (E + 1,), torch.int32, Wq.codes)
+    return _mx4_product(X, Wq, offsets, _expert_bias(bias, E, N, Wq.codes), N, out)
 
 
 def mx4_status(Wq: Mx4Tensor) -> int:

@@ -627,6 +627,32 @@ bsl_status bsl_mx4_grouped_forward(const uint8_t *x_codes, const uint8_t *x_scal
     return launch_mx4_fwd(x_codes, x_scales, T, offsets, W, bias, Y, zero_rest, static_cast<cudaStream_t>(stream));
 }
 
+size_t bsl_mx4_workspace_bytes(int32_t T, const bsl_mx4 *W)
+{
+    if (check_mx4(W) != BSL_OK || T <= 0) return 0;
+    return static_cast<size_t>(T) * (W->K / 2) + static_cast<size_t>(T) * (W->K / 32);
+}
+
+bsl_status bsl_mx4_linear(const void *X, int32_t T, const int32_t *offsets, const bsl_mx4 *W, const void *bias, void *Y,
+                          int32_t zero_rest, void *workspace, size_t workspace_bytes, void *stream)
+{
+    BSL_TRY(check_mx4(W));
+    if (T < 0 || (!offsets && W->E != 1) || !aligned(offsets, 4) || (bias && !aligned(bias, 16)))
+        return BSL_ERR_INVALID_ARG;
+    if (check_matrix(X, T) != BSL_OK || check_matrix(Y, T) != BSL_OK || check_matrix(workspace, T) != BSL_OK ||
+        workspace_bytes < bsl_mx4_workspace_bytes(T, W))
+        return BSL_ERR_INVALID_ARG;
+    if (T == 0) return BSL_OK;
+    DeviceGuard guard;
+    BSL_TRY(guard.bind(X));
+    BSL_TRY(check_device());
+    uint8_t *codes = static_cast<uint8_t *>(workspace);
+    uint8_t *scales = codes + static_cast<size_t>(T) * (W->K / 2);  // K / 2 is a multiple of 16
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    BSL_TRY(launch_mx4_quantize(X, static_cast<int64_t>(T) * W->K, codes, scales, s));
+    return launch_mx4_fwd(codes, scales, T, offsets, W, bias, Y, zero_rest, s);
+}
+
 bsl_status bsl_mx4_get_status(const bsl_mx4 *W, int32_t *status_host, void *stream)
 {
     if (!W || !W->status || !status_host) return BSL_ERR_INVALID_ARG;

@@ -182,6 +182,15 @@ def test_bad_mx4_arguments_are_refused(lib):
     grp = lambda c, s, t, o, y, b=None: lib.bsl_mx4_grouped_forward(c, s, t, o, w, b, y, 0, None)
     assert [grp(0, 4096, 8, 4096, 4096), grp(4096, 0, 8, 4096, 4096), grp(4096, 4096, -1, 4096, 4096),
             grp(4096, 4096, 8, 0, 4096), grp(4096, 4096, 8, 4096, 0), grp(4096, 4096, 8, 4098, 4096)] == [1] * 6
+    need = lib.bsl_mx4_workspace_bytes(8, w)
+    assert need == 8 * (32 + 2) and lib.bsl_mx4_workspace_bytes(0, w) == 0
+    lin = lambda x, t, o, y, ws, n, b=None, w=w: lib.bsl_mx4_linear(x, t, o, w, b, y, 0, ws, n, None)
+    assert [lin(0, 8, None, 4096, 4096, need), lin(4096, -1, None, 4096, 4096, need), lin(4096, 8, None, 0, 4096, need),
+            lin(4096, 8, None, 4096, 0, need), lin(4096, 8, None, 4096, 4104, need),
+            lin(4096, 8, None, 4096, 4096, need - 1), lin(4096, 8, 4098, 4096, 4096, need),
+            lin(4096, 8, None, 4096, 4096, need, 4104),
+            lin(4096, 8, None, 4096, 4096, need, w=ctypes.byref(_mx4(E=2)))] == [1] * 9
+    assert lin(0, 0, None, 0, 0, 0) == 0
     for fn in (lambda x, r, k, c, s: lib.bsl_mx4_quantize(x, r, k, c, s, None),
                lambda x, r, k, c, s: lib.bsl_mx4_dequantize(c, s, r, k, x, None)):
         assert [fn(0, 4, 64, 4096, 4096), fn(4096, -1, 64, 4096, 4096), fn(4096, 4, 48, 4096, 4096),
