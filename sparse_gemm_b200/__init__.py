@@ -15,6 +15,7 @@ weight gradient dW = dY^T X at the kept blocks only.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 
 import torch
@@ -812,22 +813,41 @@ class Mx4Tensor:
             raise ValueError("codes must hold a positive multiple of 32 columns (16 bytes) a row")
         _tensor_arg(codes, "codes", codes.shape, torch.uint8)
         _tensor_arg(scales, "scales", (*lead, K // 32), torch.uint8, codes)
-        self._set(codes, scales, (*lead, K))
+        self._codes, self._scales = codes, scales
+        self._set(codes, codes.data_ptr(), scales.data_ptr(), (*lead, K))
 
-    def _set(self, codes, scales, shape):
-        self.codes, self.scales, self.shape, self.K = codes, scales, shape, shape[-1]
+    def _set(self, held, codes_ptr, scales_ptr, shape):
+        self._held, self._codes_ptr, self._scales_ptr = held, codes_ptr, scales_ptr
+        self.shape, self.K = shape, shape[-1]
         self._status = self._c = None
 
     @classmethod
-    def _of(cls, codes, scales, shape):
-        """Tensors that were made for each other (no checks)."""
+    def _empty(cls, shape, like: torch.Tensor) -> "Mx4Tensor":
+        """Room for a tensor of this shape: one allocation, codes then scales, viewed when asked for."""
         self = cls.__new__(cls)
-        self._set(codes, scales, shape)
+        self._codes = self._scales = None
+        n = math.prod(shape)
+        held = like.new_empty(n // 2 + n // 32, dtype=torch.uint8)
+        self._set(held, held.data_ptr(), held.data_ptr() + n // 2, shape)
         return self
 
     @property
+    def codes(self) -> torch.Tensor:
+        if self._codes is None:
+            n = math.prod(self.shape) // 2
+            self._codes = self._held[:n].view(*self.shape[:-1], self.K // 2)
+        return self._codes
+
+    @property
+    def scales(self) -> torch.Tensor:
+        if self._scales is None:
+            n = math.prod(self.shape) // 2
+            self._scales = self._held[n:].view(*self.shape[:-1], self.K // 32)
+        return self._scales
+
+    @property
     def device(self):
-        return self.codes.device
+        return self._held.device
 
     @property
     def status(self) -> torch.Tensor:
@@ -839,7 +859,7 @@ class Mx4Tensor:
         """The weight's descriptor (one expert for a matrix)."""
         if self._c is None:
             E, N = (1, *self.shape[:-1]) if len(self.shape) == 2 else self.shape[:-1]
-            self._c = _MX4(E, N, self.K, self.codes.data_ptr(), self.scales.data_ptr(), self.status.data_ptr())
+            self._c = _MX4(E, N, self.K, self._codes_ptr, self._scales_ptr, self.status.data_ptr())
         return ctypes.byref(self._c)
 
 
@@ -851,24 +871,23 @@ def quantize_mx4(X: torch.Tensor, out: Mx4Tensor | None = None) -> Mx4Tensor:
         raise TypeError("X must be a bfloat16 CUDA tensor of at least two dimensions")
     shape = tuple(X.shape)
     _tensor_arg(X, "X", shape, torch.bfloat16)
-    *lead, K = shape
+    K = shape[-1]
     if K <= 0 or K % 32:
         raise ValueError("X's last dimension must be a positive multiple of 32")
     if out is None:
-        out = Mx4Tensor._of(X.new_empty((*lead, K // 2), dtype=torch.uint8),
-                            X.new_empty((*lead, K // 32), dtype=torch.uint8), shape)
+        out = Mx4Tensor._empty(shape, X)
     elif out.shape != shape or out.device != X.device:
         raise ValueError(f"out holds {out.shape} on {out.device}, X is {shape} on {X.device}")
-    _check(library().bsl_mx4_quantize(X.data_ptr(), X.numel() // K, K, out.codes.data_ptr(), out.scales.data_ptr(),
-                                      _stream(X)), "bsl_mx4_quantize")
+    _check(library().bsl_mx4_quantize(X.data_ptr(), X.numel() // K, K, out._codes_ptr, out._scales_ptr, _stream(X)),
+           "bsl_mx4_quantize")
     return out
 
 
 def dequantize_mx4(q: Mx4Tensor, out: torch.Tensor | None = None) -> torch.Tensor:
     """The values ``q`` stands for, as bf16 (exact)."""
-    X = _out_arg(out, q.shape, q.codes)
-    _check(library().bsl_mx4_dequantize(q.codes.data_ptr(), q.scales.data_ptr(), q.codes.numel() * 2 // q.K, q.K,
-                                        X.data_ptr(), _stream(q.codes)), "bsl_mx4_dequantize")
+    X = _out_arg(out, q.shape, q._held)
+    _check(library().bsl_mx4_dequantize(q._codes_ptr, q._scales_ptr, X.numel() // q.K, q.K, X.data_ptr(), _stream(X)),
+           "bsl_mx4_dequantize")
     return X
 
 
@@ -878,9 +897,9 @@ def _mx4_product(X, Wq: Mx4Tensor, offsets, bias_ptr, N: int, out) -> torch.Tens
             raise ValueError(f"X holds {X.shape}, expected [rows, {Wq.K}]")
         if X.device != Wq.device:
             raise ValueError(f"X must be on {Wq.device}")
-        rows, like = X.shape[0], X.codes
+        rows, like = X.shape[0], X._held
     else:
-        _tensor_arg(X, "X", (None, Wq.K), torch.bfloat16, Wq.codes)
+        _tensor_arg(X, "X", (None, Wq.K), torch.bfloat16, Wq._held)
         rows, like = X.shape[0], X
     Y = _out_arg(out, (rows, N), like)
     lib, off = library(), None if offsets is None else offsets.data_ptr()
@@ -890,10 +909,10 @@ def _mx4_product(X, Wq: Mx4Tensor, offsets, bias_ptr, N: int, out) -> torch.Tens
         st = lib.bsl_mx4_linear(X.data_ptr(), rows, off, Wq.cref(), bias_ptr, Y.data_ptr(), out is None, ws.data_ptr(),
                                 nbytes, _stream(X))
     elif offsets is None:
-        st = lib.bsl_mx4_forward(X.codes.data_ptr(), X.scales.data_ptr(), rows, Wq.cref(), bias_ptr, Y.data_ptr(),
+        st = lib.bsl_mx4_forward(X._codes_ptr, X._scales_ptr, rows, Wq.cref(), bias_ptr, Y.data_ptr(),
                                  _stream(like))
     else:
-        st = lib.bsl_mx4_grouped_forward(X.codes.data_ptr(), X.scales.data_ptr(), rows, off, Wq.cref(), bias_ptr,
+        st = lib.bsl_mx4_grouped_forward(X._codes_ptr, X._scales_ptr, rows, off, Wq.cref(), bias_ptr,
                                          Y.data_ptr(), out is None, _stream(like))
     _check(st, "bsl_mx4_linear" if like is X else "bsl_mx4_forward" if offsets is None else "bsl_mx4_grouped_forward")
     return Y
@@ -905,7 +924,7 @@ def forward_mx4(X, Wq: Mx4Tensor, bias: torch.Tensor | None = None, out: torch.T
     if len(Wq.shape) != 2:
         raise ValueError("Wq must be a weight [N, K]")
     N = Wq.shape[0]
-    return _mx4_product(X, Wq, None, _bias_ptr(bias, N, Wq.codes), N, out)
+    return _mx4_product(X, Wq, None, _bias_ptr(bias, N, Wq._held), N, out)
 
 
 def grouped_forward_mx4(X, Wq: Mx4Tensor, offsets: torch.Tensor, bias: torch.Tensor | None = None,
@@ -915,14 +934,14 @@ def grouped_forward_mx4(X, Wq: Mx4Tensor, offsets: torch.Tensor, bias: torch.Ten
     if len(Wq.shape) != 3:
         raise ValueError("Wq must be a weight [E, N, K]")
     E, N, _ = Wq.shape
-    _tensor_arg(offsets, "offsets", (E + 1,), torch.int32, Wq.codes)
-    return _mx4_product(X, Wq, offsets, _expert_bias(bias, E, N, Wq.codes), N, out)
+    _tensor_arg(offsets, "offsets", (E + 1,), torch.int32, Wq._held)
+    return _mx4_product(X, Wq, offsets, _expert_bias(bias, E, N, Wq._held), N, out)
 
 
 def mx4_status(Wq: Mx4Tensor) -> int:
     """Read and clear the weight's device status word (synchronises the stream)."""
     out = ctypes.c_int32(0)
-    _check(library().bsl_mx4_get_status(Wq.cref(), ctypes.byref(out), _stream(Wq.codes)), "bsl_mx4_get_status")
+    _check(library().bsl_mx4_get_status(Wq.cref(), ctypes.byref(out), _stream(Wq._held)), "bsl_mx4_get_status")
     return int(out.value)
 
 
