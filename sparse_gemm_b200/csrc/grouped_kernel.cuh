@@ -542,10 +542,17 @@ __global__ void __launch_bounds__(Cfg<kMode>::THREADS, 1)
         // ------------------------------------------------------------ MMA issuer (the leader's)
         if (rank == 0) {
             const uint32_t lead = lane == 0;
+            // What the loops and the MMAs' operands depend on is the same in all lanes;
+            // said so, they stay in uniform registers and an MMA is a few instructions
+            const uint32_t tm = uniform(tmem);
+            const int tiles_end = uniform(count);
             bool ok = true;
             int g = 0, h = 0, it = 0;
-            for (int t = first; ok && t < count; t += stride) {
-                const Tile x = tiles.at(t);
+            for (int t = first; ok && t < tiles_end; t += stride) {
+                Tile x = tiles.at(t);
+                x.n = uniform(x.n);
+                x.k = uniform(x.k);
+                x.kb = uniform(x.kb);
                 if (x.kb == 0) continue;  // a sum over no rows: the epilogue writes zeros
                 const int acc = it & 1;
                 if (it >= 2 && __any_sync(0xffffffffu, !mbar_wait(&aempty[acc], ((it >> 1) - 1) & 1, tmo, abort_flag))) {
@@ -554,7 +561,7 @@ __global__ void __launch_bounds__(Cfg<kMode>::THREADS, 1)
                 }
                 tc_fence_after();
                 const uint32_t idesc = C::F4 ? make_idesc_mx4(256, x.n) : make_idesc_bf16(256, x.n, C::AM, C::BN);
-                const uint32_t d = tmem + acc * C::BR;
+                const uint32_t d = tm + acc * C::BR;
                 const uint32_t bs = x.n / 2 * 8;  // K-major B: a strip of half the rows, in 16-byte units
                 for (int k = 0; k < x.kb; ++k, ++g) {
                     const int slot = g % C::S;
@@ -591,7 +598,7 @@ __global__ void __launch_bounds__(Cfg<kMode>::THREADS, 1)
                                 break;
                             }
                             tc_fence_after();
-                            const uint32_t sc = tmem + C::SC_COL + sl * C::SC_COLS;
+                            const uint32_t sc = tm + C::SC_COL + sl * C::SC_COLS;
 #pragma unroll
                             for (int i = 0; i < 4; ++i) mma(4 * j + i, sc);
                             umma_commit_lead_pair(lead, &sempty[sl]);

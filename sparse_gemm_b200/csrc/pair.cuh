@@ -10,6 +10,10 @@ namespace bsl {
 // Two CTAs of a cluster working on one tile (cta_group::2).  Rank 0 leads: it
 // issues the MMAs, and both CTAs' copies complete on its barriers.
 
+// A value that is the same in all lanes, in a form the compiler knows to be uniform.
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __reduce_or_sync(0xffffffffu, v); }
+__device__ __forceinline__ int uniform(int v) { return static_cast<int>(__reduce_or_sync(0xffffffffu, static_cast<uint32_t>(v))); }
+
 __device__ __forceinline__ uint32_t cluster_rank()
 {
     uint32_t r;
