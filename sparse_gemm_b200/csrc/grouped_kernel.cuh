@@ -336,9 +336,23 @@ __device__ __forceinline__ void copy_scales(const Tiles<kMode> &tiles, const Arg
                     buf[at] = make_uint4(w[p][i][0], w[p][i][1], w[p][i][2], w[p][i][3]);
                 }
             }
-            // all four warps reach every one of these barriers, an aborted run's too;
-            // behind the next one, this buffer has been read
+            // One warp waits for the stage's place in the ring (a waiting warp polls
+            // shared memory, which the MMAs and copies need), the barrier lets the
+            // others know.  All four reach every barrier, an aborted run's too;
+            // behind the next one, this buffer has been read.  An mbarrier tells
+            // neighbouring phases apart and no more: the set's last wait was for
+            // half h - 3 - SR or a later one, and half h cannot be finished without it.
+            const int n = halves(now.x, now.k);
+            if (q == 0) {
+                for (int i = 0; ok && i < n; ++i)
+                    if (h + i >= C::SR && __any_sync(0xffffffffu, !mbar_wait(&sempty[(h + i) % C::SR], ((h + i) / C::SR - 1) & 1,
+                                                                             args.timeout_ns, abort_flag)))
+                        ok = false;
+                if (lane == 0 && !ok) *abort_flag = 1;
+                __syncwarp();
+            }
             named_bar_sync(1 + set, 128);
+            if (*abort_flag) ok = false;
             uint32_t a[4][4], b[8][4];  // [rows lane + 32 i][chunk of 128 elements]
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -350,17 +364,10 @@ __device__ __forceinline__ void copy_scales(const Tiles<kMode> &tiles, const Arg
                 const uint4 v = i < G ? buf[128 + 32 * i + lane] : make_uint4(0, 0, 0, 0);
                 b[i][0] = v.x, b[i][1] = v.y, b[i][2] = v.z, b[i][3] = v.w;
             }
-            const int n = halves(now.x, now.k);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 if (i >= n) break;
-                // A barrier tells neighbouring phases apart and no more: this set's last
-                // wait was for half h - 3 - SR or a later one, and half h cannot be
-                // finished without this warp
                 const int slot = h % C::SR;
-                if (ok && h >= C::SR &&
-                    __any_sync(0xffffffffu, !mbar_wait(&sempty[slot], ((h / C::SR) - 1) & 1, args.timeout_ns, abort_flag)))
-                    ok = false;
                 if (ok) {
                     tc_fence_after();
                     uint32_t va[8], vb[16];
@@ -588,23 +595,22 @@ __global__ void __launch_bounds__(Cfg<kMode>::THREADS, 1)
                     };
                     const int left = x.k - k * 128;  // the copies filled the rest of the stage with zeros
                     if constexpr (C::F4) {
-                        const int n = halves(x, k);
-#pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            if (j >= n) break;
-                            const int sl = h % C::SR;
-                            if (__any_sync(0xffffffffu, !mbar_wait(&sfull[sl], (h / C::SR) & 1, tmo, abort_flag))) {
-                                ok = false;
-                                break;
-                            }
-                            tc_fence_after();
-                            const uint32_t sc = tm + C::SC_COL + sl * C::SC_COLS;
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) mma(4 * j + i, sc);
-                            umma_commit_lead_pair(lead, &sempty[sl]);
-                            ++h;
+                        // halves are handed over in order: the last one's barrier tells for both
+                        const int n = halves(x, k), s0 = h % C::SR, s1 = (h + 1) % C::SR, last = h + n - 1;
+                        if (__any_sync(0xffffffffu, !mbar_wait(&sfull[last % C::SR], (last / C::SR) & 1, tmo, abort_flag))) {
+                            ok = false;
+                            break;
                         }
-                        if (!ok) break;
+                        tc_fence_after();
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) mma(i, tm + C::SC_COL + s0 * C::SC_COLS);
+                        umma_commit_lead_pair(lead, &sempty[s0]);
+                        if (n == 2) {
+#pragma unroll
+                            for (int i = 4; i < 8; ++i) mma(i, tm + C::SC_COL + s1 * C::SC_COLS);
+                            umma_commit_lead_pair(lead, &sempty[s1]);
+                        }
+                        h += n;
                     } else if (left >= 128) {
 #pragma unroll
                         for (int i = 0; i < 8; ++i) mma(i, 0);
@@ -646,16 +652,24 @@ __global__ void __launch_bounds__(Cfg<kMode>::THREADS, 1)
         const uint32_t lanes = static_cast<uint32_t>(32 * q) << 16;
         bool ok = true;
         int it = 0, ob = 0;
-        for (int t = first; ok && t < count; t += stride) {
+        for (int t = first; t < count; t += stride) {
             const Tile x = tiles.at(t);
             const int c = x.c0 + static_cast<int>(rank) * 128 + 32 * q;
             const float bv = args.bias && c + lane < args.cols
                                  ? __bfloat162float(args.bias[static_cast<int64_t>(x.e) * args.cols + c + lane]) : 0.f;
             const int acc = it & 1;
-            if (x.kb > 0 && __any_sync(0xffffffffu, !mbar_wait(&afull[acc], (it >> 1) & 1, tmo, abort_flag))) {
-                ok = false;
-                break;
+            if (x.kb > 0) {
+                // one warp waits (a waiting warp polls shared memory, which the MMAs and
+                // copies need); all four come to every tile's barrier, an aborted run's too
+                if (ok && q == 0 && __any_sync(0xffffffffu, !mbar_wait(&afull[acc], (it >> 1) & 1, tmo, abort_flag)) &&
+                    lane == 0)
+                    *abort_flag = 1;
+                __syncwarp();
+                named_bar_sync(3, 128);
+                ++it;
             }
+            if (*abort_flag) ok = false;
+            if (!ok) continue;
             tc_fence_after();
             const int chunks = c < args.cols ? (x.valid + 31) / 32 : 0;
             for (int i = 0; i < chunks; ++i) {
@@ -689,7 +703,6 @@ __global__ void __launch_bounds__(Cfg<kMode>::THREADS, 1)
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_cluster(cluster_addr(&aempty[acc], 0));
-                ++it;
             }
         }
         if (lane == 0) {
