@@ -633,6 +633,14 @@ def _tensor_arg(t, name: str, shape, dtype, like: torch.Tensor | None = None) ->
         raise ValueError(f"{name} must be on {like.device}")
 
 
+def _row_count(t: torch.Tensor, name: str) -> int:
+    """Rows of a matrix, which the C ABI counts in 32 bits."""
+    rows = t.shape[0]
+    if rows >= 2 ** 31:
+        raise ValueError(f"{name} has {rows} rows, the limit is 2^31 - 1")
+    return rows
+
+
 def _out_arg(out, shape, like: torch.Tensor) -> torch.Tensor:
     if out is None:
         return like.new_empty(shape, dtype=torch.bfloat16)
@@ -682,8 +690,8 @@ def grouped_forward(X: torch.Tensor, Wg: GroupedWeight, offsets: torch.Tensor, b
     _tensor_arg(offsets, "offsets", (Wg.E + 1,), torch.int32, X)
     bptr = _expert_bias(bias, Wg.E, Wg.N, X)
     Y = _out_arg(out, (X.shape[0], Wg.N), X)
-    _check(library().bsl_grouped_forward(X.data_ptr(), X.shape[0], offsets.data_ptr(), Wg.cref(), bptr, Y.data_ptr(),
-                                         out is None, _stream(X)), "bsl_grouped_forward")
+    _check(library().bsl_grouped_forward(X.data_ptr(), _row_count(X, "X"), offsets.data_ptr(), Wg.cref(), bptr,
+                                         Y.data_ptr(), out is None, _stream(X)), "bsl_grouped_forward")
     return Y
 
 
@@ -693,8 +701,8 @@ def grouped_backward_input(dY: torch.Tensor, Wg: GroupedWeight, offsets: torch.T
     _tensor_arg(dY, "dY", (None, Wg.N), torch.bfloat16, Wg.weight)
     _tensor_arg(offsets, "offsets", (Wg.E + 1,), torch.int32, dY)
     dX = _out_arg(out, (dY.shape[0], Wg.K), dY)
-    _check(library().bsl_grouped_backward_input(dY.data_ptr(), dY.shape[0], offsets.data_ptr(), Wg.cref(),
-                                                dX.data_ptr(), out is None, _stream(dY)),
+    _check(library().bsl_grouped_backward_input(dY.data_ptr(), _row_count(dY, "dY"), offsets.data_ptr(),
+                                                Wg.cref(), dX.data_ptr(), out is None, _stream(dY)),
            "bsl_grouped_backward_input")
     return dX
 
@@ -708,8 +716,8 @@ def grouped_backward_weight(dY: torch.Tensor, X: torch.Tensor, Wg: GroupedWeight
     dW = _out_arg(out, (Wg.E, Wg.N, Wg.K), X)
     nbytes = Wg._workspace_bytes
     ws = X.new_empty(nbytes, dtype=torch.uint8)
-    _check(library().bsl_grouped_backward_weight(dY.data_ptr(), X.data_ptr(), X.shape[0], offsets.data_ptr(),
-                                                 Wg.cref(), dW.data_ptr(), ws.data_ptr(), nbytes, _stream(X)),
+    _check(library().bsl_grouped_backward_weight(dY.data_ptr(), X.data_ptr(), _row_count(X, "X"),
+                                                 offsets.data_ptr(), Wg.cref(), dW.data_ptr(), ws.data_ptr(), nbytes, _stream(X)),
            "bsl_grouped_backward_weight")
     return dW
 
@@ -720,7 +728,7 @@ def grouped_bias_grad(dY: torch.Tensor, offsets: torch.Tensor, out: torch.Tensor
     _tensor_arg(offsets, "offsets", (None,), torch.int32, dY)
     E, N = offsets.shape[0] - 1, dY.shape[1]
     db = _out_arg(out, (E, N), dY)
-    _check(library().bsl_grouped_bias_grad(dY.data_ptr(), dY.shape[0], offsets.data_ptr(), E, N, db.data_ptr(),
+    _check(library().bsl_grouped_bias_grad(dY.data_ptr(), _row_count(dY, "dY"), offsets.data_ptr(), E, N, db.data_ptr(),
                                            _stream(dY)), "bsl_grouped_bias_grad")
     return db
 
@@ -779,9 +787,12 @@ class GroupedLinear(torch.nn.Module):
     @property
     def packed(self) -> GroupedWeight:
         """The weight's handle, made anew when the parameter's storage was replaced."""
-        if self._packed.weight.data_ptr() != self.weight.data_ptr():
+        if self._packed is None or self._packed.weight.data_ptr() != self.weight.data_ptr():
             self._packed = GroupedWeight(self.weight)
         return self._packed
+
+    def __getstate__(self):
+        return {**self.__dict__, "_packed": None}   # made anew by the copy
 
     def forward(self, x: torch.Tensor, offsets: torch.Tensor) -> torch.Tensor:
         lead = x.shape[:-1]
@@ -815,6 +826,13 @@ class Mx4Tensor:
         _tensor_arg(scales, "scales", (*lead, K // 32), torch.uint8, codes)
         self._codes, self._scales = codes, scales
         self._set(codes, codes.data_ptr(), scales.data_ptr(), (*lead, K))
+        self.status
+
+    def __getstate__(self):
+        return {"codes": self.codes, "scales": self.scales}
+
+    def __setstate__(self, state):
+        self.__init__(state["codes"], state["scales"])
 
     def _set(self, held, codes_ptr, scales_ptr, shape):
         self._held, self._codes_ptr, self._scales_ptr = held, codes_ptr, scales_ptr
@@ -851,7 +869,11 @@ class Mx4Tensor:
 
     @property
     def status(self) -> torch.Tensor:
+        """The device status word, which outlives any graph: made when the tensor is first used as
+        a weight, at the latest before a capture."""
         if self._status is None:
+            if torch.cuda.is_current_stream_capturing():
+                raise RuntimeError("use this weight (or read its .status) once before capturing a graph with it")
             self._status = torch.zeros(1, dtype=torch.int32, device=self.device)
         return self._status
 
@@ -897,10 +919,10 @@ def _mx4_product(X, Wq: Mx4Tensor, offsets, bias_ptr, N: int, out) -> torch.Tens
             raise ValueError(f"X holds {X.shape}, expected [rows, {Wq.K}]")
         if X.device != Wq.device:
             raise ValueError(f"X must be on {Wq.device}")
-        rows, like = X.shape[0], X._held
+        rows, like = _row_count(X, "X"), X._held
     else:
         _tensor_arg(X, "X", (None, Wq.K), torch.bfloat16, Wq._held)
-        rows, like = X.shape[0], X
+        rows, like = _row_count(X, "X"), X
     Y = _out_arg(out, (rows, N), like)
     lib, off = library(), None if offsets is None else offsets.data_ptr()
     if like is X:
@@ -951,6 +973,7 @@ class Mx4Linear(torch.nn.Module):
 
     def __init__(self, weight4: Mx4Tensor, bias: torch.Tensor | None = None):
         super().__init__()
+        weight4.status
         self.weight4 = weight4
         self.in_features, self.out_features = weight4.K, weight4.shape[-2]
         if bias is not None:

@@ -15,7 +15,7 @@
 //     forward          W[e]   K-major      X     K-major     r
 //     input gradient   W[e]^T M-major      dY    K-major     r
 //     weight gradient  X^T    M-major      dY^T  N-major     k
-// The MMA's N may be any multiple of 16, so a tile with few rows costs few
+// The MMA's N may be any multiple of 32, so a tile with few rows costs few
 // rows: an expert's rows are spread evenly over the fewest tiles of 256.  Rows of
 // the next expert that a copy brings along only reach accumulator columns
 // that are never stored.  For the weight gradient, whose ragged index is
@@ -43,10 +43,13 @@
 // (clock held by power at 1.1-1.3 GHz): one 32 KB copy 1412 / 1459 / 1460 us
 // for the three, copies of 16 KB and stages of 64 k 1460 / 1575 / 1540, of 8
 // KB (gradients) 1775.  With few rows the weight's bytes bound it: 64 rows of
-// 16 experts of 11008 x 4096 take 237 us (6.1 TB/s).  There, too, the pair is
+// 16 experts of 11008 x 4096 take 236 us (6.1 TB/s).  There, too, the pair is
 // ahead of one CTA on tiles of 128 features (240 us; 93 against 110 us with
-// 4-bit operands): a dependent MMA takes about 90 clocks however few rows it
-// has, and the pair's covers twice the weight.
+// 4-bit operands).
+//
+// Waiting costs: a waiting warp polls shared memory.  So one warp of a group
+// waits and the others stand at a named barrier (4-bit, 8192 x 4096 x 14336:
+// 236 against 240 us, and 293 with waits that spin).
 //
 // Every wait is bounded (BSL_ERR_TIMEOUT in the status word, then all roles
 // leave through an abort flag).
@@ -164,9 +167,11 @@ __device__ __forceinline__ uint8_t *align1024(uint8_t *p)
 // all of them to its lanes with tcgen05.st, half a stage at a time into a ring
 // of five.
 //
-// Measured at 8192 x 4096 x 14336, tiles of 224 rows: copying them with
-// tcgen05.cp (12 of 512 bytes a stage, in order with the MMAs, some 55 clocks
-// each) 260 us, without those copies 162, so they leave the MMAs' queue.
+// Measured at 8192 x 4096 x 14336: copying them with tcgen05.cp (12 of 512
+// bytes a stage, in order with the MMAs, some 55 clocks each) 260 us, this way
+// 236, one set of warps 271; without any scales it would be 185.  An arrival
+// with release semantics at the pair's barrier waits for the warp's loads
+// under way: 529 us.
 //
 // Nothing is computed on what was loaded before its turn comes, so loads do
 // not wait for one another.  Bytes past the row's end count as zeros (a scale

@@ -164,11 +164,12 @@ def test_no_rows_at_all():
     assert not sg.grouped_bias_grad(dY, off).any()
 
 
-@pytest.mark.parametrize("raw,clamped", [([0, 9, 5, 20], [0, 9, 9, 20]), ([-4, 3, 8, 99], [0, 3, 8, 20]),
-                                         ([25, 30, 40, 50], [20, 20, 20, 20])])
-def test_bad_offsets_are_clamped_and_reported(raw, clamped):
+@pytest.mark.parametrize("T,raw,clamped", [
+    (20, [0, 9, 5, 20], [0, 9, 9, 20]), (20, [-4, 3, 8, 99], [0, 3, 8, 20]), (20, [25, 30, 40, 50], [20, 20, 20, 20]),
+    (6, [0, 4, 2, 6], [0, 4, 4, 6]), (6, [-1, 2, 3, 2 ** 31 - 1], [0, 2, 3, 6]), (6, [9, 9, -9, 9], [6, 6, 6, 6])])
+def test_bad_offsets_are_clamped_and_reported(T, raw, clamped):
     rng = np.random.default_rng(17)
-    T, N, K = 20, 64, 64
+    N, K = 64, 64
     X, _ = normal(rng, (T, K))
     dY, _ = normal(rng, (T, N))
     Wg = sg.GroupedWeight(normal(rng, (3, N, K))[0])
@@ -293,6 +294,85 @@ def test_autograd_and_module():
         Y3 = layer(X, off)
     check(Y2.reshape(T, N)[:23], experts.grouped_forward(Xf[:23], 2 * Wf, o, bf)[0], np.zeros((23, N)), 1, "Y2")
     assert torch.equal(Y2, Y3)
+
+
+def test_captured_training_step():
+    """Forward and backward in one graph: a replay gives the gradients of the inputs it finds."""
+    rng = np.random.default_rng(24)
+    layer = sg.GroupedLinear(normal(rng, (3, 72, 40))[0], normal(rng, (3, 72))[0])
+    X = normal(rng, (200, 40))[0].requires_grad_(True)
+    dY = normal(rng, (200, 72))[0]
+    off = offsets_of([120, 0, 80])[0]
+    params = (X, layer.weight, layer.bias)
+
+    def step():
+        layer(X, off).backward(dY)
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step()
+    torch.cuda.current_stream().wait_stream(s)
+    for p in params:
+        p.grad = None
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    for rows in ([120, 0, 80], [0, 37, 163]):
+        with torch.no_grad():
+            X.copy_(normal(rng, (200, 40))[0])
+            dY.copy_(normal(rng, (200, 72))[0])
+            off.copy_(offsets_of(rows)[0])
+            layer.weight.mul_(0.5)
+        g.replay()
+        torch.cuda.synchronize()
+        got = [p.grad.clone() for p in params]
+        Wg = layer.packed
+        assert torch.equal(got[0], sg.grouped_backward_input(dY, Wg, off))
+        assert torch.equal(got[1], sg.grouped_backward_weight(dY, X.detach(), Wg, off))
+        assert torch.equal(got[2], sg.grouped_bias_grad(dY, off))
+
+
+def test_module_copies():
+    """Deep copies and pickles of the module work on storage of their own."""
+    import copy
+    import io
+    rng = np.random.default_rng(22)
+    layer = sg.GroupedLinear(normal(rng, (2, 16, 24))[0], normal(rng, (2, 16))[0])
+    X, _ = normal(rng, (5, 24))
+    off = offsets_of([2, 3])[0]
+    with torch.no_grad():
+        want = layer(X, off)
+        buf = io.BytesIO()
+        torch.save(layer, buf)
+        buf.seek(0)
+        for other in (copy.deepcopy(layer), torch.load(buf, weights_only=False)):
+            assert torch.equal(other(X, off), want)
+            layer.weight.add_(1.0)
+            assert torch.equal(other(X, off), want) and not torch.equal(layer(X, off), want)
+            layer.weight.copy_(other.weight)
+
+
+def test_streams_and_strided_gradients():
+    """Calls on a stream of their own, and an upstream gradient that is a broadcast."""
+    rng = np.random.default_rng(23)
+    layer = sg.GroupedLinear(normal(rng, (3, 72, 40))[0], normal(rng, (3, 72))[0])
+    X = normal(rng, (50, 40))[0].requires_grad_(True)
+    off, o = offsets_of([20, 0, 30])
+    layer(X, off).float().sum().backward()
+    want = [X.grad.clone(), layer.weight.grad.clone(), layer.bias.grad.clone()]
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    for p in (X, layer.weight, layer.bias):
+        p.grad = None
+    with torch.cuda.stream(s):
+        layer(X, off).float().sum().backward()
+    torch.cuda.current_stream().wait_stream(s)
+    for p, w in zip((X, layer.weight, layer.bias), want):
+        assert torch.equal(p.grad, w)
+    ones = np.ones((50, 72))
+    check(want[2], *experts.grouped_bias_grad(ones, o), 16 * 30, "db")
+    check(want[0], *experts.grouped_backward_input(ones, layer.weight.detach().double().cpu().numpy(), o), 72, "dX")
 
 
 def test_refusals():

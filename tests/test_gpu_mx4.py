@@ -251,11 +251,12 @@ def test_replayed_with_new_inputs(rows):
     assert sg.mx4_status(Wq) == 0
 
 
-def test_bad_offsets_are_clamped_and_reported():
+@pytest.mark.parametrize("T,raw,clamped", [(20, [-1, 9, 5, 77], [0, 9, 9, 20]), (6, [-1, 4, 2, 77], [0, 4, 4, 6])])
+def test_bad_offsets_are_clamped_and_reported(T, raw, clamped):
     rng = np.random.default_rng(10)
     Wq, _ = weights(rng, 3, 64, 64)
-    X = rows_of(rng, 20, 64)
-    bad, good = (torch.tensor(v, dtype=torch.int32, device="cuda") for v in ([-1, 9, 5, 77], [0, 9, 9, 20]))
+    X = rows_of(rng, T, 64)
+    bad, good = (torch.tensor(v, dtype=torch.int32, device="cuda") for v in (raw, clamped))
     want = sg.grouped_forward_mx4(X, Wq, good)
     assert sg.mx4_status(Wq) == 0
     assert torch.equal(sg.grouped_forward_mx4(X, Wq, bad), want)
@@ -319,6 +320,41 @@ def test_linear_module_follows_the_dense_layer():
     y = mod(x.float().reshape(2, 3, 5, 128))
     assert y.shape == (2, 3, 5, 72)
     assert torch.equal(y.reshape(30, 72), sg.forward_mx4(x, sg.quantize_mx4(W), bias=b))
+
+
+def test_copies_and_views():
+    """codes and scales of a quantised tensor are views of it; copies and pickles stand on their own; a
+    weight whose first use would be captured is refused, one that was used is not."""
+    import copy
+    import io
+    rng = np.random.default_rng(13)
+    W, X = normal(rng, (72, 96))[0], rows_of(rng, 20, 96)
+    q = sg.quantize_mx4(W)
+    assert q.codes.shape == (72, 48) and q.scales.shape == (72, 3)
+    mod = sg.Mx4Linear(q)
+    want = mod(X)
+    buf = io.BytesIO()
+    torch.save(mod, buf)
+    buf.seek(0)
+    others = [copy.deepcopy(mod), torch.load(buf, weights_only=False)]
+    q.scales.sub_(1)                              # half of every value
+    assert torch.equal(mod(X), want / 2)
+    assert torch.equal(sg.dequantize_mx4(q), sg.dequantize_mx4(others[0].weight4) / 2)
+    for m in others:
+        assert torch.equal(m(X), want)
+    fresh = sg.quantize_mx4(W)
+    g = torch.cuda.CUDAGraph()
+    with pytest.raises(RuntimeError, match="before capturing"):
+        with torch.cuda.graph(g):
+            sg.forward_mx4(X, fresh)
+    torch.cuda.synchronize()
+    fresh.status
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        Y = sg.forward_mx4(X, fresh)
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(Y, want)
 
 
 def test_refusals():
