@@ -366,7 +366,7 @@ __device__ __forceinline__ void copy_scales(const Tiles<kMode> &tiles, const Arg
             }
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const uint4 v = i < G ? buf[128 + 32 * i + lane] : make_uint4(0, 0, 0, 0);
+                const uint4 v = i < G && 32 * i < now.x.n ? buf[128 + 32 * i + lane] : make_uint4(0, 0, 0, 0);
                 b[i][0] = v.x, b[i][1] = v.y, b[i][2] = v.z, b[i][3] = v.w;
             }
 #pragma unroll
