@@ -641,9 +641,14 @@ def _row_count(t: torch.Tensor, name: str) -> int:
     return rows
 
 
+def _new(like: torch.Tensor, *shape: int) -> torch.Tensor:
+    """An empty bf16 tensor on like's device (the form of the call that costs the host least)."""
+    return like.new_empty(*shape) if like.dtype is torch.bfloat16 else like.new_empty(shape, dtype=torch.bfloat16)
+
+
 def _out_arg(out, shape, like: torch.Tensor) -> torch.Tensor:
     if out is None:
-        return like.new_empty(shape, dtype=torch.bfloat16)
+        return _new(like, *shape)
     _tensor_arg(out, "out", shape, torch.bfloat16, like)
     return out
 
@@ -715,7 +720,7 @@ def grouped_backward_weight(dY: torch.Tensor, X: torch.Tensor, Wg: GroupedWeight
     _tensor_arg(offsets, "offsets", (Wg.E + 1,), torch.int32, X)
     dW = _out_arg(out, (Wg.E, Wg.N, Wg.K), X)
     nbytes = Wg._workspace_bytes
-    ws = X.new_empty(nbytes, dtype=torch.uint8)
+    ws = _new(X, nbytes // 2)
     _check(library().bsl_grouped_backward_weight(dY.data_ptr(), X.data_ptr(), _row_count(X, "X"),
                                                  offsets.data_ptr(), Wg.cref(), dW.data_ptr(), ws.data_ptr(), nbytes, _stream(X)),
            "bsl_grouped_backward_weight")
@@ -845,7 +850,7 @@ class Mx4Tensor:
         self = cls.__new__(cls)
         self._codes = self._scales = None
         n = math.prod(shape)
-        held = like.new_empty(n // 2 + n // 32, dtype=torch.uint8)
+        held = _new(like, (n // 2 + n // 32 + 1) // 2)
         self._set(held, held.data_ptr(), held.data_ptr() + n // 2, shape)
         return self
 
@@ -853,14 +858,14 @@ class Mx4Tensor:
     def codes(self) -> torch.Tensor:
         if self._codes is None:
             n = math.prod(self.shape) // 2
-            self._codes = self._held[:n].view(*self.shape[:-1], self.K // 2)
+            self._codes = self._held.view(torch.uint8)[:n].view(*self.shape[:-1], self.K // 2)
         return self._codes
 
     @property
     def scales(self) -> torch.Tensor:
         if self._scales is None:
             n = math.prod(self.shape) // 2
-            self._scales = self._held[n:].view(*self.shape[:-1], self.K // 32)
+            self._scales = self._held.view(torch.uint8)[n:n + n // 16].view(*self.shape[:-1], self.K // 32)
         return self._scales
 
     @property
@@ -927,7 +932,7 @@ def _mx4_product(X, Wq: Mx4Tensor, offsets, bias_ptr, N: int, out) -> torch.Tens
     lib, off = library(), None if offsets is None else offsets.data_ptr()
     if like is X:
         nbytes = rows * (Wq.K // 2 + Wq.K // 32)   # bsl_mx4_workspace_bytes
-        ws = X.new_empty(nbytes, dtype=torch.uint8)
+        ws = _new(X, (nbytes + 1) // 2)
         st = lib.bsl_mx4_linear(X.data_ptr(), rows, off, Wq.cref(), bias_ptr, Y.data_ptr(), out is None, ws.data_ptr(),
                                 nbytes, _stream(X))
     elif offsets is None:

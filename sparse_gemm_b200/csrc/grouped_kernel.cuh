@@ -748,7 +748,8 @@ inline bool row_maps(Maps &m, const void *weight, int64_t E, int64_t N, int64_t 
     bool good = make_strip_map(&m.a[0], weight, K, N, E, 128, 2) &&
                 make_map_3d(&m.a[1], weight, K, N, E, K * 2, K * 2 * N, 64, 128, 128) &&
                 map_rows(&m.b[8], A, depth, T, 64, 16, 128) && map_rows(&m.out, out, cols, T, 32, 32, 0);
-    for (int i = 0; i < 8; ++i) good = good && make_strip_map(&m.b[i], A, depth, T, 1, 16 * (i + 1), 2);
+    // (a tile has no more than T rows, rounded up to 32)
+    for (int i = 0; i < 8 && 32 * i < T; ++i) good = good && make_strip_map(&m.b[i], A, depth, T, 1, 16 * (i + 1), 2);
     return good;
 }
 
