@@ -36,7 +36,7 @@
 //
 // Clusters of two CTAs work on tiles of 256 features x up to 256 rows
 // (cta_group::2, M = 256; each CTA holds its 128 rows of A and half of B) with
-// three stages of 128 k.  With many rows the tensor pipe bounds it, as long as
+// a ring of stages of 128 k (three of full tiles).  With many rows the tensor pipe bounds it, as long as
 // the copies keep up (32 KB per 64 k and SM, 64 bytes a clock), and those go
 // by their number: an operand's stage is one copy of 32 KB, two strips of
 // 128-byte rows.  At 16384 x 4096 x 14336, 8 experts, kernels back to back
@@ -76,8 +76,8 @@ struct Cfg {
     static constexpr int BK = 128;                   // k per stage (two-byte columns)
     static constexpr int A_BYTES = 128 * BK * 2;
     static constexpr int B_BYTES = BR / 2 * BK * 2;
-    static constexpr int STAGE = A_BYTES + B_BYTES;
-    static constexpr int S = 3;
+    static constexpr int RING = (F4 ? 180 : 192) * 1024;  // three stages of full tiles, up to S of smaller ones
+    static constexpr int S = 5;
     // two accumulators, then a ring of scales: half a stage (256 elements of k), 8 columns of A's and 16 of B's
     static constexpr int SR = F4 ? 5 : 0, SC_COL = 2 * BR, SC_COLS = 24;
     static constexpr int TMEM = 512;
@@ -85,11 +85,12 @@ struct Cfg {
     static constexpr int OUT = 4 * 2 * CHUNK;        // two chunks per epilogue warp
     static constexpr int SETS = 2;                   // of four warps that bring the scales of stages in turn
     static constexpr int RAW = F4 ? SETS * 2 * (128 + BR) * 16 : 0;  // two stages' scales a set, 16 bytes a row
-    static constexpr int BARS = (2 * S + 2 * SR + 5) * 8 + 8;
-    static constexpr int SMEM = 1024 + S * STAGE + OUT + RAW + BARS + 2 * (kMaxExperts + 1) * 4;
+    static constexpr int BARS = (2 * S + 2 * SR + 5) * 8 + 16;
+    static constexpr int SMEM = 1024 + RING + OUT + RAW + BARS + 2 * (kMaxExperts + 1) * 4;
     static constexpr int THREADS = F4 ? 256 + SETS * 128 : 256;
     static_assert(SMEM <= 227 * 1024, "shared memory");
-    static_assert(STAGE % 1024 == 0, "swizzle atoms");
+    static_assert(3 * (A_BYTES + B_BYTES) <= RING, "stages");
+    static_assert(A_BYTES % 1024 == 0 && B_BYTES % 1024 == 0, "swizzle atoms");
     static_assert(SC_COL + SR * SC_COLS <= TMEM, "TMEM columns");
 };
 
@@ -407,6 +408,34 @@ __device__ __forceinline__ void copy_scales(const Tiles<kMode> &tiles, const Arg
     __syncwarp();
 }
 
+// Bytes of a stage in the ring, by the calling warp: the rows of B are those of
+// the launch's largest tile.  What few rows leave free holds more stages: with
+// five instead of three, MEASURED_RING
+template <int kMode>
+__device__ __forceinline__ int stage_bytes(const int32_t *off, int32_t E)
+{
+    using C = Cfg<kMode>;
+    if (kMode == kWeightGrad) return C::A_BYTES + C::B_BYTES;
+    int top = 1;
+    for (int e = threadIdx.x & 31; e < E; e += 32) top = max(top, off[e + 1] - off[e]);
+    top = __reduce_max_sync(0xffffffffu, top);
+    const int rows = top > C::BR ? C::BR : (top + C::STEP - 1) / C::STEP * C::STEP;
+    return C::A_BYTES + rows / 2 * C::BK * 2;
+}
+
+// A place in the ring: slot, and the parity of the phase that fills it.
+struct Place {
+    int slot = 0;
+    uint32_t parity = 0;
+    __device__ __forceinline__ void next(int S)
+    {
+        if (++slot == S) {
+            slot = 0;
+            parity ^= 1;
+        }
+    }
+};
+
 template <int kMode>
 __global__ void __launch_bounds__(Cfg<kMode>::THREADS, 1)
     k_grouped(const __grid_constant__ Maps maps, const Args args)
@@ -414,7 +443,7 @@ __global__ void __launch_bounds__(Cfg<kMode>::THREADS, 1)
     using C = Cfg<kMode>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *stages = align1024(smem_raw);
-    uint8_t *outbuf = stages + C::S * C::STAGE;
+    uint8_t *outbuf = stages + C::RING;
     uint8_t *raw = outbuf + C::OUT;
     uint64_t *full = reinterpret_cast<uint64_t *>(raw + C::RAW);     // copies of a stage landed (leader)
     uint64_t *empty = full + C::S;                                   // MMAs of a stage finished (each CTA)
@@ -425,7 +454,8 @@ __global__ void __launch_bounds__(Cfg<kMode>::THREADS, 1)
     uint64_t *drain = sempty + C::SR;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-    int32_t *off = reinterpret_cast<int32_t *>(tmem_slot + 2);
+    int *ring_slot = reinterpret_cast<int *>(tmem_slot + 2);
+    int32_t *off = reinterpret_cast<int32_t *>(tmem_slot + 4);
     int32_t *start = off + kMaxExperts + 1;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -467,6 +497,8 @@ __global__ void __launch_bounds__(Cfg<kMode>::THREADS, 1)
             const int r = kMode == kWeightGrad ? args.rows : off[e + 1] - off[e];
             return (r + C::BR - 1) / C::BR * nc;
         });
+        const int bytes = stage_bytes<kMode>(off, args.E);
+        if (lane == 0) *ring_slot = bytes;
     }
     __syncthreads();
     cluster_sync_all();  // the peer's barriers are initialised
@@ -475,6 +507,7 @@ __global__ void __launch_bounds__(Cfg<kMode>::THREADS, 1)
     const Tiles<kMode> tiles = {off, start, args.E, args.cols, args.rows, args.depth};
     const int count = start[args.E];
     const int first = blockIdx.x / 2, stride = gridDim.x / 2;
+    const int stage = *ring_slot, S = C::RING / stage < C::S ? C::RING / stage : C::S;  // a stage's bytes, stages
 
     if (warp == 0 || warp == 2) {
         // ------------------------------------------------------------ producers: warp 0 copies A, warp 2 B
@@ -483,6 +516,7 @@ __global__ void __launch_bounds__(Cfg<kMode>::THREADS, 1)
             const bool mn = is_a ? C::AM : C::BN;  // M- or N-major
             bool ok = true;
             int g = 0;  // stages issued
+            Place at_ring;
             int mapped = -1;
             const CUtensorMap *one = is_a ? &maps.a[1] : &maps.b[8], *two = &maps.a[0];  // one, two strips a copy
             Tile x, next;
@@ -507,13 +541,13 @@ __global__ void __launch_bounds__(Cfg<kMode>::THREADS, 1)
                 const int wide = is_a ? args.cols : args.rows;
                 const bool aligned = mn && strips == 2 && at % 64 == 0 && (wide % 64 == 0 || at + 128 <= wide);
                 if (!is_a && !C::BN) two = &maps.b[half / 16 - 1];  // exactly the tile's rows
-                for (int k = 0; k < x.kb; ++k, ++g) {
-                    const int slot = g % C::S;
-                    if (g >= C::S && !mbar_wait(&empty[slot], ((g / C::S) - 1) & 1, tmo, abort_flag)) {
+                for (int k = 0; k < x.kb; ++k, ++g, at_ring.next(S)) {
+                    const int slot = at_ring.slot;
+                    if (g >= S && !mbar_wait(&empty[slot], at_ring.parity ^ 1, tmo, abort_flag)) {
                         ok = false;
                         break;
                     }
-                    uint8_t *dst = stages + slot * C::STAGE + (is_a ? 0 : C::A_BYTES);
+                    uint8_t *dst = stages + slot * stage + (is_a ? 0 : C::A_BYTES);
                     if (is_a && rank == 0) mbar_arrive_expect_tx(&full[slot], bytes);
                     const uint32_t bar = cluster_addr(&full[slot], 0);
                     if (mn) {
@@ -535,8 +569,8 @@ __global__ void __launch_bounds__(Cfg<kMode>::THREADS, 1)
                 *abort_flag = 1;
                 set_status(args.status, BSL_ERR_TIMEOUT);
             } else if (is_a) {  // the MMAs' arrivals on this CTA's barriers are in
-                for (int s = 0; s < C::S && s < g; ++s) {
-                    const int fills = (g - s + C::S - 1) / C::S;
+                for (int s = 0; s < S && s < g; ++s) {
+                    const int fills = (g - s + S - 1) / S;
                     if (!mbar_wait(&empty[s], (fills - 1) & 1, tmo, abort_flag))
                         set_status(args.status, BSL_ERR_TIMEOUT);
                 }
@@ -544,8 +578,8 @@ __global__ void __launch_bounds__(Cfg<kMode>::THREADS, 1)
             // every copy lands before shared memory is released: the last fill of
             // each slot is the newest phase of its barrier, which the leader holds
             if (is_a && rank == 0)
-                for (int s = 0; s < C::S && s < g; ++s) {
-                    const int fills = (g - s + C::S - 1) / C::S;
+                for (int s = 0; s < S && s < g; ++s) {
+                    const int fills = (g - s + S - 1) / S;
                     if (!mbar_wait(&full[s], (fills - 1) & 1, tmo, nullptr)) set_status(args.status, BSL_ERR_TIMEOUT);
                 }
         }
@@ -557,9 +591,11 @@ __global__ void __launch_bounds__(Cfg<kMode>::THREADS, 1)
             // What the loops and the MMAs' operands depend on is the same in all lanes;
             // said so, they stay in uniform registers and an MMA is a few instructions
             const uint32_t tm = uniform(tmem);
-            const int tiles_end = uniform(count);
+            const int tiles_end = uniform(count), ring = uniform(S);
+            const uint32_t bytes = uniform(static_cast<uint32_t>(stage));
             bool ok = true;
-            int g = 0, h = 0, it = 0;
+            Place at;
+            int h = 0, it = 0;
             for (int t = first; ok && t < tiles_end; t += stride) {
                 Tile x = tiles.at(t);
                 x.n = uniform(x.n);
@@ -575,14 +611,14 @@ __global__ void __launch_bounds__(Cfg<kMode>::THREADS, 1)
                 const uint32_t idesc = C::F4 ? make_idesc_mx4(256, x.n) : make_idesc_bf16(256, x.n, C::AM, C::BN);
                 const uint32_t d = tm + acc * C::BR;
                 const uint32_t bs = x.n / 2 * 8;  // K-major B: a strip of half the rows, in 16-byte units
-                for (int k = 0; k < x.kb; ++k, ++g) {
-                    const int slot = g % C::S;
-                    if (__any_sync(0xffffffffu, !mbar_wait(&full[slot], (g / C::S) & 1, tmo, abort_flag))) {
+                for (int k = 0; k < x.kb; ++k, at.next(ring)) {
+                    const int slot = at.slot;
+                    if (__any_sync(0xffffffffu, !mbar_wait(&full[slot], at.parity, tmo, abort_flag))) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t a0 = smem_u32(stages + slot * C::STAGE), b0 = a0 + C::A_BYTES;
+                    const uint32_t a0 = smem_u32(stages) + slot * bytes, b0 = a0 + C::A_BYTES;
                     // K-major: 8-row atoms 1024 bytes apart, a K step of 32 bytes along the row, a strip its
                     // rows x 128 bytes; M- and N-major: strips 16384 bytes apart, a K step of 16 rows of 128 bytes
                     const uint64_t ad = make_sdesc(a0, C::AM ? 16384 : 16, 1024, kLayoutSw128);
