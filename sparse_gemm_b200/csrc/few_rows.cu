@@ -1,7 +1,7 @@
 // few_rows.cu -- forward of the expert (grouped) layer and of the 4-bit layer for
-// at most eight rows in all (single tokens): Y[t] = X[t] . W[e]^T + bias[e].
+// a few rows in all (single tokens, up to 32): Y[t] = X[t] . W[e]^T + bias[e].
 //
-// Each weight row that is used is read once and nothing else matters: bytes and
+// Each weight row that is used is read once and little else matters: bytes and
 // latency bound it.  A block owns 16 features of one expert and its 8 warps
 // cut K, so that a call spreads over every SM at once, with no set-up before
 // the first load but finding the block's expert.  A lane reads 16 bytes of a
@@ -21,7 +21,7 @@ namespace bsl {
 namespace {
 
 constexpr int kWarps = 8;
-constexpr int kRows = 8;       // rows of X in a call, at most (MMA N)
+constexpr int kRows = 8;       // rows of X in a group (MMA N); a call has up to four groups
 constexpr int kFeatures = 16;  // per block (MMA M)
 
 struct FewArgs {
@@ -53,20 +53,24 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// One step's products of 4-bit operands.
-template <bool kHigh>
-__device__ __forceinline__ void step4(float (&acc)[4], const uint4 &a, const uint4 &b, const uint4 &x, uint32_t sa,
-                                      uint32_t sb, uint32_t sx, uint32_t low)
+// One step's products of 4-bit operands, NT groups of rows.
+template <bool kHigh, int NT>
+__device__ __forceinline__ void step4(float (&acc)[NT][4], const uint4 &a, const uint4 &b, const uint4 (&x)[NT],
+                                      uint32_t sa, uint32_t sb, const uint32_t (&sx)[NT], uint32_t low)
 {
-    const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w}, xw[4] = {x.x, x.y, x.z, x.w};
+    const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         uint32_t p[4], q[4], r[4];
         decode8<kHigh>(aw[i], sa, low, p);
         decode8<kHigh>(bw[i], sb, low, q);
-        decode8<kHigh>(xw[i], sx, low, r);
-        mma_bf16(acc, p[0], q[0], p[1], q[1], r[0], r[1]);
-        mma_bf16(acc, p[2], q[2], p[3], q[3], r[2], r[3]);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const uint32_t xw[4] = {x[n].x, x[n].y, x[n].z, x[n].w};
+            decode8<kHigh>(xw[i], sx[n], low, r);
+            mma_bf16(acc[n], p[0], q[0], p[1], q[1], r[0], r[1]);
+            mma_bf16(acc[n], p[2], q[2], p[3], q[3], r[2], r[3]);
+        }
     }
 }
 
@@ -120,10 +124,11 @@ __device__ __forceinline__ Found find_expert(const FewArgs &a, int li, int &rest
     return f;
 }
 
-template <bool kF4>
-__global__ void __launch_bounds__(kWarps * 32, kF4 ? 4 : 3) k_few_rows(const FewArgs a)
+// NT groups of eight rows: 1, 2 or 4 (bf16).
+template <bool kF4, int NT>
+__global__ void __launch_bounds__(kWarps * 32, kF4 && NT == 1 ? 4 : 3) k_few_rows(const FewArgs a)
 {
-    __shared__ float part[kWarps][kRows][kFeatures];
+    __shared__ float part[kWarps][NT * kRows][kFeatures];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int li = blockIdx.x / a.blocks, n0 = (blockIdx.x - li * a.blocks) * kFeatures;
     dependents_may_launch();
@@ -133,69 +138,89 @@ __global__ void __launch_bounds__(kWarps * 32, kF4 ? 4 : 3) k_few_rows(const Few
     const Found f = find_expert(a, li, front, back, bad);
     if (bad && blockIdx.x == 0 && threadIdx.x == 0) set_status(a.status, BSL_ERR_INVALID_ARG);
     if (a.zero_rest && li == 0) {  // rows of no expert: the first expert's blocks, each its features
-        const int r = threadIdx.x / kFeatures, n = n0 + threadIdx.x % kFeatures;
-        if (r < a.T && (r < front || r >= back) && n < a.N)
-            a.Y[static_cast<int64_t>(r) * a.N + n] = __float2bfloat16(0.f);
+        const int n = n0 + threadIdx.x % kFeatures;
+        for (int r = threadIdx.x / kFeatures; r < a.T; r += kWarps * 32 / kFeatures)
+            if ((r < front || r >= back) && n < a.N) a.Y[static_cast<int64_t>(r) * a.N + n] = __float2bfloat16(0.f);
     }
     if (f.e < 0) return;
 
-    // this lane's rows: features n0 + g and n0 + g + 8 of the weight, row g of X
+    // this lane's rows: features n0 + g and n0 + g + 8 of the weight, rows g, g + 8, ... of X
     constexpr int SPAN = kF4 ? 128 : 32;  // k of a step: 16 bytes a lane
     const int64_t bytes = kF4 ? a.K / 2 : static_cast<int64_t>(a.K) * 2;
     const int64_t wr = static_cast<int64_t>(f.e) * a.N + n0 + g;
-    const bool in0 = n0 + g < a.N, in1 = n0 + g + 8 < a.N, inx = g < f.rows;
+    const bool in0 = n0 + g < a.N, in1 = n0 + g + 8 < a.N;
     const uint8_t *w0 = a.W + wr * bytes + 16 * t, *w1 = w0 + 8 * bytes;
     const uint8_t *x = a.X + static_cast<int64_t>(f.first + g) * bytes + 16 * t;
     const uint8_t *ws0 = kF4 ? a.w_scales + wr * (a.K / 32) + t : nullptr, *ws1 = kF4 ? ws0 + 8 * (a.K / 32) : nullptr;
     const uint8_t *xs = kF4 ? a.x_scales + static_cast<int64_t>(f.first + g) * (a.K / 32) + t : nullptr;
     const int steps = (a.K + SPAN - 1) / SPAN;
-    constexpr int U = kF4 ? 2 : 4;
-    float acc[4] = {};
+    constexpr int U = kF4 ? (NT == 1 ? 2 : 1) : NT == 4 ? 2 : 4;
+    const int64_t scale_row = kF4 ? 8 * (a.K / 32) : 0;
+    float acc[NT][4] = {};
     for (int s0 = warp; s0 < steps; s0 += kWarps * U) {
-        uint4 va[U], vb[U], vx[U];
-        uint32_t sa[U], sb[U], sx[U];
+        uint4 va[U], vb[U], vx[U][NT];
+        uint32_t sa[U], sb[U], sx[U][NT];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int s = s0 + u * kWarps;
             const bool in = s * SPAN + t * (SPAN / 4) < a.K;
-            va[u] = vb[u] = vx[u] = make_uint4(0, 0, 0, 0);
-            sa[u] = sb[u] = sx[u] = 0;
+            va[u] = vb[u] = make_uint4(0, 0, 0, 0);
+            sa[u] = sb[u] = 0;
             if (in && in0) va[u] = load_stream(w0 + static_cast<int64_t>(s) * 64);
             if (in && in1) vb[u] = load_stream(w1 + static_cast<int64_t>(s) * 64);
-            if (in && inx) vx[u] = __ldg(reinterpret_cast<const uint4 *>(x + static_cast<int64_t>(s) * 64));
             if constexpr (kF4) {
                 if (in && in0) sa[u] = __ldg(ws0 + 4 * s);
                 if (in && in1) sb[u] = __ldg(ws1 + 4 * s);
-                if (in && inx) sx[u] = __ldg(xs + 4 * s);
+            }
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                vx[u][n] = make_uint4(0, 0, 0, 0);
+                sx[u][n] = 0;
+                if (in && g + 8 * n < f.rows) {
+                    vx[u][n] = __ldg(reinterpret_cast<const uint4 *>(x + n * 8 * bytes + static_cast<int64_t>(s) * 64));
+                    if constexpr (kF4) sx[u][n] = __ldg(xs + n * scale_row + 4 * s);
+                }
             }
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             if constexpr (kF4) {
-                const uint32_t top = max(max(sa[u], sb[u]), sx[u]);
-                if (!__any_sync(0xffffffffu, top > 128)) {
-                    step4<false>(acc, va[u], vb[u], vx[u], sa[u], sb[u], sx[u], 0);
-                } else if (!__any_sync(0xffffffffu, top > 252 && top < 255)) {
-                    step4<true>(acc, va[u], vb[u], vx[u], sa[u], sb[u], sx[u], 0);
-                } else {  // scales of 2^126 and 2^127: both operands 2^-4 of themselves, the products 2^8 of that
-                    float sum[4] = {};
-                    step4<true>(sum, va[u], vb[u], vx[u], sa[u], sb[u], sx[u], 4);
+                uint32_t top = max(sa[u], sb[u]);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) acc[i] += 256.f * sum[i];
+                for (int n = 0; n < NT; ++n) top = max(top, sx[u][n]);
+                // (255 stands for NaN whatever it is multiplied with)
+                if (!__any_sync(0xffffffffu, top > 128)) {
+                    step4<false, NT>(acc, va[u], vb[u], vx[u], sa[u], sb[u], sx[u], 0);
+                } else {
+                    // scales of 2^126 and 2^127: both operands 2^-4 of themselves, the products 2^8 of that
+                    const bool far = __any_sync(0xffffffffu, top > 252);
+                    float sum[NT][4] = {};
+                    step4<true, NT>(sum, va[u], vb[u], vx[u], sa[u], sb[u], sx[u], far ? 4 : 0);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) acc[n][i] += far ? 256.f * sum[n][i] : sum[n][i];
                 }
             } else {
-                mma_bf16(acc, va[u].x, vb[u].x, va[u].y, vb[u].y, vx[u].x, vx[u].y);
-                mma_bf16(acc, va[u].z, vb[u].z, va[u].w, vb[u].w, vx[u].z, vx[u].w);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    mma_bf16(acc[n], va[u].x, vb[u].x, va[u].y, vb[u].y, vx[u][n].x, vx[u][n].y);
+                    mma_bf16(acc[n], va[u].z, vb[u].z, va[u].w, vb[u].w, vx[u][n].z, vx[u][n].w);
+                }
             }
         }
     }
-    part[warp][2 * t][g] = acc[0];
-    part[warp][2 * t + 1][g] = acc[1];
-    part[warp][2 * t][g + 8] = acc[2];
-    part[warp][2 * t + 1][g + 8] = acc[3];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        part[warp][8 * n + 2 * t][g] = acc[n][0];
+        part[warp][8 * n + 2 * t + 1][g] = acc[n][1];
+        part[warp][8 * n + 2 * t][g + 8] = acc[n][2];
+        part[warp][8 * n + 2 * t + 1][g + 8] = acc[n][3];
+    }
     __syncthreads();
-    const int r = threadIdx.x / kFeatures, n = n0 + threadIdx.x % kFeatures;
-    if (r < f.rows && n < a.N) {
+    const int n = n0 + threadIdx.x % kFeatures;
+    if (n >= a.N) return;
+    for (int r = threadIdx.x / kFeatures; r < f.rows; r += kWarps * 32 / kFeatures) {
         float s = 0.f;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) s += part[w][r][threadIdx.x % kFeatures];
@@ -210,21 +235,31 @@ bsl_status launch(FewArgs &a, cudaStream_t s)
     a.blocks = (a.N + kFeatures - 1) / kFeatures;
     const int64_t grid = static_cast<int64_t>(a.blocks) * (a.T < a.E ? a.T : a.E);
     if (grid > 0x7FFFFFFF) return BSL_ERR_UNSUPPORTED;
-    return cuda_status(launch_dependent(k_few_rows<kF4>, static_cast<unsigned>(grid), kWarps * 32, 0, s, a));
+    const unsigned g = static_cast<unsigned>(grid);
+    if (a.T <= kRows) return cuda_status(launch_dependent(k_few_rows<kF4, 1>, g, kWarps * 32, 0, s, a));
+    if (kF4 || a.T <= 2 * kRows) return cuda_status(launch_dependent(k_few_rows<kF4, 2>, g, kWarps * 32, 0, s, a));
+    return cuda_status(launch_dependent(k_few_rows<false, 4>, g, kWarps * 32, 0, s, a));
 }
 
 }  // namespace
 
-// bf16: ahead of the tensor-core tiles wherever it fits (T = 2 over 2 of 8 experts of 4096 x 2048: 6.1 against
-// 12.2 us; one row on 11008 x 4096: 12.0 against 19.7).
-bool few_rows(int32_t T) { return T <= kRows; }
+// Where these kernels are ahead of the tensor-core tiles, by the rows and by the
+// bytes of the weights that the rows can use (L2 cold; us here / there).
+// bf16: up to 8 rows everywhere (17 MB 5.6 / 13.7, 361 MB 60 / 67, 721 MB 114 / 114); 16 rows re-read X for every
+// 16 features, so up to 32 MB (17 MB 7.6 / 13.6, 34 MB 12.0 / 12.3, 90 MB 23.9 / 22.6); 32 rows up to 20 MB
+// (17 MB 10.1 / 13.6, 34 MB 15.6 / 12.3).
+bool few_rows(int32_t T, const bsl_grouped *W)
+{
+    const int64_t bytes = static_cast<int64_t>(T < W->E ? T : W->E) * W->N * W->K * 2;
+    return T <= kRows || (T <= 2 * kRows && bytes <= (32ll << 20)) || (T <= 4 * kRows && bytes <= 20000000);
+}
 
-// 4 bits: turning codes into numbers bounds it, so it is ahead while the weights that can be used are small
-// (one row on 4096 x 2048: 5.7 against 7.7 us; 2 experts of that: 7.0 against 8.2; 11008 x 4096: 15.0 against 11.6).
+// 4 bits: turning codes into numbers bounds it (8 rows: 4.2 MB of codes 6.7 / 8.8, 8.4 MB 11.9 / 8.2, 22 MB
+// 16.4 / 13.4; 16 rows: 0.3 MB 7.1 / 11.3, 4.2 MB 7.5 / 8.7, 8.4 MB 10.9 / 8.2).
 bool few_rows4(int32_t T, const bsl_mx4 *W)
 {
-    const int64_t live = T < W->E ? T : W->E;
-    return T <= kRows && live * W->N * (W->K / 2) <= (12ll << 20);
+    const int64_t bytes = static_cast<int64_t>(T < W->E ? T : W->E) * W->N * (W->K / 2);
+    return T <= 2 * kRows && bytes <= (4ll << 20);
 }
 
 bsl_status launch_few_rows(const void *X, int32_t T, const int32_t *offsets, const bsl_grouped *W, const void *bias,

@@ -61,7 +61,7 @@ size_t grouped_workspace_bytes(const bsl_grouped *W) { return static_cast<size_t
 bsl_status launch_grouped_rows(const void *A, int32_t T, const int32_t *offsets, const bsl_grouped *W, bool transposed,
                                const void *bias, void *out, int32_t zero_rest, cudaStream_t s)
 {
-    if (!transposed && few_rows(T)) return launch_few_rows(A, T, offsets, W, bias, out, zero_rest, s);
+    if (!transposed && few_rows(T, W)) return launch_few_rows(A, T, offsets, W, bias, out, zero_rest, s);
     Args args = {};
     args.offsets = offsets;
     args.bias = static_cast<const __nv_bfloat16 *>(bias);

@@ -152,7 +152,7 @@ bsl_status launch_grouped_bias_grad(const void *dY, int32_t T, const int32_t *of
                                     cudaStream_t s);
 
 // The forwards of both layers for calls of few rows, where these are true.
-bool few_rows(int32_t T);
+bool few_rows(int32_t T, const bsl_grouped *W);
 bool few_rows4(int32_t T, const bsl_mx4 *W);
 bsl_status launch_few_rows(const void *X, int32_t T, const int32_t *offsets, const bsl_grouped *W, const void *bias,
                            void *Y, int32_t zero_rest, cudaStream_t s);

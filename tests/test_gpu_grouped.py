@@ -72,12 +72,14 @@ def test_many_experts(E, N, K):
 
 
 FEW = [([8], 1032, 4096, 0, 0), ([7], 24, 1000, 0, 0), ([0, 3, 0, 0, 1, 0, 2], 520, 2056, 1, 1), ([1] * 8, 264, 40, 0, 0),
-       ([0] * 31 + [2] + [0] * 200 + [1, 0, 3], 72, 136, 0, 2), ([0] * 1000 + [5], 16, 264, 2, 1), ([9], 136, 1000, 0, 0)]
+       ([0] * 31 + [2] + [0] * 200 + [1, 0, 3], 72, 136, 0, 2), ([0] * 1000 + [5], 16, 264, 2, 1), ([9], 136, 1000, 0, 0),
+       ([3, 0, 11], 264, 1000, 1, 1), ([16], 1032, 520, 0, 0), ([20, 1, 0, 8], 72, 2056, 2, 1), ([32], 4096, 2048, 0, 0),
+       ([17], 8200, 4096, 0, 0), ([33], 136, 520, 0, 0)]
 
 
 @pytest.mark.parametrize("rows,N,K,first,spare", FEW)
 def test_few_rows(rows, N, K, first, spare):
-    """Up to eight rows in all, and one more: any expert, long and odd K."""
+    """Few rows in all, on both sides of 8, 16 and 32 and of the weights' sizes: any expert, long and odd K."""
     for got, ref, S, depth, what in run_all(rows, N, K, 20, first=first, spare=spare):
         check(got, ref, S, depth, what)
 

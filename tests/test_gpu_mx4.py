@@ -155,7 +155,8 @@ def test_many_tiles(M, N, K):
 
 @pytest.mark.parametrize("rows,N,K,first,spare", [
     ([8], 1032, 4096, 0, 0), ([1], 11008, 4096, 0, 0), ([0, 3, 0, 0, 1, 0, 2], 520, 2080, 1, 1),
-    ([0] * 31 + [2] + [0] * 200 + [1, 0, 3], 72, 160, 0, 2), ([0] * 1000 + [5], 16, 32, 2, 1), ([9], 136, 992, 0, 0)])
+    ([0] * 31 + [2] + [0] * 200 + [1, 0, 3], 72, 160, 0, 2), ([0] * 1000 + [5], 16, 32, 2, 1), ([9], 136, 992, 0, 0),
+    ([3, 0, 11], 264, 992, 1, 1), ([16], 1032, 512, 0, 0), ([16], 4104, 2080, 0, 0), ([17], 136, 512, 0, 0)])
 def test_few_rows(rows, N, K, first, spare):
     rng = np.random.default_rng(N + K + first)
     off, o = offsets_of(rows, first)
@@ -169,7 +170,7 @@ def test_few_rows(rows, N, K, first, spare):
     assert sg.mx4_status(Wq) == 0
 
 
-@pytest.mark.parametrize("M", [3, 40])
+@pytest.mark.parametrize("M", [3, 12, 40])
 def test_every_scale_byte(M):
     """Weight rows and activation rows under every scale byte whose products stay in the fp32 range."""
     rng = np.random.default_rng(M)
@@ -202,7 +203,7 @@ def test_many_experts():
     check(sg.grouped_forward_mx4(X, Wq, off), *experts.grouped_forward(Xf, Wf, o), 32, "many experts")
 
 
-@pytest.mark.parametrize("M", [5, 300])
+@pytest.mark.parametrize("M", [5, 15, 300])
 def test_nan_blocks_and_extreme_scales(M):
     """A NaN or an infinity in a row makes that row NaN and no other; scale bytes at both ends count."""
     rng = np.random.default_rng(8)
