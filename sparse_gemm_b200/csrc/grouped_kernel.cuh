@@ -43,9 +43,9 @@
 // (clock held by power at 1.1-1.3 GHz): one 32 KB copy 1412 / 1459 / 1460 us
 // for the three, copies of 16 KB and stages of 64 k 1460 / 1575 / 1540, of 8
 // KB (gradients) 1775.  With few rows the weight's bytes bound it: 64 rows of
-// 16 experts of 11008 x 4096 take 236 us (6.1 TB/s).  There, too, the pair is
-// ahead of one CTA on tiles of 128 features (240 us; 93 against 110 us with
-// 4-bit operands).
+// 16 experts of 11008 x 4096 take 222 us (6.5 TB/s).  There, too, the pair is
+// ahead of one CTA on tiles of 128 features (236 against 240 us with three
+// stages; 93 against 110 us with 4-bit operands).
 //
 // Waiting costs: a waiting warp polls shared memory.  So one warp of a group
 // waits and the others stand at a named barrier (4-bit, 8192 x 4096 x 14336:
@@ -77,7 +77,7 @@ struct Cfg {
     static constexpr int A_BYTES = 128 * BK * 2;
     static constexpr int B_BYTES = BR / 2 * BK * 2;
     static constexpr int RING = (F4 ? 180 : 192) * 1024;  // three stages of full tiles, up to S of smaller ones
-    static constexpr int S = 5;
+    static constexpr int S = F4 ? 4 : 5;             // (4 bits: 5 are no faster, and 0.7 us slower for one row)
     // two accumulators, then a ring of scales: half a stage (256 elements of k), 8 columns of A's and 16 of B's
     static constexpr int SR = F4 ? 5 : 0, SC_COL = 2 * BR, SC_COLS = 24;
     static constexpr int TMEM = 512;
@@ -409,8 +409,8 @@ __device__ __forceinline__ void copy_scales(const Tiles<kMode> &tiles, const Arg
 }
 
 // Bytes of a stage in the ring, by the calling warp: the rows of B are those of
-// the launch's largest tile.  What few rows leave free holds more stages: with
-// five instead of three, MEASURED_RING
+// the launch's largest tile.  What few rows leave free holds more stages: 64
+// rows of 16 experts of 11008 x 4096 take 222 us with five, 236 with three.
 template <int kMode>
 __device__ __forceinline__ int stage_bytes(const int32_t *off, int32_t E)
 {
