@@ -313,6 +313,8 @@ BSL_API bsl_status bsl_semi24_get_status(const bsl_semi24 *W, int32_t *status_ho
  * clamped (every access stays inside the matrices) and reported as
  * BSL_ERR_INVALID_ARG in the device status. */
 #define BSL_GROUPED_MAX_EXPERTS 1024
+/* Limit of N, K and the rows of a call, here and in the 4-bit products (BSL_ERR_UNSUPPORTED above it). */
+#define BSL_GROUPED_MAX_SIZE 0x7FFFF000
 
 typedef struct {
     int32_t E, N, K;    /* experts (1 .. BSL_GROUPED_MAX_EXPERTS), output and input features;
@@ -324,7 +326,7 @@ typedef struct {
 /* Y [T][N]: Y[t] = X[t] . W[e]^T (+ bias[e]) for the rows t of each expert e.
  * X is bf16 [T][K], bias bf16 [E][N] or NULL.  Rows of no expert are left as
  * they were, or set to zero when zero_rest is not 0.  T >= 0 (nothing is
- * done for T = 0). */
+ * done for T = 0).  Outputs, here and below, must not overlap inputs. */
 BSL_API bsl_status bsl_grouped_forward(const void *X, int32_t T, const int32_t *offsets, const bsl_grouped *W,
                                        const void *bias, void *Y, int32_t zero_rest, void *stream);
 

@@ -646,10 +646,14 @@ def _new(like: torch.Tensor, *shape: int) -> torch.Tensor:
     return like.new_empty(*shape) if like.dtype is torch.bfloat16 else like.new_empty(shape, dtype=torch.bfloat16)
 
 
-def _out_arg(out, shape, like: torch.Tensor) -> torch.Tensor:
+def _out_arg(out, shape, like: torch.Tensor, *inputs: torch.Tensor) -> torch.Tensor:
     if out is None:
         return _new(like, *shape)
     _tensor_arg(out, "out", shape, torch.bfloat16, like)
+    first, end = out.data_ptr(), out.data_ptr() + out.nbytes
+    for t in (like, *inputs):
+        if first < t.data_ptr() + t.nbytes and t.data_ptr() < end:
+            raise ValueError("out must not overlap an input")
     return out
 
 
@@ -672,6 +676,8 @@ class GroupedWeight:
         if not 0 < E <= GROUPED_MAX_EXPERTS or N <= 0 or K <= 0 or N % 8 or K % 8:
             raise ValueError("weight must be [E, N, K] with 1 <= E <= 1024 and N, K positive multiples of 8")
         self.weight = weight.detach()
+        if torch.cuda.is_current_stream_capturing():   # the status word outlives any graph
+            raise RuntimeError("make a GroupedWeight (or call its module once) before capturing a graph with it")
         self.E, self.N, self.K = int(E), int(N), int(K)
         self.status = torch.zeros(1, dtype=torch.int32, device=weight.device)
         self._c = _GROUPED(self.E, self.N, self.K, self.weight.data_ptr(), self.status.data_ptr())
@@ -694,7 +700,7 @@ def grouped_forward(X: torch.Tensor, Wg: GroupedWeight, offsets: torch.Tensor, b
     _tensor_arg(X, "X", (None, Wg.K), torch.bfloat16, Wg.weight)
     _tensor_arg(offsets, "offsets", (Wg.E + 1,), torch.int32, X)
     bptr = _expert_bias(bias, Wg.E, Wg.N, X)
-    Y = _out_arg(out, (X.shape[0], Wg.N), X)
+    Y = _out_arg(out, (X.shape[0], Wg.N), X, Wg.weight)
     _check(library().bsl_grouped_forward(X.data_ptr(), _row_count(X, "X"), offsets.data_ptr(), Wg.cref(), bptr,
                                          Y.data_ptr(), out is None, _stream(X)), "bsl_grouped_forward")
     return Y
@@ -705,7 +711,7 @@ def grouped_backward_input(dY: torch.Tensor, Wg: GroupedWeight, offsets: torch.T
     """dX[t] = dY[t] W[e]; rows of no expert as in :func:`grouped_forward`."""
     _tensor_arg(dY, "dY", (None, Wg.N), torch.bfloat16, Wg.weight)
     _tensor_arg(offsets, "offsets", (Wg.E + 1,), torch.int32, dY)
-    dX = _out_arg(out, (dY.shape[0], Wg.K), dY)
+    dX = _out_arg(out, (dY.shape[0], Wg.K), dY, Wg.weight)
     _check(library().bsl_grouped_backward_input(dY.data_ptr(), _row_count(dY, "dY"), offsets.data_ptr(),
                                                 Wg.cref(), dX.data_ptr(), out is None, _stream(dY)),
            "bsl_grouped_backward_input")
@@ -718,7 +724,7 @@ def grouped_backward_weight(dY: torch.Tensor, X: torch.Tensor, Wg: GroupedWeight
     _tensor_arg(dY, "dY", (None, Wg.N), torch.bfloat16, Wg.weight)
     _tensor_arg(X, "X", (dY.shape[0], Wg.K), torch.bfloat16, Wg.weight)
     _tensor_arg(offsets, "offsets", (Wg.E + 1,), torch.int32, X)
-    dW = _out_arg(out, (Wg.E, Wg.N, Wg.K), X)
+    dW = _out_arg(out, (Wg.E, Wg.N, Wg.K), X, dY)
     nbytes = Wg._workspace_bytes
     ws = _new(X, nbytes // 2)
     _check(library().bsl_grouped_backward_weight(dY.data_ptr(), X.data_ptr(), _row_count(X, "X"),
@@ -752,7 +758,8 @@ class GroupedLinearFunction(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, X, weight, offsets, Wg, bias=None):
-        if weight.data_ptr() != Wg.weight.data_ptr() or weight.shape != Wg.weight.shape:
+        if (weight.data_ptr() != Wg.weight.data_ptr() or weight.shape != Wg.weight.shape
+                or not weight.is_contiguous()):
             raise ValueError("weight must be the tensor Wg was built on")
         X = X.contiguous()
         ctx.save_for_backward(X, weight, offsets)
@@ -792,7 +799,8 @@ class GroupedLinear(torch.nn.Module):
     @property
     def packed(self) -> GroupedWeight:
         """The weight's handle, made anew when the parameter's storage was replaced."""
-        if self._packed is None or self._packed.weight.data_ptr() != self.weight.data_ptr():
+        if (self._packed is None or self._packed.weight.data_ptr() != self.weight.data_ptr()
+                or self._packed.weight.shape != self.weight.shape or not self.weight.is_contiguous()):
             self._packed = GroupedWeight(self.weight)
         return self._packed
 
@@ -928,7 +936,7 @@ def _mx4_product(X, Wq: Mx4Tensor, offsets, bias_ptr, N: int, out) -> torch.Tens
     else:
         _tensor_arg(X, "X", (None, Wq.K), torch.bfloat16, Wq._held)
         rows, like = _row_count(X, "X"), X
-    Y = _out_arg(out, (rows, N), like)
+    Y = _out_arg(out, (rows, N), like, Wq._held)
     lib, off = library(), None if offsets is None else offsets.data_ptr()
     if like is X:
         nbytes = rows * (Wq.K // 2 + Wq.K // 32)   # bsl_mx4_workspace_bytes

@@ -117,11 +117,16 @@ bsl_status check_semi24(const bsl_semi24 *W)
     return BSL_OK;
 }
 
+namespace {
+// Rows or features that the kernels' 32-bit indexes cannot count up to the end of the last tile.
+bool too_large(int32_t n) { return n > BSL_GROUPED_MAX_SIZE; }
+}  // namespace
+
 bsl_status check_grouped(const bsl_grouped *W)
 {
     if (!W) return BSL_ERR_INVALID_ARG;
     if (W->E <= 0 || W->N <= 0 || W->K <= 0 || W->N % 8 || W->K % 8) return BSL_ERR_INVALID_ARG;
-    if (W->E > BSL_GROUPED_MAX_EXPERTS) return BSL_ERR_UNSUPPORTED;
+    if (W->E > BSL_GROUPED_MAX_EXPERTS || too_large(W->N) || too_large(W->K)) return BSL_ERR_UNSUPPORTED;
     if (!W->weight || !aligned(W->weight, 16) || !W->status || !aligned(W->status, 4)) return BSL_ERR_INVALID_ARG;
     return BSL_OK;
 }
@@ -130,7 +135,7 @@ bsl_status check_mx4(const bsl_mx4 *W)
 {
     if (!W) return BSL_ERR_INVALID_ARG;
     if (W->E <= 0 || W->N <= 0 || W->K <= 0 || W->N % 8 || W->K % 32) return BSL_ERR_INVALID_ARG;
-    if (W->E > BSL_GROUPED_MAX_EXPERTS) return BSL_ERR_UNSUPPORTED;
+    if (W->E > BSL_GROUPED_MAX_EXPERTS || too_large(W->N) || too_large(W->K)) return BSL_ERR_UNSUPPORTED;
     if (!W->codes || !aligned(W->codes, 16) || !W->scales || !aligned(W->scales, 16) || !W->status ||
         !aligned(W->status, 4))
         return BSL_ERR_INVALID_ARG;
@@ -511,6 +516,7 @@ bsl_status bsl_grouped_forward(const void *X, int32_t T, const int32_t *offsets,
     if (check_matrix(X, T) != BSL_OK || check_matrix(Y, T) != BSL_OK) return BSL_ERR_INVALID_ARG;
     if (bias && !aligned(bias, 16)) return BSL_ERR_INVALID_ARG;
     if (T == 0) return BSL_OK;
+    if (too_large(T)) return BSL_ERR_UNSUPPORTED;
     DeviceGuard guard;
     BSL_TRY(guard.bind(X));
     BSL_TRY(check_device());
@@ -524,6 +530,7 @@ bsl_status bsl_grouped_backward_input(const void *dY, int32_t T, const int32_t *
     if (T < 0 || !offsets || !aligned(offsets, 4)) return BSL_ERR_INVALID_ARG;
     if (check_matrix(dY, T) != BSL_OK || check_matrix(dX, T) != BSL_OK) return BSL_ERR_INVALID_ARG;
     if (T == 0) return BSL_OK;
+    if (too_large(T)) return BSL_ERR_UNSUPPORTED;
     DeviceGuard guard;
     BSL_TRY(guard.bind(dY));
     BSL_TRY(check_device());
@@ -545,6 +552,7 @@ bsl_status bsl_grouped_backward_weight(const void *dY, const void *X, int32_t T,
         return BSL_ERR_INVALID_ARG;
     const size_t need = grouped_workspace_bytes(W);
     if (need && (!workspace || !aligned(workspace, 128) || workspace_bytes < need)) return BSL_ERR_INVALID_ARG;
+    if (too_large(T)) return BSL_ERR_UNSUPPORTED;
     DeviceGuard guard;
     BSL_TRY(guard.bind(dW));
     BSL_TRY(check_device());
@@ -559,7 +567,7 @@ bsl_status bsl_grouped_bias_grad(const void *dY, int32_t T, const int32_t *offse
 {
     if (T < 0 || E <= 0 || N <= 0 || N % 8 || !offsets || !aligned(offsets, 4)) return BSL_ERR_INVALID_ARG;
     if (check_matrix(dY, T) != BSL_OK || check_matrix(db, 1) != BSL_OK) return BSL_ERR_INVALID_ARG;
-    if (E > BSL_GROUPED_MAX_EXPERTS) return BSL_ERR_UNSUPPORTED;
+    if (E > BSL_GROUPED_MAX_EXPERTS || too_large(N) || too_large(T)) return BSL_ERR_UNSUPPORTED;
     DeviceGuard guard;
     BSL_TRY(guard.bind(db));
     BSL_TRY(check_device());
@@ -607,6 +615,7 @@ bsl_status bsl_mx4_forward(const uint8_t *x_codes, const uint8_t *x_scales, int3
     if (check_matrix(x_codes, M) != BSL_OK || check_matrix(x_scales, M) != BSL_OK || check_matrix(Y, M) != BSL_OK)
         return BSL_ERR_INVALID_ARG;
     if (M == 0) return BSL_OK;
+    if (too_large(M)) return BSL_ERR_UNSUPPORTED;
     DeviceGuard guard;
     BSL_TRY(guard.bind(x_codes));
     BSL_TRY(check_device());
@@ -621,6 +630,7 @@ bsl_status bsl_mx4_grouped_forward(const uint8_t *x_codes, const uint8_t *x_scal
     if (check_matrix(x_codes, T) != BSL_OK || check_matrix(x_scales, T) != BSL_OK || check_matrix(Y, T) != BSL_OK)
         return BSL_ERR_INVALID_ARG;
     if (T == 0) return BSL_OK;
+    if (too_large(T)) return BSL_ERR_UNSUPPORTED;
     DeviceGuard guard;
     BSL_TRY(guard.bind(x_codes));
     BSL_TRY(check_device());
@@ -643,6 +653,7 @@ bsl_status bsl_mx4_linear(const void *X, int32_t T, const int32_t *offsets, cons
         workspace_bytes < bsl_mx4_workspace_bytes(T, W))
         return BSL_ERR_INVALID_ARG;
     if (T == 0) return BSL_OK;
+    if (too_large(T)) return BSL_ERR_UNSUPPORTED;
     DeviceGuard guard;
     BSL_TRY(guard.bind(X));
     BSL_TRY(check_device());

@@ -702,7 +702,9 @@ __global__ void __launch_bounds__(Cfg<kMode>::THREADS, 1)
             if (x.kb > 0) {
                 // one warp waits (a waiting warp polls shared memory, which the MMAs and
                 // copies need); all four come to every tile's barrier, an aborted run's too
-                if (ok && q == 0 && __any_sync(0xffffffffu, !mbar_wait(&afull[acc], (it >> 1) & 1, tmo, abort_flag)) &&
+                // (a whole tile's sum: its limit grows by 4 us a stage, which takes one at most)
+                const uint64_t limit = tmo + 4096ull * static_cast<uint32_t>(x.kb);
+                if (ok && q == 0 && __any_sync(0xffffffffu, !mbar_wait(&afull[acc], (it >> 1) & 1, limit, abort_flag)) &&
                     lane == 0)
                     *abort_flag = 1;
                 __syncwarp();

@@ -201,6 +201,24 @@ def test_bad_mx4_arguments_are_refused(lib):
     assert lib.bsl_mx4_get_status(None, ctypes.byref(ctypes.c_int32()), None) == 1
 
 
+def test_sizes_past_the_index_range_are_refused(lib):
+    """The kernels count rows and features in 32 bits up to the end of the last tile."""
+    text = open(os.path.join(ROOT, "include", "bsl.h")).read()
+    most = int(re.search(r"#define BSL_GROUPED_MAX_SIZE (\w+)", text).group(1), 16)
+    big, P = 2 ** 31 - 32, 4096
+    assert most + 2048 + 128 < 2 ** 31 and big > most
+    for kw, T in (({}, most + 1), ({}, 2 ** 31 - 1), (dict(N=big), 8), (dict(K=big), 8)):
+        w, q = ctypes.byref(_grouped(**kw)), ctypes.byref(_mx4(**kw))
+        assert lib.bsl_grouped_forward(P, T, P, w, None, P, 0, None) == 2
+        assert lib.bsl_grouped_backward_input(P, T, P, w, P, 0, None) == 2
+        assert lib.bsl_grouped_backward_weight(P, P, T, P, w, P, P, 1 << 30, None) == 2
+        assert lib.bsl_mx4_forward(P, P, T, q, None, P, None) == 2
+        assert lib.bsl_mx4_grouped_forward(P, P, T, P, q, None, P, 0, None) == 2
+        assert lib.bsl_mx4_linear(P, T, None, q, None, P, 0, P, 1 << 62, None) == 2
+        if "K" not in kw:
+            assert lib.bsl_grouped_bias_grad(P, T, P, 4, kw.get("N", 64), P, None) == 2
+
+
 @pytest.mark.parametrize("name", ["_GROUPED", "_MX4"])
 def test_binding_structs_match_the_header(name):
     import sparse_gemm_b200 as sg

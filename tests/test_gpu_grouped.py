@@ -409,3 +409,50 @@ def test_refusals():
         sg.GroupedLinear(W, bias=torch.zeros(2, 24))
     with pytest.raises(ValueError):
         sg.GroupedLinearFunction.apply(X, W.clone(), off, Wg)
+
+
+def test_out_that_overlaps_an_input_is_refused():
+    buf = torch.zeros(64 * 32, dtype=torch.bfloat16, device="cuda")
+    W = torch.zeros(2, 16, 16, dtype=torch.bfloat16, device="cuda")
+    Wg = sg.GroupedWeight(W)
+    off = torch.tensor([0, 3, 8], dtype=torch.int32, device="cuda")
+    X, Y = buf[:128].view(8, 16), buf[64:192].view(8, 16)
+    for call in (lambda: sg.grouped_forward(X, Wg, off, out=X), lambda: sg.grouped_forward(X, Wg, off, out=Y),
+                 lambda: sg.grouped_forward(X, Wg, off, out=W.view(-1)[:128].view(8, 16)),
+                 lambda: sg.grouped_backward_input(X, Wg, off, out=Y),
+                 lambda: sg.grouped_backward_weight(buf[1000:1128].view(8, 16), X, Wg, off, out=buf[64:576].view(2, 16, 16)),
+                 lambda: sg.grouped_backward_weight(X, buf[1000:1128].view(8, 16), Wg, off, out=buf[64:576].view(2, 16, 16)),
+                 lambda: sg.grouped_bias_grad(X, off, out=buf[120:152].view(2, 16))):
+        with pytest.raises(ValueError, match="overlap"):
+            call()
+    sg.grouped_forward(X, Wg, off, out=buf[128:256].view(8, 16))      # neighbours are fine
+    assert sg.grouped_status(Wg) == 0
+
+
+def test_weight_that_changed_its_layout_or_meets_a_capture():
+    """A transposed view of the weight's storage is refused; so is a handle made inside a capture."""
+    rng = np.random.default_rng(31)
+    layer = sg.GroupedLinear(normal(rng, (2, 16, 16))[0])
+    X = normal(rng, (8, 16))[0]
+    off = offsets_of([3, 5])[0]
+    flat = layer.weight.detach()
+    with torch.no_grad():
+        want = layer(X, off)
+        layer.weight.data = flat.transpose(1, 2)
+        with pytest.raises(ValueError):
+            layer(X, off)
+        with pytest.raises(ValueError):
+            sg.GroupedLinearFunction.apply(X, layer.weight, off, sg.GroupedWeight(flat))
+        layer.weight.data = flat
+        assert torch.equal(layer(X, off), want)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            with pytest.raises(RuntimeError):
+                sg.GroupedWeight(flat)
+            Y = sg.grouped_forward(X, layer.packed, off)
+        g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(Y, want)

@@ -394,3 +394,14 @@ def test_refusals():
                  lambda: sg.grouped_forward_mx4(bf(2, 32), w3, off.long())):
         with pytest.raises(TypeError):
             call()
+
+
+def test_out_that_overlaps_an_input_is_refused():
+    X = torch.zeros(8, 32, dtype=torch.bfloat16, device="cuda")
+    q = sg.quantize_mx4(X)
+    w = sg.quantize_mx4(torch.zeros(32, 32, dtype=torch.bfloat16, device="cuda"))
+    inside = q._held[:64].view(2, 32)
+    for call in (lambda: sg.forward_mx4(X, w, out=X), lambda: sg.dequantize_mx4(sg.Mx4Tensor(q.codes[:2], q.scales[:2]), out=inside),
+                 lambda: sg.forward_mx4(sg.Mx4Tensor(q.codes[:2], q.scales[:2]), w, out=inside)):
+        with pytest.raises(ValueError, match="overlap"):
+            call()
