@@ -62,12 +62,13 @@
 namespace bsl {
 namespace {
 
-// kForward4: 4-bit operands, rows of scales in whole 16-byte units (K a multiple of 512); kForward4Any: any K
-enum Mode { kForward = 0, kInputGrad = 1, kWeightGrad = 2, kForward4 = 3, kForward4Any = 4 };
+// 4-bit operands by the units that a row of scales (K / 32 bytes) is whole in: kForward4 16 bytes (K a multiple of
+// 512), kForward4By8, kForward4By4, kForward4Any any number
+enum Mode { kForward, kInputGrad, kWeightGrad, kForward4, kForward4By8, kForward4By4, kForward4Any };
 
 template <int kMode>
 struct Cfg {
-    static constexpr bool F4 = kMode == kForward4 || kMode == kForward4Any;
+    static constexpr bool F4 = kMode >= kForward4;
     static constexpr bool AM = kMode == kInputGrad || kMode == kWeightGrad;  // A is M-major
     static constexpr bool BN = kMode == kWeightGrad;                         // B is N-major
     static constexpr int BC = 256;                   // features per tile
@@ -179,12 +180,11 @@ __device__ __forceinline__ uint8_t *align1024(uint8_t *p)
 // of 2^-127 on zero codes; a NaN byte of the next row must not reach them),
 // and so do rows that do not exist.
 
-// Whole rows of 16-byte units: W words of a row from byte0 on.
-template <int W>
+// W words of a row from byte0 on, of rows in whole units of V words.
+template <int W, int V>
 __device__ __forceinline__ void load_words(const uint8_t *base, int32_t stride, int64_t row, bool exists, int32_t byte0,
                                            uint32_t *w)
 {
-    constexpr int V = W < 4 ? W : 4;
     const uint8_t *at = base + row * stride + byte0;
 #pragma unroll
     for (int i = 0; i < W; i += V) {
@@ -193,50 +193,56 @@ __device__ __forceinline__ void load_words(const uint8_t *base, int32_t stride, 
             uint4 v = make_uint4(0, 0, 0, 0);
             if (in) v = __ldg(reinterpret_cast<const uint4 *>(at + 4 * i));
             w[i] = v.x, w[i + 1] = v.y, w[i + 2] = v.z, w[i + 3] = v.w;
-        } else {
+        } else if constexpr (V == 2) {
             uint2 v = make_uint2(0, 0);
             if (in) v = __ldg(reinterpret_cast<const uint2 *>(at + 4 * i));
             w[i] = v.x, w[i + 1] = v.y;
+        } else {
+            w[i] = 0;
+            if (in) w[i] = __ldg(reinterpret_cast<const uint32_t *>(at + 4 * i));
         }
     }
 }
 
 // Rows that start at any byte: the W + 1 aligned words around them, as far as
-// they lie inside the `total` bytes ...
+// they hold bytes of the row.  The last bytes of the array may fill no whole
+// word and are read one by one.
 template <int W>
 __device__ __forceinline__ void load_words_any(const uint8_t *base, int64_t total, int32_t stride, int64_t row, bool exists,
                                                int32_t byte0, uint32_t *w)
 {
-    const int64_t at = (row * stride + byte0) & ~int64_t(3);
+    const int64_t at = row * stride + byte0;
+    const int32_t skip = static_cast<int32_t>(at & 3), left = exists ? stride - byte0 + skip : 0;
+    const uint8_t *p = base + (at - skip);
+    const bool end = exists && total - at < 4 * W + 4;
+    const int32_t whole = end ? static_cast<int32_t>(total - at) + skip : 4 * W + 4;
 #pragma unroll
     for (int i = 0; i <= W; ++i) {
         w[i] = 0;
-        if (exists && at + 4 * i + 4 <= total) w[i] = __ldg(reinterpret_cast<const uint32_t *>(base + at + 4 * i));
+        if (4 * i < left && 4 * i + 4 <= whole) w[i] = __ldg(reinterpret_cast<const uint32_t *>(p + 4 * i));
+    }
+    if (end) {
+#pragma unroll
+        for (int i = 0; i <= W; ++i)
+            if (4 * i + 4 > whole)
+                for (int b = 4 * i; b < whole && b < 4 * i + 4; ++b) w[i] |= static_cast<uint32_t>(p[b]) << (8 * (b & 3));
     }
 }
 
 // ... and, when they are stored, shifted into place and cut at the row's end.
-// The last bytes of the array may fill no whole word: they are read here.
 template <int W>
-__device__ __forceinline__ void shift_words(const uint8_t *base, int64_t total, int32_t stride, int64_t row, bool exists,
-                                            int32_t byte0, const uint32_t *raw, uint32_t *w)
+__device__ __forceinline__ void shift_words(int32_t stride, int64_t row, int32_t byte0, const uint32_t *r, uint32_t *w)
 {
-    const int64_t at = row * stride + byte0, low = at & ~int64_t(3);
-    const int32_t left = exists ? stride - byte0 : 0;
-    const uint32_t shift = static_cast<uint32_t>(at & 3) * 8;
-    uint32_t r[W + 1];
+    const uint32_t shift = (static_cast<uint32_t>(row) * static_cast<uint32_t>(stride) + static_cast<uint32_t>(byte0)) % 4 * 8;
+    const int32_t left = stride - byte0;
 #pragma unroll
-    for (int i = 0; i <= W; ++i) {
-        r[i] = raw[i];
-        const int64_t a = low + 4 * i;
-        if (exists && a < total && a + 4 > total)
-            for (int b = 0; a + b < total; ++b) r[i] |= static_cast<uint32_t>(base[a + b]) << (8 * b);
-    }
+    for (int i = 0; i < W; ++i) w[i] = __funnelshift_r(r[i], r[i + 1], shift);
+    if (left < 4 * W) {
 #pragma unroll
-    for (int i = 0; i < W; ++i) {
-        const int32_t bytes = left - 4 * i;
-        const uint32_t v = __funnelshift_r(r[i], r[i + 1], shift);
-        w[i] = bytes >= 4 ? v : bytes <= 0 ? 0 : v & ((1u << (8 * bytes)) - 1u);
+        for (int i = 0; i < W; ++i) {
+            const int32_t bytes = left - 4 * i;
+            if (bytes < 4) w[i] &= bytes <= 0 ? 0 : (1u << (8 * bytes)) - 1u;
+        }
     }
 }
 
@@ -272,6 +278,7 @@ __device__ __forceinline__ void copy_scales(const Tiles<kMode> &tiles, const Arg
 {
     using C = Cfg<kMode>;
     constexpr bool kAny = kMode == kForward4Any;
+    constexpr int V = kMode == kForward4 ? 4 : kMode == kForward4By8 ? 2 : 1;
     constexpr int W = 4, R = W + kAny;  // a row's words of a stage, and as loaded
     constexpr int P = 2;                // stages of its own that a set loads ahead
     constexpr int G = C::BR / 32;       // groups of 32 rows of B
@@ -316,7 +323,7 @@ __device__ __forceinline__ void copy_scales(const Tiles<kMode> &tiles, const Arg
         for (int i = 0; i < 3; ++i) {
             const Row r = rows(ahead, i);
             if constexpr (kAny) load_words_any<W>(r.base, r.total, bytes, r.row, r.exists, 16 * ahead.k, v[i]);
-            else load_words<W>(r.base, bytes, r.row, r.exists, 16 * ahead.k, v[i]);
+            else load_words<W, V>(r.base, bytes, r.row, r.exists, 16 * ahead.k, v[i]);
         }
         ahead.next();
         ahead.next();
@@ -336,7 +343,7 @@ __device__ __forceinline__ void copy_scales(const Tiles<kMode> &tiles, const Arg
                 if constexpr (kAny) {
                     const Row r = rows(now, i);
                     uint32_t v[W];
-                    shift_words<W>(r.base, r.total, bytes, r.row, r.exists, 16 * now.k, w[p][i], v);
+                    shift_words<W>(bytes, r.row, 16 * now.k, w[p][i], v);
                     buf[at] = make_uint4(v[0], v[1], v[2], v[3]);
                 } else {
                     buf[at] = make_uint4(w[p][i][0], w[p][i][1], w[p][i][2], w[p][i][3]);

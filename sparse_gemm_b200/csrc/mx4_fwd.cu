@@ -29,7 +29,9 @@ bsl_status launch_mx4_fwd(const uint8_t *xc, const uint8_t *xs, int32_t T, const
     args.timeout_ns = wait_timeout_ns();
     Maps m;
     if (!row_maps(m, W->codes, W->E, W->N, args.depth, xc, T, args.depth, Y, W->N)) return BSL_ERR_CUDA;
-    return W->K % 512 == 0 ? run<kForward4>(m, args, s) : run<kForward4Any>(m, args, s);
+    if (W->K % 512 == 0) return run<kForward4>(m, args, s);
+    if (W->K % 256 == 0) return run<kForward4By8>(m, args, s);
+    return W->K % 128 == 0 ? run<kForward4By4>(m, args, s) : run<kForward4Any>(m, args, s);
 }
 
 }  // namespace bsl
