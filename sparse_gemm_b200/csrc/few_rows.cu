@@ -1,21 +1,16 @@
 // few_rows.cu -- forward of the expert (grouped) layer and of the 4-bit layer for
 // a few rows in all (single tokens, up to 32): Y[t] = X[t] . W[e]^T + bias[e].
 //
-// Each weight row that is used is read once and little else matters: bytes and
-// latency bound it.  A block owns 16 features of one expert and its 8 warps
-// cut K, so that a call spreads over every SM at once, with no set-up before
-// the first load but finding the block's expert.  A lane reads 16 bytes of a
-// weight row at a time (two or four steps at once) and feeds them to mma.sync
-// (m16n8k16, the rows of X on its N side) as they lie: the order of k inside
-// a product is free as long as both operands share it.  The warps' fp32 sums
-// are added in order through shared memory, and rounded once.
-//
-// 4-bit operands are turned into the bf16 numbers they stand for (mx4.cuh), five
-// instructions for two codes.
+// Each weight row that is used is read once and little else matters: bytes,
+// instructions (4 bits) and latency bound it.  A block owns 16 features of one
+// expert and its 8 warps cut K, so that a call spreads over every SM at once,
+// with no set-up before the first load but finding the block's expert.  The
+// features are mma.sync's M side, the rows of X its N side; the order of k
+// inside a product is free as long as both operands share it.  The warps' fp32
+// sums are added in order through shared memory, and rounded once.
 #include "common.cuh"
 #include "grouped.cuh"
 #include "internal.h"
-#include "mx4.cuh"
 
 namespace bsl {
 namespace {
@@ -51,27 +46,6 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1
         "{%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-// One step's products of 4-bit operands, NT groups of rows.
-template <bool kHigh, int NT>
-__device__ __forceinline__ void step4(float (&acc)[NT][4], const uint4 &a, const uint4 &b, const uint4 (&x)[NT],
-                                      uint32_t sa, uint32_t sb, const uint32_t (&sx)[NT], uint32_t low)
-{
-    const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        uint32_t p[4], q[4], r[4];
-        decode8<kHigh>(aw[i], sa, low, p);
-        decode8<kHigh>(bw[i], sb, low, q);
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            const uint32_t xw[4] = {x[n].x, x[n].y, x[n].z, x[n].w};
-            decode8<kHigh>(xw[i], sx[n], low, r);
-            mma_bf16(acc[n], p[0], q[0], p[1], q[1], r[0], r[1]);
-            mma_bf16(acc[n], p[2], q[2], p[3], q[3], r[2], r[3]);
-        }
-    }
 }
 
 // The li-th expert with rows, found by every warp on its own: e < 0 if there are
@@ -124,100 +98,18 @@ __device__ __forceinline__ Found find_expert(const FewArgs &a, int li, int &rest
     return f;
 }
 
-// NT groups of eight rows: 1, 2 or 4 (bf16).
-template <bool kF4, int NT>
-__global__ void __launch_bounds__(kWarps * 32, kF4 && NT == 1 ? 4 : 3) k_few_rows(const FewArgs a)
+// Zeros for the rows of no expert, in the block's features.
+__device__ __forceinline__ void zero_rest_rows(const FewArgs &a, int n0, int front, int back)
 {
-    __shared__ float part[kWarps][NT * kRows][kFeatures];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int li = blockIdx.x / a.blocks, n0 = (blockIdx.x - li * a.blocks) * kFeatures;
-    dependents_may_launch();
-    wait_for_prior_grid();
-    int front, back;
-    bool bad;
-    const Found f = find_expert(a, li, front, back, bad);
-    if (bad && blockIdx.x == 0 && threadIdx.x == 0) set_status(a.status, BSL_ERR_INVALID_ARG);
-    if (a.zero_rest && li == 0) {  // rows of no expert: the first expert's blocks, each its features
-        const int n = n0 + threadIdx.x % kFeatures;
-        for (int r = threadIdx.x / kFeatures; r < a.T; r += kWarps * 32 / kFeatures)
-            if ((r < front || r >= back) && n < a.N) a.Y[static_cast<int64_t>(r) * a.N + n] = __float2bfloat16(0.f);
-    }
-    if (f.e < 0) return;
+    const int n = n0 + threadIdx.x % kFeatures;
+    for (int r = threadIdx.x / kFeatures; r < a.T; r += kWarps * 32 / kFeatures)
+        if ((r < front || r >= back) && n < a.N) a.Y[static_cast<int64_t>(r) * a.N + n] = __float2bfloat16(0.f);
+}
 
-    // this lane's rows: features n0 + g and n0 + g + 8 of the weight, rows g, g + 8, ... of X
-    constexpr int SPAN = kF4 ? 128 : 32;  // k of a step: 16 bytes a lane
-    const int64_t bytes = kF4 ? a.K / 2 : static_cast<int64_t>(a.K) * 2;
-    const int64_t wr = static_cast<int64_t>(f.e) * a.N + n0 + g;
-    const bool in0 = n0 + g < a.N, in1 = n0 + g + 8 < a.N;
-    const uint8_t *w0 = a.W + wr * bytes + 16 * t, *w1 = w0 + 8 * bytes;
-    const uint8_t *x = a.X + static_cast<int64_t>(f.first + g) * bytes + 16 * t;
-    const uint8_t *ws0 = kF4 ? a.w_scales + wr * (a.K / 32) + t : nullptr, *ws1 = kF4 ? ws0 + 8 * (a.K / 32) : nullptr;
-    const uint8_t *xs = kF4 ? a.x_scales + static_cast<int64_t>(f.first + g) * (a.K / 32) + t : nullptr;
-    const int steps = (a.K + SPAN - 1) / SPAN;
-    constexpr int U = kF4 ? (NT == 1 ? 2 : 1) : NT == 4 ? 2 : 4;
-    const int64_t scale_row = kF4 ? 8 * (a.K / 32) : 0;
-    float acc[NT][4] = {};
-    for (int s0 = warp; s0 < steps; s0 += kWarps * U) {
-        uint4 va[U], vb[U], vx[U][NT];
-        uint32_t sa[U], sb[U], sx[U][NT];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int s = s0 + u * kWarps;
-            const bool in = s * SPAN + t * (SPAN / 4) < a.K;
-            va[u] = vb[u] = make_uint4(0, 0, 0, 0);
-            sa[u] = sb[u] = 0;
-            if (in && in0) va[u] = load_stream(w0 + static_cast<int64_t>(s) * 64);
-            if (in && in1) vb[u] = load_stream(w1 + static_cast<int64_t>(s) * 64);
-            if constexpr (kF4) {
-                if (in && in0) sa[u] = __ldg(ws0 + 4 * s);
-                if (in && in1) sb[u] = __ldg(ws1 + 4 * s);
-            }
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                vx[u][n] = make_uint4(0, 0, 0, 0);
-                sx[u][n] = 0;
-                if (in && g + 8 * n < f.rows) {
-                    vx[u][n] = __ldg(reinterpret_cast<const uint4 *>(x + n * 8 * bytes + static_cast<int64_t>(s) * 64));
-                    if constexpr (kF4) sx[u][n] = __ldg(xs + n * scale_row + 4 * s);
-                }
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if constexpr (kF4) {
-                uint32_t top = max(sa[u], sb[u]);
-#pragma unroll
-                for (int n = 0; n < NT; ++n) top = max(top, sx[u][n]);
-                // (255 stands for NaN whatever it is multiplied with)
-                if (!__any_sync(0xffffffffu, top > 128)) {
-                    step4<false, NT>(acc, va[u], vb[u], vx[u], sa[u], sb[u], sx[u], 0);
-                } else {
-                    // scales of 2^126 and 2^127: both operands 2^-4 of themselves, the products 2^8 of that
-                    const bool far = __any_sync(0xffffffffu, top > 252);
-                    float sum[NT][4] = {};
-                    step4<true, NT>(sum, va[u], vb[u], vx[u], sa[u], sb[u], sx[u], far ? 4 : 0);
-#pragma unroll
-                    for (int n = 0; n < NT; ++n)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) acc[n][i] += far ? 256.f * sum[n][i] : sum[n][i];
-                }
-            } else {
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    mma_bf16(acc[n], va[u].x, vb[u].x, va[u].y, vb[u].y, vx[u][n].x, vx[u][n].y);
-                    mma_bf16(acc[n], va[u].z, vb[u].z, va[u].w, vb[u].w, vx[u][n].z, vx[u][n].w);
-                }
-            }
-        }
-    }
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        part[warp][8 * n + 2 * t][g] = acc[n][0];
-        part[warp][8 * n + 2 * t + 1][g] = acc[n][1];
-        part[warp][8 * n + 2 * t][g + 8] = acc[n][2];
-        part[warp][8 * n + 2 * t + 1][g + 8] = acc[n][3];
-    }
-    __syncthreads();
+// The warps' sums, in order, and the bias to the block's features of Y.
+template <int NT>
+__device__ __forceinline__ void add_parts(const FewArgs &a, const Found &f, int n0, const float (*part)[NT * kRows][kFeatures])
+{
     const int n = n0 + threadIdx.x % kFeatures;
     if (n >= a.N) return;
     for (int r = threadIdx.x / kFeatures; r < f.rows; r += kWarps * 32 / kFeatures) {
@@ -229,16 +121,261 @@ __global__ void __launch_bounds__(kWarps * 32, kF4 && NT == 1 ? 4 : 3) k_few_row
     }
 }
 
-template <bool kF4>
-bsl_status launch(FewArgs &a, cudaStream_t s)
+// ---------------------------------------------------------------- bf16
+
+// A lane reads 16 bytes of a weight row at a time, two or four steps at once, and
+// feeds them to the MMA as they lie.  NT groups of eight rows: 1, 2 or 4.
+template <int NT>
+__global__ void __launch_bounds__(kWarps * 32, 3) k_few_rows(const FewArgs a)
+{
+    __shared__ float part[kWarps][NT * kRows][kFeatures];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int li = blockIdx.x / a.blocks, n0 = (blockIdx.x - li * a.blocks) * kFeatures;
+    dependents_may_launch();
+    wait_for_prior_grid();
+    int front, back;
+    bool bad;
+    const Found f = find_expert(a, li, front, back, bad);
+    if (bad && blockIdx.x == 0 && threadIdx.x == 0) set_status(a.status, BSL_ERR_INVALID_ARG);
+    if (a.zero_rest && li == 0) zero_rest_rows(a, n0, front, back);
+    if (f.e < 0) return;
+
+    // this lane's rows: features n0 + g and n0 + g + 8 of the weight, rows g, g + 8, ... of X
+    constexpr int SPAN = 32;  // k of a step: 16 bytes a lane
+    const int64_t bytes = static_cast<int64_t>(a.K) * 2;
+    const int64_t wr = static_cast<int64_t>(f.e) * a.N + n0 + g;
+    const bool in0 = n0 + g < a.N, in1 = n0 + g + 8 < a.N;
+    const uint8_t *w0 = a.W + wr * bytes + 16 * t, *w1 = w0 + 8 * bytes;
+    const uint8_t *x = a.X + static_cast<int64_t>(f.first + g) * bytes + 16 * t;
+    const int steps = (a.K + SPAN - 1) / SPAN;
+    constexpr int U = NT == 4 ? 2 : 4;
+    float acc[NT][4] = {};
+    for (int s0 = warp; s0 < steps; s0 += kWarps * U) {
+        uint4 va[U], vb[U], vx[U][NT];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int s = s0 + u * kWarps;
+            const bool in = s * SPAN + t * (SPAN / 4) < a.K;
+            va[u] = vb[u] = make_uint4(0, 0, 0, 0);
+            if (in && in0) va[u] = load_stream(w0 + static_cast<int64_t>(s) * 64);
+            if (in && in1) vb[u] = load_stream(w1 + static_cast<int64_t>(s) * 64);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                vx[u][n] = make_uint4(0, 0, 0, 0);
+                if (in && g + 8 * n < f.rows)
+                    vx[u][n] = __ldg(reinterpret_cast<const uint4 *>(x + n * 8 * bytes + static_cast<int64_t>(s) * 64));
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                mma_bf16(acc[n], va[u].x, vb[u].x, va[u].y, vb[u].y, vx[u][n].x, vx[u][n].y);
+                mma_bf16(acc[n], va[u].z, vb[u].z, va[u].w, vb[u].w, vx[u][n].z, vx[u][n].w);
+            }
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) part[warp][8 * n + 2 * t + (i & 1)][g + 8 * (i >> 1)] = acc[n][i];
+    __syncthreads();
+    add_parts<NT>(a, f, n0, part);
+}
+
+// ---------------------------------------------------------------- 4 bits
+
+__device__ __forceinline__ void copy16(uint8_t *dst, const uint8_t *src, bool exists)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(exists ? 16 : 0)
+                 : "memory");
+}
+
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+
+template <int N>
+__device__ __forceinline__ void copies_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Eight codes to four registers of two f16, 2^-14 of their values: the bits
+// s e e m at the sign and the lowest exponent and highest mantissa bits of the
+// upper byte, zero and 0.5 (which f16 has as a subnormal number) included; the
+// lower byte is zero.
+__device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t (&v)[4])
+{
+    const uint32_t even = (w << 4 & 0x80808080u) | (w << 1 & 0x0E0E0E0Eu);
+    const uint32_t odd = (w & 0x80808080u) | (w >> 3 & 0x0E0E0E0Eu);
+    v[0] = even & 0xFF00FF00u;
+    v[1] = __byte_perm(even, 0, 0x2404);
+    v[2] = odd & 0xFF00FF00u;
+    v[3] = __byte_perm(odd, 0, 0x2404);
+}
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1, const float (&d)[4])
+{
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%10, %11, %12, %13};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(d[0]), "f"(d[1]), "f"(d[2]), "f"(d[3]));
+}
+
+// 2^h, -127 <= h <= 127.
+__device__ __forceinline__ float power_of_2(int h) { return __uint_as_float(h > -127 ? (h + 127) << 23 : 0x400000); }
+
+// A block's sum p (2^-28 of it) under scale bytes a and b, whatever they are.
+__device__ __forceinline__ float scaled(float p, int a, int b)
+{
+    if (a == 255 || b == 255) return __uint_as_float(0x7FC00000u);
+    const int e = a + b - 254, h = e >> 1;
+    return 268435456.f * p * power_of_2(h) * power_of_2(e - h);
+}
+
+// The 32 elements of one block are an MMA's k, so its scales come in by one
+// product per result, and the codes stand for themselves.  A warp's steps of
+// 128 k (64 bytes of a row) come through a ring in shared memory, which also
+// brings the words of a block to the lanes that hold its k.  Instructions bound
+// it, 11 for eight codes and as many again for scales, loops and addresses:
+// 4096 x 4096 takes 9.3 us for one row (with a bf16 product for each pair of codes to
+// bring the scale in, straight from registers: 10.8), 11008 x 4096 14.2 (15.8).
+// Three or four steps in flight cost blocks an SM and are no faster (9.4, 9.7),
+// 32 features a block 13.3, e4m3 operands (one word for four codes) 9.7.
+template <int NT>
+struct Few4 {
+    static constexpr int ST = 2;                          // steps in flight, a warp
+    static constexpr int ROWS = kFeatures + kRows * NT;
+    static constexpr int STEP = ROWS * 64;
+    static constexpr int SMEM = kWarps * ST * STEP;
+    static_assert(kWarps * NT * kRows * kFeatures * 4 <= SMEM, "the warps' sums take the ring's place");
+};
+
+template <int NT>
+__global__ void __launch_bounds__(kWarps * 32) k_few_rows4(const FewArgs a)
+{
+    using C = Few4<NT>;
+    constexpr int ST = C::ST;
+    extern __shared__ __align__(16) uint8_t smem[];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int li = blockIdx.x / a.blocks, n0 = (blockIdx.x - li * a.blocks) * kFeatures;
+    dependents_may_launch();
+    wait_for_prior_grid();
+    int front, back;
+    bool bad;
+    const Found f = find_expert(a, li, front, back, bad);
+    if (bad && blockIdx.x == 0 && threadIdx.x == 0) set_status(a.status, BSL_ERR_INVALID_ARG);
+    if (a.zero_rest && li == 0) zero_rest_rows(a, n0, front, back);
+    if (f.e < 0) return;
+
+    const int blocks = a.K / 32, count = (blocks + 3) / 4, mine = (count - warp + kWarps - 1) / kWarps;
+    const int64_t bytes = a.K / 2, wr = static_cast<int64_t>(f.e) * a.N + n0;
+    uint8_t *ring = smem + warp * ST * C::STEP;
+    // a lane copies chunk t (block t) of rows g, g + 8, ..., of the weight and then of X, and reads their scales
+    const uint8_t *w = a.W + (wr + g) * bytes + 16 * t, *x = a.X + static_cast<int64_t>(f.first + g) * bytes + 16 * t;
+    const uint8_t *ws = a.w_scales + (wr + g) * blocks + t, *xs = a.x_scales + static_cast<int64_t>(f.first + g) * blocks + t;
+    // chunks of a row trade places by its number, so that eight rows' words of one chunk lie in different banks
+    const int put = g * 64 + ((t + (g >> 1)) & 3) * 16;
+    int sw[ST][2], sx[ST][NT];
+    auto issue = [&](int j, int slot, int (&vw)[2], int (&vx)[NT]) {
+        if (j < mine) {
+            const int s = warp + j * kWarps;
+            const bool in = 4 * s + t < blocks;
+            uint8_t *dst = ring + slot * C::STEP + put;
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                const bool exists = in && n0 + g + 8 * m < a.N;
+                copy16(dst + m * 512, exists ? w + m * 8 * bytes + static_cast<int64_t>(s) * 64 : a.W, exists);
+                vw[m] = 127;  // (zeros under a scale of one)
+                if (exists) vw[m] = __ldg(ws + m * 8 * static_cast<int64_t>(blocks) + 4 * s);
+            }
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const bool exists = in && g + 8 * n < f.rows;
+                copy16(dst + (2 + n) * 512, exists ? x + n * 8 * bytes + static_cast<int64_t>(s) * 64 : a.X, exists);
+                vx[n] = 127;
+                if (exists) vx[n] = __ldg(xs + n * 8 * static_cast<int64_t>(blocks) + 4 * s);
+            }
+        }
+        copies_commit();
+    };
+#pragma unroll
+    for (int u = 0; u < ST; ++u) issue(u, u, sw[u], sx[u]);
+    float acc[NT][4] = {};
+    for (int j0 = 0; j0 < mine; j0 += ST) {
+#pragma unroll
+        for (int u = 0; u < ST; ++u) {
+            if (j0 + u >= mine) break;
+            copies_wait<ST - 1>();
+            __syncwarp();
+            const uint8_t *src = ring + u * C::STEP + g * 64 + 4 * t;
+            // scales whose products, 2^28 and all, are normal numbers: one product a result
+            bool in_range = true;
+#pragma unroll
+            for (int m = 0; m < 2; ++m) in_range &= static_cast<uint32_t>(sw[u][m] - 50) <= 126u;
+#pragma unroll
+            for (int n = 0; n < NT; ++n) in_range &= static_cast<uint32_t>(sx[u][n] - 50) <= 126u;
+            const bool plain = __all_sync(0xffffffffu, in_range);
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                const int chunk = ((b + (g >> 1)) & 3) * 16;
+                uint32_t r[NT][4];
+                int fx[NT][2];
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    codes_to_f16(*reinterpret_cast<const uint32_t *>(src + chunk + (2 + n) * 512), r[n]);
+                    fx[n][0] = __shfl_sync(0xffffffffu, sx[u][n] << 23, 8 * t + b);
+                    fx[n][1] = __shfl_sync(0xffffffffu, sx[u][n] << 23, 8 * t + 4 + b);
+                }
+                uint32_t p[4], q[4];
+                codes_to_f16(*reinterpret_cast<const uint32_t *>(src + chunk), p);
+                codes_to_f16(*reinterpret_cast<const uint32_t *>(src + chunk + 512), q);
+                const int fw0 = __shfl_sync(0xffffffffu, sw[u][0] << 23, b, 4);
+                const int fw1 = __shfl_sync(0xffffffffu, sw[u][1] << 23, b, 4);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    const float zero[4] = {};
+                    float c[4];
+                    mma_f16(c, p[0], q[0], p[1], q[1], r[n][0], r[n][1], zero);
+                    mma_f16(c, p[2], q[2], p[3], q[3], r[n][2], r[n][3], c);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int s0 = i < 2 ? fw0 : fw1, s1 = fx[n][i & 1];
+                        if (plain)
+                            acc[n][i] += c[i] * __uint_as_float(static_cast<uint32_t>(s0) + static_cast<uint32_t>(s1) - (99u << 23));
+                        else
+                            acc[n][i] += scaled(c[i], s0 >> 23, s1 >> 23);
+                    }
+                }
+            }
+            __syncwarp();
+            issue(j0 + u + ST, u, sw[u], sx[u]);
+        }
+    }
+    copies_wait<0>();
+    __syncthreads();
+    auto part = reinterpret_cast<float(*)[NT * kRows][kFeatures]>(smem);
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) part[warp][8 * n + 2 * t + (i & 1)][g + 8 * (i >> 1)] = acc[n][i];
+    __syncthreads();
+    add_parts<NT>(a, f, n0, part);
+}
+
+bsl_status launch(void (*kern)(const FewArgs), FewArgs &a, int smem, cudaStream_t s)
 {
     a.blocks = (a.N + kFeatures - 1) / kFeatures;
     const int64_t grid = static_cast<int64_t>(a.blocks) * (a.T < a.E ? a.T : a.E);
     if (grid > 0x7FFFFFFF) return BSL_ERR_UNSUPPORTED;
-    const unsigned g = static_cast<unsigned>(grid);
-    if (a.T <= kRows) return cuda_status(launch_dependent(k_few_rows<kF4, 1>, g, kWarps * 32, 0, s, a));
-    if (kF4 || a.T <= 2 * kRows) return cuda_status(launch_dependent(k_few_rows<kF4, 2>, g, kWarps * 32, 0, s, a));
-    return cuda_status(launch_dependent(k_few_rows<false, 4>, g, kWarps * 32, 0, s, a));
+    return cuda_status(launch_dependent(kern, static_cast<unsigned>(grid), kWarps * 32, smem, s, a));
+}
+
+template <int NT>
+bsl_status launch4(FewArgs &a, cudaStream_t s)
+{
+    static_assert(Few4<NT>::SMEM <= 48 * 1024, "no attribute needed");
+    return launch(k_few_rows4<NT>, a, Few4<NT>::SMEM, s);
 }
 
 }  // namespace
@@ -254,12 +391,12 @@ bool few_rows(int32_t T, const bsl_grouped *W)
     return T <= kRows || (T <= 2 * kRows && bytes <= (32ll << 20)) || (T <= 4 * kRows && bytes <= 20000000);
 }
 
-// 4 bits: turning codes into numbers bounds it (8 rows: 4.2 MB of codes 6.7 / 8.8, 8.4 MB 11.9 / 8.2, 22 MB
-// 16.4 / 13.4; 16 rows: 0.3 MB 7.1 / 11.3, 4.2 MB 7.5 / 8.7, 8.4 MB 10.9 / 8.2).
+// 4 bits, products alone: 8 rows on 0.5 MB of codes 3.1 / 6.3, 8.4 MB 9.4 / 11.7, 22 MB 15.0 / 13.0; 16 rows on
+// 0.5 MB 4.0 / 6.4, 4.2 MB 7.4 / 8.7, 8.4 MB 11.8 / 11.7.
 bool few_rows4(int32_t T, const bsl_mx4 *W)
 {
     const int64_t bytes = static_cast<int64_t>(T < W->E ? T : W->E) * W->N * (W->K / 2);
-    return T <= 2 * kRows && bytes <= (4ll << 20);
+    return (T <= kRows && bytes <= (12ll << 20)) || (T <= 2 * kRows && bytes <= (4ll << 20));
 }
 
 bsl_status launch_few_rows(const void *X, int32_t T, const int32_t *offsets, const bsl_grouped *W, const void *bias,
@@ -268,7 +405,7 @@ bsl_status launch_few_rows(const void *X, int32_t T, const int32_t *offsets, con
     FewArgs a = {static_cast<const uint8_t *>(W->weight), nullptr, static_cast<const uint8_t *>(X), nullptr,
                  static_cast<const __nv_bfloat16 *>(bias), static_cast<__nv_bfloat16 *>(Y), offsets, W->status,
                  T, W->E, W->N, W->K, 0, zero_rest};
-    return launch<false>(a, s);
+    return launch(T <= kRows ? k_few_rows<1> : T <= 2 * kRows ? k_few_rows<2> : k_few_rows<4>, a, 0, s);
 }
 
 bsl_status launch_few_rows4(const uint8_t *xc, const uint8_t *xs, int32_t T, const int32_t *offsets, const bsl_mx4 *W,
@@ -276,7 +413,7 @@ bsl_status launch_few_rows4(const uint8_t *xc, const uint8_t *xs, int32_t T, con
 {
     FewArgs a = {W->codes, W->scales, xc, xs, static_cast<const __nv_bfloat16 *>(bias), static_cast<__nv_bfloat16 *>(Y),
                  offsets, W->status, T, W->E, W->N, W->K, 0, zero_rest};
-    return launch<true>(a, s);
+    return T <= kRows ? launch4<1>(a, s) : launch4<2>(a, s);
 }
 
 }  // namespace bsl

@@ -16,7 +16,6 @@
 // loads in flight, a block's width apart.
 #include "common.cuh"
 #include "internal.h"
-#include "mx4.cuh"
 
 namespace bsl {
 namespace {
@@ -37,6 +36,31 @@ __device__ __forceinline__ uint32_t to_e2m1x2(float lo, float hi)
         : "=r"(r)
         : "f"(lo), "f"(hi));
     return r;
+}
+
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// Eight codes to four registers of two bf16: code j and code j + 4.  A code's
+// bits s e e m, put at the sign, the lowest exponent bits and the highest
+// mantissa bit of a bf16, are 2^-126 of its value, zero and 0.5 included, and
+// one product brings 2^126 and the block's scale in.  Exact: two significant
+// bits times a power of two.  The factor 2^126 x 2^(scale - 127) is past the
+// bf16 range from scale byte 129 on: there two products bring it in.
+__device__ __forceinline__ void decode8(uint32_t w, uint32_t scale, uint32_t (&v)[4])
+{
+    const uint32_t s1 = scale == 255 ? 0x7FC0u : scale > 128 ? 0x7F00u : scale ? (scale + 126u) << 7 : 0x3F00u;
+    const uint32_t s2 = (scale > 128 && scale < 255 ? scale - 1u : 127u) << 7;
+    v[0] = (w << 12 & 0x80008000u) | (w << 6 & 0x01C001C0u);
+    v[1] = (w << 8 & 0x80008000u) | (w << 2 & 0x01C001C0u);
+    v[2] = (w << 4 & 0x80008000u) | (w >> 2 & 0x01C001C0u);
+    v[3] = (w & 0x80008000u) | (w >> 6 & 0x01C001C0u);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = mul_bf16x2(mul_bf16x2(v[i], s1 | s1 << 16), s2 | s2 << 16);
 }
 
 // Chunk i covers elements 8i .. 8i+7; n is the number of chunks, a multiple of 4.
@@ -95,7 +119,7 @@ __global__ void __launch_bounds__(kThreads)
     for (int u = 0; u < kChunks; ++u) {
         const int64_t i = i0 + u * kThreads;
         uint32_t v[4];  // codes j and j + 4
-        decode8<true>(c[u], b[u], 0, v);
+        decode8(c[u], b[u], v);
         if (i < n)
             X[i] = make_uint4(__byte_perm(v[0], v[1], 0x5410), __byte_perm(v[2], v[3], 0x5410),
                               __byte_perm(v[0], v[1], 0x7632), __byte_perm(v[2], v[3], 0x7632));

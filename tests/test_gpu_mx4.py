@@ -405,3 +405,23 @@ def test_out_that_overlaps_an_input_is_refused():
                  lambda: sg.forward_mx4(sg.Mx4Tensor(q.codes[:2], q.scales[:2]), w, out=inside)):
         with pytest.raises(ValueError, match="overlap"):
             call()
+
+
+@pytest.mark.parametrize("K", [256, 768, 11008, 128, 640, 1152, 64, 320, 32, 96, 1440, 2848])
+@pytest.mark.parametrize("M", [3, 11, 37, 301])
+def test_scale_rows_of_every_length(M, K):
+    """Rows of scales in units of 16, 8, 4, 2 and 1 bytes: the bytes of the next row, NaN there, reach
+    nobody, and the last row's end with the array."""
+    rng = np.random.default_rng(M + K)
+    N = 264
+    Wq, _ = weights(rng, N, K)
+    Xq = sg.quantize_mx4(rows_of(rng, M, K))
+    Wq.scales[5] = 255
+    Xq.scales[1] = 255
+    Xf, Wf = experts.mx4_values(*host(Xq)), experts.mx4_values(*host(Wq))
+    Y = sg.forward_mx4(Xq, Wq)
+    rows, cols = [r for r in range(M) if r != 1], [n for n in range(N) if n != 5]
+    assert torch.isnan(Y[1].float()).all() and torch.isnan(Y[:, 5].float()).all()
+    Xk, Wk = Xf[rows], Wf[cols]
+    check(Y[rows][:, cols], Xk @ Wk.T, np.abs(Xk) @ np.abs(Wk).T, K, "other rows and features")
+    assert sg.mx4_status(Wq) == 0
