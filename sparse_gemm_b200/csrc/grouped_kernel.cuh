@@ -97,7 +97,8 @@ struct Cfg {
 
 struct Maps {
     CUtensorMap a[2];  // A: two strips a copy, one strip (128 rows of K, or of features, each)
-    CUtensorMap b[9];  // K-major B: b[i] two strips of 16 (i + 1) rows, b[8] one of 16 rows
+    CUtensorMap b[8];  // K-major B: b[i] two strips of 16 (i + 1) rows
+    CUtensorMap t[8];  // ... t[i] one strip, where k ends inside one
     CUtensorMap out;
 };
 
@@ -525,7 +526,7 @@ __global__ void __launch_bounds__(Cfg<kMode>::THREADS, 1)
             int g = 0;  // stages issued
             Place at_ring;
             int mapped = -1;
-            const CUtensorMap *one = is_a ? &maps.a[1] : &maps.b[8], *two = &maps.a[0];  // one, two strips a copy
+            const CUtensorMap *one = &maps.a[1], *two = &maps.a[0];  // one, two strips a copy
             Tile x, next;
             if (first < count) next = tiles.at(first);
             for (int t = first; ok && t < count; t += stride) {
@@ -547,7 +548,10 @@ __global__ void __launch_bounds__(Cfg<kMode>::THREADS, 1)
                 // M- and N-major strips are whole along the features, K-major ones along k
                 const int wide = is_a ? args.cols : args.rows;
                 const bool aligned = mn && strips == 2 && at % 64 == 0 && (wide % 64 == 0 || at + 128 <= wide);
-                if (!is_a && !C::BN) two = &maps.b[half / 16 - 1];  // exactly the tile's rows
+                if (!is_a && !C::BN) {  // exactly the tile's rows
+                    two = &maps.b[half / 16 - 1];
+                    one = &maps.t[half / 16 - 1];
+                }
                 for (int k = 0; k < x.kb; ++k, ++g, at_ring.next(S)) {
                     const int slot = at_ring.slot;
                     if (g >= S && !mbar_wait(&empty[slot], at_ring.parity ^ 1, tmo, abort_flag)) {
@@ -567,8 +571,7 @@ __global__ void __launch_bounds__(Cfg<kMode>::THREADS, 1)
                         tma_load_4d_pair(dst, two, bar, 0, at, k * 2, plane);
                     } else {  // the last stage of a k that ends inside a strip
                         for (int i = 0; i < 2; ++i)
-                            for (int r = 0; r < rows; r += is_a ? 128 : 16)
-                                tma_load_3d_pair(dst + (i * rows + r) * 128, one, bar, k * 128 + 64 * i, at + r, plane);
+                            tma_load_3d_pair(dst + i * rows * 128, one, bar, k * 128 + 64 * i, at, plane);
                     }
                 }
             }
@@ -792,9 +795,11 @@ inline bool row_maps(Maps &m, const void *weight, int64_t E, int64_t N, int64_t 
 {
     bool good = make_strip_map(&m.a[0], weight, K, N, E, 128, 2) &&
                 make_map_3d(&m.a[1], weight, K, N, E, K * 2, K * 2 * N, 64, 128, 128) &&
-                map_rows(&m.b[8], A, depth, T, 64, 16, 128) && map_rows(&m.out, out, cols, T, 32, 32, 0);
+                map_rows(&m.out, out, cols, T, 32, 32, 0);
     // (a tile has no more than T rows, rounded up to 32)
-    for (int i = 0; i < 8 && 32 * i < T; ++i) good = good && make_strip_map(&m.b[i], A, depth, T, 1, 16 * (i + 1), 2);
+    for (int i = 0; i < 8 && 32 * i < T; ++i)
+        good = good && make_strip_map(&m.b[i], A, depth, T, 1, 16 * (i + 1), 2) &&
+               (depth % 64 == 0 || map_rows(&m.t[i], A, depth, T, 64, 16 * (i + 1), 128));
     return good;
 }
 
