@@ -782,7 +782,10 @@ class GroupedLinearFunction(torch.autograd.Function):
 class GroupedLinear(torch.nn.Module):
     """One linear layer per expert over rows sorted by expert, bf16 on an sm_100 GPU.  Parameters:
     ``weight`` [E, out_features, in_features] and ``bias`` [E, out_features] or None.  The input's
-    leading dimensions are the rows; ``offsets`` as in :func:`grouped_forward`."""
+    leading dimensions are the rows; ``offsets`` as in :func:`grouped_forward`.
+
+    A backward pass may be captured into a CUDA graph once no eager graph over the same leaves is
+    alive (torch accumulates a leaf's gradient on the stream of the first graph that holds it)."""
 
     def __init__(self, weight: torch.Tensor, bias: torch.Tensor | None = None):
         super().__init__()
