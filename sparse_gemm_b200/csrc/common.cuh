@@ -45,6 +45,43 @@ __device__ __forceinline__ void wait_for_prior_grid()
     asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
+// Loads of what the kernel before may have written (inputs, scales, offsets, and
+// weights too, which a call may just have made): ordinary loads behind
+// wait_for_prior_grid.  Not the read-only path (ld.global.nc, __ldg, or const
+// __restrict__ kernel arguments, which let the compiler take it): that is for
+// data that nobody writes while this kernel is resident, and a dependent is
+// resident before its producers end.
+template <typename V>
+__device__ __forceinline__ V load_global(const V *p)
+{
+    static_assert(sizeof(V) == 16 || sizeof(V) == 8 || sizeof(V) == 4 || sizeof(V) == 1, "width");
+    V v;
+    if constexpr (sizeof(V) == 16)
+        asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                     : "l"(__cvta_generic_to_global(p)));
+    else if constexpr (sizeof(V) == 8)
+        asm volatile("ld.global.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(__cvta_generic_to_global(p)));
+    else if constexpr (sizeof(V) == 4)
+        asm volatile("ld.global.u32 %0, [%1];" : "=r"(v) : "l"(__cvta_generic_to_global(p)));
+    else {
+        uint32_t w;
+        asm volatile("ld.global.u8 %0, [%1];" : "=r"(w) : "l"(__cvta_generic_to_global(p)));
+        v = static_cast<V>(w);
+    }
+    return v;
+}
+
+// The same for data that is read once: 16 bytes that take no room in L1.
+__device__ __forceinline__ uint4 load_stream(const void *p)
+{
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(__cvta_generic_to_global(p)));
+    return v;
+}
+
 // ---------------------------------------------------------------- smem / mbarrier
 
 __device__ __forceinline__ uint32_t smem_u32(const void *p)

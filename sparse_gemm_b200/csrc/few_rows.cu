@@ -29,15 +29,6 @@ struct FewArgs {
     int32_t zero_rest;
 };
 
-__device__ __forceinline__ uint4 load_stream(const void *p)
-{
-    uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
-    return v;
-}
-
 __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1)
 {
@@ -66,13 +57,13 @@ __device__ __forceinline__ Found find_expert(const FewArgs &a, int li, int &rest
     }
     const int lane = threadIdx.x & 31;
     auto clamp = [&](int v) { return v < 0 ? 0 : v > a.T ? a.T : v; };
-    const int raw0 = a.offsets[0];
+    const int raw0 = load_global(a.offsets);
     int carry = clamp(raw0), seen = 0;
     bad = carry != raw0;
     rest_front = carry;
     for (int i0 = 0; i0 < a.E; i0 += 32) {
         const int i = i0 + lane;
-        const int raw = i < a.E ? a.offsets[i + 1] : 0;
+        const int raw = i < a.E ? load_global(a.offsets + i + 1) : 0;
         int v = clamp(raw);
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -163,7 +154,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) k_few_rows(const FewArgs a)
             for (int n = 0; n < NT; ++n) {
                 vx[u][n] = make_uint4(0, 0, 0, 0);
                 if (in && g + 8 * n < f.rows)
-                    vx[u][n] = __ldg(reinterpret_cast<const uint4 *>(x + n * 8 * bytes + static_cast<int64_t>(s) * 64));
+                    vx[u][n] = load_global(reinterpret_cast<const uint4 *>(x + n * 8 * bytes + static_cast<int64_t>(s) * 64));
             }
         }
 #pragma unroll
@@ -287,14 +278,14 @@ __global__ void __launch_bounds__(kWarps * 32) k_few_rows4(const FewArgs a)
                 const bool exists = in && n0 + g + 8 * m < a.N;
                 copy16(dst + m * 512, exists ? w + m * 8 * bytes + static_cast<int64_t>(s) * 64 : a.W, exists);
                 vw[m] = 127;  // (zeros under a scale of one)
-                if (exists) vw[m] = __ldg(ws + m * 8 * static_cast<int64_t>(blocks) + 4 * s);
+                if (exists) vw[m] = load_global(ws + m * 8 * static_cast<int64_t>(blocks) + 4 * s);
             }
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 const bool exists = in && g + 8 * n < f.rows;
                 copy16(dst + (2 + n) * 512, exists ? x + n * 8 * bytes + static_cast<int64_t>(s) * 64 : a.X, exists);
                 vx[n] = 127;
-                if (exists) vx[n] = __ldg(xs + n * 8 * static_cast<int64_t>(blocks) + 4 * s);
+                if (exists) vx[n] = load_global(xs + n * 8 * static_cast<int64_t>(blocks) + 4 * s);
             }
         }
         copies_commit();

@@ -14,7 +14,7 @@ constexpr int kMaxExperts = BSL_GROUPED_MAX_EXPERTS;
 // all rows.
 __device__ __forceinline__ void fetch_offsets(const int32_t *offsets, int32_t E, int32_t T, int32_t *off)
 {
-    for (int i = threadIdx.x; i <= E; i += blockDim.x) off[i] = offsets ? offsets[i] : i ? T : 0;
+    for (int i = threadIdx.x; i <= E; i += blockDim.x) off[i] = offsets ? load_global(offsets + i) : i ? T : 0;
 }
 
 // Make them safe, by one warp: every entry is clamped to [previous entry, T],

@@ -35,8 +35,8 @@ __device__ __forceinline__ void add8(float (&acc)[8], const uint4 &v)
 }
 
 __global__ void __launch_bounds__(kWarps * 32)
-    k_grouped_bias_grad(const uint4 *__restrict__ dY, int32_t T, const int32_t *__restrict__ offsets, int32_t E,
-                        int32_t N, int32_t S, __nv_bfloat16 *__restrict__ db)
+    k_grouped_bias_grad(const uint4 *dY, int32_t T, const int32_t *offsets, int32_t E, int32_t N, int32_t S,
+                        __nv_bfloat16 *db)
 {
     __shared__ int32_t off[kMaxExperts + 1];
     __shared__ float part[kWarps][kCols];
@@ -62,11 +62,11 @@ __global__ void __launch_bounds__(kWarps * 32)
         for (; m + (kLoads - 1) * kWarps < end; m += kLoads * kWarps) {
             uint4 v[kLoads];
 #pragma unroll
-            for (int u = 0; u < kLoads; ++u) v[u] = __ldg(base + static_cast<int64_t>(m + u * kWarps) * stride);
+            for (int u = 0; u < kLoads; ++u) v[u] = load_global(base + static_cast<int64_t>(m + u * kWarps) * stride);
 #pragma unroll
             for (int u = 0; u < kLoads; ++u) add8(acc, v[u]);
         }
-        for (; m < end; m += kWarps) add8(acc, __ldg(base + static_cast<int64_t>(m) * stride));
+        for (; m < end; m += kWarps) add8(acc, load_global(base + static_cast<int64_t>(m) * stride));
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) part[warp][i * 32 + lane] = acc[i];  // column 8 * lane + i

@@ -192,15 +192,15 @@ __device__ __forceinline__ void load_words(const uint8_t *base, int32_t stride, 
         const bool in = exists && byte0 + 4 * i < stride;
         if constexpr (V == 4) {
             uint4 v = make_uint4(0, 0, 0, 0);
-            if (in) v = __ldg(reinterpret_cast<const uint4 *>(at + 4 * i));
+            if (in) v = load_global(reinterpret_cast<const uint4 *>(at + 4 * i));
             w[i] = v.x, w[i + 1] = v.y, w[i + 2] = v.z, w[i + 3] = v.w;
         } else if constexpr (V == 2) {
             uint2 v = make_uint2(0, 0);
-            if (in) v = __ldg(reinterpret_cast<const uint2 *>(at + 4 * i));
+            if (in) v = load_global(reinterpret_cast<const uint2 *>(at + 4 * i));
             w[i] = v.x, w[i + 1] = v.y;
         } else {
             w[i] = 0;
-            if (in) w[i] = __ldg(reinterpret_cast<const uint32_t *>(at + 4 * i));
+            if (in) w[i] = load_global(reinterpret_cast<const uint32_t *>(at + 4 * i));
         }
     }
 }
@@ -220,7 +220,7 @@ __device__ __forceinline__ void load_words_any(const uint8_t *base, int64_t tota
 #pragma unroll
     for (int i = 0; i <= W; ++i) {
         w[i] = 0;
-        if (4 * i < left && 4 * i + 4 <= whole) w[i] = __ldg(reinterpret_cast<const uint32_t *>(p + 4 * i));
+        if (4 * i < left && 4 * i + 4 <= whole) w[i] = load_global(reinterpret_cast<const uint32_t *>(p + 4 * i));
     }
     if (end) {
 #pragma unroll

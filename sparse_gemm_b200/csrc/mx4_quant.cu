@@ -65,7 +65,7 @@ __device__ __forceinline__ void decode8(uint32_t w, uint32_t scale, uint32_t (&v
 
 // Chunk i covers elements 8i .. 8i+7; n is the number of chunks, a multiple of 4.
 __global__ void __launch_bounds__(kThreads)
-    k_mx4_quantize(const uint4 *__restrict__ X, int64_t n, uint32_t *__restrict__ codes, uint8_t *__restrict__ scales)
+    k_mx4_quantize(const uint4 *X, int64_t n, uint32_t *codes, uint8_t *scales)
 {
     const int64_t i0 = static_cast<int64_t>(blockIdx.x) * kThreads * kChunks + threadIdx.x;
     dependents_may_launch();
@@ -74,7 +74,7 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
     for (int u = 0; u < kChunks; ++u) {
         const int64_t i = i0 + u * kThreads;
-        x[u] = i < n ? X[i] : make_uint4(0, 0, 0, 0);  // a block's four lanes are in or out together
+        x[u] = i < n ? load_global(X + i) : make_uint4(0, 0, 0, 0);  // a block's four lanes are in or out together
     }
 #pragma unroll
     for (int u = 0; u < kChunks; ++u) {
@@ -102,8 +102,7 @@ __global__ void __launch_bounds__(kThreads)
 }
 
 __global__ void __launch_bounds__(kThreads)
-    k_mx4_dequantize(const uint32_t *__restrict__ codes, const uint8_t *__restrict__ scales, int64_t n,
-                     uint4 *__restrict__ X)
+    k_mx4_dequantize(const uint32_t *codes, const uint8_t *scales, int64_t n, uint4 *X)
 {
     const int64_t i0 = static_cast<int64_t>(blockIdx.x) * kThreads * kChunks + threadIdx.x;
     dependents_may_launch();
@@ -112,8 +111,8 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
     for (int u = 0; u < kChunks; ++u) {
         const int64_t i = i0 + u * kThreads;
-        c[u] = i < n ? codes[i] : 0;
-        b[u] = i < n ? scales[i >> 2] : 0;
+        c[u] = i < n ? load_global(codes + i) : 0;
+        b[u] = i < n ? load_global(scales + (i >> 2)) : 0;
     }
 #pragma unroll
     for (int u = 0; u < kChunks; ++u) {

@@ -1,0 +1,29 @@
+"""Source check of the expert and 4-bit kernels.  Each is resident before the
+kernel that writes its inputs has ended, so nothing it reads is read-only for
+as long as it lives, and none may take the read-only load path."""
+import glob
+import os
+import re
+
+import pytest
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "sparse_gemm_b200", "csrc")
+FILES = sorted(os.path.basename(p) for pattern in ("few_rows*", "grouped*", "mx4_*")
+               for p in glob.glob(os.path.join(CSRC, pattern)))
+
+
+def code_of(name):
+    text = open(os.path.join(CSRC, name)).read()
+    return re.sub(r"//[^\n]*", "", re.sub(r"/\*.*?\*/", "", text, flags=re.S))
+
+
+def test_the_kernels_are_looked_at():
+    assert {"few_rows.cu", "grouped.cu", "grouped.cuh", "grouped_kernel.cuh", "grouped_bias.cu", "mx4_quant.cu"} <= set(FILES)
+    assert all("wait_for_prior_grid()" in code_of(f) for f in ("few_rows.cu", "grouped_kernel.cuh", "grouped_bias.cu",
+                                                               "mx4_quant.cu", "grouped.cu"))
+
+
+@pytest.mark.parametrize("name", FILES)
+def test_no_read_only_loads_in_dependent_kernels(name):
+    found = re.findall(r"__ldg\w*\s*\(|ld\.global\.nc[\w.:]*|__restrict__", code_of(name))
+    assert not found, (name, found)
