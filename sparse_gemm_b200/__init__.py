@@ -985,18 +985,58 @@ def mx4_status(Wq: Mx4Tensor) -> int:
 
 class Mx4Linear(torch.nn.Module):
     """Inference ``nn.Linear`` with weight and activations in 4 bits.  Built with :meth:`from_dense`;
-    inputs may have any leading dimensions."""
+    inputs may have any leading dimensions.  The weight is part of the module's state, as the uint8
+    buffers ``codes`` and ``scales`` (those of the tensor it was made of, not copies); ``weight4`` is
+    the handle on them.  The products add the bias in bf16, whatever type the module was cast to."""
 
     def __init__(self, weight4: Mx4Tensor, bias: torch.Tensor | None = None):
         super().__init__()
-        weight4.status
-        self.weight4 = weight4
-        self.in_features, self.out_features = weight4.K, weight4.shape[-2]
         if bias is not None:
             if tuple(bias.shape) != weight4.shape[:-1]:
                 raise ValueError(f"bias must have shape {weight4.shape[:-1]}")
             bias = bias.detach().to(device=weight4.device, dtype=torch.bfloat16).contiguous()
+        self.register_buffer("codes", None)
+        self.register_buffer("scales", None)
         self.register_buffer("bias", bias)
+        self.weight4 = weight4
+
+    @property
+    def weight4(self) -> Mx4Tensor:
+        """The weight's handle, made anew when a buffer's storage was replaced."""
+        if not self._handle_is_current():
+            self._weight4 = Mx4Tensor(self.codes, self.scales)
+        return self._weight4
+
+    @weight4.setter
+    def weight4(self, weight4: Mx4Tensor):
+        weight4.status
+        self.codes, self.scales, self._weight4 = weight4.codes, weight4.scales, weight4
+        self.in_features, self.out_features = weight4.K, weight4.shape[-2]
+
+    def _handle_is_current(self) -> bool:
+        w, codes, scales = self._weight4, self._buffers["codes"], self._buffers["scales"]
+        return (w is not None and w._codes_ptr == codes.data_ptr() and w._scales_ptr == scales.data_ptr()
+                and w.codes.shape == codes.shape and codes.is_contiguous() and scales.is_contiguous())
+
+    def _apply(self, fn, recurse=True):
+        super()._apply(fn, recurse)
+        if not self._handle_is_current():   # it would hold the memory that the module just left
+            self._weight4 = None
+        return self
+
+    def __getstate__(self):
+        return {**self.__dict__, "_weight4": None}   # made anew by the copy
+
+    def __setstate__(self, state):
+        super().__setstate__(state)
+        weight4 = self.__dict__.pop("weight4", None)   # pickled when the weight was a plain attribute
+        if weight4 is not None:
+            self._buffers.update(codes=None, scales=None)
+            self.weight4 = weight4
+
+    def _bias(self):
+        b = self._buffers["bias"]
+        return b if b is None or b.dtype is torch.bfloat16 else b.to(torch.bfloat16)
 
     @classmethod
     def from_dense(cls, weight: torch.Tensor, bias: torch.Tensor | None = None):
@@ -1009,7 +1049,7 @@ class Mx4Linear(torch.nn.Module):
 
     @torch.no_grad()
     def forward(self, x: torch.Tensor) -> torch.Tensor:
-        y = forward_mx4(self._rows(x), self.weight4, bias=self.bias)
+        y = forward_mx4(self._rows(x), self.weight4, bias=self._bias())
         return y.reshape(*x.shape[:-1], self.out_features)
 
 
@@ -1019,5 +1059,5 @@ class GroupedMx4Linear(Mx4Linear):
 
     @torch.no_grad()
     def forward(self, x: torch.Tensor, offsets: torch.Tensor) -> torch.Tensor:
-        y = grouped_forward_mx4(self._rows(x), self.weight4, offsets, bias=self.bias)
+        y = grouped_forward_mx4(self._rows(x), self.weight4, offsets, bias=self._bias())
         return y.reshape(*x.shape[:-1], self.out_features)
