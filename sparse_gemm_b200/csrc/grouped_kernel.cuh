@@ -52,7 +52,7 @@
 // 236 against 240 us, and 293 with waits that spin).
 //
 // Every wait is bounded (BSL_ERR_TIMEOUT in the status word, then all roles
-// leave through an abort flag).
+// leave through an abort flag, and the CTAs end when no copy can be under way).
 #pragma once
 
 #include "common.cuh"
@@ -773,6 +773,15 @@ __global__ void __launch_bounds__(Cfg<kMode>::THREADS, 1)
     // the leader's last arrival on this CTA is in before the CTA may end
     if (rank != 0 && threadIdx.x == 0 && !mbar_wait(drain, 0, tmo, nullptr)) set_status(args.status, BSL_ERR_TIMEOUT);
     __syncthreads();
+    // An aborted run's producers gave up one by one, and one of the four may have
+    // started a copy of a stage that the leader never armed: no barrier tells of it
+    // (a stage that is not armed is never multiplied, so both CTAs give up).
+    // Such a copy ends by itself in some microseconds: wait a thousand.
+    if (*abort_flag) {
+        const uint64_t t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < 1000000) __nanosleep(1000);
+        __syncwarp();
+    }
     cluster_sync_all();  // no MMA, copy or arrival of the pair is left
     if (warp == 1) {
         tc_fence_after();

@@ -27,3 +27,13 @@ def test_the_kernels_are_looked_at():
 def test_no_read_only_loads_in_dependent_kernels(name):
     found = re.findall(r"__ldg\w*\s*\(|ld\.global\.nc[\w.:]*|__restrict__", code_of(name))
     assert not found, (name, found)
+
+
+def test_an_aborted_pair_waits_for_its_copies():
+    """Two producers a CTA give up at stages of their own: behind the last role and before the pair's
+    last barrier, an aborted run waits until a copy that no barrier counts has ended."""
+    code = code_of("grouped_kernel.cuh")
+    kernel = code[code.index("k_grouped(const"):code.index("tmem_dealloc_pair(tmem")]
+    tail = kernel[kernel.rindex("bulk_wait_group<0>()"):]
+    order = [tail.rindex("mbar_wait(drain"), tail.index("if (*abort_flag)"), tail.index("__nanosleep"), tail.rindex("cluster_sync_all()")]
+    assert order == sorted(order)
