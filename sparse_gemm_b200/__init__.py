@@ -646,14 +646,30 @@ def _new(like: torch.Tensor, *shape: int) -> torch.Tensor:
     return like.new_empty(*shape) if like.dtype is torch.bfloat16 else like.new_empty(shape, dtype=torch.bfloat16)
 
 
-def _out_arg(out, shape, like: torch.Tensor, *inputs: torch.Tensor) -> torch.Tensor:
+def _memory(t):
+    """The memory of an argument as (address, bytes) pairs: a tensor's, a 4-bit tensor's codes and scales."""
+    if t is None:
+        return ()
+    if isinstance(t, Mx4Tensor):
+        n = math.prod(t.shape)
+        return (t._codes_ptr, n // 2), (t._scales_ptr, n // 32)
+    return ((t.data_ptr(), t.nbytes),)
+
+
+def _refuse_overlap(out, *inputs) -> None:
+    for a, n in _memory(out):
+        for t in inputs:
+            for b, m in _memory(t):
+                if n and m and a < b + m and b < a + n:
+                    raise ValueError("out must not overlap an input")
+
+
+def _out_arg(out, shape, like: torch.Tensor, *inputs) -> torch.Tensor:
+    """``out`` checked (its type and place are like's, it overlaps neither ``like`` nor an input), or a new tensor."""
     if out is None:
         return _new(like, *shape)
     _tensor_arg(out, "out", shape, torch.bfloat16, like)
-    first, end = out.data_ptr(), out.data_ptr() + out.nbytes
-    for t in (like, *inputs):
-        if first < t.data_ptr() + t.nbytes and t.data_ptr() < end:
-            raise ValueError("out must not overlap an input")
+    _refuse_overlap(out, like, *inputs)
     return out
 
 
@@ -700,7 +716,7 @@ def grouped_forward(X: torch.Tensor, Wg: GroupedWeight, offsets: torch.Tensor, b
     _tensor_arg(X, "X", (None, Wg.K), torch.bfloat16, Wg.weight)
     _tensor_arg(offsets, "offsets", (Wg.E + 1,), torch.int32, X)
     bptr = _expert_bias(bias, Wg.E, Wg.N, X)
-    Y = _out_arg(out, (X.shape[0], Wg.N), X, Wg.weight)
+    Y = _out_arg(out, (X.shape[0], Wg.N), X, Wg.weight, offsets, bias)
     _check(library().bsl_grouped_forward(X.data_ptr(), _row_count(X, "X"), offsets.data_ptr(), Wg.cref(), bptr,
                                          Y.data_ptr(), out is None, _stream(X)), "bsl_grouped_forward")
     return Y
@@ -711,7 +727,7 @@ def grouped_backward_input(dY: torch.Tensor, Wg: GroupedWeight, offsets: torch.T
     """dX[t] = dY[t] W[e]; rows of no expert as in :func:`grouped_forward`."""
     _tensor_arg(dY, "dY", (None, Wg.N), torch.bfloat16, Wg.weight)
     _tensor_arg(offsets, "offsets", (Wg.E + 1,), torch.int32, dY)
-    dX = _out_arg(out, (dY.shape[0], Wg.K), dY, Wg.weight)
+    dX = _out_arg(out, (dY.shape[0], Wg.K), dY, Wg.weight, offsets)
     _check(library().bsl_grouped_backward_input(dY.data_ptr(), _row_count(dY, "dY"), offsets.data_ptr(),
                                                 Wg.cref(), dX.data_ptr(), out is None, _stream(dY)),
            "bsl_grouped_backward_input")
@@ -724,7 +740,7 @@ def grouped_backward_weight(dY: torch.Tensor, X: torch.Tensor, Wg: GroupedWeight
     _tensor_arg(dY, "dY", (None, Wg.N), torch.bfloat16, Wg.weight)
     _tensor_arg(X, "X", (dY.shape[0], Wg.K), torch.bfloat16, Wg.weight)
     _tensor_arg(offsets, "offsets", (Wg.E + 1,), torch.int32, X)
-    dW = _out_arg(out, (Wg.E, Wg.N, Wg.K), X, dY)
+    dW = _out_arg(out, (Wg.E, Wg.N, Wg.K), X, dY, offsets)
     nbytes = Wg._workspace_bytes
     ws = _new(X, nbytes // 2)
     _check(library().bsl_grouped_backward_weight(dY.data_ptr(), X.data_ptr(), _row_count(X, "X"),
@@ -738,7 +754,7 @@ def grouped_bias_grad(dY: torch.Tensor, offsets: torch.Tensor, out: torch.Tensor
     _tensor_arg(dY, "dY", (None, None), torch.bfloat16)
     _tensor_arg(offsets, "offsets", (None,), torch.int32, dY)
     E, N = offsets.shape[0] - 1, dY.shape[1]
-    db = _out_arg(out, (E, N), dY)
+    db = _out_arg(out, (E, N), dY, offsets)
     _check(library().bsl_grouped_bias_grad(dY.data_ptr(), _row_count(dY, "dY"), offsets.data_ptr(), E, N, db.data_ptr(),
                                            _stream(dY)), "bsl_grouped_bias_grad")
     return db
@@ -916,6 +932,8 @@ def quantize_mx4(X: torch.Tensor, out: Mx4Tensor | None = None) -> Mx4Tensor:
         out = Mx4Tensor._empty(shape, X)
     elif out.shape != shape or out.device != X.device:
         raise ValueError(f"out holds {out.shape} on {out.device}, X is {shape} on {X.device}")
+    else:
+        _refuse_overlap(out, X)
     _check(library().bsl_mx4_quantize(X.data_ptr(), X.numel() // K, K, out._codes_ptr, out._scales_ptr, _stream(X)),
            "bsl_mx4_quantize")
     return out
@@ -923,13 +941,13 @@ def quantize_mx4(X: torch.Tensor, out: Mx4Tensor | None = None) -> Mx4Tensor:
 
 def dequantize_mx4(q: Mx4Tensor, out: torch.Tensor | None = None) -> torch.Tensor:
     """The values ``q`` stands for, as bf16 (exact)."""
-    X = _out_arg(out, q.shape, q._held)
+    X = _out_arg(out, q.shape, q._held, q)
     _check(library().bsl_mx4_dequantize(q._codes_ptr, q._scales_ptr, X.numel() // q.K, q.K, X.data_ptr(), _stream(X)),
            "bsl_mx4_dequantize")
     return X
 
 
-def _mx4_product(X, Wq: Mx4Tensor, offsets, bias_ptr, N: int, out) -> torch.Tensor:
+def _mx4_product(X, Wq: Mx4Tensor, offsets, bias, bias_ptr, N: int, out) -> torch.Tensor:
     if isinstance(X, Mx4Tensor):
         if len(X.shape) != 2 or X.K != Wq.K:
             raise ValueError(f"X holds {X.shape}, expected [rows, {Wq.K}]")
@@ -939,7 +957,7 @@ def _mx4_product(X, Wq: Mx4Tensor, offsets, bias_ptr, N: int, out) -> torch.Tens
     else:
         _tensor_arg(X, "X", (None, Wq.K), torch.bfloat16, Wq._held)
         rows, like = _row_count(X, "X"), X
-    Y = _out_arg(out, (rows, N), like, Wq._held)
+    Y = _out_arg(out, (rows, N), like, X, Wq, offsets, bias)
     lib, off = library(), None if offsets is None else offsets.data_ptr()
     if like is X:
         nbytes = rows * (Wq.K // 2 + Wq.K // 32)   # bsl_mx4_workspace_bytes
@@ -962,7 +980,7 @@ def forward_mx4(X, Wq: Mx4Tensor, bias: torch.Tensor | None = None, out: torch.T
     if len(Wq.shape) != 2:
         raise ValueError("Wq must be a weight [N, K]")
     N = Wq.shape[0]
-    return _mx4_product(X, Wq, None, _bias_ptr(bias, N, Wq._held), N, out)
+    return _mx4_product(X, Wq, None, bias, _bias_ptr(bias, N, Wq._held), N, out)
 
 
 def grouped_forward_mx4(X, Wq: Mx4Tensor, offsets: torch.Tensor, bias: torch.Tensor | None = None,
@@ -973,7 +991,7 @@ def grouped_forward_mx4(X, Wq: Mx4Tensor, offsets: torch.Tensor, bias: torch.Ten
         raise ValueError("Wq must be a weight [E, N, K]")
     E, N, _ = Wq.shape
     _tensor_arg(offsets, "offsets", (E + 1,), torch.int32, Wq._held)
-    return _mx4_product(X, Wq, offsets, _expert_bias(bias, E, N, Wq._held), N, out)
+    return _mx4_product(X, Wq, offsets, bias, _expert_bias(bias, E, N, Wq._held), N, out)
 
 
 def mx4_status(Wq: Mx4Tensor) -> int:
