@@ -646,6 +646,13 @@ def _new(like: torch.Tensor, *shape: int) -> torch.Tensor:
     return like.new_empty(*shape) if like.dtype is torch.bfloat16 else like.new_empty(shape, dtype=torch.bfloat16)
 
 
+def _readable(t: torch.Tensor) -> torch.Tensor:
+    """``t`` as the kernels read it, contiguous and on a 16-byte boundary: a copy where it is not (a
+    gradient, say, that is a part of a flat one)."""
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
 def _memory(t):
     """The memory of an argument as (address, bytes) pairs: a tensor's, a 4-bit tensor's codes and scales."""
     if t is None:
@@ -777,7 +784,7 @@ class GroupedLinearFunction(torch.autograd.Function):
         if (weight.data_ptr() != Wg.weight.data_ptr() or weight.shape != Wg.weight.shape
                 or not weight.is_contiguous()):
             raise ValueError("weight must be the tensor Wg was built on")
-        X = X.contiguous()
+        X = _readable(X)
         ctx.save_for_backward(X, weight, offsets)
         ctx.Wg = Wg
         ctx.has_bias = bias is not None
@@ -788,7 +795,7 @@ class GroupedLinearFunction(torch.autograd.Function):
     def backward(ctx, dY):
         X, _, offsets = ctx.saved_tensors
         Wg = ctx.Wg
-        dY = dY.contiguous()
+        dY = _readable(dY)
         dX = grouped_backward_input(dY, Wg, offsets) if ctx.needs_input_grad[0] else None
         dW = grouped_backward_weight(dY, X, Wg, offsets) if ctx.needs_input_grad[1] else None
         db = grouped_bias_grad(dY, offsets) if ctx.has_bias and ctx.needs_input_grad[4] else None
@@ -805,14 +812,14 @@ class GroupedLinear(torch.nn.Module):
 
     def __init__(self, weight: torch.Tensor, bias: torch.Tensor | None = None):
         super().__init__()
-        weight = weight.detach().to(torch.bfloat16).contiguous()
+        weight = _readable(weight.detach().to(torch.bfloat16))
         self._packed = GroupedWeight(weight)
         self.experts, self.out_features, self.in_features = weight.shape
         self.weight = torch.nn.Parameter(weight)
         if bias is not None:
             if bias.shape != weight.shape[:2]:
                 raise ValueError("bias must be [experts, out_features]")
-            bias = torch.nn.Parameter(bias.detach().to(device=weight.device, dtype=torch.bfloat16).contiguous())
+            bias = torch.nn.Parameter(_readable(bias.detach().to(device=weight.device, dtype=torch.bfloat16)))
         self.bias = bias
 
     @property
@@ -1012,7 +1019,7 @@ class Mx4Linear(torch.nn.Module):
         if bias is not None:
             if tuple(bias.shape) != weight4.shape[:-1]:
                 raise ValueError(f"bias must have shape {weight4.shape[:-1]}")
-            bias = bias.detach().to(device=weight4.device, dtype=torch.bfloat16).contiguous()
+            bias = _readable(bias.detach().to(device=weight4.device, dtype=torch.bfloat16))
         self.register_buffer("codes", None)
         self.register_buffer("scales", None)
         self.register_buffer("bias", bias)
@@ -1059,11 +1066,11 @@ class Mx4Linear(torch.nn.Module):
     @classmethod
     def from_dense(cls, weight: torch.Tensor, bias: torch.Tensor | None = None):
         """Quantise a [out_features, in_features] weight (in_features a multiple of 32)."""
-        return cls(quantize_mx4(weight.detach().to(torch.bfloat16).contiguous()), bias)
+        return cls(quantize_mx4(_readable(weight.detach().to(torch.bfloat16))), bias)
 
     def _rows(self, x: torch.Tensor) -> torch.Tensor:
         x2 = x.reshape(-1, self.in_features)
-        return (x2 if x2.dtype == torch.bfloat16 else x2.to(torch.bfloat16)).contiguous()
+        return _readable(x2 if x2.dtype == torch.bfloat16 else x2.to(torch.bfloat16))
 
     @torch.no_grad()
     def forward(self, x: torch.Tensor) -> torch.Tensor:
