@@ -825,10 +825,20 @@ class GroupedLinear(torch.nn.Module):
     @property
     def packed(self) -> GroupedWeight:
         """The weight's handle, made anew when the parameter's storage was replaced."""
-        if (self._packed is None or self._packed.weight.data_ptr() != self.weight.data_ptr()
-                or self._packed.weight.shape != self.weight.shape or not self.weight.is_contiguous()):
+        if not self._handle_is_current():
             self._packed = GroupedWeight(self.weight)
         return self._packed
+
+    def _handle_is_current(self) -> bool:
+        held, weight = self._packed, self.weight
+        return (held is not None and held.weight.data_ptr() == weight.data_ptr()
+                and held.weight.shape == weight.shape and weight.is_contiguous())
+
+    def _apply(self, fn, recurse=True):
+        super()._apply(fn, recurse)
+        if not self._handle_is_current():   # it would hold the memory that the module just left
+            self._packed = None
+        return self
 
     def __getstate__(self):
         return {**self.__dict__, "_packed": None}   # made anew by the copy
