@@ -336,14 +336,12 @@ BSL_API bsl_status bsl_grouped_backward_input(const void *dY, int32_t T, const i
 
 /* dW [E][N][K]: dW[e] = sum over the rows t of e of dY[t]^T . X[t]; an expert
  * without rows gets zeros.  W gives E, N, K and the status word (its weight
- * is not read).  workspace: bsl_grouped_workspace_bytes(W) bytes of device
- * scratch, 128-byte aligned, written before it is read (may be NULL when that
- * size is 0); calls that use one workspace must not overlap on the GPU. */
+ * is not read).  Needs no scratch: workspace is not used and may be NULL. */
 BSL_API bsl_status bsl_grouped_backward_weight(const void *dY, const void *X, int32_t T, const int32_t *offsets,
                                                const bsl_grouped *W, void *dW, void *workspace,
                                                size_t workspace_bytes, void *stream);
 
-/* Scratch bytes of bsl_grouped_backward_weight. */
+/* Scratch bytes of bsl_grouped_backward_weight: 0. */
 BSL_API size_t bsl_grouped_workspace_bytes(const bsl_grouped *W);
 
 /* db [E][N]: sums of each expert's rows of dY [T][N] (zeros for an expert

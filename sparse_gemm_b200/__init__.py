@@ -704,7 +704,6 @@ class GroupedWeight:
         self.E, self.N, self.K = int(E), int(N), int(K)
         self.status = torch.zeros(1, dtype=torch.int32, device=weight.device)
         self._c = _GROUPED(self.E, self.N, self.K, self.weight.data_ptr(), self.status.data_ptr())
-        self._workspace_bytes = int(library().bsl_grouped_workspace_bytes(self.cref()))
 
     @property
     def device(self):
@@ -748,10 +747,8 @@ def grouped_backward_weight(dY: torch.Tensor, X: torch.Tensor, Wg: GroupedWeight
     _tensor_arg(X, "X", (dY.shape[0], Wg.K), torch.bfloat16, Wg.weight)
     _tensor_arg(offsets, "offsets", (Wg.E + 1,), torch.int32, X)
     dW = _out_arg(out, (Wg.E, Wg.N, Wg.K), X, dY, offsets)
-    nbytes = Wg._workspace_bytes
-    ws = _new(X, nbytes // 2)
     _check(library().bsl_grouped_backward_weight(dY.data_ptr(), X.data_ptr(), _row_count(X, "X"),
-                                                 offsets.data_ptr(), Wg.cref(), dW.data_ptr(), ws.data_ptr(), nbytes, _stream(X)),
+                                                 offsets.data_ptr(), Wg.cref(), dW.data_ptr(), None, 0, _stream(X)),
            "bsl_grouped_backward_weight")
     return dW
 

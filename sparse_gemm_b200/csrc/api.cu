@@ -537,21 +537,15 @@ bsl_status bsl_grouped_backward_input(const void *dY, int32_t T, const int32_t *
     return launch_grouped_rows(dY, T, offsets, W, true, nullptr, dX, zero_rest, static_cast<cudaStream_t>(stream));
 }
 
-size_t bsl_grouped_workspace_bytes(const bsl_grouped *W)
-{
-    return check_grouped(W) == BSL_OK ? grouped_workspace_bytes(W) : 0;
-}
+size_t bsl_grouped_workspace_bytes(const bsl_grouped *) { return 0; }
 
 bsl_status bsl_grouped_backward_weight(const void *dY, const void *X, int32_t T, const int32_t *offsets,
-                                       const bsl_grouped *W, void *dW, void *workspace, size_t workspace_bytes,
-                                       void *stream)
+                                       const bsl_grouped *W, void *dW, void *, size_t, void *stream)
 {
     BSL_TRY(check_grouped(W));
     if (T < 0 || !offsets || !aligned(offsets, 4)) return BSL_ERR_INVALID_ARG;
     if (check_matrix(dY, T) != BSL_OK || check_matrix(X, T) != BSL_OK || check_matrix(dW, 1) != BSL_OK)
         return BSL_ERR_INVALID_ARG;
-    const size_t need = grouped_workspace_bytes(W);
-    if (need && (!workspace || !aligned(workspace, 128) || workspace_bytes < need)) return BSL_ERR_INVALID_ARG;
     if (too_large(T)) return BSL_ERR_UNSUPPORTED;
     DeviceGuard guard;
     BSL_TRY(guard.bind(dW));
@@ -559,7 +553,7 @@ bsl_status bsl_grouped_backward_weight(const void *dY, const void *X, int32_t T,
     if (T == 0)
         return cuda_status(cudaMemsetAsync(dW, 0, static_cast<size_t>(W->E) * W->N * W->K * 2,
                                            static_cast<cudaStream_t>(stream)));
-    return launch_grouped_dw(dY, X, T, offsets, W, dW, workspace, static_cast<cudaStream_t>(stream));
+    return launch_grouped_dw(dY, X, T, offsets, W, dW, static_cast<cudaStream_t>(stream));
 }
 
 bsl_status bsl_grouped_bias_grad(const void *dY, int32_t T, const int32_t *offsets, int32_t E, int32_t N, void *db,

@@ -19,9 +19,11 @@
 // rows: an expert's rows are spread evenly over the fewest tiles of 256.  Rows of
 // the next expert that a copy brings along only reach accumulator columns
 // that are never stored.  For the weight gradient, whose ragged index is
-// summed over, k_expert_maps first writes a tensor map for each expert's rows,
-// and the copies fill the rows behind its last one with zeros (a NaN there
-// must not meet a zero).
+// summed over, a row behind the expert's last one must be zero in both operands
+// (a NaN there must not meet a zero), up to the next multiple of 16 rows, the k
+// of an MMA.  So an expert's last stage, if it is not whole, comes in copies of
+// 64, 32, .. 1 rows, as the rows left have ones in binary, and the zeros behind
+// them in copies from behind the matrix.
 //
 // Persistent kernels, programmatic dependents, 8 warps a CTA:
 //   warps 0, 2 TMA producers of A and of B (a ring of stages);
@@ -96,9 +98,9 @@ struct Cfg {
 };
 
 struct Maps {
-    CUtensorMap a[2];  // A: two strips a copy, one strip (128 rows of K, or of features, each)
-    CUtensorMap b[8];  // K-major B: b[i] two strips of 16 (i + 1) rows
-    CUtensorMap t[8];  // ... t[i] one strip, where k ends inside one
+    CUtensorMap a[2];   // A: two strips a copy, one strip (128 rows of K, or of features, each)
+    CUtensorMap b[16];  // K-major B: b[i] two strips of 16 (i + 1) rows, b[8 + i] one, where k ends inside one
+                        // N-major B: b[0], b[1] as a[0], a[1]; b[2 + j] one strip of 64 >> j rows, b[9 + j] of A
     CUtensorMap out;
 };
 
@@ -106,7 +108,6 @@ struct Args {
     const int32_t *offsets;
     const __nv_bfloat16 *bias;
     __nv_bfloat16 *out;
-    const CUtensorMap *expert_maps;      // weight gradient: [E][4], see k_expert_maps
     int32_t *status;
     int32_t T, E;
     int32_t cols, rows, depth;           // of the product; the ragged one is unused
@@ -121,6 +122,7 @@ struct Tile {
     int r0;        // first row: of the matrix, or of the expert's dW
     int n, valid;  // MMA N, rows that exist
     int k, kb;     // length of the sums, stages
+    int k0;        // first k: the expert's first row in the weight gradient, else 0
 };
 
 // The tile list of a launch, the same in every CTA.
@@ -149,6 +151,7 @@ struct Tiles {
         x.r0 = kMode == kWeightGrad ? r0 : first + r0;
         x.k = kMode == kWeightGrad ? own : depth;
         x.kb = (x.k + C::BK - 1) / C::BK;
+        x.k0 = kMode == kWeightGrad ? first : 0;
         return x;
     }
 };
@@ -525,20 +528,13 @@ __global__ void __launch_bounds__(Cfg<kMode>::THREADS, 1)
             bool ok = true;
             int g = 0;  // stages issued
             Place at_ring;
-            int mapped = -1;
-            const CUtensorMap *one = &maps.a[1], *two = &maps.a[0];  // one, two strips a copy
+            // one, two strips a copy
+            const CUtensorMap *one = C::BN && !is_a ? &maps.b[1] : &maps.a[1], *two = C::BN && !is_a ? &maps.b[0] : &maps.a[0];
             Tile x, next;
             if (first < count) next = tiles.at(first);
             for (int t = first; ok && t < count; t += stride) {
                 x = next;
                 if (t + stride < count) next = tiles.at(t + stride);
-                if (kMode == kWeightGrad && x.kb > 0 && x.e != mapped) {
-                    mapped = x.e;
-                    one = args.expert_maps + 4 * static_cast<size_t>(x.e) + is_a;
-                    two = one + 2;
-                    asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(one) : "memory");
-                    asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(two) : "memory");
-                }
                 const int half = x.n / 2;  // rows of B in this CTA
                 const int at = is_a ? x.c0 + static_cast<int>(rank) * 128 : x.r0 + static_cast<int>(rank) * half;
                 const int plane = is_a && kMode != kWeightGrad ? x.e : 0;
@@ -550,7 +546,7 @@ __global__ void __launch_bounds__(Cfg<kMode>::THREADS, 1)
                 const bool aligned = mn && strips == 2 && at % 64 == 0 && (wide % 64 == 0 || at + 128 <= wide);
                 if (!is_a && !C::BN) {  // exactly the tile's rows
                     two = &maps.b[half / 16 - 1];
-                    one = &maps.t[half / 16 - 1];
+                    one = two + 8;
                 }
                 for (int k = 0; k < x.kb; ++k, ++g, at_ring.next(S)) {
                     const int slot = at_ring.slot;
@@ -559,14 +555,34 @@ __global__ void __launch_bounds__(Cfg<kMode>::THREADS, 1)
                         break;
                     }
                     uint8_t *dst = stages + slot * stage + (is_a ? 0 : C::A_BYTES);
-                    if (is_a && rank == 0) mbar_arrive_expect_tx(&full[slot], bytes);
+                    const int left = x.k - k * 128, row = x.k0 + k * 128;
+                    const bool rest = kMode == kWeightGrad && left < 128;  // of the expert's rows, not a whole stage
+                    const int lines = (left + 15) / 16 * 16;               // ... and the zeros behind them
+                    if (is_a && rank == 0) mbar_arrive_expect_tx(&full[slot], rest ? bytes / 128 * lines : bytes);
                     const uint32_t bar = cluster_addr(&full[slot], 0);
-                    if (mn) {
+                    if (rest) {
+                        const CUtensorMap *part = &maps.b[is_a ? 9 : 2];
+                        for (int i = 0; i < strips; ++i) {
+                            uint8_t *to = dst + i * 16384;
+                            int y = row;
+                            for (int j = 0; j < 7; ++j)
+                                if (left >> (6 - j) & 1) {
+                                    tma_load_3d_pair(to, part + j, bar, at + 64 * i, y, 0);
+                                    y += 64 >> j;
+                                    to += 8192 >> j;
+                                }
+                            for (int j = 3; j < 7; ++j)
+                                if ((lines - left) >> (6 - j) & 1) {
+                                    tma_load_3d_pair(to, part + j, bar, at + 64 * i, args.T, 0);  // no such row: zeros
+                                    to += 8192 >> j;
+                                }
+                        }
+                    } else if (mn) {
                         if (aligned)
-                            tma_load_4d_pair(dst, two, bar, 0, k * 128, at / 64, plane);
+                            tma_load_4d_pair(dst, two, bar, 0, row, at / 64, plane);
                         else
                             for (int i = 0; i < strips; ++i)
-                                tma_load_3d_pair(dst + i * 16384, one, bar, at + 64 * i, k * 128, plane);
+                                tma_load_3d_pair(dst + i * 16384, one, bar, at + 64 * i, row, plane);
                     } else if (x.k % 64 == 0 || k * 128 + 128 <= x.k) {
                         tma_load_4d_pair(dst, two, bar, 0, at, k * 2, plane);
                     } else {  // the last stage of a k that ends inside a strip
@@ -739,7 +755,7 @@ __global__ void __launch_bounds__(Cfg<kMode>::THREADS, 1)
                 uint8_t *dst = wbuf + ob * C::CHUNK;
                 stage_chunk(dst, v, bv, lane);
                 const int left = x.valid - 32 * i;
-                if (kMode == kWeightGrad || left >= 32) {  // dW's map ends with the expert's rows
+                if (kMode == kWeightGrad || left >= 32) {  // dW's map ends with each plane's rows
                     fence_async_smem();
                     __syncwarp();
                     if (lane == 0)
@@ -808,7 +824,7 @@ inline bool row_maps(Maps &m, const void *weight, int64_t E, int64_t N, int64_t 
     // (a tile has no more than T rows, rounded up to 32)
     for (int i = 0; i < 8 && 32 * i < T; ++i)
         good = good && make_strip_map(&m.b[i], A, depth, T, 1, 16 * (i + 1), 2) &&
-               (depth % 64 == 0 || map_rows(&m.t[i], A, depth, T, 64, 16 * (i + 1), 128));
+               (depth % 64 == 0 || map_rows(&m.b[8 + i], A, depth, T, 64, 16 * (i + 1), 128));
     return good;
 }
 

@@ -143,11 +143,10 @@ bsl_status launch_bsr24_fwd(const void *X, int32_t M, const bsl_bsr *W, const vo
 
 // Expert (grouped) layer.  launch_grouped_rows: forward (A = X, out = Y) or,
 // transposed, the input gradient (A = dY, out = dX).
-size_t grouped_workspace_bytes(const bsl_grouped *W);
 bsl_status launch_grouped_rows(const void *A, int32_t T, const int32_t *offsets, const bsl_grouped *W, bool transposed,
                                const void *bias, void *out, int32_t zero_rest, cudaStream_t s);
 bsl_status launch_grouped_dw(const void *dY, const void *X, int32_t T, const int32_t *offsets, const bsl_grouped *W,
-                             void *dW, void *workspace, cudaStream_t s);
+                             void *dW, cudaStream_t s);
 bsl_status launch_grouped_bias_grad(const void *dY, int32_t T, const int32_t *offsets, int32_t E, int32_t N, void *db,
                                     cudaStream_t s);
 

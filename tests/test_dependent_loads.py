@@ -37,3 +37,11 @@ def test_an_aborted_pair_waits_for_its_copies():
     tail = kernel[kernel.rindex("bulk_wait_group<0>()"):]
     order = [tail.rindex("mbar_wait(drain"), tail.index("if (*abort_flag)"), tail.index("__nanosleep"), tail.rindex("cluster_sync_all()")]
     assert order == sorted(order)
+
+
+def test_no_tensor_map_is_changed_on_the_device():
+    """Copies go through maps of whole matrices, encoded by the driver.  Maps that a kernel moved to an
+    expert's first row, with its row count, reached past the matrix where the box did."""
+    for name in FILES:
+        found = re.findall(r"tensormap\.(?:replace|cp_fenceproxy)|fence\.proxy\.tensormap", code_of(name))
+        assert not found, (name, found)
