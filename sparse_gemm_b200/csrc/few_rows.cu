@@ -373,6 +373,9 @@ bsl_status launch4(FewArgs &a, cudaStream_t s)
 
 // Where these kernels are ahead of the tensor-core tiles, by the rows and by the
 // bytes of the weights that the rows can use (L2 cold; us here / there).
+// Single calls behind other work also pay the tiles' set-up, some 5 us: there these stay ahead past each border
+// (16 rows up to 64 MB, 32 rows up to 28 MB on one expert), or lose up to 7 % just below it (16 rows of 4 bits on
+// eight experts, 4 MB: 14.3 / 13.3).
 // bf16: up to 8 rows everywhere (17 MB 5.6 / 13.7, 361 MB 60 / 67, 721 MB 114 / 114); 16 rows re-read X for every
 // 16 features, so up to 32 MB (17 MB 7.6 / 13.6, 34 MB 12.0 / 12.3, 90 MB 23.9 / 22.6); 32 rows up to 20 MB
 // (17 MB 10.1 / 13.6, 34 MB 15.6 / 12.3).
