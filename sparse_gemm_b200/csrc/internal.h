@@ -26,7 +26,8 @@ bool make_map_3d(CUtensorMap *map, const void *base, uint64_t d0, uint64_t d1, u
 // Encode the strips of bf16 planes [planes][rows][cols] as a 4-D tensor map (x = column inside a strip of 64,
 // y = row, z = strip, w = plane) with a box of 64 columns x box_rows rows x box_strips strips, 128-byte swizzle:
 // one copy brings box_rows rows of 64 * box_strips columns, strip after strip of 128-byte rows.  Whole strips
-// only (cols / 64 of them).
+// only (cols / 64 of them).  Strides need not grow from dimension to dimension: what lies outside is told
+// coordinate by coordinate, and is neither read (fewer L2 sectors by as much) nor part of the result.
 bool make_strip_map(CUtensorMap *map, const void *base, uint64_t cols, uint64_t rows, uint64_t planes,
                     uint32_t box_rows, uint32_t box_strips);
 
