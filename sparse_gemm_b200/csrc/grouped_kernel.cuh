@@ -560,7 +560,7 @@ __global__ void __launch_bounds__(Cfg<kMode>::THREADS, 1)
                     const int lines = (left + 15) / 16 * 16;               // ... and the zeros behind them
                     if (is_a && rank == 0) mbar_arrive_expect_tx(&full[slot], rest ? bytes / 128 * lines : bytes);
                     const uint32_t bar = cluster_addr(&full[slot], 0);
-                    if (rest) {
+                    if (rest) {  // (the swizzle goes by the address, so a copy may begin at any line)
                         const CUtensorMap *part = &maps.b[is_a ? 9 : 2];
                         for (int i = 0; i < strips; ++i) {
                             uint8_t *to = dst + i * 16384;
