@@ -414,6 +414,56 @@ BSL_API size_t bsl_mx4_workspace_bytes(int32_t T, const bsl_mx4 *W);
  * *status_host (a bsl_status value) and resets it to BSL_OK. */
 BSL_API bsl_status bsl_mx4_get_status(const bsl_mx4 *W, int32_t *status_host, void *stream);
 
+/* ---------------------------------------------------------------- 8 bits, a scale per block of 128
+ *
+ * 8-bit floating point (e4m3: largest value 448, codes 0x7F and 0xFF NaN) with an fp32 scale for each block
+ * of 128 along K.  A block is 128 neighbours of one row (activations, block_rows = 1) or a tile of 128 rows
+ * by 128 columns (weights, block_rows = 128); the last of a row or column may be shorter.
+ *   codes   uint8 [planes][rows][K], K a multiple of 16;
+ *   scales  float [planes][rows][ceil(K / 128)] or [planes][ceil(rows / 128)][ceil(K / 128)].
+ * Both 16-byte aligned.  An element's value is its code's times its block's scale. */
+
+/* X bf16 [planes][rows][K] to codes and scales.  With a the largest magnitude of a block and 2^-100, all in
+ * fp32: the scale is a / 448, a code is the e4m3 number nearest to x * (448 / a), ties to even.  A block
+ * holding an infinity or a NaN becomes NaN (scale NaN, codes 0).  planes, rows >= 0. */
+BSL_API bsl_status bsl_fp8_quantize(const void *X, int64_t planes, int64_t rows, int32_t K, int32_t block_rows,
+                                    uint8_t *codes, float *scales, void *stream);
+
+/* The values codes and scales stand for, rounded to bf16 [planes][rows][K]. */
+BSL_API bsl_status bsl_fp8_dequantize(const uint8_t *codes, const float *scales, int64_t planes, int64_t rows, int32_t K,
+                                      int32_t block_rows, void *X, void *stream);
+
+/* A weight in that form, in tiles: a linear layer's (E = 1) or one per expert. */
+typedef struct {
+    int32_t E, N, K;          /* experts (1 .. BSL_GROUPED_MAX_EXPERTS); N a multiple of 8, K of 16 */
+    const uint8_t *codes;     /* [E][N][K] */
+    const float *scales;      /* [E][ceil(N / 128)][ceil(K / 128)] */
+    int32_t *status;          /* [1] device status word; must be zeroed once at allocation */
+} bsl_fp8;
+
+/* The layer's products with rows in codes and scales (block_rows = 1), fp32 sums:
+ *   transposed 0: out [T][N] = A . W[e]^T (+ bias[e]), rows of length K;
+ *   transposed 1: out [T][K] = A . W[e], rows of length N (a multiple of 16): the input gradient, no bias.
+ * offsets, bias [E][N] (bf16, or NULL) and zero_rest as for bsl_grouped_forward; offsets NULL: W has E = 1
+ * and owns all rows.  T >= 0. */
+BSL_API bsl_status bsl_fp8_product(const uint8_t *codes, const float *scales, int32_t T, const int32_t *offsets,
+                                   const bsl_fp8 *W, int32_t transposed, const void *bias, void *out, int32_t zero_rest,
+                                   void *stream);
+
+/* The same from bf16 rows A, quantised as by bsl_fp8_quantize on the way (into the workspace).
+ * workspace: bsl_fp8_workspace_bytes(T, W, transposed) bytes of device scratch, 16-byte aligned, written
+ * before it is read; calls that use one workspace must not overlap on the GPU. */
+BSL_API bsl_status bsl_fp8_linear(const void *A, int32_t T, const int32_t *offsets, const bsl_fp8 *W, int32_t transposed,
+                                  const void *bias, void *out, int32_t zero_rest, void *workspace, size_t workspace_bytes,
+                                  void *stream);
+
+/* Scratch bytes of bsl_fp8_linear for T rows (0 for T <= 0). */
+BSL_API size_t bsl_fp8_workspace_bytes(int32_t T, const bsl_fp8 *W, int32_t transposed);
+
+/* SYNCHRONOUS: waits for the stream, copies the device status word of W to
+ * *status_host (a bsl_status value) and resets it to BSL_OK. */
+BSL_API bsl_status bsl_fp8_get_status(const bsl_fp8 *W, int32_t *status_host, void *stream);
+
 /* SYNCHRONOUS: waits for the stream, copies the device status word of W to
  * *status_host (a bsl_status value) and resets it to BSL_OK. */
 BSL_API bsl_status bsl_get_device_status(const bsl_bsr *W, int32_t *status_host, void *stream);

@@ -1,4 +1,4 @@
-"""Plain CPU oracle of the expert (grouped) layer and of microscaled 4-bit
+"""Plain CPU oracle of the expert (grouped) layer, of microscaled 4-bit and of 8-bit
 floating point, in fp64 (test infrastructure only, as the package).
 
 * Expert layer: rows offsets[e] .. offsets[e+1] belong to expert e;
@@ -94,3 +94,50 @@ def mx4_values(codes, scales):
     s = np.ldexp(1.0, scales.astype(np.int64) - 127)
     s[scales == 255] = np.nan
     return v * np.repeat(s, 32, axis=-1)
+
+
+def e4m3_nearest(u):
+    """fp64 -> the nearest e4m3 number, ties to the even code, at most 448."""
+    m = np.abs(u)
+    with np.errstate(divide="ignore"):
+        e = np.maximum(np.floor(np.log2(np.where(m > 0, m, 1.0))), -6)   # -6: the subnormal numbers' step is 2^-9
+    e = np.where(m >= 2.0 ** (e + 1), e + 1, np.where((m < 2.0 ** e) & (e > -6), e - 1, e))
+    step = 2.0 ** (e - 3)
+    return np.copysign(np.minimum(np.round(m / step) * step, 448.0), u)
+
+
+def fp8_quantize(X, block_rows):
+    """fp64 (bf16 numbers) [R, K] -> (values of the codes [R, K], scales [rows or tiles, ceil(K / 128)]).
+
+    A block is block_rows x 128; a = max(max|x|, 2^-100), scale a / 448 and factor 448 / a rounded to fp32, the
+    product of x and the factor too.  A block that holds an infinity or a NaN has scale NaN and codes 0."""
+    R, K = X.shape
+    nr, nk = -(-R // block_rows), -(-K // 128)
+    codes, scales = np.zeros((R, K)), np.zeros((nr, nk), dtype=np.float32)
+    for i in range(nr):
+        for j in range(nk):
+            at = np.s_[block_rows * i:block_rows * (i + 1), 128 * j:128 * (j + 1)]
+            x = X[at]
+            if not np.isfinite(x).all():
+                scales[i, j] = np.nan
+                continue
+            a = np.float32(max(np.abs(x).max(), 2.0 ** -100))
+            scales[i, j] = a / np.float32(448)
+            codes[at] = e4m3_nearest((x.astype(np.float32) * (np.float32(448) / a)).astype(np.float64))
+    return codes, scales
+
+
+def fp8_values(codes, scales):
+    """Values of codes [R, K] (as numbers) under scales by row or by tile, fp64."""
+    R, K = codes.shape
+    s = scales.astype(np.float64)
+    s = s if s.shape[0] == R else np.repeat(s, 128, axis=0)[:R]
+    return codes * np.repeat(s, 128, axis=1)[:, :K]
+
+
+def fp8_product(A, As, W, Ws, transposed=False):
+    """Rows' code values [T, depth] with scales by row times a weight's [N, K] in tiles (or its transpose):
+    (product, S) with S the sum of |term|."""
+    a, w = fp8_values(A, As), fp8_values(W, Ws)
+    w = w if transposed else w.T
+    return a @ w, np.abs(a) @ np.abs(w)

@@ -32,6 +32,8 @@ __all__ = [
     "grouped_bias_grad", "grouped_status", "GroupedLinearFunction", "GroupedLinear",
     "Mx4Tensor", "quantize_mx4", "dequantize_mx4", "forward_mx4", "grouped_forward_mx4", "mx4_status",
     "Mx4Linear", "GroupedMx4Linear",
+    "Fp8Tensor", "quantize_fp8", "dequantize_fp8", "forward_fp8", "grouped_forward_fp8", "backward_input_fp8",
+    "grouped_backward_input_fp8", "fp8_status", "Fp8LinearFunction", "Fp8Linear", "GroupedFp8Linear",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -73,6 +75,11 @@ class _MX4(ctypes.Structure):
                 ("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("status", ctypes.c_void_p)]
 
 
+class _FP8(ctypes.Structure):
+    _fields_ = [("E", ctypes.c_int32), ("N", ctypes.c_int32), ("K", ctypes.c_int32),
+                ("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("status", ctypes.c_void_p)]
+
+
 # experts of a grouped layer (BSL_GROUPED_MAX_EXPERTS in include/bsl.h)
 GROUPED_MAX_EXPERTS = 1024
 
@@ -92,6 +99,7 @@ def library() -> ctypes.CDLL:
         lib = ctypes.CDLL(LIB_PATH)
         P, I32, SZ, U64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t, ctypes.c_uint64
         I64, GP, XP = ctypes.c_int64, ctypes.POINTER(_GROUPED), ctypes.POINTER(_MX4)
+        FP = ctypes.POINTER(_FP8)
         BP = ctypes.POINTER(_BSR)
         SP = ctypes.POINTER(_SEMI24)
         sig = {
@@ -129,6 +137,12 @@ def library() -> ctypes.CDLL:
             "bsl_mx4_linear": (ctypes.c_int, [P, I32, P, XP, P, P, I32, P, SZ, P]),
             "bsl_mx4_workspace_bytes": (SZ, [I32, XP]),
             "bsl_mx4_get_status": (ctypes.c_int, [XP, ctypes.POINTER(I32), P]),
+            "bsl_fp8_quantize": (ctypes.c_int, [P, I64, I64, I32, I32, P, P, P]),
+            "bsl_fp8_dequantize": (ctypes.c_int, [P, P, I64, I64, I32, I32, P, P]),
+            "bsl_fp8_product": (ctypes.c_int, [P, P, I32, P, FP, I32, P, P, I32, P]),
+            "bsl_fp8_linear": (ctypes.c_int, [P, I32, P, FP, I32, P, P, I32, P, SZ, P]),
+            "bsl_fp8_workspace_bytes": (SZ, [I32, FP, I32]),
+            "bsl_fp8_get_status": (ctypes.c_int, [FP, ctypes.POINTER(I32), P]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(lib, name)
@@ -654,9 +668,11 @@ def _readable(t: torch.Tensor) -> torch.Tensor:
 
 
 def _memory(t):
-    """The memory of an argument as (address, bytes) pairs: a tensor's, a 4-bit tensor's codes and scales."""
+    """The memory of an argument as (address, bytes) pairs: a tensor's, a 4- or 8-bit tensor's codes and scales."""
     if t is None:
         return ()
+    if isinstance(t, Fp8Tensor):
+        return (t._codes_ptr, t.codes.nbytes), (t._scales_ptr, t.scales.nbytes)
     if isinstance(t, Mx4Tensor):
         n = math.prod(t.shape)
         return (t._codes_ptr, n // 2), (t._scales_ptr, n // 32)
@@ -1093,3 +1109,273 @@ class GroupedMx4Linear(Mx4Linear):
     def forward(self, x: torch.Tensor, offsets: torch.Tensor) -> torch.Tensor:
         y = grouped_forward_mx4(self._rows(x), self.weight4, offsets, bias=self._bias())
         return y.reshape(*x.shape[:-1], self.out_features)
+
+
+# ---------------------------------------------------------------- 8 bits, a scale per block of 128
+
+
+class Fp8Tensor:
+    """A matrix (or a stack of them) in 8-bit floating point with a scale for each block of 128:
+    ``codes`` float8_e4m3fn (or their bits as uint8) [..., R, K], K a multiple of 16, and ``scales``
+    float32, one for 128 neighbours of a row ([..., R, ceil(K / 128)], activations) or for a tile of
+    128 x 128 ([..., ceil(R / 128), ceil(K / 128)], weights); ``block_rows`` says which, 1 or 128.
+    An element is its code times its block's scale.  As a weight, in tiles, [N, K] or [E, N, K], it
+    carries the device status word of the products that use it."""
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor):
+        if not (isinstance(codes, torch.Tensor) and codes.dim() >= 2 and codes.dtype in (torch.float8_e4m3fn, torch.uint8)):
+            raise TypeError("codes must be a float8_e4m3fn (or uint8) CUDA tensor of at least two dimensions")
+        shape = tuple(codes.shape)
+        R, K = shape[-2:]
+        if K <= 0 or K % 16:
+            raise ValueError("codes must have a positive multiple of 16 columns")
+        codes = codes if codes.dtype is torch.float8_e4m3fn else codes.view(torch.float8_e4m3fn)
+        _tensor_arg(codes, "codes", shape, torch.float8_e4m3fn)
+        rows = R if isinstance(scales, torch.Tensor) and scales.dim() >= 2 and scales.shape[-2] == R else -(-R // 128)
+        _tensor_arg(scales, "scales", (*shape[:-2], rows, -(-K // 128)), torch.float32, codes)
+        if codes.data_ptr() % 16 or scales.data_ptr() % 16:
+            raise ValueError("codes and scales must begin on a 16-byte boundary")
+        self._set(codes, scales, 1 if rows == R else 128)
+
+    def __getstate__(self):
+        return {"codes": self.codes, "scales": self.scales}
+
+    def __setstate__(self, state):
+        self.__init__(state["codes"], state["scales"])
+
+    def _set(self, codes, scales, block_rows):
+        self.codes, self.scales, self.block_rows = codes, scales, block_rows
+        self._codes_ptr, self._scales_ptr = codes.data_ptr(), scales.data_ptr()
+        self.shape, self.K = tuple(codes.shape), codes.shape[-1]
+        self._status = self._c = None
+
+    @property
+    def device(self):
+        return self.codes.device
+
+    @property
+    def status(self) -> torch.Tensor:
+        """The device status word, which outlives any graph: made when the tensor is first used as
+        a weight, at the latest before a capture."""
+        if self._status is None:
+            if torch.cuda.is_current_stream_capturing():
+                raise RuntimeError("use this weight (or read its .status) once before capturing a graph with it")
+            self._status = torch.zeros(1, dtype=torch.int32, device=self.device)
+        return self._status
+
+    def cref(self):
+        """The weight's descriptor (one expert for a matrix)."""
+        if self._c is None:
+            shape = self.shape
+            if len(shape) not in (2, 3) or (self.block_rows != 128 and shape[-2] != 1):
+                raise ValueError("a weight is [N, K] or [E, N, K] with a scale for each tile of 128 x 128")
+            E, N = (1, shape[0]) if len(shape) == 2 else shape[:2]
+            if not 0 < E <= GROUPED_MAX_EXPERTS or N <= 0 or N % 8:
+                raise ValueError("a weight has 1 to 1024 experts and a positive multiple of 8 output features")
+            self._c = _FP8(E, N, self.K, self._codes_ptr, self._scales_ptr, self.status.data_ptr())
+        return ctypes.byref(self._c)
+
+
+def quantize_fp8(X: torch.Tensor, block_rows: int = 1, out: Fp8Tensor | None = None) -> Fp8Tensor:
+    """A bf16 tensor [..., R, K], K a multiple of 16, in 8 bits with a scale for each block of 128
+    neighbours of a row (``block_rows`` 1, activations) or of 128 x 128 (``block_rows`` 128, weights):
+    with a = max(max|x|, 2^-100) the scale is a / 448 and the codes are x * (448 / a), in fp32,
+    rounded to e4m3 (ties to even).  A block with an infinity or a NaN becomes NaN."""
+    if not (isinstance(X, torch.Tensor) and X.dim() >= 2):
+        raise TypeError("X must be a bfloat16 CUDA tensor of at least two dimensions")
+    shape = tuple(X.shape)
+    _tensor_arg(X, "X", shape, torch.bfloat16)
+    R, K = shape[-2:]
+    if K <= 0 or K % 16:
+        raise ValueError("X's last dimension must be a positive multiple of 16")
+    if block_rows not in (1, 128):
+        raise ValueError("block_rows must be 1 or 128")
+    if out is None:
+        out = Fp8Tensor.__new__(Fp8Tensor)
+        out._set(X.new_empty(shape, dtype=torch.float8_e4m3fn),
+                 X.new_empty((*shape[:-2], R if block_rows == 1 else -(-R // 128), -(-K // 128)), dtype=torch.float32),
+                 block_rows)
+    elif out.shape != shape or out.device != X.device or (out.block_rows != block_rows and R != 1):
+        raise ValueError(f"out holds {out.shape} in blocks of {out.block_rows} rows on {out.device}, X is {shape} in "
+                         f"blocks of {block_rows} on {X.device}")
+    else:
+        _refuse_overlap(out, X)
+    planes, rows = (1, X.numel() // K) if block_rows == 1 else (math.prod(shape[:-2]), R)
+    _check(library().bsl_fp8_quantize(X.data_ptr(), planes, rows, K, block_rows, out._codes_ptr, out._scales_ptr,
+                                      _stream(X)), "bsl_fp8_quantize")
+    return out
+
+
+def dequantize_fp8(q: Fp8Tensor, out: torch.Tensor | None = None) -> torch.Tensor:
+    """The values ``q`` stands for, rounded to bf16."""
+    X = _out_arg(out, q.shape, q.codes, q)
+    planes, rows = (1, X.numel() // q.K) if q.block_rows == 1 else (math.prod(q.shape[:-2]), q.shape[-2])
+    _check(library().bsl_fp8_dequantize(q._codes_ptr, q._scales_ptr, planes, rows, q.K, q.block_rows, X.data_ptr(),
+                                        _stream(X)), "bsl_fp8_dequantize")
+    return X
+
+
+def _fp8_product(A, Wq: Fp8Tensor, dims: int, transposed: bool, offsets, bias, out) -> torch.Tensor:
+    """``A`` (bf16, or an Fp8Tensor with scales by row) times the weight or its transpose."""
+    if not isinstance(Wq, Fp8Tensor) or len(Wq.shape) != dims:
+        raise ValueError(f"Wq must be an Fp8Tensor {'[N, K]' if dims == 2 else '[E, N, K]'}")
+    wref = Wq.cref()
+    E, N, K = Wq._c.E, Wq._c.N, Wq._c.K
+    depth, cols = (N, K) if transposed else (K, N)
+    name = "dY" if transposed else "X"
+    if transposed and N % 16:
+        raise ValueError("the input gradient takes output features in multiples of 16")
+    if isinstance(A, Fp8Tensor):
+        if len(A.shape) != 2 or A.K != depth or (A.block_rows != 1 and A.shape[0] != 1):
+            raise ValueError(f"{name} holds {A.shape} in blocks of {A.block_rows} rows, expected [rows, {depth}] in "
+                             f"blocks of one")
+        if A.device != Wq.device:
+            raise ValueError(f"{name} must be on {Wq.device}")
+        like = A.codes
+    else:
+        _tensor_arg(A, name, (None, depth), torch.bfloat16, Wq.codes)
+        like = A
+    rows = _row_count(A, name)
+    off = bptr = None
+    if dims == 3:
+        _tensor_arg(offsets, "offsets", (E + 1,), torch.int32, Wq.codes)
+        off = offsets.data_ptr()
+    if bias is not None:
+        _tensor_arg(bias, "bias", (N,) if dims == 2 else (E, N), torch.bfloat16, Wq.codes)
+        bptr = bias.data_ptr()
+    Y = _out_arg(out, (rows, cols), like, A, Wq, offsets, bias)
+    lib, zero = library(), out is None
+    if like is A:
+        nbytes = rows * (depth + 4 * (-(-depth // 128)))   # bsl_fp8_workspace_bytes
+        ws = _new(A, nbytes // 2)
+        _check(lib.bsl_fp8_linear(A.data_ptr(), rows, off, wref, transposed, bptr, Y.data_ptr(), zero, ws.data_ptr(),
+                                  nbytes, _stream(A)), "bsl_fp8_linear")
+    else:
+        _check(lib.bsl_fp8_product(A._codes_ptr, A._scales_ptr, rows, off, wref, transposed, bptr, Y.data_ptr(), zero,
+                                   _stream(like)), "bsl_fp8_product")
+    return Y
+
+
+def forward_fp8(X, Wq: Fp8Tensor, bias: torch.Tensor | None = None, out: torch.Tensor | None = None) -> torch.Tensor:
+    """Y = Q(X) Q(W)^T (+ bias), bf16 [M, N], 8-bit products with fp32 sums and scales.  X is bf16
+    [M, K] (quantised on the way as by :func:`quantize_fp8`) or an Fp8Tensor with scales by row,
+    ``Wq`` a weight [N, K] in tiles, N a multiple of 8."""
+    return _fp8_product(X, Wq, 2, False, None, bias, out)
+
+
+def backward_input_fp8(dY, Wq: Fp8Tensor, out: torch.Tensor | None = None) -> torch.Tensor:
+    """dX = Q(dY) Q(W), bf16 [M, K]; N must be a multiple of 16."""
+    return _fp8_product(dY, Wq, 2, True, None, None, out)
+
+
+def grouped_forward_fp8(X, Wq: Fp8Tensor, offsets: torch.Tensor, bias: torch.Tensor | None = None,
+                        out: torch.Tensor | None = None) -> torch.Tensor:
+    """:func:`grouped_forward` with the experts' weights [E, N, K] and the rows in 8 bits; bad offsets
+    are reported by :func:`fp8_status`."""
+    return _fp8_product(X, Wq, 3, False, offsets, bias, out)
+
+
+def grouped_backward_input_fp8(dY, Wq: Fp8Tensor, offsets: torch.Tensor, out: torch.Tensor | None = None) -> torch.Tensor:
+    """:func:`grouped_backward_input` with the experts' weights and the rows in 8 bits (N a multiple of 16)."""
+    return _fp8_product(dY, Wq, 3, True, offsets, None, out)
+
+
+def fp8_status(Wq: Fp8Tensor) -> int:
+    """Read and clear the weight's device status word (synchronises the stream)."""
+    out = ctypes.c_int32(0)
+    _check(library().bsl_fp8_get_status(Wq.cref(), ctypes.byref(out), _stream(Wq.codes)), "bsl_fp8_get_status")
+    return int(out.value)
+
+
+class Fp8LinearFunction(torch.autograd.Function):
+    """Autograd wrapper of the 8-bit layer over a frozen weight: forward as :func:`forward_fp8` (or
+    :func:`grouped_forward_fp8`, with offsets), backward the input's gradient, quantised by row too."""
+
+    @staticmethod
+    def forward(ctx, X, Wq, offsets=None, bias=None):
+        ctx.Wq = Wq
+        ctx.save_for_backward(*(() if offsets is None else (offsets,)))
+        return _fp8_product(_readable(X), Wq, len(Wq.shape), False, offsets, bias, None)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dY):
+        dX = None
+        if ctx.needs_input_grad[0]:
+            offsets = ctx.saved_tensors[0] if ctx.saved_tensors else None
+            dX = _fp8_product(_readable(dY), ctx.Wq, len(ctx.Wq.shape), True, offsets, None, None)
+        return dX, None, None, None
+
+
+class Fp8Linear(torch.nn.Module):
+    """``nn.Linear`` over a frozen weight in 8 bits with a scale for each tile of 128 x 128, activations
+    quantised by row and block of 128; the gradient flows to the input (out_features a multiple of 16).
+    Built with :meth:`from_dense`; inputs may have any leading dimensions.  The weight is part of the
+    module's state, as the buffers ``codes`` (uint8) and ``scales`` (the bits of the fp32 scales as
+    int32: a cast of the module leaves both alone), those of the tensor it was made of, not copies;
+    ``weight8`` is the handle on them.  The bias is a buffer too, added in bf16."""
+
+    def __init__(self, weight8: Fp8Tensor, bias: torch.Tensor | None = None):
+        super().__init__()
+        weight8.cref()
+        if bias is not None:
+            if tuple(bias.shape) != weight8.shape[:-1]:
+                raise ValueError(f"bias must have shape {weight8.shape[:-1]}")
+            bias = _readable(bias.detach().to(device=weight8.device, dtype=torch.bfloat16))
+        self.in_features, self.out_features = weight8.K, weight8.shape[-2]
+        self.register_buffer("codes", weight8.codes.view(torch.uint8))
+        self.register_buffer("scales", weight8.scales.view(torch.int32))
+        self.register_buffer("bias", bias)
+        self._weight8 = weight8
+
+    @property
+    def weight8(self) -> Fp8Tensor:
+        """The weight's handle, made anew when a buffer's storage was replaced."""
+        if not self._handle_is_current():
+            self._weight8 = Fp8Tensor(self.codes, self.scales.view(torch.float32))
+        return self._weight8
+
+    def _handle_is_current(self) -> bool:
+        w, codes, scales = self._weight8, self._buffers["codes"], self._buffers["scales"]
+        return (w is not None and w._codes_ptr == codes.data_ptr() and w._scales_ptr == scales.data_ptr()
+                and w.shape == codes.shape and codes.is_contiguous() and scales.is_contiguous())
+
+    def _apply(self, fn, recurse=True):
+        super()._apply(fn, recurse)
+        if not self._handle_is_current():   # it would hold the memory that the module just left
+            self._weight8 = None
+        return self
+
+    def __getstate__(self):
+        return {**self.__dict__, "_weight8": None}   # made anew by the copy
+
+    @classmethod
+    def from_dense(cls, weight: torch.Tensor, bias: torch.Tensor | None = None):
+        """Quantise a weight [out_features, in_features] (in_features a multiple of 16, out_features of 8)."""
+        return cls(quantize_fp8(_readable(weight.detach().to(torch.bfloat16)), block_rows=128), bias)
+
+    def _product(self, x: torch.Tensor, offsets) -> torch.Tensor:
+        x2 = x.reshape(-1, self.in_features)
+        if x2.dtype != torch.bfloat16:
+            x2 = x2.to(torch.bfloat16)
+        if x2.requires_grad and torch.is_grad_enabled() and self.out_features % 16:
+            raise ValueError("a gradient needs out_features in multiples of 16")
+        b = self._buffers["bias"]
+        if b is not None and b.dtype is not torch.bfloat16:
+            b = b.to(torch.bfloat16)
+        y = Fp8LinearFunction.apply(x2, self.weight8, offsets, b)
+        return y.reshape(*x.shape[:-1], self.out_features)
+
+    def forward(self, x: torch.Tensor) -> torch.Tensor:
+        return self._product(x, None)
+
+    def extra_repr(self) -> str:
+        return f"in_features={self.in_features}, out_features={self.out_features}, bias={self.bias is not None}"
+
+
+class GroupedFp8Linear(Fp8Linear):
+    """:class:`GroupedLinear` over frozen 8-bit weights: :meth:`from_dense` takes weights
+    [E, out_features, in_features] and bias [E, out_features]; ``offsets`` as in :func:`grouped_forward`."""
+
+    def forward(self, x: torch.Tensor, offsets: torch.Tensor) -> torch.Tensor:
+        return self._product(x, offsets)

@@ -142,6 +142,17 @@ bsl_status check_mx4(const bsl_mx4 *W)
     return BSL_OK;
 }
 
+bsl_status check_fp8(const bsl_fp8 *W)
+{
+    if (!W) return BSL_ERR_INVALID_ARG;
+    if (W->E <= 0 || W->N <= 0 || W->K <= 0 || W->N % 8 || W->K % 16) return BSL_ERR_INVALID_ARG;
+    if (W->E > BSL_GROUPED_MAX_EXPERTS || too_large(W->N) || too_large(W->K)) return BSL_ERR_UNSUPPORTED;
+    if (!W->codes || !aligned(W->codes, 16) || !W->scales || !aligned(W->scales, 16) || !W->status ||
+        !aligned(W->status, 4))
+        return BSL_ERR_INVALID_ARG;
+    return BSL_OK;
+}
+
 namespace {
 // Device status word -> host, cleared (synchronous).
 bsl_status read_status(int32_t *status, int32_t *status_host, void *stream)
@@ -659,6 +670,94 @@ bsl_status bsl_mx4_linear(const void *X, int32_t T, const int32_t *offsets, cons
 }
 
 bsl_status bsl_mx4_get_status(const bsl_mx4 *W, int32_t *status_host, void *stream)
+{
+    if (!W || !W->status || !status_host) return BSL_ERR_INVALID_ARG;
+    return read_status(W->status, status_host, stream);
+}
+
+bsl_status bsl_fp8_quantize(const void *X, int64_t planes, int64_t rows, int32_t K, int32_t block_rows, uint8_t *codes,
+                            float *scales, void *stream)
+{
+    if (planes < 0 || rows < 0 || K <= 0 || K % 16 || (block_rows != 1 && block_rows != 128)) return BSL_ERR_INVALID_ARG;
+    if (planes == 0 || rows == 0) return BSL_OK;
+    if (check_matrix(X, rows) != BSL_OK || check_matrix(codes, rows) != BSL_OK || check_matrix(scales, rows) != BSL_OK)
+        return BSL_ERR_INVALID_ARG;
+    if (too_large(K) || rows > INT64_MAX / K / planes) return BSL_ERR_UNSUPPORTED;
+    DeviceGuard guard;
+    BSL_TRY(guard.bind(X));
+    BSL_TRY(check_device());
+    return launch_fp8_quantize(X, planes, rows, K, block_rows == 128, codes, scales, static_cast<cudaStream_t>(stream));
+}
+
+bsl_status bsl_fp8_dequantize(const uint8_t *codes, const float *scales, int64_t planes, int64_t rows, int32_t K,
+                              int32_t block_rows, void *X, void *stream)
+{
+    if (planes < 0 || rows < 0 || K <= 0 || K % 16 || (block_rows != 1 && block_rows != 128)) return BSL_ERR_INVALID_ARG;
+    if (planes == 0 || rows == 0) return BSL_OK;
+    if (check_matrix(X, rows) != BSL_OK || check_matrix(codes, rows) != BSL_OK || check_matrix(scales, rows) != BSL_OK)
+        return BSL_ERR_INVALID_ARG;
+    if (too_large(K) || rows > INT64_MAX / K / planes) return BSL_ERR_UNSUPPORTED;
+    DeviceGuard guard;
+    BSL_TRY(guard.bind(X));
+    BSL_TRY(check_device());
+    return launch_fp8_dequantize(codes, scales, planes, rows, K, block_rows == 128, X, static_cast<cudaStream_t>(stream));
+}
+
+namespace {
+// What the 8-bit products ask of their arguments; `transposed`: the input gradient, whose rows are N long.
+bsl_status check_fp8_call(int32_t T, const int32_t *offsets, const bsl_fp8 *W, int32_t transposed, const void *bias,
+                          const void *out)
+{
+    BSL_TRY(check_fp8(W));
+    if (T < 0 || (!offsets && W->E != 1) || !aligned(offsets, 4) || (bias && !aligned(bias, 16)) || (transposed && bias) ||
+        (transposed && W->N % 16) || check_matrix(out, T) != BSL_OK)
+        return BSL_ERR_INVALID_ARG;
+    return too_large(T) ? BSL_ERR_UNSUPPORTED : BSL_OK;
+}
+
+int32_t fp8_depth(const bsl_fp8 *W, int32_t transposed) { return transposed ? W->N : W->K; }
+}  // namespace
+
+bsl_status bsl_fp8_product(const uint8_t *codes, const float *scales, int32_t T, const int32_t *offsets, const bsl_fp8 *W,
+                           int32_t transposed, const void *bias, void *out, int32_t zero_rest, void *stream)
+{
+    BSL_TRY(check_fp8_call(T, offsets, W, transposed, bias, out));
+    if (check_matrix(codes, T) != BSL_OK || check_matrix(scales, T) != BSL_OK) return BSL_ERR_INVALID_ARG;
+    if (T == 0) return BSL_OK;
+    DeviceGuard guard;
+    BSL_TRY(guard.bind(codes));
+    BSL_TRY(check_device());
+    return launch_fp8(codes, scales, T, offsets, W, transposed, bias, out, zero_rest, static_cast<cudaStream_t>(stream));
+}
+
+size_t bsl_fp8_workspace_bytes(int32_t T, const bsl_fp8 *W, int32_t transposed)
+{
+    if (check_fp8(W) != BSL_OK || T <= 0 || (transposed && W->N % 16)) return 0;
+    const size_t depth = fp8_depth(W, transposed);
+    return T * depth + T * ((depth + 127) / 128) * 4;
+}
+
+bsl_status bsl_fp8_linear(const void *A, int32_t T, const int32_t *offsets, const bsl_fp8 *W, int32_t transposed,
+                          const void *bias, void *out, int32_t zero_rest, void *workspace, size_t workspace_bytes,
+                          void *stream)
+{
+    BSL_TRY(check_fp8_call(T, offsets, W, transposed, bias, out));
+    if (check_matrix(A, T) != BSL_OK || check_matrix(workspace, T) != BSL_OK ||
+        workspace_bytes < bsl_fp8_workspace_bytes(T, W, transposed))
+        return BSL_ERR_INVALID_ARG;
+    if (T == 0) return BSL_OK;
+    DeviceGuard guard;
+    BSL_TRY(guard.bind(A));
+    BSL_TRY(check_device());
+    const int32_t depth = fp8_depth(W, transposed);
+    uint8_t *codes = static_cast<uint8_t *>(workspace);
+    float *scales = reinterpret_cast<float *>(codes + static_cast<size_t>(T) * depth);  // depth is a multiple of 16
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    BSL_TRY(launch_fp8_quantize(A, 1, T, depth, false, codes, scales, s));
+    return launch_fp8(codes, scales, T, offsets, W, transposed, bias, out, zero_rest, s);
+}
+
+bsl_status bsl_fp8_get_status(const bsl_fp8 *W, int32_t *status_host, void *stream)
 {
     if (!W || !W->status || !status_host) return BSL_ERR_INVALID_ARG;
     return read_status(W->status, status_host, stream);

@@ -72,6 +72,11 @@ __device__ __forceinline__ V load_global(const V *p)
     return v;
 }
 
+__device__ __forceinline__ float load_float(const float *p)
+{
+    return __uint_as_float(load_global(reinterpret_cast<const uint32_t *>(p)));
+}
+
 // The same for data that is read once: 16 bytes that take no room in L1.
 __device__ __forceinline__ uint4 load_stream(const void *p)
 {

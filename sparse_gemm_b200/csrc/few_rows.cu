@@ -1,4 +1,4 @@
-// few_rows.cu -- forward of the expert (grouped) layer and of the 4-bit layer for
+// few_rows.cu -- forward of the expert (grouped) layer and of the 4- and 8-bit layers for
 // a few rows in all (single tokens, up to 32): Y[t] = X[t] . W[e]^T + bias[e].
 //
 // Each weight row that is used is read once and little else matters: bytes,
@@ -354,6 +354,96 @@ __global__ void __launch_bounds__(kWarps * 32) k_few_rows4(const FewArgs a)
     add_parts<NT>(a, f, n0, part);
 }
 
+// ---------------------------------------------------------------- 8 bits
+
+__device__ __forceinline__ void mma_e4m3(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1)
+{
+    asm volatile(
+        "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// A warp's step is one block of 128 k, whose sum gets its scales when it is
+// complete: the weight's is one number for the 16 features, the rows' come two
+// to a lane.  The codes go to the MMA as they lie.
+template <int NT>
+__global__ void __launch_bounds__(kWarps * 32, 3) k_few_rows8(const FewArgs a)
+{
+    __shared__ float part[kWarps][NT * kRows][kFeatures];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int li = blockIdx.x / a.blocks, n0 = (blockIdx.x - li * a.blocks) * kFeatures;
+    dependents_may_launch();
+    wait_for_prior_grid();
+    int front, back;
+    bool bad;
+    const Found f = find_expert(a, li, front, back, bad);
+    if (bad && blockIdx.x == 0 && threadIdx.x == 0) set_status(a.status, BSL_ERR_INVALID_ARG);
+    if (a.zero_rest && li == 0) zero_rest_rows(a, n0, front, back);
+    if (f.e < 0) return;
+
+    const int64_t bytes = a.K;
+    const bool in0 = n0 + g < a.N, in1 = n0 + g + 8 < a.N;
+    const uint8_t *w0 = a.W + (static_cast<int64_t>(f.e) * a.N + n0 + g) * bytes + 16 * t, *w1 = w0 + 8 * bytes;
+    const uint8_t *x = a.X + static_cast<int64_t>(f.first + g) * bytes + 16 * t;
+    const int blocks = (a.K + 127) / 128;
+    const float *ws = reinterpret_cast<const float *>(a.w_scales) +
+                      (static_cast<int64_t>(f.e) * ((a.N + 127) / 128) + n0 / 128) * blocks;
+    const float *xs = reinterpret_cast<const float *>(a.x_scales) + static_cast<int64_t>(f.first + 2 * t) * blocks;
+    constexpr int U = NT == 4 ? 1 : 2;
+    float acc[NT][4] = {};
+    for (int b0 = warp; b0 < blocks; b0 += kWarps * U) {
+        uint4 va[U][2], vb[U][2], vx[U][2][NT];
+        float sw[U], sx[U][NT][2];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int b = b0 + u * kWarps;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int64_t at = static_cast<int64_t>(b) * 128 + 64 * h;
+                const bool in = at + 16 * t < a.K;
+                va[u][h] = vb[u][h] = make_uint4(0, 0, 0, 0);
+                if (in && in0) va[u][h] = load_stream(w0 + at);
+                if (in && in1) vb[u][h] = load_stream(w1 + at);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    vx[u][h][n] = make_uint4(0, 0, 0, 0);
+                    if (in && g + 8 * n < f.rows)
+                        vx[u][h][n] = load_global(reinterpret_cast<const uint4 *>(x + n * 8 * bytes + at));
+                }
+            }
+            sw[u] = b < blocks ? load_float(ws + b) : 0.f;
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    sx[u][n][i] = b < blocks && 8 * n + 2 * t + i < f.rows
+                                      ? load_float(xs + (8 * n + i) * static_cast<int64_t>(blocks) + b) : 0.f;
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                float c[4] = {};
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    mma_e4m3(c, va[u][h].x, vb[u][h].x, va[u][h].y, vb[u][h].y, vx[u][h][n].x, vx[u][h][n].y);
+                    mma_e4m3(c, va[u][h].z, vb[u][h].z, va[u][h].w, vb[u][h].w, vx[u][h][n].z, vx[u][h][n].w);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[n][i] += c[i] * (sw[u] * sx[u][n][i & 1]);
+            }
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) part[warp][8 * n + 2 * t + (i & 1)][g + 8 * (i >> 1)] = acc[n][i];
+    __syncthreads();
+    add_parts<NT>(a, f, n0, part);
+}
+
 bsl_status launch(void (*kern)(const FewArgs), FewArgs &a, int smem, cudaStream_t s)
 {
     a.blocks = (a.N + kFeatures - 1) / kFeatures;
@@ -393,6 +483,13 @@ bool few_rows4(int32_t T, const bsl_mx4 *W)
     return (T <= kRows && bytes <= (12ll << 20)) || (T <= 2 * kRows && bytes <= (4ll << 20));
 }
 
+// 8 bits, products alone.
+bool few_rows8(int32_t T, const bsl_fp8 *W)
+{
+    const int64_t bytes = static_cast<int64_t>(T < W->E ? T : W->E) * W->N * W->K;
+    return T <= kRows || (T <= 2 * kRows && bytes <= (32ll << 20)) || (T <= 4 * kRows && bytes <= 20000000);
+}
+
 bsl_status launch_few_rows(const void *X, int32_t T, const int32_t *offsets, const bsl_grouped *W, const void *bias,
                            void *Y, int32_t zero_rest, cudaStream_t s)
 {
@@ -408,6 +505,15 @@ bsl_status launch_few_rows4(const uint8_t *xc, const uint8_t *xs, int32_t T, con
     FewArgs a = {W->codes, W->scales, xc, xs, static_cast<const __nv_bfloat16 *>(bias), static_cast<__nv_bfloat16 *>(Y),
                  offsets, W->status, T, W->E, W->N, W->K, 0, zero_rest};
     return T <= kRows ? launch4<1>(a, s) : launch4<2>(a, s);
+}
+
+bsl_status launch_few_rows8(const uint8_t *xc, const float *xs, int32_t T, const int32_t *offsets, const bsl_fp8 *W,
+                            const void *bias, void *Y, int32_t zero_rest, cudaStream_t s)
+{
+    FewArgs a = {W->codes, reinterpret_cast<const uint8_t *>(W->scales), xc, reinterpret_cast<const uint8_t *>(xs),
+                 static_cast<const __nv_bfloat16 *>(bias), static_cast<__nv_bfloat16 *>(Y), offsets, W->status,
+                 T, W->E, W->N, W->K, 0, zero_rest};
+    return launch(T <= kRows ? k_few_rows8<1> : T <= 2 * kRows ? k_few_rows8<2> : k_few_rows8<4>, a, 0, s);
 }
 
 }  // namespace bsl

@@ -109,6 +109,7 @@ bsl_status check_bsr(const bsl_bsr *W);
 bsl_status check_semi24(const bsl_semi24 *W);
 bsl_status check_grouped(const bsl_grouped *W);
 bsl_status check_mx4(const bsl_mx4 *W);
+bsl_status check_fp8(const bsl_fp8 *W);
 uint64_t wait_timeout_ns();
 bsl_status cuda_status(cudaError_t e);
 void note_driver_error(int code);
@@ -151,12 +152,15 @@ bsl_status launch_grouped_dw(const void *dY, const void *X, int32_t T, const int
 bsl_status launch_grouped_bias_grad(const void *dY, int32_t T, const int32_t *offsets, int32_t E, int32_t N, void *db,
                                     cudaStream_t s);
 
-// The forwards of both layers for calls of few rows, where these are true.
+// The forwards of the layers for calls of few rows, where these are true.
 bool few_rows(int32_t T, const bsl_grouped *W);
 bool few_rows4(int32_t T, const bsl_mx4 *W);
+bool few_rows8(int32_t T, const bsl_fp8 *W);
 bsl_status launch_few_rows(const void *X, int32_t T, const int32_t *offsets, const bsl_grouped *W, const void *bias,
                            void *Y, int32_t zero_rest, cudaStream_t s);
 bsl_status launch_few_rows4(const uint8_t *xc, const uint8_t *xs, int32_t T, const int32_t *offsets, const bsl_mx4 *W,
+                            const void *bias, void *Y, int32_t zero_rest, cudaStream_t s);
+bsl_status launch_few_rows8(const uint8_t *xc, const float *xs, int32_t T, const int32_t *offsets, const bsl_fp8 *W,
                             const void *bias, void *Y, int32_t zero_rest, cudaStream_t s);
 
 // Microscaled 4-bit: conversion, and the product (offsets null: one group of all rows).
@@ -164,6 +168,15 @@ bsl_status launch_mx4_quantize(const void *X, int64_t elems, uint8_t *codes, uin
 bsl_status launch_mx4_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t elems, void *X, cudaStream_t s);
 bsl_status launch_mx4_fwd(const uint8_t *xc, const uint8_t *xs, int32_t T, const int32_t *offsets, const bsl_mx4 *W,
                           const void *bias, void *Y, int32_t zero_rest, cudaStream_t s);
+
+// 8 bits with a scale for each block of 128: conversion, and the products (offsets null: one group of all rows;
+// transposed: the input gradient).
+bsl_status launch_fp8_quantize(const void *X, int64_t planes, int64_t rows, int32_t K, bool tiles, uint8_t *codes,
+                               float *scales, cudaStream_t s);
+bsl_status launch_fp8_dequantize(const uint8_t *codes, const float *scales, int64_t planes, int64_t rows, int32_t K,
+                                 bool tiles, void *X, cudaStream_t s);
+bsl_status launch_fp8(const uint8_t *codes, const float *scales, int32_t T, const int32_t *offsets, const bsl_fp8 *W,
+                      bool transposed, const void *bias, void *out, int32_t zero_rest, cudaStream_t s);
 
 bsl_status launch_debug_wait(int32_t *status, uint64_t timeout_ns, cudaStream_t s);
 
