@@ -464,6 +464,59 @@ BSL_API size_t bsl_fp8_workspace_bytes(int32_t T, const bsl_fp8 *W, int32_t tran
  * *status_host (a bsl_status value) and resets it to BSL_OK. */
 BSL_API bsl_status bsl_fp8_get_status(const bsl_fp8 *W, int32_t *status_host, void *stream);
 
+/* ---------------------------------------------------------------- router
+ *
+ * From logits [T][E] (logits_type 0: float, 1: bf16) the k experts with the largest ones of each token, in
+ * descending order, ties to the lowest expert (-0 equals 0; a NaN comes after everything), and their weights:
+ * with the scores s_i = exp(l_i) / sum_j exp(l_j) (score 0) or 1 / (1 + exp(-l_i)) (score 1), and S the sum
+ * of the chosen scores, factor * s or (renormalize not 0) factor * s / S.  A logit of -inf has the score 0,
+ * also in a row that holds nothing else; then the row's weights are 0.  Softmax rows with a NaN or +inf give NaN.
+ * 1 <= k <= E <= BSL_GROUPED_MAX_EXPERTS, k <= BSL_ROUTE_MAX_K. */
+#define BSL_ROUTE_MAX_K 32
+
+/* experts int32 [T][k], weights float [T][k].  offsets and order (both, or both NULL): the pairs t * k + j
+ * sorted by expert, in order int32 [T * k], ascending within an expert; expert e's are order[offsets[e]] ..
+ * order[offsets[e + 1] - 1], offsets int32 [E + 1], as bsl_grouped_forward takes them for the rows
+ * X[order / k].  workspace: bsl_route_workspace_bytes(T, E, k) bytes of device scratch, 4-byte aligned, written
+ * before it is read; calls that use one workspace must not overlap on the GPU (not used without order).
+ * T >= 0. */
+BSL_API bsl_status bsl_route(const void *logits, int32_t logits_type, int32_t T, int32_t E, int32_t k, int32_t score,
+                             int32_t renormalize, float factor, int32_t *experts, float *weights, int32_t *offsets,
+                             int32_t *order, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Scratch bytes of bsl_route with order (0 for arguments that it refuses). */
+BSL_API size_t bsl_route_workspace_bytes(int32_t T, int32_t E, int32_t k);
+
+/* dlogits [T][E], of the logits' type: the gradient of the logits from the weights' dweights float [T][k], for
+ * the choices `experts` that bsl_route made of them (choices outside 0 .. E - 1 count for nothing). */
+BSL_API bsl_status bsl_route_backward(const float *dweights, const void *logits, int32_t logits_type, int32_t T, int32_t E,
+                                      int32_t k, const int32_t *experts, int32_t score, int32_t renormalize, float factor,
+                                      void *dlogits, void *stream);
+
+/* ---------------------------------------------------------------- whole expert layer, few tokens
+ *
+ * Y [T][H]: Y[t] = sum_j weights[t][j] * W2[e] . h with e = experts[t][j] and
+ *     h = silu(G[e] . X[t]) * (U[e] . X[t]),  W13[e] = (G[e]; U[e]) [2 I][H],  W2[e] [H][I],
+ * silu(g) = g / (1 + exp(-g)), in two kernels; bf16 X [T][H], Y and h (times the weight, rounded once), fp32
+ * sums.  T <= BSL_MOE_MAX_TOKENS (more are routed, sorted and multiplied by the grouped products), k <=
+ * BSL_ROUTE_MAX_K.  A choice outside 0 .. E - 1 counts for nothing and is reported as BSL_ERR_INVALID_ARG in
+ * W13's device status; an expert that a token chose more than once counts once, with the sum of its weights.
+ * workspace: bsl_moe_workspace_bytes(T, k, I) bytes of device scratch, 16-byte aligned, written before it is
+ * read; calls that use one workspace must not overlap on the GPU. */
+#define BSL_MOE_MAX_TOKENS 64
+
+BSL_API bsl_status bsl_moe_forward(const void *X, int32_t T, const int32_t *experts, const float *weights, int32_t k,
+                                   const bsl_grouped *W13, const bsl_grouped *W2, void *Y, void *workspace,
+                                   size_t workspace_bytes, void *stream);
+
+/* The same with weights in 8 bits; X and h stay in bf16. */
+BSL_API bsl_status bsl_moe_forward_fp8(const void *X, int32_t T, const int32_t *experts, const float *weights, int32_t k,
+                                       const bsl_fp8 *W13, const bsl_fp8 *W2, void *Y, void *workspace,
+                                       size_t workspace_bytes, void *stream);
+
+/* Scratch bytes of both (0 for T, k or I <= 0). */
+BSL_API size_t bsl_moe_workspace_bytes(int32_t T, int32_t k, int32_t I);
+
 /* SYNCHRONOUS: waits for the stream, copies the device status word of W to
  * *status_host (a bsl_status value) and resets it to BSL_OK. */
 BSL_API bsl_status bsl_get_device_status(const bsl_bsr *W, int32_t *status_host, void *stream);

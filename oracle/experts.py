@@ -141,3 +141,85 @@ def fp8_product(A, As, W, Ws, transposed=False):
     a, w = fp8_values(A, As), fp8_values(W, Ws)
     w = w if transposed else w.T
     return a @ w, np.abs(a) @ np.abs(w)
+
+
+def route(logits, k, score="softmax", renormalize=True, factor=1.0):
+    """Logits [T, E], fp64 -> (experts [T, k], weights [T, k], offsets [E + 1], order [T k]), plain Python choices.
+
+    Descending by logit, ties to the lowest expert, NaN after everything; -inf scores 0, in rows of nothing else too."""
+    T, E = logits.shape
+    experts, weights = np.zeros((T, k), dtype=np.int64), np.zeros((T, k))
+    for t in range(T):
+        row = [float(v) for v in logits[t]]
+        best = sorted(range(E), key=lambda e: (math.isnan(row[e]), -row[e] if not math.isnan(row[e]) else 0.0, e))[:k]
+        experts[t] = best
+        if score == "softmax":
+            top = max(v for v in row) if not any(map(math.isnan, row)) else math.nan
+            if top == -math.inf:
+                continue
+            if math.isnan(top) or top == math.inf:
+                weights[t] = math.nan
+                continue
+            s = np.array([math.exp(row[e] - top) for e in best])
+            weights[t] = s / (s.sum() if renormalize else sum(math.exp(v - top) for v in row))
+        else:
+            s = np.array([math.nan if math.isnan(row[e]) else 0.0 if row[e] < -700 else 1 / (1 + math.exp(-row[e])) for e in best])
+            weights[t] = s / (s.sum() or 1.0) if renormalize else s
+    flat = experts.ravel()
+    order = np.array(sorted(range(T * k), key=lambda p: (flat[p], p)), dtype=np.int64)
+    offsets = np.array([int((flat < e).sum()) for e in range(E + 1)])
+    return experts, weights * factor, offsets, order
+
+
+def route_backward(g, logits, experts, score="softmax", renormalize=True, factor=1.0):
+    """(gradient of finite logits, S) for the weights' gradient g [T, k]; S the sum of |term|."""
+    T, E = logits.shape
+    if score == "softmax":
+        s = np.exp(logits - logits.max(axis=1, keepdims=True))
+        s /= s.sum(axis=1, keepdims=True)
+    else:
+        s = 1 / (1 + np.exp(-logits))
+    grad, S = np.zeros((T, E)), np.zeros((T, E))
+    for t in range(T):
+        chosen = list(experts[t])
+        p = s[t, chosen]
+        P = p.sum() if renormalize else 1.0
+        # dw_j / ds_i over the choices
+        jac = np.eye(len(chosen)) / P - (np.outer(p, np.ones(len(chosen))) / P ** 2 if renormalize else 0.0)
+        terms = g[t][:, None] * jac
+        ds, dS = np.zeros(E), np.zeros(E)
+        ds[chosen], dS[chosen] = terms.sum(0), np.abs(g[t] / P) + (np.abs(g[t] * p).sum() / P ** 2 if renormalize else 0.0)
+        if score == "softmax":
+            grad[t] = s[t] * (ds - (ds * s[t]).sum())
+            S[t] = s[t] * (dS + (dS * s[t]).sum())
+        else:
+            grad[t] = ds * s[t] * (1 - s[t])
+            S[t] = dS * s[t] * (1 - s[t])
+    return grad * factor, S * abs(factor)
+
+
+def moe_forward(X, W13, W2, experts, weights):
+    """X [T, H], W13 [E, 2 I, H] (gate, up), W2 [E, H, I], fp64 -> (Y, bound): the layer's output and how far one
+    that rounds h to bf16 and sums in fp32 may be from it, before its own rounding.
+
+    Sums of n terms are off by (n / 16 + 8) 2^-22 of their absolute terms (tests/_experts.py); silu has a slope of at
+    most 1.1 and its exponential is off by 2^-18 (a fast one, |g| <= 40); the product with the weight by 2^-22 more;
+    h is rounded by 2^-8."""
+    T, H = X.shape
+    I = W2.shape[2]
+    Y, B = np.zeros((T, H)), np.zeros((T, H))
+    with np.errstate(over="ignore", invalid="ignore"):
+        for t in range(T):
+            for e, w in zip(experts[t], weights[t]):
+                if not 0 <= e < W13.shape[0]:
+                    continue
+                z, S = W13[e] @ X[t], (H / 16 + 8) * 2.0 ** -22 * (np.abs(W13[e]) @ np.abs(X[t]))
+                g, u = z[:I], z[I:]
+                a = g / (1 + np.exp(-g))
+                off = 1.1 * S[:I] * (np.abs(u) + S[I:]) + np.abs(a) * S[I:] + (2.0 ** -18 + 2.0 ** -21) * np.abs(a * u)
+                h = w * a * u
+                Y[t] += W2[e] @ h
+                terms = np.abs(W2[e])
+                B[t] += terms @ (2.0 ** -8 * np.abs(h) + (1 + 2.0 ** -8) * abs(w) * off)
+                B[t] += (I * len(experts[t]) / 16 + 32) * 2.0 ** -22 * 1.01 * (terms @ (np.abs(h) + abs(w) * off))
+    return Y, B

@@ -17,6 +17,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+from typing import NamedTuple
 
 import torch
 
@@ -34,6 +35,7 @@ __all__ = [
     "Mx4Linear", "GroupedMx4Linear",
     "Fp8Tensor", "quantize_fp8", "dequantize_fp8", "forward_fp8", "grouped_forward_fp8", "backward_input_fp8",
     "grouped_backward_input_fp8", "fp8_status", "Fp8LinearFunction", "Fp8Linear", "GroupedFp8Linear",
+    "Routing", "route", "route_backward", "RouteFunction", "moe_forward",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -80,8 +82,10 @@ class _FP8(ctypes.Structure):
                 ("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("status", ctypes.c_void_p)]
 
 
-# experts of a grouped layer (BSL_GROUPED_MAX_EXPERTS in include/bsl.h)
+# experts of a grouped layer, choices of a token, tokens of moe_forward (BSL_* in include/bsl.h)
 GROUPED_MAX_EXPERTS = 1024
+ROUTE_MAX_K = 32
+MOE_MAX_TOKENS = 64
 
 # int32 entries of bsl_bsr.sbounds (BSL_SBOUNDS_LEN in include/bsl.h)
 SBOUNDS_LEN = 1026
@@ -98,6 +102,7 @@ def library() -> ctypes.CDLL:
             raise RuntimeError(f"{LIB_PATH} is missing: build it with `python -m sparse_gemm_b200.build`")
         lib = ctypes.CDLL(LIB_PATH)
         P, I32, SZ, U64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t, ctypes.c_uint64
+        F32 = ctypes.c_float
         I64, GP, XP = ctypes.c_int64, ctypes.POINTER(_GROUPED), ctypes.POINTER(_MX4)
         FP = ctypes.POINTER(_FP8)
         BP = ctypes.POINTER(_BSR)
@@ -142,6 +147,12 @@ def library() -> ctypes.CDLL:
             "bsl_fp8_product": (ctypes.c_int, [P, P, I32, P, FP, I32, P, P, I32, P]),
             "bsl_fp8_linear": (ctypes.c_int, [P, I32, P, FP, I32, P, P, I32, P, SZ, P]),
             "bsl_fp8_workspace_bytes": (SZ, [I32, FP, I32]),
+            "bsl_route": (ctypes.c_int, [P, I32, I32, I32, I32, I32, I32, F32, P, P, P, P, P, SZ, P]),
+            "bsl_route_workspace_bytes": (SZ, [I32, I32, I32]),
+            "bsl_route_backward": (ctypes.c_int, [P, P, I32, I32, I32, I32, P, I32, I32, F32, P, P]),
+            "bsl_moe_forward": (ctypes.c_int, [P, I32, P, P, I32, GP, GP, P, P, SZ, P]),
+            "bsl_moe_forward_fp8": (ctypes.c_int, [P, I32, P, P, I32, FP, FP, P, P, SZ, P]),
+            "bsl_moe_workspace_bytes": (SZ, [I32, I32, I32]),
             "bsl_fp8_get_status": (ctypes.c_int, [FP, ctypes.POINTER(I32), P]),
         }
         for name, (res, args) in sig.items():
@@ -1379,3 +1390,141 @@ class GroupedFp8Linear(Fp8Linear):
 
     def forward(self, x: torch.Tensor, offsets: torch.Tensor) -> torch.Tensor:
         return self._product(x, offsets)
+
+
+# ---------------------------------------------------------------- router and whole expert layer
+
+
+class Routing(NamedTuple):
+    """What :func:`route` returns: ``experts`` int32 [T, k], descending by logit, ``weights`` float32
+    [T, k], and the pairs t * k + j sorted by expert: ``order`` int32 [T * k], of which expert e owns
+    ``offsets[e]`` .. ``offsets[e + 1]`` (int32 [E + 1]), or None for both."""
+    experts: torch.Tensor
+    weights: torch.Tensor
+    offsets: torch.Tensor | None
+    order: torch.Tensor | None
+
+
+_SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+def _route_args(logits, k: int, score: str):
+    if not (isinstance(logits, torch.Tensor) and logits.is_cuda and logits.dim() == 2
+            and logits.dtype in (torch.float32, torch.bfloat16)):
+        raise TypeError("logits must be a 2-D float32 or bfloat16 CUDA tensor")
+    if not logits.is_contiguous():
+        raise ValueError("logits must be contiguous")
+    T, E = logits.shape
+    if not 1 <= E <= GROUPED_MAX_EXPERTS or not 1 <= k <= min(E, ROUTE_MAX_K):
+        raise ValueError("1 <= k <= experts is needed, with at most 32 choices and 1024 experts")
+    if T * k >= 2 ** 31:
+        raise ValueError(f"{T} x {k} choices, the limit is 2^31 - 1")
+    if score not in _SCORES:
+        raise ValueError("score must be 'softmax' or 'sigmoid'")
+    return T, E, int(logits.dtype is torch.bfloat16), _SCORES[score]
+
+
+def _route(logits, k, score, renormalize, factor, sort) -> Routing:
+    T, E, half, kind = _route_args(logits, k, score)
+    experts = logits.new_empty((T, k), dtype=torch.int32)
+    weights = logits.new_empty((T, k), dtype=torch.float32)
+    offsets = order = ws = None
+    lib, ptrs, nbytes = library(), (None, None, None), 0
+    if sort:
+        held = logits.new_empty(E + 1 + T * k, dtype=torch.int32)
+        offsets, order = held[:E + 1], held[E + 1:]
+        nbytes = lib.bsl_route_workspace_bytes(T, E, k)
+        ws = logits.new_empty(nbytes // 4, dtype=torch.int32) if nbytes else None
+        at = held.data_ptr()
+        ptrs = (at, at + 4 * (E + 1), None if ws is None else ws.data_ptr())
+    _check(lib.bsl_route(logits.data_ptr(), half, T, E, k, kind, renormalize, factor, experts.data_ptr(), weights.data_ptr(),
+                         *ptrs, nbytes, _stream(logits)), "bsl_route")
+    return Routing(experts, weights, offsets, order)
+
+
+def route(logits: torch.Tensor, k: int, score: str = "softmax", renormalize: bool = True, factor: float = 1.0,
+          sort: bool = True) -> Routing:
+    """The ``k`` experts with the largest logits [T, E] (float32 or bfloat16) of each token, ties to the
+    lowest expert, and their weights: ``factor`` times the softmax over all experts, or each logit's
+    sigmoid, divided by the sum over the token's choices if ``renormalize``.  With ``sort`` also the
+    (token, choice) pairs sorted by expert, as the grouped products take them::
+
+        r = route(logits, k)
+        rows = X[r.order // k]                               # sorted by expert
+        Y = grouped_forward(rows, Wg, r.offsets)
+        out = torch.zeros_like(X).index_add_(0, r.order // k, Y * r.weights.flatten()[r.order, None].to(Y.dtype))
+
+    Logits of -inf weigh 0, in a row of nothing else too.  The weights' gradient flows to the logits."""
+    if logits.requires_grad and torch.is_grad_enabled():
+        return Routing(*RouteFunction.apply(logits, k, score, bool(renormalize), float(factor), sort))
+    return _route(logits, k, score, bool(renormalize), float(factor), sort)
+
+
+def route_backward(dweights: torch.Tensor, logits: torch.Tensor, experts: torch.Tensor, score: str = "softmax",
+                   renormalize: bool = True, factor: float = 1.0) -> torch.Tensor:
+    """The gradient of :func:`route`'s logits, of their type, from that of its weights (float32 [T, k])
+    and its ``experts``; the other arguments as given there."""
+    _tensor_arg(experts, "experts", (None, None), torch.int32)
+    T, E, half, kind = _route_args(logits, experts.shape[1], score)
+    _tensor_arg(experts, "experts", (T, experts.shape[1]), torch.int32, logits)
+    _tensor_arg(dweights, "dweights", tuple(experts.shape), torch.float32, logits)
+    dlogits = torch.empty_like(logits)
+    _check(library().bsl_route_backward(dweights.data_ptr(), logits.data_ptr(), half, T, E, experts.shape[1],
+                                        experts.data_ptr(), kind, bool(renormalize), float(factor), dlogits.data_ptr(),
+                                        _stream(logits)), "bsl_route_backward")
+    return dlogits
+
+
+class RouteFunction(torch.autograd.Function):
+    """Autograd wrapper of the router: :func:`route`, and the logits' gradient from the weights'."""
+
+    @staticmethod
+    def forward(ctx, logits, k, score, renormalize, factor, sort):
+        r = _route(logits, k, score, renormalize, factor, sort)
+        ctx.save_for_backward(logits, r.experts)
+        ctx.how = (score, renormalize, factor)
+        ctx.mark_non_differentiable(*(t for t in (r.experts, r.offsets, r.order) if t is not None))
+        return tuple(r)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, _experts, dweights, _offsets, _order):
+        logits, experts = ctx.saved_tensors
+        return route_backward(dweights.contiguous(), logits, experts, *ctx.how), None, None, None, None, None
+
+
+def moe_forward(X: torch.Tensor, W13, W2, experts: torch.Tensor, weights: torch.Tensor,
+                out: torch.Tensor | None = None) -> torch.Tensor:
+    """A whole mixture-of-experts layer for up to 64 tokens, bf16 [T, H], in two kernels::
+
+        Y[t] = sum_j weights[t, j] W2[e] (silu(G X[t]) * (U X[t])),  e = experts[t, j], W13[e] = (G; U)
+
+    ``W13`` [E, 2 I, H] (gate rows, then up rows) and ``W2`` [E, H, I] are two :class:`GroupedWeight` or
+    two :class:`Fp8Tensor` in tiles; ``experts`` int32 and ``weights`` float32 [T, k] as :func:`route`
+    gives them.  Experts out of range count for nothing and are reported in W13's status word
+    (:func:`grouped_status`, :func:`fp8_status`).  For inference: no gradient."""
+    fp8 = isinstance(W13, Fp8Tensor)
+    if not isinstance(W13, (Fp8Tensor, GroupedWeight)) or not isinstance(W2, Fp8Tensor if fp8 else GroupedWeight):
+        raise TypeError("W13 and W2 must be two GroupedWeight or two Fp8Tensor")
+    r13, r2 = W13.cref(), W2.cref()
+    (E, N13, H), (E2, H2, I) = (W13.shape, W2.shape) if fp8 and len(W13.shape) == len(W2.shape) == 3 else         ((w._c.E, w._c.N, w._c.K) for w in (W13, W2))
+    if E != E2 or H != H2 or N13 != 2 * I:
+        raise ValueError(f"W13 [{E}, {N13}, {H}] and W2 [{E2}, {H2}, {I}] must be [E, 2 I, H] and [E, H, I]")
+    held13, held2 = (W13.codes, W2.codes) if fp8 else (W13.weight, W2.weight)
+    if held13.get_device() != held2.get_device():
+        raise ValueError(f"W2 must be on {held13.device}")
+    _tensor_arg(X, "X", (None, H), torch.bfloat16, held13)
+    T = X.shape[0]
+    if T > MOE_MAX_TOKENS:
+        raise ValueError(f"{T} tokens, the limit is {MOE_MAX_TOKENS}: route, sort and multiply by grouped_forward")
+    _tensor_arg(experts, "experts", (T, None), torch.int32, X)
+    k = experts.shape[1]
+    if not 1 <= k <= ROUTE_MAX_K:
+        raise ValueError("a token has 1 to 32 experts")
+    _tensor_arg(weights, "weights", (T, k), torch.float32, X)
+    Y = _out_arg(out, (T, H), X, *((W13, W2) if fp8 else (held13, held2)), experts, weights)
+    ws = _new(X, T * k * I)   # bsl_moe_workspace_bytes
+    fn = library().bsl_moe_forward_fp8 if fp8 else library().bsl_moe_forward
+    _check(fn(X.data_ptr(), T, experts.data_ptr(), weights.data_ptr(), k, r13, r2, Y.data_ptr(), ws.data_ptr(), 2 * T * k * I,
+              _stream(X)), "bsl_moe_forward_fp8" if fp8 else "bsl_moe_forward")
+    return Y

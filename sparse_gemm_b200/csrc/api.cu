@@ -763,6 +763,117 @@ bsl_status bsl_fp8_get_status(const bsl_fp8 *W, int32_t *status_host, void *stre
     return read_status(W->status, status_host, stream);
 }
 
+namespace {
+bsl_status check_route(int32_t T, int32_t E, int32_t k)
+{
+    if (T < 0 || E <= 0 || k <= 0 || k > E) return BSL_ERR_INVALID_ARG;
+    if (E > BSL_GROUPED_MAX_EXPERTS || k > BSL_ROUTE_MAX_K || too_large(T) || static_cast<int64_t>(T) * k > INT32_MAX)
+        return BSL_ERR_UNSUPPORTED;
+    return BSL_OK;
+}
+
+// Logits as far as their type wants them aligned.
+bool logits_ok(const void *p, int32_t type) { return p && (type == 0 || type == 1) && aligned(p, type ? 2 : 4); }
+}  // namespace
+
+size_t bsl_route_workspace_bytes(int32_t T, int32_t E, int32_t k)
+{
+    return check_route(T, E, k) != BSL_OK ? 0 : route_workspace_bytes(T, E);
+}
+
+bsl_status bsl_route(const void *logits, int32_t logits_type, int32_t T, int32_t E, int32_t k, int32_t score,
+                     int32_t renormalize, float factor, int32_t *experts, float *weights, int32_t *offsets, int32_t *order,
+                     void *workspace, size_t workspace_bytes, void *stream)
+{
+    BSL_TRY(check_route(T, E, k));
+    if ((score != 0 && score != 1) || !offsets != !order || !aligned(offsets, 4) || !aligned(order, 4))
+        return BSL_ERR_INVALID_ARG;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (T == 0 && !offsets) return BSL_OK;
+    if (T == 0) {
+        DeviceGuard guard;
+        BSL_TRY(guard.bind(offsets));
+        return cuda_status(cudaMemsetAsync(offsets, 0, (static_cast<size_t>(E) + 1) * 4, s));
+    }
+    if (!logits_ok(logits, logits_type) || !experts || !aligned(experts, 4) || !weights || !aligned(weights, 4))
+        return BSL_ERR_INVALID_ARG;
+    if (order && route_workspace_bytes(T, E) > 0 &&
+        (!workspace || !aligned(workspace, 4) || workspace_bytes < route_workspace_bytes(T, E)))
+        return BSL_ERR_INVALID_ARG;
+    DeviceGuard guard;
+    BSL_TRY(guard.bind(logits));
+    BSL_TRY(check_device());
+    return launch_route(logits, logits_type == 1, T, E, k, score == 1, renormalize, factor, experts, weights, offsets, order,
+                        workspace, s);
+}
+
+bsl_status bsl_route_backward(const float *dweights, const void *logits, int32_t logits_type, int32_t T, int32_t E, int32_t k,
+                              const int32_t *experts, int32_t score, int32_t renormalize, float factor, void *dlogits,
+                              void *stream)
+{
+    BSL_TRY(check_route(T, E, k));
+    if (score != 0 && score != 1) return BSL_ERR_INVALID_ARG;
+    if (T == 0) return BSL_OK;
+    if (!logits_ok(logits, logits_type) || !logits_ok(dlogits, logits_type) || !dweights || !aligned(dweights, 4) || !experts ||
+        !aligned(experts, 4))
+        return BSL_ERR_INVALID_ARG;
+    DeviceGuard guard;
+    BSL_TRY(guard.bind(logits));
+    BSL_TRY(check_device());
+    return launch_route_backward(dweights, logits, logits_type == 1, T, E, k, experts, score == 1, renormalize, factor, dlogits,
+                                 static_cast<cudaStream_t>(stream));
+}
+
+namespace {
+bsl_status check_moe(const void *X, int32_t T, const int32_t *experts, const float *weights, int32_t k, int32_t E13, int32_t N13,
+                     int32_t K13, int32_t E2, int32_t N2, int32_t K2, const void *Y, const void *workspace,
+                     size_t workspace_bytes)
+{
+    if (T < 0 || k <= 0 || E13 != E2 || K13 != N2 || K2 > INT32_MAX / 2 || N13 != 2 * K2) return BSL_ERR_INVALID_ARG;
+    if (T > BSL_MOE_MAX_TOKENS || k > BSL_ROUTE_MAX_K) return BSL_ERR_UNSUPPORTED;
+    if (T == 0) return BSL_OK;
+    if (check_matrix(X, T) != BSL_OK || check_matrix(Y, T) != BSL_OK || check_matrix(workspace, T) != BSL_OK || !experts ||
+        !aligned(experts, 4) || !weights || !aligned(weights, 4) || workspace_bytes < bsl_moe_workspace_bytes(T, k, K2))
+        return BSL_ERR_INVALID_ARG;
+    return BSL_OK;
+}
+}  // namespace
+
+size_t bsl_moe_workspace_bytes(int32_t T, int32_t k, int32_t I)
+{
+    return T <= 0 || k <= 0 || I <= 0 ? 0 : static_cast<size_t>(T) * k * I * 2;
+}
+
+bsl_status bsl_moe_forward(const void *X, int32_t T, const int32_t *experts, const float *weights, int32_t k,
+                           const bsl_grouped *W13, const bsl_grouped *W2, void *Y, void *workspace, size_t workspace_bytes,
+                           void *stream)
+{
+    BSL_TRY(check_grouped(W13));
+    BSL_TRY(check_grouped(W2));
+    BSL_TRY(check_moe(X, T, experts, weights, k, W13->E, W13->N, W13->K, W2->E, W2->N, W2->K, Y, workspace, workspace_bytes));
+    if (T == 0) return BSL_OK;
+    DeviceGuard guard;
+    BSL_TRY(guard.bind(X));
+    BSL_TRY(check_device());
+    return launch_moe(X, T, experts, weights, k, W13->weight, nullptr, W2->weight, nullptr, W2->E, W2->N, W2->K, W13->status,
+                      workspace, Y, static_cast<cudaStream_t>(stream));
+}
+
+bsl_status bsl_moe_forward_fp8(const void *X, int32_t T, const int32_t *experts, const float *weights, int32_t k,
+                               const bsl_fp8 *W13, const bsl_fp8 *W2, void *Y, void *workspace, size_t workspace_bytes,
+                               void *stream)
+{
+    BSL_TRY(check_fp8(W13));
+    BSL_TRY(check_fp8(W2));
+    BSL_TRY(check_moe(X, T, experts, weights, k, W13->E, W13->N, W13->K, W2->E, W2->N, W2->K, Y, workspace, workspace_bytes));
+    if (T == 0) return BSL_OK;
+    DeviceGuard guard;
+    BSL_TRY(guard.bind(X));
+    BSL_TRY(check_device());
+    return launch_moe(X, T, experts, weights, k, W13->codes, W13->scales, W2->codes, W2->scales, W2->E, W2->N, W2->K,
+                      W13->status, workspace, Y, static_cast<cudaStream_t>(stream));
+}
+
 bsl_status bsl_semi24_get_status(const bsl_semi24 *W, int32_t *status_host, void *stream)
 {
     if (!W || !W->status || !status_host) return BSL_ERR_INVALID_ARG;

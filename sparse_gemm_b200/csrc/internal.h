@@ -178,6 +178,20 @@ bsl_status launch_fp8_dequantize(const uint8_t *codes, const float *scales, int6
 bsl_status launch_fp8(const uint8_t *codes, const float *scales, int32_t T, const int32_t *offsets, const bsl_fp8 *W,
                       bool transposed, const void *bias, void *out, int32_t zero_rest, cudaStream_t s);
 
+// Router: choices, weights and (where order is not null) the pairs sorted by expert; the logits' gradient.
+size_t route_workspace_bytes(int32_t T, int32_t E);
+bsl_status launch_route(const void *logits, bool half, int32_t T, int32_t E, int32_t k, bool sigmoid, bool renormalize,
+                        float factor, int32_t *experts, float *weights, int32_t *offsets, int32_t *order, void *workspace,
+                        cudaStream_t s);
+bsl_status launch_route_backward(const float *dweights, const void *logits, bool half, int32_t T, int32_t E, int32_t k,
+                                 const int32_t *experts, bool sigmoid, bool renormalize, float factor, void *dlogits,
+                                 cudaStream_t s);
+
+// A whole expert layer for a few tokens; s13 and s2 null: bf16 weights, else 8 bits.
+bsl_status launch_moe(const void *X, int32_t T, const int32_t *experts, const float *weights, int32_t k, const void *W13,
+                      const float *s13, const void *W2, const float *s2, int32_t E, int32_t H, int32_t I, int32_t *status,
+                      void *workspace, void *Y, cudaStream_t s);
+
 bsl_status launch_debug_wait(int32_t *status, uint64_t timeout_ns, cudaStream_t s);
 
 }  // namespace bsl
