@@ -5,33 +5,41 @@
 //
 // The scales are fp32 numbers, which the tensor cores do not take, and change
 // every 128 elements of the sum.  So each block's sum is an accumulator of its
-// own in TMEM, and eight warps bring it to registers, multiply it by the two
+// own in TMEM; sixteen warps bring it to registers, multiply it by the two
 // scales and add it to the output's sum there, 32 bits throughout, while the
 // MMAs fill the other accumulator.  The rows t go to the MMA's M side, the
-// TMEM lanes: a lane's scale is then one number per thread and block, and the
-// weight's is one per warp (its 128 columns are one tile of the weight), so
-// a block costs a thread one FMA per column.  With the features on the lanes, as
-// in the bf16 kernel, every column would need a scale of its own from shared
-// memory: four times the bytes of the sum itself.
+// TMEM lanes: a block's scales, of the row and of the weight's tile, are then one
+// number for all of a thread's columns.  (With the features on the lanes, as in the
+// bf16 kernel, every column would need one of its own from shared memory.)
 //
 // Clusters of two CTAs work on tiles of up to 256 rows x 256 columns
 // (cta_group::2, M = 256): each CTA holds half of the tile's rows, its 128 lanes,
-// and half of the weight's columns.  A stage is one block: 16 KB of each
-// operand, at 512 clocks of MMA, 256 of FMA and 256 of TMEM reads.  An
-// expert's rows are spread evenly over the fewest tiles, and copies bring
-// exactly a tile's rows.  The weight is K-major in the forward and N-major
+// and half of the weight's columns.  A stage is one block, 16 KB of each
+// operand.  An expert's rows are spread evenly over the fewest tiles, and copies
+// bring exactly a tile's rows.  The weight is K-major in the forward and N-major
 // in the gradient, the same codes for both.
 //
-// Persistent kernels, programmatic dependents, 12 warps a CTA:
-//   warps 0, 2  TMA producers of the rows and of the weight (a ring of stages);
+// Persistent kernels, programmatic dependents, 20 warps a CTA:
+//   warp 0      TMA producer (a ring of stages);
 //   warp 1      MMA issuer and TMEM owner;
+//   warp 2      products of the two scales of each row and block, some stages
+//               ahead, into shared memory; and the one that waits for the MMAs of a
+//               stage: the sums stand at a named barrier (a waiting warp polls shared
+//               memory, which the MMAs and copies need);
 //   warp 3      zeros for the rows of no expert, on request;
-//   warps 4-11  sums: TMEM -> registers; warp 4 + 4g + q owns lanes 32q .. of
-//               columns 128g .. and holds their 128 x 32 sums in 128 registers a
-//               thread (setmaxnreg: 216 for these, 72 for the others).
-// A tile's output goes from registers to global memory in whole sectors, 32
-// bytes a lane.  Tiles are dealt round robin; no workspace is shared by
-// calls, and every output is one sum in a fixed order.
+//   warps 4-19  sums: warp 4 + 4 p + q owns lanes 32 q .. of columns 64 p ..
+// Tiles are dealt round robin; no workspace is shared by calls, and every output
+// is one sum in a fixed order.
+//
+// What bounds it with many rows is the turn of an accumulator, two of which fill
+// TMEM: MMAs 690 clocks (the four of a stage, beside copies and TMEM reads), 190
+// until the sums see them, 600 until they have read it out (their FMAs take 280 of
+// it), 180 until the next MMAs; half of that a stage.  Measured at 8192 x 4096 x 14336:
+// 500 us (1920 TFLOP/s); MMAs and copies alone 305.  Eight warps with twice the
+// columns take 525 (and 1050 as soon as the compiler spills one of their 128 sums),
+// sums that wait on the mbarrier each by themselves 560, plain stores of the output,
+// which all SMs issue at the same time, 555 instead of copies from shared memory,
+// MMAs of 128 columns with twice the accumulators 400 without any sums.
 //
 // Every wait is bounded (BSL_ERR_TIMEOUT in the status word, then all roles
 // leave through an abort flag, and the CTAs end when no copy can be under way).
@@ -47,21 +55,22 @@ constexpr int kBC = 256, kBR = 256;             // columns and rows of a tile
 constexpr int kStep = 32;                       // granularity of the rows
 constexpr int kBlock = 128;                     // elements that share a scale: a stage
 constexpr int kWBytes = 128 * kBlock;           // a CTA's half of the weight's part of a stage
-constexpr int kRing = 192 * 1024;
-constexpr int kStages = 12;                     // at most
-constexpr int kSumWarps = 8;
+constexpr int kRing = 144 * 1024;
+constexpr int kStages = 8;                      // at most; four of full tiles
+constexpr int kSumWarps = 16, kWidth = 64;      // columns of a sum warp
 constexpr int kThreads = 128 + 32 * kSumWarps;
+constexpr int kChunk = 32 * kWidth * 2;         // a sum warp's output
 constexpr int kTmem = 512;                      // two accumulators
-constexpr int kBars = (2 * kStages + 5) * 8 + 16;
-constexpr int kSmem = 1024 + kRing + kBars + 2 * (kMaxExperts + 1) * 4;
+constexpr int kAhead = 4, kScales = kAhead + 2;  // stages whose scales are made ahead
+constexpr int kInfos = 16;                      // tiles that warp 2 may be ahead of a sum, and more: kAhead + 5
+constexpr int kBars = (2 * kStages + 3) * 8 + 16;
+constexpr int kSmem = 1024 + kRing + kSumWarps * kChunk + kScales * 1024 + kInfos * 16 + kBars + 2 * (kMaxExperts + 1) * 4;
 static_assert(kSmem <= 227 * 1024, "shared memory");
-// setmaxnreg moves registers inside the block's own: 384 threads x 168
-constexpr int kLaunchRegs = 168, kSumRegs = 216, kOtherRegs = 72;
-static_assert(32 * kSumWarps * kSumRegs + 128 * kOtherRegs <= kThreads * kLaunchRegs, "registers");
 
 struct Maps {
     CUtensorMap rows[8];  // [i]: one block of 16 (i + 1) rows
     CUtensorMap weight;   // forward: 128 rows of W; gradient: 128 columns
+    CUtensorMap out;
 };
 
 struct Args {
@@ -72,7 +81,8 @@ struct Args {
     int32_t *status;
     int32_t T, E;
     int32_t cols, depth;  // of the product
-    int32_t zero_rest, wide;  // wide: 32-byte stores may be used
+    int32_t zero_rest;
+    int32_t scale_stride;  // of row_scales
     uint64_t timeout_ns;
 };
 
@@ -129,18 +139,6 @@ __device__ __forceinline__ void umma_e4m3_lead_pair(uint32_t leader, uint32_t d_
         : "memory");
 }
 
-template <int kRegs>
-__device__ __forceinline__ void more_registers()
-{
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
-}
-
-template <int kRegs>
-__device__ __forceinline__ void fewer_registers()
-{
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
-}
-
 // Two sums at a time: acc += v s.
 __device__ __forceinline__ void fma2(uint64_t &acc, uint32_t v0, uint32_t v1, uint64_t s)
 {
@@ -152,7 +150,7 @@ __device__ __forceinline__ void fma2(uint64_t &acc, uint32_t v0, uint32_t v1, ui
 __device__ __forceinline__ uint64_t twice(float s)
 {
     uint64_t r;
-    asm("mov.b64 %0, {%1, %1};" : "=l"(r) : "f"(s));
+    asm volatile("mov.b64 %0, {%1, %1};" : "=l"(r) : "f"(s));
     return r;
 }
 
@@ -163,51 +161,72 @@ __device__ __forceinline__ float2 both(uint64_t v)
     return f;
 }
 
-// The scales of four blocks b .. b + 3 of a row (of `count` blocks `step` apart); past the end: zero.
-__device__ __forceinline__ void load_scales(const float *row, int b, int count, int64_t step, bool vec, bool exists,
+// The scales of blocks b .. b + 3 of a row, of `count` blocks that lie `step` apart (in whole 16 bytes, if quads);
+// past the end: zero.
+__device__ __forceinline__ void load_scales(const float *row, int b, int count, int64_t step, bool quads, bool exists,
                                             float (&s)[4])
 {
-    if (vec && exists && b < count) {
-        const uint4 v = load_global(reinterpret_cast<const uint4 *>(row + b));
+    exists &= b < count;
+    if (quads) {
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (exists) v = load_global(reinterpret_cast<const uint4 *>(row + b));
         s[0] = __uint_as_float(v.x), s[1] = __uint_as_float(v.y), s[2] = __uint_as_float(v.z), s[3] = __uint_as_float(v.w);
-        return;
-    }
+    } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) s[i] = exists && b + i < count ? load_float(row + (b + i) * step) : 0.f;
+        for (int i = 0; i < 4; ++i) s[i] = exists && b + i < count ? load_float(row + (b + i) * step) : 0.f;
+    }
 }
 
-// 128 columns of a row, from column c on: sums, bias, one rounding, whole sectors.
-__device__ __forceinline__ void write_row(const Args &args, const uint64_t (&acc)[64], int e, int64_t row, int c)
+// A warp's 32 rows x 64 columns, from column c on: sums, bias, one rounding, into shared memory (rows of 128 bytes,
+// swizzled) and out by a copy, which takes its time while the next tile is summed; by plain stores where rows are
+// missing: `rows` exist.
+__device__ __forceinline__ void write_part(const Args &args, const CUtensorMap &map, uint8_t *buf, const uint64_t (&acc)[kWidth / 2],
+                                           int e, int row0, int c, int rows, int lane)
 {
-    __nv_bfloat16 *out = args.out + row * args.cols + c;
     const __nv_bfloat16 *bias = args.bias ? args.bias + static_cast<int64_t>(e) * args.cols + c : nullptr;
     const int left = args.cols - c;  // a multiple of 8
+    if (lane == 0) bulk_wait_group_read<0>();  // the tile before was read out
+    __syncwarp();
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        uint32_t w[8];
+    for (int j = 0; j < kWidth / 8; ++j) {
+        uint4 bv = make_uint4(0, 0, 0, 0);
+        if (bias && 8 * j < left) bv = load_global(reinterpret_cast<const uint4 *>(bias) + j);
+        const uint32_t bw[4] = {bv.x, bv.y, bv.z, bv.w};
+        uint32_t w[4];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            uint4 bv = make_uint4(0, 0, 0, 0);
-            if (bias && 16 * j + 8 * h < left) bv = load_global(reinterpret_cast<const uint4 *>(bias + 16 * j + 8 * h));
-            const uint32_t bw[4] = {bv.x, bv.y, bv.z, bv.w};
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                float2 f = both(acc[8 * j + 4 * h + u]);
-                if (bias) f.x += __uint_as_float(bw[u] << 16), f.y += __uint_as_float(bw[u] & 0xFFFF0000u);
-                w[4 * h + u] = pack_bf16x2(f.x, f.y);
-            }
+        for (int u = 0; u < 4; ++u) {
+            const float2 f = both(acc[4 * j + u]);
+            w[u] = pack_bf16x2(f.x + __uint_as_float(bw[u] << 16), f.y + __uint_as_float(bw[u] & 0xFFFF0000u));
         }
-        __nv_bfloat16 *to = out + 16 * j;
-        if (args.wide && 16 * j + 16 <= left) {
-            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(
-                             __cvta_generic_to_global(to)),
-                         "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-                         : "memory");
-        } else {
-            if (16 * j < left) *reinterpret_cast<uint4 *>(to) = make_uint4(w[0], w[1], w[2], w[3]);
-            if (16 * j + 8 < left) *reinterpret_cast<uint4 *>(to + 8) = make_uint4(w[4], w[5], w[6], w[7]);
-        }
+        *reinterpret_cast<uint4 *>(buf + lane * 128 + ((j ^ lane) & 7) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
     }
+    if (rows >= 32) {
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) tma_store_3d(&map, buf, c, row0, 0);
+    } else {
+        __syncwarp();
+        const int j = lane & 7;
+        for (int r = lane >> 3; r < rows; r += 4)
+            if (8 * j < left)
+                *reinterpret_cast<uint4 *>(args.out + static_cast<int64_t>(row0 + r) * args.cols + c + 8 * j) =
+                    *reinterpret_cast<const uint4 *>(buf + r * 128 + ((j ^ r) & 7) * 16);
+        __syncwarp();
+    }
+    if (lane == 0) bulk_commit_group();  // one group a tile, an empty one for plain stores
+}
+
+__device__ __forceinline__ void named_bar_arrive(uint32_t id, uint32_t count)
+{
+    asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(count) : "memory");
+}
+
+// An accumulator was read out, as far as this warp reads it.
+__device__ __forceinline__ void release(uint32_t bar, int lane)
+{
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive_cluster(bar);
 }
 
 // Bytes of a stage: a CTA's rows are half of the launch's largest tile.
@@ -238,10 +257,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp8(const __grid_constant__ Map
 {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *stages = align1024(smem_raw);
-    uint64_t *full = reinterpret_cast<uint64_t *>(stages + kRing);  // copies of a stage landed (leader)
-    uint64_t *empty = full + kStages;                               // MMAs of a stage finished (each CTA)
-    uint64_t *afull = empty + kStages;                              // a block's sum complete (each CTA)
-    uint64_t *aempty = afull + 2;                                   // ... read out (leader)
+    uint8_t *chunks = stages + kRing;  // 1024-byte aligned, as the swizzle wants
+    float *scales = reinterpret_cast<float *>(chunks + kSumWarps * kChunk);      // [kScales][2][128]
+    int4 *infos = reinterpret_cast<int4 *>(scales + kScales * 256);
+    uint64_t *full = reinterpret_cast<uint64_t *>(infos + kInfos);  // copies of a stage landed (leader)
+    uint64_t *empty = full + kStages;   // MMAs of a stage finished (each CTA)
+    uint64_t *aempty = empty + kStages; // an accumulator was read out (leader)
     uint64_t *drain = aempty + 2;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
@@ -259,14 +280,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp8(const __grid_constant__ Map
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
         }
-        for (int a = 0; a < 2; ++a) {
-            mbar_init(&afull[a], 1);
-            mbar_init(&aempty[a], 2 * kSumWarps);
-        }
+        for (int a = 0; a < 2; ++a) mbar_init(&aempty[a], 2 * kSumWarps);
         mbar_init(drain, 1);
         *abort_flag = 0;
         fence_barrier_init();
         tma_prefetch_map(&maps.weight);
+        tma_prefetch_map(&maps.out);
     }
     if (warp == 1) {
         tmem_alloc_pair(tmem_slot, kTmem);
@@ -294,46 +313,43 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp8(const __grid_constant__ Map
     const int blocks = (args.depth + kBlock - 1) / kBlock;
 
     if (warp < 4) {
-        fewer_registers<kOtherRegs>();
-        if (warp == 0 || warp == 2) {
-            // -------------------------------------------------------- producers: warp 0 copies rows, warp 2 the weight
+        if (warp == 0) {
+            // ------------------------------------------------------------ producer: copies of the rows and of the weight
             if (lane == 0) {
-                const bool is_a = warp == 0;
                 bool ok = true;
                 int g = 0;  // stages issued
                 Place at;
                 for (int t = first; ok && t < count; t += stride) {
                     const Tile x = tiles.at(t);
                     const int row = x.r0 + static_cast<int>(rank) * x.half, col = x.c0 + static_cast<int>(rank) * 128;
-                    const CUtensorMap *map = is_a ? &maps.rows[x.half / 16 - 1] : &maps.weight;
+                    const CUtensorMap *map = &maps.rows[x.half / 16 - 1];
                     const uint32_t bytes = 2 * (kWBytes + x.half * kBlock);
                     for (int b = 0; b < blocks; ++b, ++g, at.next(S)) {
                         if (g >= S && !mbar_wait(&empty[at.slot], at.parity ^ 1, tmo, abort_flag)) {
                             ok = false;
                             break;
                         }
-                        uint8_t *dst = stages + at.slot * stage + (is_a ? kWBytes : 0);
-                        if (is_a && rank == 0) mbar_arrive_expect_tx(&full[at.slot], bytes);
+                        uint8_t *dst = stages + at.slot * stage;
+                        if (rank == 0) mbar_arrive_expect_tx(&full[at.slot], bytes);
                         const uint32_t bar = cluster_addr(&full[at.slot], 0);
                         // (maps count two-byte columns: 64 are a block)
-                        if (is_a) tma_load_3d_pair(dst, map, bar, b * 64, row, 0);
-                        else if (kGrad) tma_load_3d_pair(dst, map, bar, col / 2, b * kBlock, x.e);
-                        else tma_load_3d_pair(dst, map, bar, b * 64, col, x.e);
+                        if (kGrad) tma_load_3d_pair(dst, &maps.weight, bar, col / 2, b * kBlock, x.e);
+                        else tma_load_3d_pair(dst, &maps.weight, bar, b * 64, col, x.e);
+                        tma_load_3d_pair(dst + kWBytes, map, bar, b * 64, row, 0);
                     }
                 }
                 if (!ok) {
                     *abort_flag = 1;
                     set_status(args.status, BSL_ERR_TIMEOUT);
-                } else if (is_a) {  // the MMAs' arrivals on this CTA's barriers are in
+                } else {  // the MMAs' arrivals on this CTA's barriers are in
                     for (int s = 0; s < S && s < g; ++s) {
                         const int fills = (g - s + S - 1) / S;
-                        if (!mbar_wait(&empty[s], (fills - 1) & 1, tmo, abort_flag))
-                            set_status(args.status, BSL_ERR_TIMEOUT);
+                        if (!mbar_wait(&empty[s], (fills - 1) & 1, tmo, abort_flag)) set_status(args.status, BSL_ERR_TIMEOUT);
                     }
                 }
                 // every copy lands before shared memory is released: the last fill of
                 // each slot is the newest phase of its barrier, which the leader holds
-                if (is_a && rank == 0)
+                if (rank == 0)
                     for (int s = 0; s < S && s < g; ++s) {
                         const int fills = (g - s + S - 1) / S;
                         if (!mbar_wait(&full[s], (fills - 1) & 1, tmo, nullptr)) set_status(args.status, BSL_ERR_TIMEOUT);
@@ -341,43 +357,36 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp8(const __grid_constant__ Map
             }
             __syncwarp();
         } else if (warp == 1) {
-            // -------------------------------------------------------- MMA issuer (the leader's)
+            // ------------------------------------------------------------ MMA issuer (the leader's)
+            // What a stage costs this warp is time that the tensor pipe may stand idle, so the loop is flat and one commit
+            // tells the producers and the sums.
             if (rank == 0) {
                 const uint32_t lead = lane == 0;
                 // (the same in all lanes, and said so: an MMA's operands stay in uniform registers)
-                const uint32_t tm = uniform(tmem);
-                const int tiles_end = uniform(count), ring = uniform(S);
-                const uint32_t bytes = uniform(static_cast<uint32_t>(stage));
+                const uint32_t tm = uniform(tmem), bytes = uniform(static_cast<uint32_t>(stage));
+                const int ring = uniform(S), total = uniform(count > first ? (count - first + stride - 1) / stride * blocks : 0);
                 const uint32_t idesc = make_idesc_e4m3(256, kBC, kGrad);
+                // K-major: 8-row atoms 1024 bytes apart, a K step of 32 bytes along the row; N-major: atoms of
+                // 8 rows 1024 bytes apart, a K step of 32 rows of 128 bytes
+                const uint64_t desc = make_sdesc(smem_u32(stages), 16, 1024, kLayoutSw128);
+                const uint32_t base = uniform(static_cast<uint32_t>(desc)), hi = uniform(static_cast<uint32_t>(desc >> 32));
                 bool ok = true;
                 Place at;
-                int it = 0;  // blocks so far
-                for (int t = first; ok && t < tiles_end; t += stride) {
-                    for (int b = 0; b < blocks; ++b, ++it, at.next(ring)) {
-                        const int acc = it & 1;
-                        if (__any_sync(0xffffffffu, !mbar_wait(&full[at.slot], at.parity, tmo, abort_flag)) ||
-                            (it >= 2 &&
-                             __any_sync(0xffffffffu, !mbar_wait(&aempty[acc], ((it >> 1) - 1) & 1, tmo, abort_flag)))) {
-                            ok = false;
-                            break;
-                        }
-                        tc_fence_after();
-                        const uint32_t b0 = smem_u32(stages) + at.slot * bytes, a0 = b0 + kWBytes;
-                        // K-major: 8-row atoms 1024 bytes apart, a K step of 32 bytes along the row; N-major: atoms of
-                        // 8 rows 1024 bytes apart, a K step of 32 rows of 128 bytes
-                        const uint64_t ad = make_sdesc(a0, 16, 1024, kLayoutSw128);
-                        const uint64_t bd = make_sdesc(b0, 16, 1024, kLayoutSw128);
-                        const uint32_t alo = static_cast<uint32_t>(ad), ahi = static_cast<uint32_t>(ad >> 32);
-                        const uint32_t blo = static_cast<uint32_t>(bd), bhi = static_cast<uint32_t>(bd >> 32);
+                for (int it = 0; it < total; ++it) {
+                    const int acc = it & 1;
+                    if (!mbar_wait(&full[at.slot], at.parity, tmo, abort_flag) ||
+                        (it >= 2 && !mbar_wait(&aempty[acc], ((it >> 1) - 1) & 1, tmo, abort_flag)))
+                        ok = false;
+                    if (__any_sync(0xffffffffu, !ok)) break;
+                    tc_fence_after();
+                    const uint32_t blo = base + at.slot * (bytes >> 4), alo = blo + (kWBytes >> 4);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            umma_e4m3_lead_pair(lead, tm + acc * kBC, alo + 2 * i, ahi, blo + (kGrad ? 256 : 2) * i, bhi, idesc,
-                                                i != 0);
-                        umma_commit_lead_pair(lead, &empty[at.slot]);
-                        umma_commit_lead_pair(lead, &afull[acc]);
-                        __syncwarp();
-                    }
+                    for (int i = 0; i < 4; ++i)
+                        umma_e4m3_lead_pair(lead, tm + acc * kBC, alo + 2 * i, hi, blo + (kGrad ? 256 : 2) * i, hi, idesc, i != 0);
+                    umma_commit_lead_pair(lead, &empty[at.slot]);
+                    at.next(ring);
                 }
+                ok = !__any_sync(0xffffffffu, !ok);
                 if (lane == 0 && !ok) {
                     *abort_flag = 1;
                     set_status(args.status, BSL_ERR_TIMEOUT);
@@ -388,74 +397,126 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp8(const __grid_constant__ Map
             }
             __syncwarp();
         } else {
-            // -------------------------------------------------------- rows of no expert
-            if (args.zero_rest) {
+            // -------------------------------------------------------- scales, and the wait for the MMAs
+            if (warp == 2) {
+                const int wide_blocks = (args.cols + 127) / 128;
+                const int64_t plane = static_cast<int64_t>(wide_blocks) * blocks, wstep = kGrad ? wide_blocks : 1;
+                bool ok = true;
+                Place at;
+                // the walk that is kAhead stages ahead: tile, its rows, block
+                int t = first, b = 0, n = 0, ring = 0;
+                const float *rs = nullptr, *ws = nullptr;
+                int rows = 0;
+                bool second = false;
+                float row[2][4], col[2][2];  // two stages' scales on the way
+                auto load = [&](float (&r)[4], float (&c)[2]) {
+                    if (t >= count) return;
+                    if (b == 0) {
+                        const Tile x = tiles.at(t);
+                        const int in_tile = static_cast<int>(rank) * x.half;
+                        rows = max(0, min(x.half, x.valid - in_tile));
+                        if (lane == 0) infos[n % kInfos] = make_int4(x.e, x.c0, x.r0 + in_tile, rows);
+                        rs = args.row_scales + (static_cast<int64_t>(x.r0) + in_tile + lane) * args.scale_stride;
+                        ws = args.weight_scales + x.e * plane + x.c0 / 128 * (kGrad ? 1 : static_cast<int64_t>(blocks));
+                        second = x.c0 + 128 < args.cols;
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        r[i] = lane + 32 * i < rows ? load_float(rs + 32 * i * static_cast<int64_t>(args.scale_stride) + b) : 0.f;
+                    c[0] = load_float(ws + b * wstep);
+                    c[1] = second ? load_float(ws + (kGrad ? 1 : blocks) + b * wstep) : 0.f;
+                    if (++b == blocks) b = 0, t += stride, ++n;
+                };
+                auto put = [&](const float (&r)[4], const float (&c)[2]) {
+                    float *to = scales + ring * 256 + lane;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) to[32 * i] = r[i] * c[0], to[128 + 32 * i] = r[i] * c[1];
+                    if (++ring == kScales) ring = 0;
+                };
+                const int total = count > first ? (count - first + stride - 1) / stride * blocks : 0;
+                load(row[0], col[0]);
+                load(row[1], col[1]);
+#pragma unroll
+                for (int i = 0; i < kAhead; ++i) {
+                    put(row[i & 1], col[i & 1]);
+                    load(row[i & 1], col[i & 1]);
+                }
+                // stage it + kAhead goes where stage it - 2 was, whose sums were read out before the MMAs of it began
+                for (int it = 0; it < total; it += 2) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        if (it + i >= total) break;
+                        if (ok && __any_sync(0xffffffffu, !mbar_wait(&empty[at.slot], at.parity, tmo, abort_flag))) {
+                            ok = false;
+                            if (lane == 0) *abort_flag = 1;
+                            __syncwarp();
+                        }
+                        at.next(S);
+                        if (ok) {
+                            named_bar_arrive(1 + i, 32 * kSumWarps + 32);
+                            put(row[i], col[i]);
+                            load(row[i], col[i]);
+                        } else {  // an aborted run's sums go on to the end, in step
+                            named_bar_sync(1 + i, 32 * kSumWarps + 32);
+                        }
+                    }
+                }
+                if (lane == 0 && !ok) {
+                    *abort_flag = 1;
+                    set_status(args.status, BSL_ERR_TIMEOUT);
+                }
+            } else if (args.zero_rest) {  // rows of no expert
                 zero_range(args.out, 0, static_cast<int64_t>(off[0]) * args.cols, lane);
-                zero_range(args.out, static_cast<int64_t>(off[args.E]) * args.cols,
-                           static_cast<int64_t>(args.T) * args.cols, lane);
+                zero_range(args.out, static_cast<int64_t>(off[args.E]) * args.cols, static_cast<int64_t>(args.T) * args.cols,
+                           lane);
             }
             __syncwarp();
         }
     } else {
         // ------------------------------------------------------------ sums
-        more_registers<kSumRegs>();
         const int q = warp & 3, part = (warp - 4) >> 2;
-        const uint32_t mine = tmem + (static_cast<uint32_t>(32 * q) << 16) + part * 128;
-        const int wide_blocks = (args.cols + 127) / 128;                   // tiles of the weight along the columns
-        const int64_t plane = static_cast<int64_t>(wide_blocks) * blocks;  // its scales
-        const bool vec = blocks % 4 == 0;
+        const uint32_t mine = tmem + (static_cast<uint32_t>(32 * q) << 16) + part * kWidth;
+        uint8_t *chunk = chunks + (warp - 4) * kChunk;
+        const float *my_scales = scales + part / 2 * 128 + 32 * q + lane;
         bool ok = true;
-        int it = 0;
-        for (int t = first; ok && t < count; t += stride) {
-            const Tile x = tiles.at(t);
-            const int c = x.c0 + 128 * part, lrow = 32 * q + lane, in_tile = static_cast<int>(rank) * x.half + lrow;
-            const bool exists = lrow < x.half && in_tile < x.valid && c < args.cols;
-            const int64_t row = x.r0 + in_tile;
-            const bool any = c < args.cols && 32 * q < x.half && static_cast<int>(rank) * x.half + 32 * q < x.valid;
-            const float *rs = args.row_scales + row * blocks;
-            const float *ws = args.weight_scales + x.e * plane + (kGrad ? c / 128 : static_cast<int64_t>(c / 128) * blocks);
-            uint64_t acc[64];
+        int it = 0, ring = 0, n = 0;
+        for (int t = first; t < count; t += stride, ++n) {
+            uint64_t acc[kWidth / 2];
 #pragma unroll
-            for (int i = 0; i < 64; ++i) acc[i] = 0;
-            float sr[4], sw[4];
-            load_scales(rs, 0, blocks, 1, vec, exists, sr);
-            load_scales(ws, 0, blocks, kGrad ? wide_blocks : 1, !kGrad && vec, any, sw);
-            for (int b0 = 0; ok && b0 < blocks; b0 += 4) {
-                float s[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) s[i] = sr[i] * sw[i];
-                load_scales(rs, b0 + 4, blocks, 1, vec, exists, sr);
-                load_scales(ws, b0 + 4, blocks, kGrad ? wide_blocks : 1, !kGrad && vec, any, sw);
+            for (int i = 0; i < kWidth / 2; ++i) acc[i] = 0;
+            bool live = false;
 #pragma unroll 1
-                for (int i = 0; i < 4 && b0 + i < blocks; ++i, ++it) {
-                    const int buf = it & 1;
-                    const uint64_t s2 = twice(s[0]);
-                    s[0] = s[1], s[1] = s[2], s[2] = s[3];
-                    if (__any_sync(0xffffffffu, !mbar_wait(&afull[buf], (it >> 1) & 1, tmo, abort_flag))) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    if (any) {
-                        const uint32_t at = mine + buf * kBC;
-                        uint32_t v[2][32];
-                        tmem_ld32(at, v[0]);
+            for (int b = 0; b < blocks; ++b, ++it) {
+                const int buf = it & 1;
+                named_bar_sync(1 + buf, 32 * kSumWarps + 32);
+                tc_fence_after();
+                if (b == 0) live = infos[n % kInfos].w > 32 * q && infos[n % kInfos].y + kWidth * part < args.cols;
+                const uint64_t s2 = twice(my_scales[ring * 256]);
+                if (++ring == kScales) ring = 0;
+                if (live) {
+                    const uint32_t from = mine + buf * kBC;
+                    uint32_t v[2][16];
+                    tmem_ld16(from, v[0]);
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            tmem_wait_ld();
-                            if (j < 3) tmem_ld32(at + 32 * (j + 1), v[(j + 1) & 1]);
-                            else tc_fence_before();
+                    for (int j = 0; j < kWidth / 16; ++j) {
+                        tmem_wait_ld();
+                        if (j + 1 < kWidth / 16) tmem_ld16(from + 16 * (j + 1), v[(j + 1) & 1]);
+                        else release(cluster_addr(&aempty[buf], 0), lane);
 #pragma unroll
-                            for (int u = 0; u < 16; ++u) fma2(acc[16 * j + u], v[j & 1][2 * u], v[j & 1][2 * u + 1], s2);
-                        }
+                        for (int u = 0; u < 8; ++u) fma2(acc[8 * j + u], v[j & 1][2 * u], v[j & 1][2 * u + 1], s2);
                     }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_cluster(cluster_addr(&aempty[buf], 0));
+                } else {
+                    release(cluster_addr(&aempty[buf], 0), lane);
                 }
             }
-            if (ok && exists) write_row(args, acc, x.e, row, c);
+            if (*abort_flag) ok = false;
+            if (ok && live) {
+                const int4 x = infos[n % kInfos];  // expert, first column, first row, rows
+                write_part(args, maps.out, chunk, acc, x.x, x.z + 32 * q, x.y + kWidth * part, x.w - 32 * q, lane);
+            }
             __syncwarp();
         }
+        if (lane == 0) bulk_wait_group<0>();
         if (lane == 0 && !ok) {
             *abort_flag = 1;
             set_status(args.status, BSL_ERR_TIMEOUT);
@@ -490,12 +551,6 @@ bsl_status run(const Maps &maps, const Args &args, cudaStream_t s)
     auto kern = k_fp8<kGrad>;
     const bsl_status sa = set_smem_once(reinterpret_cast<const void *>(kern), kSmem);
     if (sa != BSL_OK) return sa;
-    // the register split waits for ever if the block is launched with fewer than it adds up to
-    static const int regs = [] {
-        cudaFuncAttributes at = {};
-        return cudaFuncGetAttributes(&at, k_fp8<kGrad>) == cudaSuccess ? at.numRegs : 0;
-    }();
-    if (regs < kLaunchRegs) return BSL_ERR_UNSUPPORTED;
     return cuda_status(launch_dependent_cluster(kern, num_sms() / 2 * 2, 2, kThreads, kSmem, s, maps, args));
 }
 
@@ -517,11 +572,13 @@ bsl_status launch_fp8(const uint8_t *codes, const float *scales, int32_t T, cons
     args.cols = transposed ? W->K : W->N;
     args.depth = transposed ? W->N : W->K;
     args.zero_rest = zero_rest;
-    args.wide = args.cols % 16 == 0 && reinterpret_cast<uintptr_t>(out) % 32 == 0;
+    args.scale_stride = (args.depth + 127) / 128;
     args.timeout_ns = wait_timeout_ns();
     Maps m;
     const int64_t K = W->K, N = W->N;
-    bool good = make_map_3d(&m.weight, W->codes, K / 2, N, W->E, K, K * N, 64, 128, 128);
+    bool good = make_map_3d(&m.weight, W->codes, K / 2, N, W->E, K, K * N, 64, 128, 128) &&
+                make_map_3d(&m.out, out, args.cols, T, 1, static_cast<uint64_t>(args.cols) * 2,
+                            static_cast<uint64_t>(args.cols) * 2 * T, kWidth, 32, 128);
     // (a CTA has no more than T rows, rounded up to 16)
     for (int i = 0; i < 8 && 16 * i < T; ++i)
         good = good && make_map_3d(&m.rows[i], codes, args.depth / 2, T, 1, args.depth,
