@@ -23,6 +23,7 @@
 // sum of the weights.
 #include "common.cuh"
 #include "internal.h"
+#include "pair.cuh"
 
 namespace bsl {
 namespace {
@@ -243,9 +244,10 @@ __device__ __forceinline__ Vec<F8> load_vec(const __nv_bfloat16 *row, int at, bo
 constexpr int kUpWarps = 8;
 
 template <bool F8, int NT>
-__global__ void __launch_bounds__(kUpWarps * 32, NT == 1 ? 3 : 2) k_moe_up(const MoeArgs a)
+__global__ void __launch_bounds__(kUpWarps * 32, NT == 4 ? 2 : 3) k_moe_up(const MoeArgs a)
 {
-    constexpr int U = NT == 1 ? 4 : 2, SPAN = chunk_of<F8>();
+    // chunks of the weight on the way at once, and of the tokens' vectors (which come from L1 and L2)
+    constexpr int U = NT == 4 ? 2 : 4, V = F8 ? (NT == 1 ? 2 : 1) : U, SPAN = chunk_of<F8>();
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ float part[kUpWarps][NT * kRows][17];
     const Plan plan(smem, a.E, a.T * a.k);
@@ -257,16 +259,14 @@ __global__ void __launch_bounds__(kUpWarps * 32, NT == 1 ? 3 : 2) k_moe_up(const
     make_plan(a, plan, NT * kRows);
     const int tiles = a.I / 8, units = *plan.count * tiles;
     const int chunks = (a.H + SPAN - 1) / SPAN, kb = (a.H + 127) / 128;
-    const int64_t bytes = static_cast<int64_t>(a.H) * (F8 ? 1 : 2);
+    const int64_t bytes = static_cast<int64_t>(a.H) * (F8 ? 1 : 2), up_rows = a.I * bytes;
+
     for (int u = blockIdx.x; u < units; u += gridDim.x) {
         const Group group = plan.groups[u / tiles];
-        const int i0 = u % tiles * 8;
-        const int64_t row = static_cast<int64_t>(group.expert) * 2 * a.I + i0;
-        const uint8_t *lo = a.W13 + (row + g) * bytes + 16 * t, *hi = lo + a.I * bytes;
-        const int64_t plane = static_cast<int64_t>((2 * a.I + 127) / 128) * kb * group.expert;
-        const float *s_lo = a.s13 + plane + i0 / 128 * static_cast<int64_t>(kb);
-        const float *s_hi = a.s13 + plane + (a.I + i0) / 128 * static_cast<int64_t>(kb);
-        const int live = (group.rows + kRows - 1) / kRows;
+        const int live = (group.rows + kRows - 1) / kRows, i0 = u % tiles * 8;
+        const uint8_t *rows = a.W13 + (static_cast<int64_t>(group.expert) * 2 * a.I + i0 + g) * bytes + 16 * t;
+        const float *plane = F8 ? a.s13 + static_cast<int64_t>((2 * a.I + 127) / 128) * kb * group.expert : nullptr;
+        const float *s_gate = plane + i0 / 128 * static_cast<int64_t>(kb), *s_up = plane + (a.I + i0) / 128 * static_cast<int64_t>(kb);
         const __nv_bfloat16 *x[NT];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
@@ -277,36 +277,45 @@ __global__ void __launch_bounds__(kUpWarps * 32, NT == 1 ? 3 : 2) k_moe_up(const
         uint32_t nan[2] = {};
         for (int c0 = warp; c0 < chunks; c0 += kUpWarps * U) {
             Weights w[U];
-            Vec<F8> v[U][NT];
-            float sl[U], sh[U];
+            float sg[U], su[U];
 #pragma unroll
             for (int i = 0; i < U; ++i) {
                 const int c = c0 + i * kUpWarps;
-                const bool in = c * SPAN + t * (SPAN / 4) < a.H;
                 w[i].lo = w[i].hi = make_uint4(0, 0, 0, 0);
-                if (in) {
-                    w[i].lo = load_stream(lo + static_cast<int64_t>(c) * 64);
-                    w[i].hi = load_stream(hi + static_cast<int64_t>(c) * 64);
+                if (c * SPAN + t * (SPAN / 4) < a.H) {
+                    w[i].lo = load_stream(rows + static_cast<int64_t>(c) * 64);
+                    w[i].hi = load_stream(rows + up_rows + static_cast<int64_t>(c) * 64);
                 }
-                sl[i] = sh[i] = 0.f;
-                if (F8 && c < chunks) sl[i] = load_float(s_lo + c / 2), sh[i] = load_float(s_hi + c / 2);
-#pragma unroll
-                for (int n = 0; n < NT; ++n) v[i][n] = load_vec<F8>(x[n], c * SPAN, in && 8 * n + g < group.rows);
+                sg[i] = su[i] = 0.f;
+                if (F8 && c < chunks) sg[i] = load_float(s_gate + c / 2), su[i] = load_float(s_up + c / 2);
             }
+            Vec<F8> v[V][NT];
 #pragma unroll
-            for (int i = 0; i < U; ++i) add_chunk<F8, NT>(acc, w[i], v[i], live, sl[i], sh[i], nan);
+            for (int j = 0; j < U; j += V) {
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const int c = c0 + (i + j) * kUpWarps;
+                    const bool in = c * SPAN + t * (SPAN / 4) < a.H;
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+                        if (n < live) v[i][n] = load_vec<F8>(x[n], c * SPAN, in && 8 * n + g < group.rows);
+                }
+#pragma unroll
+                for (int i = 0; i < V; ++i) add_chunk<F8, NT>(acc, w[i + j], v[i], live, sg[i + j], su[i + j], nan);
+            }
         }
         if (F8) spread_nan<NT>(acc, nan);
 #pragma unroll
         for (int n = 0; n < NT; ++n)
+            if (n < live)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) part[warp][8 * n + 2 * t + (i & 1)][g + 8 * (i >> 1)] = acc[n][i];
+                for (int i = 0; i < 4; ++i) part[warp][8 * n + 2 * t + (i & 1)][g + 8 * (i >> 1)] = acc[n][i];
         __syncthreads();
         for (int i = threadIdx.x; i < group.rows * 8; i += kUpWarps * 32) {
             const int r = i / 8, f = i % 8;
             float gate = 0.f, up = 0.f;
 #pragma unroll
-            for (int w = 0; w < kUpWarps; ++w) gate += part[w][r][f], up += part[w][r][f + 8];
+            for (int j = 0; j < kUpWarps; ++j) gate += part[j][r][f], up += part[j][r][f + 8];
             // (__expf is off by some 2^-20, the rounding of h by up to 2^-8)
             const float h = gate / (1.f + __expf(-gate)) * up * plan.share[group.slot + r];
             a.h[static_cast<int64_t>(group.slot + r) * a.I + i0 + f] = __float2bfloat16(h);
@@ -317,23 +326,23 @@ __global__ void __launch_bounds__(kUpWarps * 32, NT == 1 ? 3 : 2) k_moe_up(const
 
 // ---------------------------------------------------------------- down
 
+// CTAs of a cluster share the list of a tile of 16 features, so that few tiles keep the SMs busy too.
 template <int NT>
 struct Down {
     static constexpr int WARPS = NT == 1 ? 16 : 8;
-    static constexpr int U = NT == 1 ? 4 : 2;
     static constexpr int STRIDE = 17;  // of a token's 16 sums
     static size_t bytes(int T) { return static_cast<size_t>(WARPS) * T * STRIDE * 4; }
 };
 
 template <bool F8, int NT>
-__global__ void __launch_bounds__(Down<NT>::WARPS * 32) k_moe_down(const MoeArgs a)
+__global__ void __launch_bounds__(Down<NT>::WARPS * 32, 2) k_moe_down(const MoeArgs a, const int parts)
 {
-    constexpr int U = Down<NT>::U, WARPS = Down<NT>::WARPS, STRIDE = Down<NT>::STRIDE, SPAN = chunk_of<F8>();
+    constexpr int U = 4, WARPS = Down<NT>::WARPS, STRIDE = Down<NT>::STRIDE, SPAN = chunk_of<F8>();
     extern __shared__ __align__(16) uint8_t smem[];
     const Plan plan(smem, a.E, a.T * a.k);
     float *sums = reinterpret_cast<float *>(smem + Plan::bytes(a.E, a.T * a.k));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int n0 = blockIdx.x * 16;
+    const int n0 = blockIdx.x / parts * 16, rank = blockIdx.x % parts;
     dependents_may_launch();
     for (int i = threadIdx.x; i < WARPS * a.T * STRIDE; i += WARPS * 32) sums[i] = 0.f;
     make_plan(a, plan, NT * kRows);
@@ -341,85 +350,96 @@ __global__ void __launch_bounds__(Down<NT>::WARPS * 32) k_moe_down(const MoeArgs
     const int chunks = (a.I + SPAN - 1) / SPAN, kb = (a.I + 127) / 128;
     const int64_t bytes = static_cast<int64_t>(a.I) * (F8 ? 1 : 2), nb = (a.H + 127) / 128;
     const bool in0 = n0 + g < a.H, in1 = n0 + g + 8 < a.H;
-    const int64_t all = static_cast<int64_t>(*plan.count) * chunks;
-    int64_t left = all * (warp + 1) / WARPS - all * warp / WARPS;  // of this warp's chunks
-    const int64_t q0 = all * warp / WARPS;
-    int at = static_cast<int>(q0 / chunks), c = static_cast<int>(q0 - static_cast<int64_t>(at) * chunks);  // group, chunk
+    // this warp's run of all (group, chunk) pairs
+    const int64_t all = static_cast<int64_t>(*plan.count) * chunks, workers = WARPS * parts, me = rank * WARPS + warp;
+    const int64_t q0 = all * me / workers;
+    int left = static_cast<int>(all * (me + 1) / workers - q0);
+    int at = static_cast<int>(q0 / chunks), c = static_cast<int>(q0 - static_cast<int64_t>(at) * chunks);
 
-    // the weights of the next U chunks, from (at, c) on
+    // what is fetched next: group, chunk, how many are left
+    int fat = at, fc = c, fleft = left;
     Weights w[U];
     float s[U];
-    auto fetch = [&] {
-        int a1 = at, c1 = c;
-#pragma unroll
-        for (int i = 0; i < U; ++i) {
-            w[i].lo = w[i].hi = make_uint4(0, 0, 0, 0);
-            s[i] = 0.f;
-            if (i < left) {
-                const int e = plan.groups[a1].expert;
-                const uint8_t *p = a.W2 + (static_cast<int64_t>(e) * a.H + n0 + g) * bytes + 16 * t + static_cast<int64_t>(c1) * 64;
-                const bool in = c1 * SPAN + t * (SPAN / 4) < a.I;
-                if (in && in0) w[i].lo = load_stream(p);
-                if (in && in1) w[i].hi = load_stream(p + 8 * bytes);
-                if (F8) s[i] = load_float(a.s2 + (e * nb + n0 / 128) * kb + c1 / 2);
-                if (++c1 == chunks) c1 = 0, ++a1;
-            }
+    const uint8_t *rows = nullptr;
+    const float *s2 = nullptr;
+    auto open = [&] {
+        const int64_t e = plan.groups[fat].expert;
+        rows = a.W2 + (e * a.H + n0 + g) * bytes + 16 * t;
+        if (F8) s2 = a.s2 + (e * nb + n0 / 128) * kb;
+    };
+    auto fetch = [&](int i) {
+        if (fleft-- <= 0) return;
+        const bool in = fc * SPAN + t * (SPAN / 4) < a.I;
+        w[i].lo = w[i].hi = make_uint4(0, 0, 0, 0);
+        if (in && in0) w[i].lo = load_stream(rows + static_cast<int64_t>(fc) * 64);
+        if (in && in1) w[i].hi = load_stream(rows + 8 * bytes + static_cast<int64_t>(fc) * 64);
+        if (F8) s[i] = load_float(s2 + fc / 2);
+        if (++fc == chunks) {
+            fc = 0, ++fat;
+            if (fleft > 0) open();
         }
     };
-    fetch();
+    if (left > 0) open();
+#pragma unroll
+    for (int i = 0; i < U; ++i) fetch(i);
     wait_for_prior_grid();  // h is there
     float acc[NT][4] = {};
     uint32_t nan[2] = {};
     float *mine = sums + warp * a.T * STRIDE;
     while (left > 0) {
-        Vec<F8> v[U][NT];
-        {
-            int a1 = at, c1 = c;
 #pragma unroll
-            for (int i = 0; i < U; ++i)
-                if (i < left) {
-                    const Group group = plan.groups[a1];
-                    const int k = c1 * SPAN + t * (SPAN / 4);
+        for (int i = 0; i < U; ++i) {
+            if (left <= 0) break;
+            const Group group = plan.groups[at];
+            const int live = (group.rows + kRows - 1) / kRows, k = c * SPAN + t * (SPAN / 4);
+            Vec<F8> v[NT];
 #pragma unroll
-                    for (int n = 0; n < NT; ++n)
-                        v[i][n] = load_vec<F8>(a.h + static_cast<int64_t>(group.slot + 8 * n + g) * a.I, k,
-                                               k < a.I && 8 * n + g < group.rows);
-                    if (++c1 == chunks) c1 = 0, ++a1;
-                }
-        }
+            for (int n = 0; n < NT; ++n)
+                if (n < live)
+                    v[n] = load_vec<F8>(a.h + static_cast<int64_t>(group.slot + 8 * n + g) * a.I, k, k < a.I && 8 * n + g < group.rows);
+            add_chunk<F8, NT>(acc, w[i], v, live, s[i], s[i], nan);
+            fetch(i);
+            --left;
+            const bool last = ++c == chunks;
+            if (last || left == 0) {  // the group's sum, as far as this warp has it, to its tokens
+                if (F8) spread_nan<NT>(acc, nan);
+                nan[0] = nan[1] = 0;
 #pragma unroll
-        for (int i = 0; i < U; ++i)
-            if (i < left) {
-                const Group group = plan.groups[at];
-                add_chunk<F8, NT>(acc, w[i], v[i], (group.rows + kRows - 1) / kRows, s[i], s[i], nan);
-                const bool last = ++c == chunks;
-                if (last || i + 1 == left) {  // the group's sum, as far as this warp has it, to its tokens
-                    if (F8) spread_nan<NT>(acc, nan);
-                    nan[0] = nan[1] = 0;
+                for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int n = 0; n < NT; ++n)
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const int r = 8 * n + 2 * t + (j & 1);
-                            if (r < group.rows) mine[plan.token[group.slot + r] * STRIDE + g + 8 * (j >> 1)] += acc[n][j];
-                            acc[n][j] = 0.f;
-                        }
-                    __syncwarp();
-                }
-                if (last) c = 0, ++at;
+                    for (int j = 0; j < 4; ++j) {
+                        const int r = 8 * n + 2 * t + (j & 1);
+                        if (r < group.rows) mine[plan.token[group.slot + r] * STRIDE + g + 8 * (j >> 1)] += acc[n][j];
+                        acc[n][j] = 0.f;
+                    }
+                __syncwarp();
             }
-        left -= U;
-        fetch();
+            if (last) c = 0, ++at;
+        }
     }
     __syncthreads();
+    // the warps' sums in order, then the CTAs' in order
     for (int i = threadIdx.x; i < a.T * 16; i += WARPS * 32) {
         const int r = i / 16, f = i % 16;
-        if (n0 + f >= a.H) continue;
         float y = 0.f;
 #pragma unroll
         for (int j = 0; j < WARPS; ++j) y += sums[(j * a.T + r) * STRIDE + f];
-        a.Y[static_cast<int64_t>(r) * a.H + n0 + f] = __float2bfloat16(y);
+        if (parts > 1) sums[r * STRIDE + f] = y;  // (nobody else reads or writes this one)
+        else if (n0 + f < a.H) a.Y[static_cast<int64_t>(r) * a.H + n0 + f] = __float2bfloat16(y);
     }
+    if (parts == 1) return;
+    cluster_sync_all();
+    for (int i = rank * WARPS * 32 + threadIdx.x; i < a.T * 16; i += parts * WARPS * 32) {
+        const int r = i / 16, f = i % 16;
+        float y = 0.f;
+        for (int p = 0; p < parts; ++p) {
+            float other;
+            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(other) : "r"(cluster_addr(sums + r * STRIDE + f, p)) : "memory");
+            y += other;
+        }
+        if (n0 + f < a.H) a.Y[static_cast<int64_t>(r) * a.H + n0 + f] = __float2bfloat16(y);
+    }
+    cluster_sync_all();  // until the others have read this CTA's sums
 }
 
 template <bool F8, int NT>
@@ -438,17 +458,25 @@ bsl_status run(const MoeArgs &a, cudaStream_t s)
         if (sa != BSL_OK) return sa;
     }
     const int64_t units = static_cast<int64_t>(a.I / 8) * (pairs < a.E ? pairs : a.E);
-    const int64_t room = static_cast<int64_t>(num_sms()) * (NT == 1 ? 3 : 2);
+    const int64_t room = static_cast<int64_t>(num_sms()) * (NT == 4 ? 2 : 3);
     const bsl_status up = cuda_status(launch_dependent(k_moe_up<F8, NT>, static_cast<unsigned>(units < room ? units : room),
                                                        kUpWarps * 32, plan, s, a));
     if (up != BSL_OK) return up;
-    return cuda_status(launch_dependent(k_moe_down<F8, NT>, (a.H + 15) / 16, Down<NT>::WARPS * 32, down, s, a));
+    // as many CTAs a tile as two an SM have room for
+    const int tiles = (a.H + 15) / 16;
+    int parts = 1;
+    while (parts < 8 && 2 * parts * tiles <= 2 * num_sms()) parts *= 2;
+    return cuda_status(launch_dependent_cluster(k_moe_down<F8, NT>, tiles * parts, parts, Down<NT>::WARPS * 32, down, s, a, parts));
 }
 
+// Tokens a group takes: as many as an expert has on the average, in eights.  An expert with more is read again for
+// its next group, mostly from L2, by CTAs that run at about the same time.
 template <bool F8>
 bsl_status run(const MoeArgs &a, cudaStream_t s)
 {
-    return a.T <= kRows ? run<F8, 1>(a, s) : a.T <= 2 * kRows ? run<F8, 2>(a, s) : run<F8, 4>(a, s);
+    const int reach = a.T * a.k, mean = (reach + a.E - 1) / a.E;
+    const int rows = a.T < mean ? a.T : mean;
+    return rows <= kRows ? run<F8, 1>(a, s) : rows <= 2 * kRows ? run<F8, 2>(a, s) : run<F8, 4>(a, s);
 }
 
 }  // namespace
