@@ -21,6 +21,8 @@
 // Who has which tokens is worked out by each CTA from the T x k choices: a mask of
 // tokens for each expert.  An expert chosen twice by a token counts once, with the
 // sum of the weights.
+#include <type_traits>
+
 #include "common.cuh"
 #include "internal.h"
 #include "pair.cuh"
@@ -137,80 +139,129 @@ __device__ __forceinline__ void make_plan(const MoeArgs &a, const Plan &p, int m
     __syncthreads();
 }
 
-// ---------------------------------------------------------------- a chunk: 64 bytes of 16 weight rows
+// ---------------------------------------------------------------- steps: 128 bytes of 16 weight rows
+// 64 bf16 elements, or a block of 128 codes.  A warp brings its steps through a ring of its own in shared memory with
+// copies that need no registers, kRing of them under way whatever is summed meanwhile.  In a step's rows the 16-byte
+// units of odd rows trade halves, so that a lane's reads (units t and 4 + t of rows g and g + 8) meet no bank twice.
 
-// Two e4m3 codes, in the lower half of w, to two bf16: the bits s e e e e m m m
-// go to the sign and to the lowest exponent and highest mantissa bits, which is
-// 2^-120 of the value, subnormal codes included, and one exact product brings it
-// in.  The NaN codes come out as 480 and are looked for apart (nan_codes).
-__device__ __forceinline__ uint32_t bf16_of_codes(uint32_t spread)
+constexpr int kWarps = 8;
+constexpr int kRing = 4, kStep = 16 * 128;
+constexpr int kRingBytes = kWarps * kRing * kStep;
+
+template <bool F8>
+constexpr int step_of() { return F8 ? 128 : 64; }  // elements
+
+// Four copies a lane: unit lane & 7 of rows lane / 8 + 4 j at `from` + `off[j]`; zeros where there is none.
+__device__ __forceinline__ void copy_step(uint8_t *slot, const uint8_t *from, const int64_t (&off)[4], const bool (&exists)[4],
+                                          const uint8_t *any)
 {
-    const uint32_t v = (spread & 0x007F007Fu) * 16 | (spread * 256 & 0x80008000u);
+    const int lane = threadIdx.x & 31, r = lane >> 3, u = lane & 7;
+    const uint32_t dst = smem_u32(slot) + r * 128 + ((u ^ (r & 1) << 2) << 4);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + j * 512), "l"(exists[j] ? from + off[j] : any),
+                     "r"(exists[j] ? 16 : 0)
+                     : "memory");
+}
+
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+
+// The oldest step of kRing is there.
+__device__ __forceinline__ void copies_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 1) : "memory");
+    __syncwarp();
+}
+
+// What the lane's bytes of a step meet of a token's vector.
+template <bool F8>
+struct Vec {
+    uint4 v[F8 ? 4 : 2];  // of unit t, and of unit 4 + t
+};
+
+template <bool F8>
+__device__ __forceinline__ void load_vec(Vec<F8> &x, const __nv_bfloat16 *row, int k0, int t, int K, bool exists)
+{
+    constexpr int UNIT = F8 ? 16 : 8;  // elements
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int k = k0 + (4 * h + t) * UNIT;
+        const bool in = exists && k < K;
+#pragma unroll
+        for (int i = 0; i < UNIT / 8; ++i) {
+            uint4 &v = x.v[h * (UNIT / 8) + i];
+            v = make_uint4(0, 0, 0, 0);
+            if (in) v = load_global(reinterpret_cast<const uint4 *>(row + k) + i);
+        }
+    }
+}
+
+// Two e4m3 codes to two bf16: the bits s e e e e m m m go to the sign and to the lowest exponent and highest mantissa
+// bits, which is 2^-120 of the value, subnormal codes included, and one exact product brings it in.  `w`: the codes in
+// the upper bytes of the halves (and anything below), `m`: the same without their signs, and zeros below.  The NaN
+// codes come out as 480 and are looked for apart.
+__device__ __forceinline__ uint32_t bf16_of_codes(uint32_t w, uint32_t m)
+{
+    const uint32_t v = (w & 0x80008000u) | m >> 4;
     uint32_t r;
     asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(0x7B807B80u));
     return r;
 }
 
-// Bit 7 of a byte whose code is NaN.
-__device__ __forceinline__ uint32_t nan_codes(uint32_t w) { return (w & 0x7F7F7F7Fu) + 0x01010101u; }
-
-// What a lane holds of a chunk of the weight: 16 bytes of rows g and g + 8.
-struct Weights {
-    uint4 lo, hi;
-};
-
-// ... and of a token's vector: the elements that these bytes meet.
-template <bool F8>
-struct Vec {
-    uint4 v[F8 ? 2 : 1];
-};
-
-template <bool F8>
-__device__ __forceinline__ void multiply(float (&c)[4], const Weights &w, const Vec<F8> &x)
+// Four codes to two registers of two bf16, codes 0, 2 and codes 1, 3; bit 7 of a byte of `nan` is set if its code is NaN.
+__device__ __forceinline__ void decode4(uint32_t w, uint32_t &even, uint32_t &odd, uint32_t &nan)
 {
-    if constexpr (!F8) {
-        mma_bf16(c, w.lo.x, w.hi.x, w.lo.y, w.hi.y, x.v[0].x, x.v[0].y);
-        mma_bf16(c, w.lo.z, w.hi.z, w.lo.w, w.hi.w, x.v[0].z, x.v[0].w);
-    }
+    const uint32_t m = w & 0x7F7F7F7Fu;
+    nan |= m + 0x01010101u;
+    even = bf16_of_codes(w << 8, m << 8 & 0xFF00FF00u);
+    odd = bf16_of_codes(w, m & 0xFF00FF00u);
 }
 
-// The chunk's products, added to acc: NT groups of tokens, `groups` of them live.  8 bits: the sum of the chunk times
-// the rows' scales.
+// A step's products, added to acc: NT groups of tokens, `live` of them there.  8 bits: the sum of the block times the
+// rows' scales; the codes of a word are taken as 0, 2 and 1, 3, and so are the tokens' elements.
 template <bool F8, int NT>
-__device__ __forceinline__ void add_chunk(float (&acc)[NT][4], const Weights &w, const Vec<F8> (&x)[NT], int groups, float s_lo,
-                                          float s_hi, uint32_t (&nan)[2])
+__device__ __forceinline__ void add_step(float (&acc)[NT][4], const uint8_t *slot, const Vec<F8> (&x)[NT], int live, float s_lo,
+                                         float s_hi, uint32_t (&nan)[2])
 {
-    if constexpr (F8) {
-        const uint32_t lo[4] = {w.lo.x, w.lo.y, w.lo.z, w.lo.w}, hi[4] = {w.hi.x, w.hi.y, w.hi.z, w.hi.w};
-        float c[NT][4] = {};
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    float c[NT][4] = {};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            nan[0] |= nan_codes(lo[i]);
-            nan[1] |= nan_codes(hi[i]);
-            const uint32_t a0 = bf16_of_codes(__byte_perm(lo[i], 0, 0x4140)), a1 = bf16_of_codes(__byte_perm(hi[i], 0, 0x4140));
-            const uint32_t a2 = bf16_of_codes(__byte_perm(lo[i], 0, 0x4342)), a3 = bf16_of_codes(__byte_perm(hi[i], 0, 0x4342));
+    for (int h = 0; h < 2; ++h) {
+        const uint8_t *at = slot + g * 128 + (((4 * h + t) ^ (g & 1) << 2) << 4);
+        const uint4 wl = *reinterpret_cast<const uint4 *>(at), wh = *reinterpret_cast<const uint4 *>(at + 1024);
+        if constexpr (F8) {
+            const uint32_t lo[4] = {wl.x, wl.y, wl.z, wl.w}, hi[4] = {wh.x, wh.y, wh.z, wh.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                uint32_t a[4];
+                decode4(lo[i], a[0], a[2], nan[0]);
+                decode4(hi[i], a[1], a[3], nan[1]);
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+                    if (n < live) {
+                        const uint4 &v = x[n].v[2 * h + i / 2];
+                        const uint32_t b0 = i & 1 ? v.z : v.x, b1 = i & 1 ? v.w : v.y;
+                        mma_bf16(c[n], a[0], a[1], a[2], a[3], __byte_perm(b0, b1, 0x5410), __byte_perm(b0, b1, 0x7632));
+                    }
+            }
+        } else {
 #pragma unroll
             for (int n = 0; n < NT; ++n)
-                if (n < groups) {
-                    const uint4 &v = x[n].v[i / 2];
-                    mma_bf16(c[n], a0, a1, a2, a3, i & 1 ? v.z : v.x, i & 1 ? v.w : v.y);
+                if (n < live) {
+                    const uint4 &v = x[n].v[h];
+                    mma_bf16(acc[n], wl.x, wh.x, wl.y, wh.y, v.x, v.y);
+                    mma_bf16(acc[n], wl.z, wh.z, wl.w, wh.w, v.z, v.w);
                 }
         }
+    }
+    if constexpr (F8) {
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             acc[n][0] += s_lo * c[n][0], acc[n][1] += s_lo * c[n][1];
             acc[n][2] += s_hi * c[n][2], acc[n][3] += s_hi * c[n][3];
         }
-    } else {
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-            if (n < groups) multiply<F8>(acc[n], w, x[n]);
     }
 }
-
-// Elements of a chunk.
-template <bool F8>
-constexpr int chunk_of() { return F8 ? 64 : 32; }
 
 // NaN codes in a lane's rows: to the row's other lanes (the four of a group), and into its sums.
 template <int NT>
@@ -227,82 +278,78 @@ __device__ __forceinline__ void spread_nan(float (&acc)[NT][4], const uint32_t (
     }
 }
 
-template <bool F8>
-__device__ __forceinline__ Vec<F8> load_vec(const __nv_bfloat16 *row, int at, bool exists)
-{
-    Vec<F8> x;
-#pragma unroll
-    for (int i = 0; i < (F8 ? 2 : 1); ++i) {
-        x.v[i] = make_uint4(0, 0, 0, 0);
-        if (exists) x.v[i] = load_global(reinterpret_cast<const uint4 *>(row + at) + i);
-    }
-    return x;
-}
+// CTAs of an SM that the kernels are compiled for.
+constexpr int ctas_of(int NT) { return NT == 1 ? 3 : 2; }
 
 // ---------------------------------------------------------------- gate and up
 
-constexpr int kUpWarps = 8;
-
 template <bool F8, int NT>
-__global__ void __launch_bounds__(kUpWarps * 32, NT == 4 ? 2 : 3) k_moe_up(const MoeArgs a)
+__global__ void __launch_bounds__(kWarps * 32, ctas_of(NT)) k_moe_up(const MoeArgs a)
 {
-    // chunks of the weight on the way at once, and of the tokens' vectors (which come from L1 and L2)
-    constexpr int U = NT == 4 ? 2 : 4, V = F8 ? (NT == 1 ? 2 : 1) : U, SPAN = chunk_of<F8>();
+    constexpr int SPAN = step_of<F8>();
     extern __shared__ __align__(16) uint8_t smem[];
-    __shared__ float part[kUpWarps][NT * kRows][17];
-    const Plan plan(smem, a.E, a.T * a.k);
+    __shared__ float part[kWarps][NT * kRows][17];
+    const Plan plan(smem + kRingBytes, a.E, a.T * a.k);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    uint8_t *ring = smem + warp * kRing * kStep;
     wait_for_prior_grid();
     // behind the wait: what came before this kernel has ended when the next one starts, which reads choices and
     // weights before its own wait
     dependents_may_launch();
     make_plan(a, plan, NT * kRows);
     const int tiles = a.I / 8, units = *plan.count * tiles;
-    const int chunks = (a.H + SPAN - 1) / SPAN, kb = (a.H + 127) / 128;
+    const int steps = (a.H + SPAN - 1) / SPAN, kb = (a.H + 127) / 128;
     const int64_t bytes = static_cast<int64_t>(a.H) * (F8 ? 1 : 2), up_rows = a.I * bytes;
+    const int64_t off[4] = {0, 4 * bytes, up_rows, up_rows + 4 * bytes};
 
+    // the copies' place: unit of work, step, and the lane's first byte there
+    int fu = warp < steps ? static_cast<int>(blockIdx.x) : units, fc = warp, slot = 0;
+    const uint8_t *from = nullptr;
+    auto open = [&] {
+        if (fu < units)
+            from = a.W13 + (static_cast<int64_t>(plan.groups[fu / tiles].expert) * 2 * a.I + fu % tiles * 8 + (lane >> 3)) * bytes +
+                   16 * (lane & 7);
+    };
+    auto issue = [&](int at) {
+        if (fu < units) {
+            const int64_t first = static_cast<int64_t>(fc) * 128;
+            const bool in = first + 16 * (lane & 7) < bytes, exists[4] = {in, in, in, in};
+            copy_step(ring + at * kStep, from + first, off, exists, a.W13);
+            if ((fc += kWarps) >= steps) {
+                fc = warp;
+                fu += gridDim.x;
+                open();
+            }
+        }
+        copies_commit();
+    };
+    open();
+#pragma unroll
+    for (int i = 0; i < kRing; ++i) issue(i);
     for (int u = blockIdx.x; u < units; u += gridDim.x) {
         const Group group = plan.groups[u / tiles];
         const int live = (group.rows + kRows - 1) / kRows, i0 = u % tiles * 8;
-        const uint8_t *rows = a.W13 + (static_cast<int64_t>(group.expert) * 2 * a.I + i0 + g) * bytes + 16 * t;
         const float *plane = F8 ? a.s13 + static_cast<int64_t>((2 * a.I + 127) / 128) * kb * group.expert : nullptr;
         const float *s_gate = plane + i0 / 128 * static_cast<int64_t>(kb), *s_up = plane + (a.I + i0) / 128 * static_cast<int64_t>(kb);
         const __nv_bfloat16 *x[NT];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             const int r = 8 * n + g;
-            x[n] = a.X + (r < group.rows ? static_cast<int64_t>(plan.token[group.slot + r]) * a.H : 0) + SPAN / 4 * t;
+            x[n] = a.X + (r < group.rows ? static_cast<int64_t>(plan.token[group.slot + r]) * a.H : 0);
         }
         float acc[NT][4] = {};
         uint32_t nan[2] = {};
-        for (int c0 = warp; c0 < chunks; c0 += kUpWarps * U) {
-            Weights w[U];
-            float sg[U], su[U];
+        for (int c = warp; c < steps; c += kWarps) {
+            Vec<F8> v[NT];
 #pragma unroll
-            for (int i = 0; i < U; ++i) {
-                const int c = c0 + i * kUpWarps;
-                w[i].lo = w[i].hi = make_uint4(0, 0, 0, 0);
-                if (c * SPAN + t * (SPAN / 4) < a.H) {
-                    w[i].lo = load_stream(rows + static_cast<int64_t>(c) * 64);
-                    w[i].hi = load_stream(rows + up_rows + static_cast<int64_t>(c) * 64);
-                }
-                sg[i] = su[i] = 0.f;
-                if (F8 && c < chunks) sg[i] = load_float(s_gate + c / 2), su[i] = load_float(s_up + c / 2);
-            }
-            Vec<F8> v[V][NT];
-#pragma unroll
-            for (int j = 0; j < U; j += V) {
-#pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    const int c = c0 + (i + j) * kUpWarps;
-                    const bool in = c * SPAN + t * (SPAN / 4) < a.H;
-#pragma unroll
-                    for (int n = 0; n < NT; ++n)
-                        if (n < live) v[i][n] = load_vec<F8>(x[n], c * SPAN, in && 8 * n + g < group.rows);
-                }
-#pragma unroll
-                for (int i = 0; i < V; ++i) add_chunk<F8, NT>(acc, w[i + j], v[i], live, sg[i + j], su[i + j], nan);
-            }
+            for (int n = 0; n < NT; ++n)
+                if (n < live) load_vec<F8>(v[n], x[n], c * SPAN, t, a.H, 8 * n + g < group.rows);
+            const float sg = F8 ? load_float(s_gate + c) : 1.f, su = F8 ? load_float(s_up + c) : 1.f;
+            copies_wait();
+            add_step<F8, NT>(acc, ring + slot * kStep, v, live, sg, su, nan);
+            __syncwarp();
+            issue(slot);
+            slot = (slot + 1) % kRing;
         }
         if (F8) spread_nan<NT>(acc, nan);
 #pragma unroll
@@ -311,130 +358,129 @@ __global__ void __launch_bounds__(kUpWarps * 32, NT == 4 ? 2 : 3) k_moe_up(const
 #pragma unroll
                 for (int i = 0; i < 4; ++i) part[warp][8 * n + 2 * t + (i & 1)][g + 8 * (i >> 1)] = acc[n][i];
         __syncthreads();
-        for (int i = threadIdx.x; i < group.rows * 8; i += kUpWarps * 32) {
+        for (int i = threadIdx.x; i < group.rows * 8; i += kWarps * 32) {
             const int r = i / 8, f = i % 8;
             float gate = 0.f, up = 0.f;
 #pragma unroll
-            for (int j = 0; j < kUpWarps; ++j) gate += part[j][r][f], up += part[j][r][f + 8];
+            for (int j = 0; j < kWarps; ++j) gate += part[j][r][f], up += part[j][r][f + 8];
             // (__expf is off by some 2^-20, the rounding of h by up to 2^-8)
             const float h = gate / (1.f + __expf(-gate)) * up * plan.share[group.slot + r];
             a.h[static_cast<int64_t>(group.slot + r) * a.I + i0 + f] = __float2bfloat16(h);
         }
         __syncthreads();
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
 // ---------------------------------------------------------------- down
 
-// CTAs of a cluster share the list of a tile of 16 features, so that few tiles keep the SMs busy too.
-template <int NT>
-struct Down {
-    static constexpr int WARPS = NT == 1 ? 16 : 8;
-    static constexpr int STRIDE = 17;  // of a token's 16 sums
-    static size_t bytes(int T) { return static_cast<size_t>(WARPS) * T * STRIDE * 4; }
-};
+constexpr int kStride = 17;  // of a token's 16 sums
 
+size_t sums_bytes(int T) { return static_cast<size_t>(kWarps) * T * kStride * 4; }
+
+// CTAs of a cluster share the list of a tile of 16 features, so that few tiles keep the SMs busy too.
 template <bool F8, int NT>
-__global__ void __launch_bounds__(Down<NT>::WARPS * 32, 2) k_moe_down(const MoeArgs a, const int parts)
+__global__ void __launch_bounds__(kWarps * 32, ctas_of(NT)) k_moe_down(const MoeArgs a, const int parts)
 {
-    constexpr int U = 4, WARPS = Down<NT>::WARPS, STRIDE = Down<NT>::STRIDE, SPAN = chunk_of<F8>();
+    constexpr int SPAN = step_of<F8>();
     extern __shared__ __align__(16) uint8_t smem[];
-    const Plan plan(smem, a.E, a.T * a.k);
-    float *sums = reinterpret_cast<float *>(smem + Plan::bytes(a.E, a.T * a.k));
+    const Plan plan(smem + kRingBytes, a.E, a.T * a.k);
+    float *sums = reinterpret_cast<float *>(smem + kRingBytes + Plan::bytes(a.E, a.T * a.k));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    uint8_t *ring = smem + warp * kRing * kStep;
     const int n0 = blockIdx.x / parts * 16, rank = blockIdx.x % parts;
     dependents_may_launch();
-    for (int i = threadIdx.x; i < WARPS * a.T * STRIDE; i += WARPS * 32) sums[i] = 0.f;
+    for (int i = threadIdx.x; i < kWarps * a.T * kStride; i += kWarps * 32) sums[i] = 0.f;
     make_plan(a, plan, NT * kRows);
 
-    const int chunks = (a.I + SPAN - 1) / SPAN, kb = (a.I + 127) / 128;
+    const int steps = (a.I + SPAN - 1) / SPAN, kb = (a.I + 127) / 128;
     const int64_t bytes = static_cast<int64_t>(a.I) * (F8 ? 1 : 2), nb = (a.H + 127) / 128;
-    const bool in0 = n0 + g < a.H, in1 = n0 + g + 8 < a.H;
-    // this warp's run of all (group, chunk) pairs
-    const int64_t all = static_cast<int64_t>(*plan.count) * chunks, workers = WARPS * parts, me = rank * WARPS + warp;
+    const int64_t off[4] = {0, 4 * bytes, 8 * bytes, 12 * bytes};
+    // this warp's run of all (group, step) pairs
+    const int64_t all = static_cast<int64_t>(*plan.count) * steps, workers = kWarps * parts, me = rank * kWarps + warp;
     const int64_t q0 = all * me / workers;
-    int left = static_cast<int>(all * (me + 1) / workers - q0);
-    int at = static_cast<int>(q0 / chunks), c = static_cast<int>(q0 - static_cast<int64_t>(at) * chunks);
+    int left = static_cast<int>(all * (me + 1) / workers - q0), slot = 0;
+    int at = static_cast<int>(q0 / steps), c = static_cast<int>(q0 - static_cast<int64_t>(at) * steps);
 
-    // what is fetched next: group, chunk, how many are left
+    // the copies' place: group, step, how many are left
     int fat = at, fc = c, fleft = left;
-    Weights w[U];
-    float s[U];
-    const uint8_t *rows = nullptr;
-    const float *s2 = nullptr;
+    const uint8_t *from = nullptr;
     auto open = [&] {
-        const int64_t e = plan.groups[fat].expert;
-        rows = a.W2 + (e * a.H + n0 + g) * bytes + 16 * t;
-        if (F8) s2 = a.s2 + (e * nb + n0 / 128) * kb;
+        if (fleft > 0)
+            from = a.W2 + (static_cast<int64_t>(plan.groups[fat].expert) * a.H + n0 + (lane >> 3)) * bytes + 16 * (lane & 7);
     };
-    auto fetch = [&](int i) {
-        if (fleft-- <= 0) return;
-        const bool in = fc * SPAN + t * (SPAN / 4) < a.I;
-        w[i].lo = w[i].hi = make_uint4(0, 0, 0, 0);
-        if (in && in0) w[i].lo = load_stream(rows + static_cast<int64_t>(fc) * 64);
-        if (in && in1) w[i].hi = load_stream(rows + 8 * bytes + static_cast<int64_t>(fc) * 64);
-        if (F8) s[i] = load_float(s2 + fc / 2);
-        if (++fc == chunks) {
-            fc = 0, ++fat;
-            if (fleft > 0) open();
+    auto issue = [&](int into) {
+        if (fleft > 0) {
+            const int64_t first = static_cast<int64_t>(fc) * 128;
+            const bool in = first + 16 * (lane & 7) < bytes;
+            const int rows = a.H - n0 - (lane >> 3);
+            const bool exists[4] = {in && rows > 0, in && rows > 4, in && rows > 8, in && rows > 12};
+            copy_step(ring + into * kStep, from + first, off, exists, a.W2);
+            --fleft;
+            if (++fc == steps) {
+                fc = 0;
+                ++fat;
+                open();
+            }
         }
+        copies_commit();
     };
-    if (left > 0) open();
+    open();
 #pragma unroll
-    for (int i = 0; i < U; ++i) fetch(i);
+    for (int i = 0; i < kRing; ++i) issue(i);
     wait_for_prior_grid();  // h is there
     float acc[NT][4] = {};
     uint32_t nan[2] = {};
-    float *mine = sums + warp * a.T * STRIDE;
-    while (left > 0) {
+    float *mine = sums + warp * a.T * kStride;
+    for (; left > 0; --left) {
+        const Group group = plan.groups[at];
+        const int live = (group.rows + kRows - 1) / kRows;
+        Vec<F8> v[NT];
 #pragma unroll
-        for (int i = 0; i < U; ++i) {
-            if (left <= 0) break;
-            const Group group = plan.groups[at];
-            const int live = (group.rows + kRows - 1) / kRows, k = c * SPAN + t * (SPAN / 4);
-            Vec<F8> v[NT];
+        for (int n = 0; n < NT; ++n)
+            if (n < live)
+                load_vec<F8>(v[n], a.h + static_cast<int64_t>(group.slot + 8 * n + g) * a.I, c * SPAN, t, a.I, 8 * n + g < group.rows);
+        const float s = F8 ? load_float(a.s2 + (group.expert * nb + n0 / 128) * kb + c) : 1.f;
+        copies_wait();
+        add_step<F8, NT>(acc, ring + slot * kStep, v, live, s, s, nan);
+        __syncwarp();
+        issue(slot);
+        slot = (slot + 1) % kRing;
+        const bool last = ++c == steps;
+        if (last || left == 1) {  // the group's sum, as far as this warp has it, to its tokens
+            if (F8) spread_nan<NT>(acc, nan);
+            nan[0] = nan[1] = 0;
 #pragma unroll
             for (int n = 0; n < NT; ++n)
-                if (n < live)
-                    v[n] = load_vec<F8>(a.h + static_cast<int64_t>(group.slot + 8 * n + g) * a.I, k, k < a.I && 8 * n + g < group.rows);
-            add_chunk<F8, NT>(acc, w[i], v, live, s[i], s[i], nan);
-            fetch(i);
-            --left;
-            const bool last = ++c == chunks;
-            if (last || left == 0) {  // the group's sum, as far as this warp has it, to its tokens
-                if (F8) spread_nan<NT>(acc, nan);
-                nan[0] = nan[1] = 0;
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int r = 8 * n + 2 * t + (j & 1);
-                        if (r < group.rows) mine[plan.token[group.slot + r] * STRIDE + g + 8 * (j >> 1)] += acc[n][j];
-                        acc[n][j] = 0.f;
-                    }
-                __syncwarp();
-            }
-            if (last) c = 0, ++at;
+                for (int j = 0; j < 4; ++j) {
+                    const int r = 8 * n + 2 * t + (j & 1);
+                    if (r < group.rows) mine[plan.token[group.slot + r] * kStride + g + 8 * (j >> 1)] += acc[n][j];
+                    acc[n][j] = 0.f;
+                }
+            __syncwarp();
         }
+        if (last) c = 0, ++at;
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
     __syncthreads();
     // the warps' sums in order, then the CTAs' in order
-    for (int i = threadIdx.x; i < a.T * 16; i += WARPS * 32) {
+    for (int i = threadIdx.x; i < a.T * 16; i += kWarps * 32) {
         const int r = i / 16, f = i % 16;
         float y = 0.f;
 #pragma unroll
-        for (int j = 0; j < WARPS; ++j) y += sums[(j * a.T + r) * STRIDE + f];
-        if (parts > 1) sums[r * STRIDE + f] = y;  // (nobody else reads or writes this one)
+        for (int j = 0; j < kWarps; ++j) y += sums[(j * a.T + r) * kStride + f];
+        if (parts > 1) sums[r * kStride + f] = y;  // (nobody else reads or writes this one)
         else if (n0 + f < a.H) a.Y[static_cast<int64_t>(r) * a.H + n0 + f] = __float2bfloat16(y);
     }
     if (parts == 1) return;
     cluster_sync_all();
-    for (int i = rank * WARPS * 32 + threadIdx.x; i < a.T * 16; i += parts * WARPS * 32) {
+    for (int i = rank * kWarps * 32 + threadIdx.x; i < a.T * 16; i += parts * kWarps * 32) {
         const int r = i / 16, f = i % 16;
         float y = 0.f;
         for (int p = 0; p < parts; ++p) {
             float other;
-            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(other) : "r"(cluster_addr(sums + r * STRIDE + f, p)) : "memory");
+            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(other) : "r"(cluster_addr(sums + r * kStride + f, p)) : "memory");
             y += other;
         }
         if (n0 + f < a.H) a.Y[static_cast<int64_t>(r) * a.H + n0 + f] = __float2bfloat16(y);
@@ -445,28 +491,21 @@ __global__ void __launch_bounds__(Down<NT>::WARPS * 32, 2) k_moe_down(const MoeA
 template <bool F8, int NT>
 bsl_status run(const MoeArgs &a, cudaStream_t s)
 {
+    constexpr int kMost = 150 * 1024;
     const int pairs = a.T * a.k;
-    const size_t plan = Plan::bytes(a.E, pairs), down = plan + Down<NT>::bytes(a.T);
-    const size_t part = static_cast<size_t>(kUpWarps) * NT * kRows * 17 * 4;
-    constexpr int kMost = 96 * 1024;
-    if (plan + part > 48 * 1024) {
-        const bsl_status sa = set_smem_once(reinterpret_cast<const void *>(&k_moe_up<F8, NT>), kMost);
-        if (sa != BSL_OK) return sa;
-    }
-    if (down > 48 * 1024) {
-        const bsl_status sa = set_smem_once(reinterpret_cast<const void *>(&k_moe_down<F8, NT>), kMost);
-        if (sa != BSL_OK) return sa;
-    }
+    const size_t up = kRingBytes + Plan::bytes(a.E, pairs), down = up + sums_bytes(a.T);
+    bsl_status st = set_smem_once(reinterpret_cast<const void *>(&k_moe_up<F8, NT>), kMost);
+    if (st == BSL_OK) st = set_smem_once(reinterpret_cast<const void *>(&k_moe_down<F8, NT>), kMost);
+    if (st != BSL_OK) return st;
     const int64_t units = static_cast<int64_t>(a.I / 8) * (pairs < a.E ? pairs : a.E);
-    const int64_t room = static_cast<int64_t>(num_sms()) * (NT == 4 ? 2 : 3);
-    const bsl_status up = cuda_status(launch_dependent(k_moe_up<F8, NT>, static_cast<unsigned>(units < room ? units : room),
-                                                       kUpWarps * 32, plan, s, a));
-    if (up != BSL_OK) return up;
-    // as many CTAs a tile as two an SM have room for
+    const int64_t room = static_cast<int64_t>(num_sms()) * ctas_of(NT);
+    st = cuda_status(launch_dependent(k_moe_up<F8, NT>, static_cast<unsigned>(units < room ? units : room), kWarps * 32, up, s, a));
+    if (st != BSL_OK) return st;
+    // as many CTAs a tile as there is room for on the SMs
     const int tiles = (a.H + 15) / 16;
     int parts = 1;
-    while (parts < 8 && 2 * parts * tiles <= 2 * num_sms()) parts *= 2;
-    return cuda_status(launch_dependent_cluster(k_moe_down<F8, NT>, tiles * parts, parts, Down<NT>::WARPS * 32, down, s, a, parts));
+    while (parts < 8 && 2 * parts * tiles <= room) parts *= 2;
+    return cuda_status(launch_dependent_cluster(k_moe_down<F8, NT>, tiles * parts, parts, kWarps * 32, down, s, a, parts));
 }
 
 // Tokens a group takes: as many as an expert has on the average, in eights.  An expert with more is read again for
