@@ -196,25 +196,18 @@ __device__ __forceinline__ void load_vec(Vec<F8> &x, const __nv_bfloat16 *row, i
     }
 }
 
-// Two e4m3 codes to two bf16: the bits s e e e e m m m go to the sign and to the lowest exponent and highest mantissa
-// bits, which is 2^-120 of the value, subnormal codes included, and one exact product brings it in.  `w`: the codes in
-// the upper bytes of the halves (and anything below), `m`: the same without their signs, and zeros below.  The NaN
-// codes come out as 480 and are looked for apart.
-__device__ __forceinline__ uint32_t bf16_of_codes(uint32_t w, uint32_t m)
-{
-    const uint32_t v = (w & 0x80008000u) | m >> 4;
-    uint32_t r;
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(0x7B807B80u));
-    return r;
-}
-
-// Four codes to two registers of two bf16, codes 0, 2 and codes 1, 3; bit 7 of a byte of `nan` is set if its code is NaN.
-__device__ __forceinline__ void decode4(uint32_t w, uint32_t &even, uint32_t &odd, uint32_t &nan)
+// Four e4m3 codes to two registers of two bf16, codes 0, 2 and codes 1, 3: the bits s e e e e m m m go to the sign and
+// to the lowest exponent and highest mantissa bits, which is 2^-120 of the value, subnormal codes included, and one
+// exact product brings it in.  The NaN codes come out as 480 and are looked for apart: they, and no other, have bit 7
+// of their byte set in what is returned.
+__device__ __forceinline__ uint32_t decode4(uint32_t w, uint32_t &even, uint32_t &odd)
 {
     const uint32_t m = w & 0x7F7F7F7Fu;
-    nan |= m + 0x01010101u;
-    even = bf16_of_codes(w << 8, m << 8 & 0xFF00FF00u);
-    odd = bf16_of_codes(w, m & 0xFF00FF00u);
+    even = (w * 256 & 0x80008000u) | (m & 0x007F007Fu) * 16;
+    odd = (w & 0x80008000u) | (m >> 4 & 0x07F007F0u);
+    asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(even) : "r"(0x7B807B80u));
+    asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(odd) : "r"(0x7B807B80u));
+    return m + 0x01010101u;
 }
 
 // A step's products, added to acc: NT groups of tokens, `live` of them there.  8 bits: the sum of the block times the
@@ -234,8 +227,8 @@ __device__ __forceinline__ void add_step(float (&acc)[NT][4], const uint8_t *slo
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 uint32_t a[4];
-                decode4(lo[i], a[0], a[2], nan[0]);
-                decode4(hi[i], a[1], a[3], nan[1]);
+                nan[0] |= decode4(lo[i], a[0], a[2]);
+                nan[1] |= decode4(hi[i], a[1], a[3]);
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
                     if (n < live) {

@@ -178,8 +178,9 @@ struct RouteSmem {
     static size_t bytes(int E, int pairs) { return 4 * (static_cast<size_t>(E) + 1 + kSortWarps * E) + 6 * static_cast<size_t>(pairs); }
 };
 
-// Threads of k_route: a CTA that sorts has many tokens and no others beside it.
-constexpr int route_threads(int NE, int sort) { return sort == 2 ? (NE >= 16 ? 512 : 1024) : 256; }
+// Threads of k_route: a CTA that counts or sorts has up to 128 tokens, and latency bounds a token, so that many warps
+// share them (16384 tokens, 128 experts: 8 warps 35 us, 32 warps 11).
+constexpr int route_threads(int NE, int sort) { return sort == 0 ? 256 : NE >= 16 ? 512 : 1024; }
 
 // Choices of a run of tokens; kSort 1: with their counts for k_sort, 2: and sorted here (one CTA).
 template <int NE, int kSort>
@@ -240,11 +241,18 @@ __global__ void __launch_bounds__(512) k_sort(const RouteArgs a)
         const int e = i % a.E, part = i / a.E;
         int all = 0, prior = 0;
         const int end = (part + 1) * runs / parts;
-#pragma unroll 8
-        for (int c = part * runs / parts; c < end; ++c) {
-            const int v = static_cast<int>(load_global(reinterpret_cast<const uint32_t *>(a.counts + static_cast<int64_t>(c) * a.E + e)));
-            all += v;
-            prior += c < static_cast<int>(blockIdx.x) ? v : 0;
+        for (int c0 = part * runs / parts; c0 < end; c0 += 16) {  // sixteen loads on the way
+            int v[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                v[j] = c0 + j < end ? static_cast<int>(load_global(reinterpret_cast<const uint32_t *>(
+                                          a.counts + static_cast<int64_t>(c0 + j) * a.E + e)))
+                                    : 0;
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                all += v[j];
+                prior += c0 + j < static_cast<int>(blockIdx.x) ? v[j] : 0;
+            }
         }
         if (all) atomicAdd(&m.count[e], all);
         if (prior) atomicAdd(&before[e], prior);
@@ -353,7 +361,7 @@ bsl_status route_of(RouteArgs &a, int sort, cudaStream_t s)
 {
     const unsigned runs = (a.T + a.run - 1) / a.run;
     const size_t smem = sort ? RouteSmem::bytes(a.E, a.run * a.k) : 0;
-    const unsigned threads = sort == 2 && a.T > 8 ? route_threads(NE, 2) : 256;
+    const unsigned threads = a.T > 8 ? route_threads(NE, sort) : 256;
     auto kern = sort == 0 ? k_route<NE, 0> : sort == 1 ? k_route<NE, 1> : k_route<NE, 2>;
     if (smem > 48 * 1024) {
         const bsl_status sa = set_smem_once(reinterpret_cast<const void *>(kern), 100 * 1024);
