@@ -22,11 +22,12 @@
 // Persistent kernels, programmatic dependents, 20 warps a CTA:
 //   warp 0      TMA producer (a ring of stages);
 //   warp 1      MMA issuer and TMEM owner;
-//   warp 2      products of the two scales of each row and block, some stages
-//               ahead, into shared memory; and the one that waits for the MMAs of a
-//               stage: the sums stand at a named barrier (a waiting warp polls shared
-//               memory, which the MMAs and copies need);
-//   warp 3      zeros for the rows of no expert, on request;
+//   warp 2      the one that waits for the MMAs of a stage: the sums stand at a
+//               named barrier (a waiting warp polls shared memory, which the MMAs and
+//               copies need);
+//   warp 3      products of the two scales of each row and block, some stages
+//               ahead, into shared memory; then zeros for the rows of no expert, on
+//               request;
 //   warps 4-19  sums: warp 4 + 4 p + q owns lanes 32 q .. of columns 64 p ..
 // Tiles are dealt round robin; no workspace is shared by calls, and every output
 // is one sum in a fixed order.
@@ -62,8 +63,8 @@ constexpr int kThreads = 128 + 32 * kSumWarps;
 constexpr int kChunk = 32 * kWidth * 2;         // a sum warp's output
 constexpr int kTmem = 512;                      // two accumulators
 constexpr int kAhead = 4, kScales = kAhead + 2;  // stages whose scales are made ahead
-constexpr int kInfos = 16;                      // tiles that warp 2 may be ahead of a sum, and more: kAhead + 5
-constexpr int kBars = (2 * kStages + 3) * 8 + 16;
+constexpr int kInfos = 16;                      // more tiles than warp 2 may be ahead of a sum
+constexpr int kBars = (2 * kStages + kScales + 3) * 8 + 16;
 constexpr int kSmem = 1024 + kRing + kSumWarps * kChunk + kScales * 1024 + kInfos * 16 + kBars + 2 * (kMaxExperts + 1) * 4;
 static_assert(kSmem <= 227 * 1024, "shared memory");
 
@@ -161,19 +162,17 @@ __device__ __forceinline__ float2 both(uint64_t v)
     return f;
 }
 
-// The scales of blocks b .. b + 3 of a row, of `count` blocks that lie `step` apart (in whole 16 bytes, if quads);
-// past the end: zero.
-__device__ __forceinline__ void load_scales(const float *row, int b, int count, int64_t step, bool quads, bool exists,
-                                            float (&s)[4])
+// The scales of `n` blocks, up to four, that lie `step` apart, in whole 16 bytes if quads (n is 4 then); zero for the
+// others, or if there are none.
+__device__ __forceinline__ void load_scales(const float *at, int n, int64_t step, bool quads, bool exists, float (&s)[4])
 {
-    exists &= b < count;
     if (quads) {
         uint4 v = make_uint4(0, 0, 0, 0);
-        if (exists) v = load_global(reinterpret_cast<const uint4 *>(row + b));
+        if (exists) v = load_global(reinterpret_cast<const uint4 *>(at));
         s[0] = __uint_as_float(v.x), s[1] = __uint_as_float(v.y), s[2] = __uint_as_float(v.z), s[3] = __uint_as_float(v.w);
     } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) s[i] = exists && b + i < count ? load_float(row + (b + i) * step) : 0.f;
+        for (int i = 0; i < 4; ++i) s[i] = exists && i < n ? load_float(at + i * step) : 0.f;
     }
 }
 
@@ -221,6 +220,18 @@ __device__ __forceinline__ void named_bar_arrive(uint32_t id, uint32_t count)
     asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(count) : "memory");
 }
 
+// Until *count is `value` or more; bounded as mbar_wait.
+__device__ __forceinline__ bool reached(const volatile int *count, int value, uint64_t timeout_ns, const volatile int *abort)
+{
+    if (*count >= value) return true;
+    const uint64_t t0 = globaltimer_ns();
+    while (true) {
+        __nanosleep(100);
+        if (*count >= value) return true;
+        if (*abort || globaltimer_ns() - t0 > timeout_ns) return false;
+    }
+}
+
 // An accumulator was read out, as far as this warp reads it.
 __device__ __forceinline__ void release(uint32_t bar, int lane)
 {
@@ -263,10 +274,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp8(const __grid_constant__ Map
     uint64_t *full = reinterpret_cast<uint64_t *>(infos + kInfos);  // copies of a stage landed (leader)
     uint64_t *empty = full + kStages;   // MMAs of a stage finished (each CTA)
     uint64_t *aempty = empty + kStages; // an accumulator was read out (leader)
-    uint64_t *drain = aempty + 2;
+    uint64_t *ready = aempty + 2;       // a stage's scales are there
+    uint64_t *drain = ready + kScales;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     int *ring_slot = reinterpret_cast<int *>(tmem_slot + 2);
+    volatile int *progress = reinterpret_cast<volatile int *>(tmem_slot + 3);  // stages whose MMAs are done
     int32_t *off = reinterpret_cast<int32_t *>(tmem_slot + 4);
     int32_t *start = off + kMaxExperts + 1;
 
@@ -281,8 +294,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp8(const __grid_constant__ Map
             mbar_init(&empty[s], 1);
         }
         for (int a = 0; a < 2; ++a) mbar_init(&aempty[a], 2 * kSumWarps);
+        for (int s = 0; s < kScales; ++s) mbar_init(&ready[s], 1);
         mbar_init(drain, 1);
         *abort_flag = 0;
+        *progress = 0;
         fence_barrier_init();
         tma_prefetch_map(&maps.weight);
         tma_prefetch_map(&maps.out);
@@ -397,19 +412,37 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp8(const __grid_constant__ Map
             }
             __syncwarp();
         } else {
-            // -------------------------------------------------------- scales, and the wait for the MMAs
+            const int total = count > first ? (count - first + stride - 1) / stride * blocks : 0;
+            bool ok = true;
             if (warp == 2) {
+                // ---------------------------------------------------- the wait for the MMAs of a stage, for the sums
+                Place at, sc;
+                for (int it = 0; it < total; ++it, at.next(S), sc.next(kScales)) {
+                    if (ok && (__any_sync(0xffffffffu, !mbar_wait(&empty[at.slot], at.parity, tmo, abort_flag)) ||
+                               __any_sync(0xffffffffu, !mbar_wait(&ready[sc.slot], sc.parity, tmo, abort_flag)))) {
+                        ok = false;
+                        if (lane == 0) *abort_flag = 1;
+                        __syncwarp();
+                    }
+                    if (ok) named_bar_arrive(1 + (it & 1), 32 * kSumWarps + 32);
+                    else named_bar_sync(1 + (it & 1), 32 * kSumWarps + 32);  // an aborted run's sums go on to the end, in step
+                    if (lane == 0) *progress = it + 1;
+                }
+            } else {
+                // ---------------------------------------------------- scales
                 const int wide_blocks = (args.cols + 127) / 128;
                 const int64_t plane = static_cast<int64_t>(wide_blocks) * blocks, wstep = kGrad ? wide_blocks : 1;
-                bool ok = true;
-                Place at;
-                // the walk that is kAhead stages ahead: tile, its rows, block
-                int t = first, b = 0, n = 0, ring = 0;
+                // what is loaded next: tile, block, and what is known of the tile
+                int t = first, b = 0, n = 0, ring = 0, rows = 0;
                 const float *rs = nullptr, *ws = nullptr;
-                int rows = 0;
                 bool second = false;
-                float row[2][4], col[2][2];  // two stages' scales on the way
-                auto load = [&](float (&r)[4], float (&c)[2]) {
+                const bool quads = args.scale_stride % 4 == 0, wquads = !kGrad && blocks % 4 == 0;
+                struct Four {  // blocks' scales: of this lane's rows 32 apart, and of the weight's two tiles
+                    float row[4][4], col[2][4];
+                    int n;
+                };
+                auto load = [&](Four &f) {
+                    f.n = 0;
                     if (t >= count) return;
                     if (b == 0) {
                         const Tile x = tiles.at(t);
@@ -420,55 +453,54 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp8(const __grid_constant__ Map
                         ws = args.weight_scales + x.e * plane + x.c0 / 128 * (kGrad ? 1 : static_cast<int64_t>(blocks));
                         second = x.c0 + 128 < args.cols;
                     }
+                    f.n = min(4, blocks - b);
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        r[i] = lane + 32 * i < rows ? load_float(rs + 32 * i * static_cast<int64_t>(args.scale_stride) + b) : 0.f;
-                    c[0] = load_float(ws + b * wstep);
-                    c[1] = second ? load_float(ws + (kGrad ? 1 : blocks) + b * wstep) : 0.f;
-                    if (++b == blocks) b = 0, t += stride, ++n;
+                        load_scales(rs + 32 * i * static_cast<int64_t>(args.scale_stride) + b, f.n, 1, quads, lane + 32 * i < rows,
+                                    f.row[i]);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        load_scales(ws + i * (kGrad ? 1 : static_cast<int64_t>(blocks)) + b * wstep, f.n, wstep, wquads, !i || second,
+                                    f.col[i]);
+                    if ((b += f.n) == blocks) b = 0, t += stride, ++n;
                 };
-                auto put = [&](const float (&r)[4], const float (&c)[2]) {
-                    float *to = scales + ring * 256 + lane;
+                int made = 0;
+                // stage `made` goes where stage made - kScales was, whose sums were read out before the MMAs of stage
+                // made - kAhead began: those are done
+                auto make = [&](const Four &f) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) to[32 * i] = r[i] * c[0], to[128 + 32 * i] = r[i] * c[1];
-                    if (++ring == kScales) ring = 0;
-                };
-                const int total = count > first ? (count - first + stride - 1) / stride * blocks : 0;
-                load(row[0], col[0]);
-                load(row[1], col[1]);
+                    for (int j = 0; j < 4; ++j) {
+                        if (!ok || j >= f.n) break;
+                        if (made >= kAhead) ok = __all_sync(0xffffffffu, reached(progress, made - kAhead + 1, tmo, abort_flag));
+                        if (!ok) break;
+                        float *to = scales + ring * 256 + lane;
 #pragma unroll
-                for (int i = 0; i < kAhead; ++i) {
-                    put(row[i & 1], col[i & 1]);
-                    load(row[i & 1], col[i & 1]);
-                }
-                // stage it + kAhead goes where stage it - 2 was, whose sums were read out before the MMAs of it began
-                for (int it = 0; it < total; it += 2) {
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        if (it + i >= total) break;
-                        if (ok && __any_sync(0xffffffffu, !mbar_wait(&empty[at.slot], at.parity, tmo, abort_flag))) {
-                            ok = false;
-                            if (lane == 0) *abort_flag = 1;
-                            __syncwarp();
-                        }
-                        at.next(S);
-                        if (ok) {
-                            named_bar_arrive(1 + i, 32 * kSumWarps + 32);
-                            put(row[i], col[i]);
-                            load(row[i], col[i]);
-                        } else {  // an aborted run's sums go on to the end, in step
-                            named_bar_sync(1 + i, 32 * kSumWarps + 32);
-                        }
+                        for (int i = 0; i < 4; ++i) to[32 * i] = f.row[i][j] * f.col[0][j], to[128 + 32 * i] = f.row[i][j] * f.col[1][j];
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&ready[ring]);
+                        if (++ring == kScales) ring = 0;
+                        ++made;
                     }
+                };
+                // two sets of four blocks in turn: one's loads have the other's stages to arrive
+                Four f, g;
+                load(f);
+                load(g);
+                while (ok && made < total) {
+                    make(f);
+                    load(f);
+                    make(g);
+                    load(g);
                 }
-                if (lane == 0 && !ok) {
-                    *abort_flag = 1;
-                    set_status(args.status, BSL_ERR_TIMEOUT);
+                if (args.zero_rest) {  // rows of no expert
+                    zero_range(args.out, 0, static_cast<int64_t>(off[0]) * args.cols, lane);
+                    zero_range(args.out, static_cast<int64_t>(off[args.E]) * args.cols, static_cast<int64_t>(args.T) * args.cols,
+                               lane);
                 }
-            } else if (args.zero_rest) {  // rows of no expert
-                zero_range(args.out, 0, static_cast<int64_t>(off[0]) * args.cols, lane);
-                zero_range(args.out, static_cast<int64_t>(off[args.E]) * args.cols, static_cast<int64_t>(args.T) * args.cols,
-                           lane);
+            }
+            if (lane == 0 && !ok) {
+                *abort_flag = 1;
+                set_status(args.status, BSL_ERR_TIMEOUT);
             }
             __syncwarp();
         }
