@@ -727,7 +727,7 @@ bsl_status bsl_fp8_product(const uint8_t *codes, const float *scales, int32_t T,
     DeviceGuard guard;
     BSL_TRY(guard.bind(codes));
     BSL_TRY(check_device());
-    return launch_fp8(codes, scales, T, offsets, W, transposed, bias, out, zero_rest, static_cast<cudaStream_t>(stream));
+    return launch_fp8(codes, scales, T, offsets, W, transposed, bias, out, zero_rest, false, static_cast<cudaStream_t>(stream));
 }
 
 size_t bsl_fp8_workspace_bytes(int32_t T, const bsl_fp8 *W, int32_t transposed)
@@ -754,7 +754,7 @@ bsl_status bsl_fp8_linear(const void *A, int32_t T, const int32_t *offsets, cons
     float *scales = reinterpret_cast<float *>(codes + static_cast<size_t>(T) * depth);  // depth is a multiple of 16
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     BSL_TRY(launch_fp8_quantize(A, 1, T, depth, false, codes, scales, s));
-    return launch_fp8(codes, scales, T, offsets, W, transposed, bias, out, zero_rest, s);
+    return launch_fp8(codes, scales, T, offsets, W, transposed, bias, out, zero_rest, true, s);
 }
 
 bsl_status bsl_fp8_get_status(const bsl_fp8 *W, int32_t *status_host, void *stream)

@@ -368,11 +368,11 @@ __device__ __forceinline__ void mma_e4m3(float (&c)[4], uint32_t a0, uint32_t a1
 
 // A warp's step is one block of 128 k, whose sum gets its scales when it is
 // complete: the weight's is one number for the 16 features, the rows' come two
-// to a lane.  The codes go to the MMA as they lie.
-template <int NT>
+// to a lane.  The codes go to the MMA as they lie, which unpacks them by instructions:
+// 4.5 TB/s at most, so only the smallest calls come here.
 __global__ void __launch_bounds__(kWarps * 32, 3) k_few_rows8(const FewArgs a)
 {
-    __shared__ float part[kWarps][NT * kRows][kFeatures];
+    __shared__ float part[kWarps][kRows][kFeatures];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int li = blockIdx.x / a.blocks, n0 = (blockIdx.x - li * a.blocks) * kFeatures;
     dependents_may_launch();
@@ -392,11 +392,11 @@ __global__ void __launch_bounds__(kWarps * 32, 3) k_few_rows8(const FewArgs a)
     const float *ws = reinterpret_cast<const float *>(a.w_scales) +
                       (static_cast<int64_t>(f.e) * ((a.N + 127) / 128) + n0 / 128) * blocks;
     const float *xs = reinterpret_cast<const float *>(a.x_scales) + static_cast<int64_t>(f.first + 2 * t) * blocks;
-    constexpr int U = NT == 4 ? 1 : 2;
-    float acc[NT][4] = {};
+    constexpr int U = 2;  // blocks on the way
+    float acc[4] = {};
     for (int b0 = warp; b0 < blocks; b0 += kWarps * U) {
-        uint4 va[U][2], vb[U][2], vx[U][2][NT];
-        float sw[U], sx[U][NT][2];
+        uint4 va[U][2], vb[U][2], vx[U][2];
+        float sw[U], sx[U][2];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int b = b0 + u * kWarps;
@@ -407,41 +407,30 @@ __global__ void __launch_bounds__(kWarps * 32, 3) k_few_rows8(const FewArgs a)
                 va[u][h] = vb[u][h] = make_uint4(0, 0, 0, 0);
                 if (in && in0) va[u][h] = load_stream(w0 + at);
                 if (in && in1) vb[u][h] = load_stream(w1 + at);
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    vx[u][h][n] = make_uint4(0, 0, 0, 0);
-                    if (in && g + 8 * n < f.rows)
-                        vx[u][h][n] = load_global(reinterpret_cast<const uint4 *>(x + n * 8 * bytes + at));
-                }
+                vx[u][h] = make_uint4(0, 0, 0, 0);
+                if (in && g < f.rows) vx[u][h] = load_global(reinterpret_cast<const uint4 *>(x + at));
             }
             sw[u] = b < blocks ? load_float(ws + b) : 0.f;
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    sx[u][n][i] = b < blocks && 8 * n + 2 * t + i < f.rows
-                                      ? load_float(xs + (8 * n + i) * static_cast<int64_t>(blocks) + b) : 0.f;
+            for (int i = 0; i < 2; ++i)
+                sx[u][i] = b < blocks && 2 * t + i < f.rows ? load_float(xs + i * static_cast<int64_t>(blocks) + b) : 0.f;
         }
 #pragma unroll
-        for (int u = 0; u < U; ++u)
+        for (int u = 0; u < U; ++u) {
+            float c[4] = {};
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                float c[4] = {};
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    mma_e4m3(c, va[u][h].x, vb[u][h].x, va[u][h].y, vb[u][h].y, vx[u][h][n].x, vx[u][h][n].y);
-                    mma_e4m3(c, va[u][h].z, vb[u][h].z, va[u][h].w, vb[u][h].w, vx[u][h][n].z, vx[u][h][n].w);
-                }
-#pragma unroll
-                for (int i = 0; i < 4; ++i) acc[n][i] += c[i] * (sw[u] * sx[u][n][i & 1]);
+            for (int h = 0; h < 2; ++h) {
+                mma_e4m3(c, va[u][h].x, vb[u][h].x, va[u][h].y, vb[u][h].y, vx[u][h].x, vx[u][h].y);
+                mma_e4m3(c, va[u][h].z, vb[u][h].z, va[u][h].w, vb[u][h].w, vx[u][h].z, vx[u][h].w);
             }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[i] += c[i] * (sw[u] * sx[u][i & 1]);
+        }
     }
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) part[warp][8 * n + 2 * t + (i & 1)][g + 8 * (i >> 1)] = acc[n][i];
+    for (int i = 0; i < 4; ++i) part[warp][2 * t + (i & 1)][g + 8 * (i >> 1)] = acc[i];
     __syncthreads();
-    add_parts<NT>(a, f, n0, part);
+    add_parts<1>(a, f, n0, part);
 }
 
 bsl_status launch(void (*kern)(const FewArgs), FewArgs &a, int smem, cudaStream_t s)
@@ -483,12 +472,9 @@ bool few_rows4(int32_t T, const bsl_mx4 *W)
     return (T <= kRows && bytes <= (12ll << 20)) || (T <= 2 * kRows && bytes <= (4ll << 20));
 }
 
-// 8 bits, products alone.
-bool few_rows8(int32_t T, const bsl_fp8 *W)
-{
-    const int64_t bytes = static_cast<int64_t>(T < W->E ? T : W->E) * W->N * W->K;
-    return T <= kRows || (T <= 2 * kRows && bytes <= (32ll << 20)) || (T <= 4 * kRows && bytes <= 20000000);
-}
+// 8 bits, products alone, here / on the tensor-core tiles of few rows (fp8_few.cu): up to 8 rows on 1 MB 8.2 / 12.3,
+// 17 MB 12.3 / 16.4, 45 MB 18.4 / 24.6, 361 MB on eight experts 80 / 84; 16 rows on 17 MB 18.4 / 16.4.
+bool few_rows8(int32_t T) { return T <= kRows; }
 
 bsl_status launch_few_rows(const void *X, int32_t T, const int32_t *offsets, const bsl_grouped *W, const void *bias,
                            void *Y, int32_t zero_rest, cudaStream_t s)
@@ -513,7 +499,7 @@ bsl_status launch_few_rows8(const uint8_t *xc, const float *xs, int32_t T, const
     FewArgs a = {W->codes, reinterpret_cast<const uint8_t *>(W->scales), xc, reinterpret_cast<const uint8_t *>(xs),
                  static_cast<const __nv_bfloat16 *>(bias), static_cast<__nv_bfloat16 *>(Y), offsets, W->status,
                  T, W->E, W->N, W->K, 0, zero_rest};
-    return launch(T <= kRows ? k_few_rows8<1> : T <= 2 * kRows ? k_few_rows8<2> : k_few_rows8<4>, a, 0, s);
+    return launch(k_few_rows8, a, 0, s);
 }
 
 }  // namespace bsl

@@ -589,9 +589,11 @@ bsl_status run(const Maps &maps, const Args &args, cudaStream_t s)
 }  // namespace
 
 bsl_status launch_fp8(const uint8_t *codes, const float *scales, int32_t T, const int32_t *offsets, const bsl_fp8 *W,
-                      bool transposed, const void *bias, void *out, int32_t zero_rest, cudaStream_t s)
+                      bool transposed, const void *bias, void *out, int32_t zero_rest, bool early, cudaStream_t s)
 {
-    if (!transposed && few_rows8(T, W)) return launch_few_rows8(codes, scales, T, offsets, W, bias, out, zero_rest, s);
+    if (!transposed && few_rows8(T)) return launch_few_rows8(codes, scales, T, offsets, W, bias, out, zero_rest, s);
+    if (fp8_few(T, W->E, transposed ? W->K : W->N))
+        return launch_fp8_few(codes, scales, T, offsets, W, transposed, bias, out, zero_rest, early, s);
     Args args = {};
     args.offsets = offsets;
     args.row_scales = scales;

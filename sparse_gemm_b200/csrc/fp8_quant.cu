@@ -107,8 +107,9 @@ __global__ void __launch_bounds__(kThreads) k_fp8_quantize_rows(const Fp8Args a)
     const int64_t first = (row0 * a.K + col) / 8;
     const int64_t stride = static_cast<int64_t>(step) * a.K / 8;
     const bool in = col < a.K;
-    dependents_may_launch();
     wait_for_prior_grid();
+    // behind the wait: the product that follows reads weights and offsets before its own wait
+    dependents_may_launch();
     uint4 x[8];
     uint32_t top[8];
     const uint4 *from = a.X + first;

@@ -155,7 +155,7 @@ bsl_status launch_grouped_bias_grad(const void *dY, int32_t T, const int32_t *of
 // The forwards of the layers for calls of few rows, where these are true.
 bool few_rows(int32_t T, const bsl_grouped *W);
 bool few_rows4(int32_t T, const bsl_mx4 *W);
-bool few_rows8(int32_t T, const bsl_fp8 *W);
+bool few_rows8(int32_t T);
 bsl_status launch_few_rows(const void *X, int32_t T, const int32_t *offsets, const bsl_grouped *W, const void *bias,
                            void *Y, int32_t zero_rest, cudaStream_t s);
 bsl_status launch_few_rows4(const uint8_t *xc, const uint8_t *xs, int32_t T, const int32_t *offsets, const bsl_mx4 *W,
@@ -170,13 +170,17 @@ bsl_status launch_mx4_fwd(const uint8_t *xc, const uint8_t *xs, int32_t T, const
                           const void *bias, void *Y, int32_t zero_rest, cudaStream_t s);
 
 // 8 bits with a scale for each block of 128: conversion, and the products (offsets null: one group of all rows;
-// transposed: the input gradient).
+// transposed: the input gradient; early: launched right behind the conversion of its rows, so that anything else that
+// it reads is older than that kernel).
 bsl_status launch_fp8_quantize(const void *X, int64_t planes, int64_t rows, int32_t K, bool tiles, uint8_t *codes,
                                float *scales, cudaStream_t s);
 bsl_status launch_fp8_dequantize(const uint8_t *codes, const float *scales, int64_t planes, int64_t rows, int32_t K,
                                  bool tiles, void *X, cudaStream_t s);
 bsl_status launch_fp8(const uint8_t *codes, const float *scales, int32_t T, const int32_t *offsets, const bsl_fp8 *W,
-                      bool transposed, const void *bias, void *out, int32_t zero_rest, cudaStream_t s);
+                      bool transposed, const void *bias, void *out, int32_t zero_rest, bool early, cudaStream_t s);
+bool fp8_few(int32_t T, int32_t E, int32_t cols);
+bsl_status launch_fp8_few(const uint8_t *codes, const float *scales, int32_t T, const int32_t *offsets, const bsl_fp8 *W,
+                          bool transposed, const void *bias, void *out, int32_t zero_rest, bool early, cudaStream_t s);
 
 // Router: choices, weights and (where order is not null) the pairs sorted by expert; the logits' gradient.
 size_t route_workspace_bytes(int32_t T, int32_t E);

@@ -26,13 +26,13 @@
 #include "common.cuh"
 #include "internal.h"
 #include "pair.cuh"
+#include "ring.cuh"
 
 namespace bsl {
 namespace {
 
 constexpr int kMaxTokens = BSL_MOE_MAX_TOKENS;
 constexpr int kMaxPairs = kMaxTokens * BSL_ROUTE_MAX_K;
-constexpr int kRows = 8;  // tokens in a group (MMA N)
 static_assert(kMaxTokens <= 64, "a mask of 64 bits");
 
 struct MoeArgs {
@@ -139,39 +139,10 @@ __device__ __forceinline__ void make_plan(const MoeArgs &a, const Plan &p, int m
     __syncthreads();
 }
 
-// ---------------------------------------------------------------- steps: 128 bytes of 16 weight rows
-// 64 bf16 elements, or a block of 128 codes.  A warp brings its steps through a ring of its own in shared memory with
-// copies that need no registers, kRing of them under way whatever is summed meanwhile.  In a step's rows the 16-byte
-// units of odd rows trade halves, so that a lane's reads (units t and 4 + t of rows g and g + 8) meet no bank twice.
-
-constexpr int kWarps = 8;
-constexpr int kRing = 4, kStep = 16 * 128;
-constexpr int kRingBytes = kWarps * kRing * kStep;
+// ---------------------------------------------------------------- steps: 64 bf16 elements, or a block of 128 codes
 
 template <bool F8>
 constexpr int step_of() { return F8 ? 128 : 64; }  // elements
-
-// Four copies a lane: unit lane & 7 of rows lane / 8 + 4 j at `from` + `off[j]`; zeros where there is none.
-__device__ __forceinline__ void copy_step(uint8_t *slot, const uint8_t *from, const int64_t (&off)[4], const bool (&exists)[4],
-                                          const uint8_t *any)
-{
-    const int lane = threadIdx.x & 31, r = lane >> 3, u = lane & 7;
-    const uint32_t dst = smem_u32(slot) + r * 128 + ((u ^ (r & 1) << 2) << 4);
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + j * 512), "l"(exists[j] ? from + off[j] : any),
-                     "r"(exists[j] ? 16 : 0)
-                     : "memory");
-}
-
-__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-
-// The oldest step of kRing is there.
-__device__ __forceinline__ void copies_wait()
-{
-    asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 1) : "memory");
-    __syncwarp();
-}
 
 // What the lane's bytes of a step meet of a token's vector.
 template <bool F8>
@@ -216,12 +187,11 @@ template <bool F8, int NT>
 __device__ __forceinline__ void add_step(float (&acc)[NT][4], const uint8_t *slot, const Vec<F8> (&x)[NT], int live, float s_lo,
                                          float s_hi, uint32_t (&nan)[2])
 {
-    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     float c[NT][4] = {};
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        const uint8_t *at = slot + g * 128 + (((4 * h + t) ^ (g & 1) << 2) << 4);
-        const uint4 wl = *reinterpret_cast<const uint4 *>(at), wh = *reinterpret_cast<const uint4 *>(at + 1024);
+        uint4 wl, wh;
+        read_step(slot, h, wl, wh);
         if constexpr (F8) {
             const uint32_t lo[4] = {wl.x, wl.y, wl.z, wl.w}, hi[4] = {wh.x, wh.y, wh.z, wh.w};
 #pragma unroll
@@ -277,7 +247,7 @@ constexpr int ctas_of(int NT) { return NT == 1 ? 3 : 2; }
 // ---------------------------------------------------------------- gate and up
 
 template <bool F8, int NT>
-__global__ void __launch_bounds__(kWarps * 32, ctas_of(NT)) k_moe_up(const MoeArgs a)
+__global__ void __launch_bounds__(kWarps * 32, ctas_of(NT)) k_moe_up(const MoeArgs a, const int team)
 {
     constexpr int SPAN = step_of<F8>();
     extern __shared__ __align__(16) uint8_t smem[];
@@ -285,6 +255,7 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_of(NT)) k_moe_up(const MoeAr
     const Plan plan(smem + kRingBytes, a.E, a.T * a.k);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     uint8_t *ring = smem + warp * kRing * kStep;
+    const int mine = warp / team, member = warp % team, teams = kWarps / team, stride = gridDim.x * teams;
     wait_for_prior_grid();
     // behind the wait: what came before this kernel has ended when the next one starts, which reads choices and
     // weights before its own wait
@@ -296,7 +267,7 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_of(NT)) k_moe_up(const MoeAr
     const int64_t off[4] = {0, 4 * bytes, up_rows, up_rows + 4 * bytes};
 
     // the copies' place: unit of work, step, and the lane's first byte there
-    int fu = warp < steps ? static_cast<int>(blockIdx.x) : units, fc = warp, slot = 0;
+    int fu = member < steps ? blockIdx.x * teams + mine : units, fc = member, slot = 0;
     const uint8_t *from = nullptr;
     auto open = [&] {
         if (fu < units)
@@ -308,9 +279,9 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_of(NT)) k_moe_up(const MoeAr
             const int64_t first = static_cast<int64_t>(fc) * 128;
             const bool in = first + 16 * (lane & 7) < bytes, exists[4] = {in, in, in, in};
             copy_step(ring + at * kStep, from + first, off, exists, a.W13);
-            if ((fc += kWarps) >= steps) {
-                fc = warp;
-                fu += gridDim.x;
+            if ((fc += team) >= steps) {
+                fc = member;
+                fu += stride;
                 open();
             }
         }
@@ -319,7 +290,7 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_of(NT)) k_moe_up(const MoeAr
     open();
 #pragma unroll
     for (int i = 0; i < kRing; ++i) issue(i);
-    for (int u = blockIdx.x; u < units; u += gridDim.x) {
+    for (int u = blockIdx.x * teams + mine; u < units; u += stride) {
         const Group group = plan.groups[u / tiles];
         const int live = (group.rows + kRows - 1) / kRows, i0 = u % tiles * 8;
         const float *plane = F8 ? a.s13 + static_cast<int64_t>((2 * a.I + 127) / 128) * kb * group.expert : nullptr;
@@ -332,7 +303,7 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_of(NT)) k_moe_up(const MoeAr
         }
         float acc[NT][4] = {};
         uint32_t nan[2] = {};
-        for (int c = warp; c < steps; c += kWarps) {
+        for (int c = member; c < steps; c += team) {
             Vec<F8> v[NT];
 #pragma unroll
             for (int n = 0; n < NT; ++n)
@@ -350,19 +321,18 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_of(NT)) k_moe_up(const MoeAr
             if (n < live)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) part[warp][8 * n + 2 * t + (i & 1)][g + 8 * (i >> 1)] = acc[n][i];
-        __syncthreads();
-        for (int i = threadIdx.x; i < group.rows * 8; i += kWarps * 32) {
+        named_bar_sync(1 + mine, 32 * team);
+        for (int i = threadIdx.x - 32 * team * mine; i < group.rows * 8; i += 32 * team) {
             const int r = i / 8, f = i % 8;
             float gate = 0.f, up = 0.f;
-#pragma unroll
-            for (int j = 0; j < kWarps; ++j) gate += part[j][r][f], up += part[j][r][f + 8];
+            for (int j = mine * team; j < (mine + 1) * team; ++j) gate += part[j][r][f], up += part[j][r][f + 8];  // in order
             // (__expf is off by some 2^-20, the rounding of h by up to 2^-8)
             const float h = gate / (1.f + __expf(-gate)) * up * plan.share[group.slot + r];
             a.h[static_cast<int64_t>(group.slot + r) * a.I + i0 + f] = __float2bfloat16(h);
         }
-        __syncthreads();
+        named_bar_sync(1 + mine, 32 * team);
     }
-    asm volatile("cp.async.wait_all;" ::: "memory");
+    copies_end();
 }
 
 // ---------------------------------------------------------------- down
@@ -455,7 +425,7 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_of(NT)) k_moe_down(const Moe
         }
         if (last) c = 0, ++at;
     }
-    asm volatile("cp.async.wait_all;" ::: "memory");
+    copies_end();
     __syncthreads();
     // the warps' sums in order, then the CTAs' in order
     for (int i = threadIdx.x; i < a.T * 16; i += kWarps * 32) {
@@ -492,7 +462,9 @@ bsl_status run(const MoeArgs &a, cudaStream_t s)
     if (st != BSL_OK) return st;
     const int64_t units = static_cast<int64_t>(a.I / 8) * (pairs < a.E ? pairs : a.E);
     const int64_t room = static_cast<int64_t>(num_sms()) * ctas_of(NT);
-    st = cuda_status(launch_dependent(k_moe_up<F8, NT>, static_cast<unsigned>(units < room ? units : room), kWarps * 32, up, s, a));
+    const int team = team_of((a.H + step_of<F8>() - 1) / step_of<F8>());
+    const int64_t ctas = (units * team + kWarps - 1) / kWarps;
+    st = cuda_status(launch_dependent(k_moe_up<F8, NT>, static_cast<unsigned>(ctas < room ? ctas : room), kWarps * 32, up, s, a, team));
     if (st != BSL_OK) return st;
     // as many CTAs a tile as there is room for on the SMs
     const int tiles = (a.H + 15) / 16;
