@@ -1455,7 +1455,7 @@ def route(logits: torch.Tensor, k: int, score: str = "softmax", renormalize: boo
         out = torch.zeros_like(X).index_add_(0, r.order // k, Y * r.weights.flatten()[r.order, None].to(Y.dtype))
 
     Logits of -inf weigh 0, in a row of nothing else too.  The weights' gradient flows to the logits."""
-    if logits.requires_grad and torch.is_grad_enabled():
+    if getattr(logits, "requires_grad", False) and torch.is_grad_enabled():
         return Routing(*RouteFunction.apply(logits, k, score, bool(renormalize), float(factor), sort))
     return _route(logits, k, score, bool(renormalize), float(factor), sort)
 
