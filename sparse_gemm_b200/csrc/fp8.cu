@@ -36,11 +36,13 @@
 // TMEM: MMAs 690 clocks (the four of a stage, beside copies and TMEM reads), 190
 // until the sums see them, 600 until they have read it out (their FMAs take 280 of
 // it), 180 until the next MMAs; half of that a stage.  Measured at 8192 x 4096 x 14336:
-// 500 us (1920 TFLOP/s); MMAs and copies alone 305.  Eight warps with twice the
-// columns take 525 (and 1050 as soon as the compiler spills one of their 128 sums),
-// sums that wait on the mbarrier each by themselves 560, plain stores of the output,
-// which all SMs issue at the same time, 555 instead of copies from shared memory,
-// MMAs of 128 columns with twice the accumulators 400 without any sums.
+// 500 us (1920 TFLOP/s), 598 with the rows' conversion (17) in long runs, which power holds back; MMAs and copies
+// alone 305.  Steps and what they took: output by plain stores, which all SMs issue at
+// the same time, 562, by copies from shared memory 545; without a split of the
+// registers by setmaxnreg 502.  Eight sum warps with twice the columns took 530, and
+// 800 to 1050 where the compiler spilled some of their 128 sums; MMAs of 128 columns
+// with twice the accumulators 402 without any sums.  One waiting warp instead of
+// sixteen is worth 380 against 428 with the sums left out, nothing with them (562, 561).
 //
 // Every wait is bounded (BSL_ERR_TIMEOUT in the status word, then all roles
 // leave through an abort flag, and the CTAs end when no copy can be under way).

@@ -1,5 +1,5 @@
-// ring.cuh -- weight rows streamed to few tokens: what the kernels that feed
-// mma.sync from rings of asynchronous copies share (fp8_few.cu, moe.cu).
+// ring.cuh -- weight rows streamed to few tokens: rings of asynchronous copies that
+// feed mma.sync (moe.cu's two kernels).
 //
 // A step is 128 bytes of 16 weight rows.  A warp brings its steps through a ring of
 // its own in shared memory, by copies that need no registers, kRing of them under way

@@ -179,7 +179,7 @@ struct RouteSmem {
 };
 
 // Threads of k_route: a CTA that counts or sorts has up to 128 tokens, and latency bounds a token, so that many warps
-// share them (16384 tokens, 128 experts: 8 warps 35 us, 32 warps 11).
+// share them (16384 tokens, 128 experts: 8 warps 35 us, 32 warps 17).
 constexpr int route_threads(int NE, int sort) { return sort == 0 ? 256 : NE >= 16 ? 512 : 1024; }
 
 // Choices of a run of tokens; kSort 1: with their counts for k_sort, 2: and sorted here (one CTA).
