@@ -498,7 +498,7 @@ BSL_API bsl_status bsl_route_backward(const float *dweights, const void *logits,
  * Y [T][H]: Y[t] = sum_j weights[t][j] * W2[e] . h with e = experts[t][j] and
  *     h = silu(G[e] . X[t]) * (U[e] . X[t]),  W13[e] = (G[e]; U[e]) [2 I][H],  W2[e] [H][I],
  * silu(g) = g / (1 + exp(-g)), in two kernels; bf16 X [T][H], Y and h (times the weight, rounded once), fp32
- * sums.  T <= BSL_MOE_MAX_TOKENS (more are routed, sorted and multiplied by the grouped products), k <=
+ * sums.  T <= BSL_MOE_MAX_TOKENS (more are routed, sorted and multiplied by the grouped products), T k I / 8 < 2^30, k <=
  * BSL_ROUTE_MAX_K.  A choice outside 0 .. E - 1 counts for nothing and is reported as BSL_ERR_INVALID_ARG in
  * W13's device status; an expert that a token chose more than once counts once, with the sum of its weights.
  * workspace: bsl_moe_workspace_bytes(T, k, I) bytes of device scratch, 16-byte aligned, written before it is

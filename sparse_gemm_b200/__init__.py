@@ -1507,7 +1507,7 @@ def moe_forward(X: torch.Tensor, W13, W2, experts: torch.Tensor, weights: torch.
     if not isinstance(W13, (Fp8Tensor, GroupedWeight)) or not isinstance(W2, Fp8Tensor if fp8 else GroupedWeight):
         raise TypeError("W13 and W2 must be two GroupedWeight or two Fp8Tensor")
     r13, r2 = W13.cref(), W2.cref()
-    (E, N13, H), (E2, H2, I) = (W13.shape, W2.shape) if fp8 and len(W13.shape) == len(W2.shape) == 3 else         ((w._c.E, w._c.N, w._c.K) for w in (W13, W2))
+    (E, N13, H), (E2, H2, I) = ((w._c.E, w._c.N, w._c.K) for w in (W13, W2))
     if E != E2 or H != H2 or N13 != 2 * I:
         raise ValueError(f"W13 [{E}, {N13}, {H}] and W2 [{E2}, {H2}, {I}] must be [E, 2 I, H] and [E, H, I]")
     held13, held2 = (W13.codes, W2.codes) if fp8 else (W13.weight, W2.weight)

@@ -831,6 +831,7 @@ bsl_status check_moe(const void *X, int32_t T, const int32_t *experts, const flo
 {
     if (T < 0 || k <= 0 || E13 != E2 || K13 != N2 || K2 > INT32_MAX / 2 || N13 != 2 * K2) return BSL_ERR_INVALID_ARG;
     if (T > BSL_MOE_MAX_TOKENS || k > BSL_ROUTE_MAX_K) return BSL_ERR_UNSUPPORTED;
+    if (static_cast<int64_t>(T) * k * (K2 / 8) > INT32_MAX / 2) return BSL_ERR_UNSUPPORTED;  // units of work, counted in 32 bits
     if (T == 0) return BSL_OK;
     if (check_matrix(X, T) != BSL_OK || check_matrix(Y, T) != BSL_OK || check_matrix(workspace, T) != BSL_OK || !experts ||
         !aligned(experts, 4) || !weights || !aligned(weights, 4) || workspace_bytes < bsl_moe_workspace_bytes(T, k, K2))

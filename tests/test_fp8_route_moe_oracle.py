@@ -214,6 +214,15 @@ def test_bad_moe_arguments_are_refused(lib):
     assert lib.bsl_moe_workspace_bytes(0, 2, 64) == 0
 
 
+def test_moe_refuses_more_units_than_it_counts(lib):
+    """Tokens x choices x I / 8 units of work are counted in 32 bits."""
+    wide = 2 ** 23 + 16   # 64 x 32 x 2^20 = 2^31 units and more
+    for name, make in (("bsl_moe_forward", _grouped), ("bsl_moe_forward_fp8", _fp8)):
+        shape = {} if make is _grouped else {"E": 4}
+        w13, w2 = make(N=2 * wide, K=16, **shape), make(N=16, K=wide, **shape)
+        assert getattr(lib, name)(P, 64, P, P, 32, ctypes.byref(w13), ctypes.byref(w2), P, P, 1 << 50, None) == 2
+
+
 def test_the_binding_matches_the_header():
     import sparse_gemm_b200 as sg
     text = open(os.path.join(ROOT, "include", "bsl.h")).read()
