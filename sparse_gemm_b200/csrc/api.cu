@@ -778,7 +778,7 @@ bool logits_ok(const void *p, int32_t type) { return p && (type == 0 || type == 
 
 size_t bsl_route_workspace_bytes(int32_t T, int32_t E, int32_t k)
 {
-    return check_route(T, E, k) != BSL_OK ? 0 : route_workspace_bytes(T, E);
+    return check_route(T, E, k) != BSL_OK ? 0 : route_workspace_bytes(T, E, k);
 }
 
 bsl_status bsl_route(const void *logits, int32_t logits_type, int32_t T, int32_t E, int32_t k, int32_t score,
@@ -797,8 +797,8 @@ bsl_status bsl_route(const void *logits, int32_t logits_type, int32_t T, int32_t
     }
     if (!logits_ok(logits, logits_type) || !experts || !aligned(experts, 4) || !weights || !aligned(weights, 4))
         return BSL_ERR_INVALID_ARG;
-    if (order && route_workspace_bytes(T, E) > 0 &&
-        (!workspace || !aligned(workspace, 4) || workspace_bytes < route_workspace_bytes(T, E)))
+    if (order && route_workspace_bytes(T, E, k) > 0 &&
+        (!workspace || !aligned(workspace, 4) || workspace_bytes < route_workspace_bytes(T, E, k)))
         return BSL_ERR_INVALID_ARG;
     DeviceGuard guard;
     BSL_TRY(guard.bind(logits));

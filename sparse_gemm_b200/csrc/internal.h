@@ -183,7 +183,7 @@ bsl_status launch_fp8_few(const uint8_t *codes, const float *scales, int32_t T, 
                           bool transposed, const void *bias, void *out, int32_t zero_rest, bool early, cudaStream_t s);
 
 // Router: choices, weights and (where order is not null) the pairs sorted by expert; the logits' gradient.
-size_t route_workspace_bytes(int32_t T, int32_t E);
+size_t route_workspace_bytes(int32_t T, int32_t E, int32_t k);
 bsl_status launch_route(const void *logits, bool half, int32_t T, int32_t E, int32_t k, bool sigmoid, bool renormalize,
                         float factor, int32_t *experts, float *weights, int32_t *offsets, int32_t *order, void *workspace,
                         cudaStream_t s);

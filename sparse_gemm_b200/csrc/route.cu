@@ -348,18 +348,24 @@ __global__ void __launch_bounds__(256) k_route_backward(const RouteArgs a)
     }
 }
 
-// Tokens of a CTA: all of a few, else as many as make 128 CTAs (and fit in its memory).
-int run_of(int32_t T)
+// Tokens of a CTA: all of a few, else as many as make 128 CTAs, 128 at most; of very many as many as make 1024 CTAs,
+// since each CTA of k_sort reads all the others' counts, and as its memory holds (128 experts, 8 choices, 2^18 tokens: 574 us
+// with 2048 runs, 328 with 1024; 2^20 tokens 5751 with 8192, 933 with 1024; 2^17 tokens 207).
+constexpr int kMostRuns = 1024, kMostPairs = 8192;
+int run_of(int32_t T, int32_t k)
 {
     if (T <= kSmallTokens) return T;
     const int run = (T + 127) / 128;
-    return run < 8 ? 8 : run > kSmallTokens ? kSmallTokens : run;
+    if (run <= kSmallTokens) return run < 8 ? 8 : run;
+    const int many = static_cast<int>((static_cast<int64_t>(T) + kMostRuns - 1) / kMostRuns), most = kMostPairs / k;
+    return many < kSmallTokens ? kSmallTokens : many < most ? many : most;
 }
+static_assert(kMostPairs / BSL_ROUTE_MAX_K >= kSmallTokens && kMostPairs <= 65535, "runs that grow, ranks of 16 bits");
 
 template <int NE>
 bsl_status route_of(RouteArgs &a, int sort, cudaStream_t s)
 {
-    const unsigned runs = (a.T + a.run - 1) / a.run;
+    const unsigned runs = static_cast<unsigned>((static_cast<int64_t>(a.T) + a.run - 1) / a.run);
     const size_t smem = sort ? RouteSmem::bytes(a.E, a.run * a.k) : 0;
     const unsigned threads = a.T > 8 ? route_threads(NE, sort) : 256;
     auto kern = sort == 0 ? k_route<NE, 0> : sort == 1 ? k_route<NE, 1> : k_route<NE, 2>;
@@ -383,11 +389,11 @@ bsl_status by_width(int E, F f)
 
 }  // namespace
 
-size_t route_workspace_bytes(int32_t T, int32_t E)
+size_t route_workspace_bytes(int32_t T, int32_t E, int32_t k)
 {
     if (T <= kSmallTokens) return 0;
-    const int run = run_of(T);
-    return static_cast<size_t>((T + run - 1) / run) * E * 4;
+    const int run = run_of(T, k);
+    return (static_cast<size_t>(T) + run - 1) / run * E * 4;
 }
 
 bsl_status launch_route(const void *logits, bool half, int32_t T, int32_t E, int32_t k, bool sigmoid, bool renormalize,
@@ -404,7 +410,7 @@ bsl_status launch_route(const void *logits, bool half, int32_t T, int32_t E, int
     a.T = T;
     a.E = E;
     a.k = k;
-    a.run = order ? run_of(T) : 8;
+    a.run = order ? run_of(T, k) : 8;
     a.half = half;
     a.sigmoid = sigmoid;
     a.renormalize = renormalize;
@@ -417,7 +423,7 @@ bsl_status launch_route(const void *logits, bool half, int32_t T, int32_t E, int
         const bsl_status sa = set_smem_once(reinterpret_cast<const void *>(&k_sort), 100 * 1024);
         if (sa != BSL_OK) return sa;
     }
-    return cuda_status(launch_dependent(k_sort, (T + a.run - 1) / a.run, 512, smem, s, a));
+    return cuda_status(launch_dependent(k_sort, static_cast<unsigned>((static_cast<int64_t>(T) + a.run - 1) / a.run), 512, smem, s, a));
 }
 
 bsl_status launch_route_backward(const float *dweights, const void *logits, bool half, int32_t T, int32_t E, int32_t k,
@@ -437,7 +443,7 @@ bsl_status launch_route_backward(const float *dweights, const void *logits, bool
     a.renormalize = renormalize;
     a.factor = factor;
     return by_width(E, [&](auto n) {
-        return cuda_status(launch_dependent(k_route_backward<decltype(n)::value>, (T + 7) / 8, 256, 0, s, a));
+        return cuda_status(launch_dependent(k_route_backward<decltype(n)::value>, static_cast<unsigned>((static_cast<int64_t>(T) + 7) / 8), 256, 0, s, a));
     });
 }
 

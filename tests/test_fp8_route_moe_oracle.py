@@ -223,6 +223,14 @@ def test_moe_refuses_more_units_than_it_counts(lib):
         assert getattr(lib, name)(P, 64, P, P, 32, ctypes.byref(w13), ctypes.byref(w2), P, P, 1 << 50, None) == 2
 
 
+@pytest.mark.parametrize("T,E,k", [(129, 8, 2), (16384, 128, 8), (131072, 128, 8), (131073, 128, 32), (1 << 20, 128, 8), (1 << 23, 16, 1)])
+def test_the_sorts_counts_grow_with_the_tokens(lib, T, E, k):
+    """Every CTA of the sort reads the counts of all runs: their number stays small, whatever the tokens, as long as a
+    run's pairs (8192 at most) fit in shared memory."""
+    runs = lib.bsl_route_workspace_bytes(T, E, k) // (4 * E)
+    assert 0 < runs <= max(1024, -(-T // (8192 // k)))
+
+
 def test_the_binding_matches_the_header():
     import sparse_gemm_b200 as sg
     text = open(os.path.join(ROOT, "include", "bsl.h")).read()

@@ -78,6 +78,14 @@ def test_route_of_a_long_prompt():
     assert_routed(sg.route(l, 4), f, 4)
 
 
+@pytest.mark.parametrize("T,E,k", [(131073, 8, 2), (300001, 12, 3), (140000, 40, 32)])
+def test_route_of_very_many_tokens(T, E, k):
+    """Runs longer than 128 tokens, up to what a CTA's memory holds."""
+    rng = np.random.default_rng(T)
+    l, f = logits_of(rng, T, E)
+    assert_routed(sg.route(l, k), f, k)
+
+
 def test_route_ties_and_what_is_not_finite():
     inf, nan = float("inf"), float("nan")
     rows = [[1, 1, 1, 1, 1, 1], [0.0, -0.0, 0.0, -0.0, -1, 1], [-inf] * 6, [-inf, 2, -inf, -inf, -inf, -inf], [nan, 1, 2, 3, nan, 0],
