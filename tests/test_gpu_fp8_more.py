@@ -230,3 +230,69 @@ def test_calls_on_two_streams_at_once():
         torch.cuda.synchronize()
         for a, b in zip(got, want):
             assert all(torch.equal(x, y) for x, y in zip(a, b)), rep
+
+
+@pytest.mark.parametrize("T", [100, 5000])
+def test_routers_of_two_graphs_and_their_gradients(T):
+    """One CTA, and two kernels with counts between them; the same pool, replayed in turn with other logits."""
+    rng = np.random.default_rng(T)
+    make = lambda: torch.from_numpy(rng.standard_normal((T, 72)).astype(np.float32)).cuda()
+    graphs = []
+    for k in (3, 8):
+        l, d = make(), torch.ones(T, k, device="cuda")
+        sg.route_backward(d, l, sg.route(l, k).experts)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, pool=graphs[0][0].pool() if graphs else None):
+            r = sg.route(l, k, renormalize=False)
+            dl = sg.route_backward(r.weights, l, r.experts, renormalize=False)
+        graphs.append((g, k, l, r, dl))
+    for _ in range(3):
+        for g, k, l, r, dl in graphs:
+            l.copy_(make())
+            g.replay()
+            want = sg.route(l, k, renormalize=False)
+            assert all(torch.equal(a, b) for a, b in zip(r, want))
+            assert torch.equal(dl, sg.route_backward(want.weights, l, want.experts, renormalize=False))
+
+
+def test_broadcast_and_unused_gradients_of_the_router():
+    """The gradient of a sum is a broadcast scalar; weights that nothing uses have a gradient of zeros."""
+    l = torch.randn(50, 24, device="cuda").requires_grad_(True)
+    r = sg.route(l, 4, score="sigmoid", renormalize=False)
+    r.weights.sum().backward()
+    assert torch.equal(l.grad, sg.route_backward(torch.ones(50, 4, device="cuda"), l.detach(), r.experts, "sigmoid", False))
+    chosen = torch.zeros(50, 24, dtype=torch.bool, device="cuda").scatter_(1, r.experts.long(), True)
+    assert not l.grad[~chosen].any() and (l.grad[chosen] > 0).all()
+    l.grad = None
+    (sg.route(l, 4).weights * 0 + l[:, :4]).sum().backward()
+    assert torch.equal(l.grad, torch.ones_like(l) * (torch.arange(24, device="cuda") < 4))
+
+
+def test_state_dict_assigned_and_moved_buffers():
+    """Buffers whose storage is replaced: the handle is made anew, with its status word."""
+    rng = np.random.default_rng(21)
+    W, _ = normal(rng, (144, 272))
+    x, _ = normal(rng, (9, 272))
+    a = sg.Fp8Linear.from_dense(W)
+    b = sg.Fp8Linear.from_dense(torch.zeros_like(W))
+    before = b.weight8
+    b.load_state_dict({n: t.clone() for n, t in a.state_dict().items()}, assign=True)
+    assert torch.equal(a(x), b(x)) and b.weight8 is not before and sg.fp8_status(b.weight8) == 0
+    assert torch.equal(b.to("cpu").to("cuda")(x), a(x))
+
+
+def test_results_repeat_to_the_bit():
+    """Every output is a sum in a fixed order, whatever else the GPU does: clusters, teams and shared sums included."""
+    rng = np.random.default_rng(22)
+    Wq, _ = weights(rng, 6, 272, 528)
+    off, _ = offsets_of([3, 0, 65, 1, 130, 20], 0)
+    X, _ = normal(rng, (219, 528))
+    W13, W2 = sg.quantize_fp8(normal(rng, (6, 288, 528), 0.05)[0], 128), sg.quantize_fp8(normal(rng, (6, 528, 144), 0.08)[0], 128)
+    r = sg.route(torch.randn(40, 6, device="cuda"), 3)
+    calls = (lambda: sg.grouped_forward_fp8(X, Wq, off), lambda: sg.forward_fp8(X[:5].contiguous(), sg.Fp8Tensor(Wq.codes[0], Wq.scales[0])),
+             lambda: sg.moe_forward(X[:40].contiguous(), W13, W2, r.experts, r.weights))
+    first = [c() for c in calls]
+    for _ in range(20):
+        for c, y in zip(calls, first):
+            assert torch.equal(c(), y)
