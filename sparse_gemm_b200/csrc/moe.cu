@@ -248,7 +248,11 @@ __device__ __forceinline__ void spread_nan(float (&acc)[NT][4], const uint32_t (
 // CTAs of an SM that the kernels are compiled for.
 constexpr int ctas_of(int NT) { return NT == 1 ? 3 : 2; }
 
+constexpr size_t ring_bytes(int ring) { return static_cast<size_t>(kWarps) * ring * kStep; }
+
 // ---------------------------------------------------------------- gate and up
+
+constexpr int kUpRing = 4;
 
 template <bool F8, int NT>
 __global__ void __launch_bounds__(kWarps * 32, ctas_of(NT)) k_moe_up(const MoeArgs a, const int team)
@@ -256,9 +260,9 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_of(NT)) k_moe_up(const MoeAr
     constexpr int SPAN = step_of<F8>();
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ float part[kWarps][NT * kRows][17];
-    const Plan plan(smem + kRingBytes, a.E, a.T * a.k);
+    const Plan plan(smem + ring_bytes(kUpRing), a.E, a.T * a.k);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    uint8_t *ring = smem + warp * kRing * kStep;
+    uint8_t *ring = smem + warp * kUpRing * kStep;
     const int mine = warp / team, member = warp % team, teams = kWarps / team, stride = gridDim.x * teams;
     wait_for_prior_grid();
     // behind the wait: what came before this kernel has ended when the next one starts, which reads choices and
@@ -293,7 +297,7 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_of(NT)) k_moe_up(const MoeAr
     };
     open();
 #pragma unroll
-    for (int i = 0; i < kRing; ++i) issue(i);
+    for (int i = 0; i < kUpRing; ++i) issue(i);
     for (int u = blockIdx.x * teams + mine; u < units; u += stride) {
         const Group group = plan.groups[u / tiles];
         const int live = (group.rows + kRows - 1) / kRows, i0 = u % tiles * 8;
@@ -313,11 +317,11 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_of(NT)) k_moe_up(const MoeAr
             for (int n = 0; n < NT; ++n)
                 if (n < live) load_vec<F8>(v[n], x[n], c * SPAN, t, a.H, 8 * n + g < group.rows);
             const float sg = F8 ? load_float(s_gate + c) : 1.f, su = F8 ? load_float(s_up + c) : 1.f;
-            copies_wait();
+            copies_wait<kUpRing>();
             add_step<F8, NT>(acc, ring + slot * kStep, v, live, sg, su, nan);
             __syncwarp();
             issue(slot);
-            slot = (slot + 1) % kRing;
+            slot = (slot + 1) % kUpRing;
         }
         if (F8) spread_nan<NT>(acc, nan);
 #pragma unroll
@@ -342,20 +346,26 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_of(NT)) k_moe_up(const MoeAr
 // ---------------------------------------------------------------- down
 
 constexpr int kStride = 17;   // of a token's 16 sums
-constexpr int kDownCtas = 2;  // of an SM
 
 size_t sums_bytes(int T) { return static_cast<size_t>(kWarps) * T * kStride * 4; }
 
+// CTAs of an SM, and steps under way in each warp: more CTAs with shorter rings where the registers are few (one token,
+// two experts of 4096 x 14336 in bf16, the whole call: 136 us with four CTAs and three steps, 144 with three CTAs and four
+// steps, 147 with two and four).  The 8-bit kernel spills with more than two (32 tokens: 171 us, 200 with three CTAs).
+constexpr bool light(bool f8, int NT) { return !f8 && NT == 1; }
+constexpr int down_ctas(bool f8, int NT) { return light(f8, NT) ? 4 : 2; }
+constexpr int down_ring(bool f8, int NT) { return light(f8, NT) ? 3 : 4; }
+
 // CTAs of a cluster share the list of a tile of 16 features, so that few tiles keep the SMs busy too.
 template <bool F8, int NT>
-__global__ void __launch_bounds__(kWarps * 32, kDownCtas) k_moe_down(const MoeArgs a, const int parts)
+__global__ void __launch_bounds__(kWarps * 32, down_ctas(F8, NT)) k_moe_down(const MoeArgs a, const int parts)
 {
-    constexpr int SPAN = step_of<F8>();
+    constexpr int SPAN = step_of<F8>(), RING = down_ring(F8, NT);
     extern __shared__ __align__(16) uint8_t smem[];
-    const Plan plan(smem + kRingBytes, a.E, a.T * a.k);
-    float *sums = reinterpret_cast<float *>(smem + kRingBytes + Plan::bytes(a.E, a.T * a.k));
+    const Plan plan(smem + ring_bytes(RING), a.E, a.T * a.k);
+    float *sums = reinterpret_cast<float *>(smem + ring_bytes(RING) + Plan::bytes(a.E, a.T * a.k));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    uint8_t *ring = smem + warp * kRing * kStep;
+    uint8_t *ring = smem + warp * RING * kStep;
     const int n0 = blockIdx.x / parts * 16, rank = blockIdx.x % parts;
     dependents_may_launch();
     for (int i = threadIdx.x; i < kWarps * a.T * kStride; i += kWarps * 32) sums[i] = 0.f;
@@ -404,7 +414,7 @@ __global__ void __launch_bounds__(kWarps * 32, kDownCtas) k_moe_down(const MoeAr
     };
     open();
 #pragma unroll
-    for (int i = 0; i < kRing; ++i) issue(i);
+    for (int i = 0; i < RING; ++i) issue(i);
     wait_for_prior_grid();  // h is there
     // h comes from L2 (every CTA reads all of it), so the loads are P steps ahead where registers allow it
     constexpr int P = F8 && NT > 1 || NT > 2 ? 1 : 2;
@@ -435,12 +445,12 @@ __global__ void __launch_bounds__(kWarps * 32, kDownCtas) k_moe_down(const MoeAr
         for (int i = 0; i < P; ++i) {
             if (left <= 0) break;
             const Group group = plan.groups[at];
-            copies_wait();
+            copies_wait<RING>();
             add_step<F8, NT>(acc, ring + slot * kStep, v[i], (group.rows + kRows - 1) / kRows, s[i], s[i], nan);
             __syncwarp();
             issue(slot);
             load(i);
-            slot = (slot + 1) % kRing;
+            slot = (slot + 1) % RING;
             const bool last = (c += inc) >= steps;
             if (last || left == 1) {  // the group's sum, as far as this warp has it, to its tokens
                 if (F8) spread_nan<NT>(acc, nan);
@@ -490,7 +500,8 @@ bsl_status run(const MoeArgs &a, cudaStream_t s)
 {
     constexpr int kMost = 150 * 1024;
     const int pairs = a.T * a.k;
-    const size_t up = kRingBytes + Plan::bytes(a.E, pairs), down = up + sums_bytes(a.T);
+    const size_t plan = Plan::bytes(a.E, pairs), up = ring_bytes(kUpRing) + plan;
+    const size_t down = ring_bytes(down_ring(F8, NT)) + plan + sums_bytes(a.T);
     bsl_status st = set_smem_once(reinterpret_cast<const void *>(&k_moe_up<F8, NT>), kMost);
     if (st == BSL_OK) st = set_smem_once(reinterpret_cast<const void *>(&k_moe_down<F8, NT>), kMost);
     if (st != BSL_OK) return st;
@@ -503,7 +514,8 @@ bsl_status run(const MoeArgs &a, cudaStream_t s)
     // as many CTAs a tile as there is room for
     const int tiles = (a.H + 15) / 16;
     int parts = 1;
-    while (parts < 8 && 2 * parts * tiles <= kDownCtas * num_sms()) parts *= 2;
+    const int fit = static_cast<int>(227 * 1024 / (down + 1024)), ctas_an_sm = fit < down_ctas(F8, NT) ? fit : down_ctas(F8, NT);
+    while (parts < 8 && 2 * parts * tiles <= ctas_an_sm * num_sms()) parts *= 2;
     return cuda_status(launch_dependent_cluster(k_moe_down<F8, NT>, tiles * parts, parts, kWarps * 32, down, s, a, parts));
 }
 

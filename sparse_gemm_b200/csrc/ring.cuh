@@ -2,7 +2,7 @@
 // feed mma.sync (moe.cu's two kernels).
 //
 // A step is 128 bytes of 16 weight rows.  A warp brings its steps through a ring of
-// its own in shared memory, by copies that need no registers, kRing of them under way
+// its own in shared memory, by copies that need no registers, Ring of them under way
 // whatever is summed meanwhile, over the borders of units of work too.  In a step's
 // rows the 16-byte units of odd rows trade halves, so that a lane's reads (units t and
 // 4 + t of rows g and g + 8, the MMA's A operand; k in the order in which the bytes
@@ -18,8 +18,7 @@
 namespace bsl {
 
 constexpr int kWarps = 8;
-constexpr int kRing = 4, kStep = 16 * 128;
-constexpr int kRingBytes = kWarps * kRing * kStep;
+constexpr int kStep = 16 * 128;
 constexpr int kRows = 8;  // tokens in a group (MMA N)
 
 // Four copies a lane: unit lane & 7 of rows lane / 8 + 4 j at `from` + off[j]; zeros where there is none.
@@ -37,10 +36,11 @@ __device__ __forceinline__ void copy_step(uint8_t *slot, const uint8_t *from, co
 
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 
-// The oldest step of kRing is there, for the whole warp.
+// The oldest step of Ring is there, for the whole warp.
+template <int Ring>
 __device__ __forceinline__ void copies_wait()
 {
-    asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 1) : "memory");
+    asm volatile("cp.async.wait_group %0;" ::"n"(Ring - 1) : "memory");
     __syncwarp();
 }
 
