@@ -10,9 +10,9 @@
 // (ring.cuh), and they are mma.sync's M side (16 weight rows), the tokens of the
 // expert its N side, k in the order in which the bytes lie; 8-bit weights become bf16
 // by bit moves, exactly.  Measured: one token, two experts of 4096 x 14336 in bf16, up 75 us
-// (6.3 TB/s), down 54; 32 tokens, 64 experts of 2048 x 1408 in 8 bits, up 105, down 63,
-// which instruction issue bounds, not the bytes (85 for both).  With the weights loaded
-// straight to registers those were 75, 52, 137 and 79.
+// (6.2 TB/s), down 42 (5.6); 32 tokens, 64 experts of 2048 x 1408 in 8 bits, up 105, down 63,
+// which instructions bound (442 for a step of 2 KB, the issue slots 69 % used), not the
+// bytes (85 for both).  With the weights loaded straight to registers: 75, 52, 137, 79.
 //   k_moe_up    a CTA's unit is eight features of one expert, gate and up rows
 //               together: lane by lane the two stand in one accumulator, and the
 //               warps, which cut k, add up through shared memory.
@@ -375,7 +375,7 @@ __global__ void __launch_bounds__(kWarps * 32, down_ctas(F8, NT)) k_moe_down(con
     const int64_t bytes = static_cast<int64_t>(a.I) * (F8 ? 1 : 2), nb = (a.H + 127) / 128;
     const int64_t off[4] = {0, 4 * bytes, 8 * bytes, 12 * bytes};
     // This warp's share of all (group, step) pairs: every so many steps of each group, so that the warps read side by
-    // side (one token, two experts of 4096 x 14336 in bf16: 54 us, runs 56); or, where that is not some steps a group,
+    // side (one token, two experts of 4096 x 14336 in bf16, then with two CTAs an SM: 54 us, runs 56); or, where that is not some steps a group,
     // a run of the whole list.
     const int workers = kWarps * parts, me = rank * kWarps + warp;
     const int64_t all = static_cast<int64_t>(*plan.count) * steps, q0 = all * me / workers;
