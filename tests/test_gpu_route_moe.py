@@ -220,6 +220,20 @@ def test_moe(T, E, k, H, I, fp8):
     assert layer.status() == 0
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("T,E,k,H,I", [(64, 1024, 32, 32, 48), (1, 1024, 32, 4112, 16)])
+def test_moe_of_the_most_experts_tokens_and_choices(T, E, k, H, I, fp8):
+    rng = np.random.default_rng(T * 11 + E)
+    layer = Layer(rng, E, H, I, fp8)
+    X, Xf = normal(rng, (T, H))
+    e, w, ef, wf = choices(rng, T, E, k)
+    Y = sg.moe_forward(X, layer.W13, layer.W2, e, w)
+    assert_layer(Y, Xf, layer, ef, wf)
+    out = torch.full_like(Y, float("nan"))
+    assert sg.moe_forward(X, layer.W13, layer.W2, e, w, out=out) is out and torch.equal(out, Y)
+    assert layer.status() == 0
+
+
 @pytest.mark.parametrize("T,E,k,H,I", [(3, 5, 2, 1000, 712), (20, 4, 2, 8, 8), (64, 2, 1, 24, 40), (1, 2, 2, 712, 1000)])
 def test_moe_multiples_of_eight(T, E, k, H, I):
     rng = np.random.default_rng(T)
