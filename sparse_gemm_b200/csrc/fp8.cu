@@ -64,9 +64,9 @@ constexpr int kSumWarps = 16, kWidth = 64;      // columns of a sum warp
 constexpr int kThreads = 128 + 32 * kSumWarps;
 constexpr int kChunk = 32 * kWidth * 2;         // a sum warp's output
 constexpr int kTmem = 512;                      // two accumulators
-constexpr int kAhead = 4, kScales = kAhead + 2;  // stages whose scales are made ahead
-constexpr int kInfos = 16;                      // more tiles than warp 2 may be ahead of a sum
-constexpr int kBars = (2 * kStages + kScales + 3) * 8 + 16;
+constexpr int kScales = 6;                      // stages whose scales are made ahead
+constexpr int kInfos = 16;                      // more tiles than warp 3 may be ahead of a sum: kScales and two loads
+constexpr int kBars = (2 * kStages + 2 * kScales + 3) * 8 + 16;
 constexpr int kSmem = 1024 + kRing + kSumWarps * kChunk + kScales * 1024 + kInfos * 16 + kBars + 2 * (kMaxExperts + 1) * 4;
 static_assert(kSmem <= 227 * 1024, "shared memory");
 
@@ -222,24 +222,30 @@ __device__ __forceinline__ void named_bar_arrive(uint32_t id, uint32_t count)
     asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(count) : "memory");
 }
 
-// Until *count is `value` or more; bounded as mbar_wait.
-__device__ __forceinline__ bool reached(const volatile int *count, int value, uint64_t timeout_ns, const volatile int *abort)
+// mbar_wait for a phase that is stages away: looks every 200 ns instead of sleeping inside try_wait, which polls shared
+// memory (input gradient of 8192 rows, eight experts of 14336 x 4096: 557 us, 568 with mbar_wait; forward the same).
+__device__ __forceinline__ bool wait_slowly(uint64_t *bar, uint32_t parity, uint64_t timeout_ns, const volatile int *abort)
 {
-    if (*count >= value) return true;
+    const uint32_t a = smem_u32(bar);
+    if (mbar_test_wait(a, parity)) return true;
     const uint64_t t0 = globaltimer_ns();
     while (true) {
-        __nanosleep(100);
-        if (*count >= value) return true;
+        __nanosleep(200);
+        if (mbar_test_wait(a, parity)) return true;
         if (*abort || globaltimer_ns() - t0 > timeout_ns) return false;
     }
 }
 
-// An accumulator was read out, as far as this warp reads it.
-__device__ __forceinline__ void release(uint32_t bar, int lane)
+// An accumulator was read out and the stage's scales were read, as far as this warp reads them: `scales`, of this CTA, is
+// released, so that those reads come before the slot is written again.
+__device__ __forceinline__ void release(uint32_t bar, uint64_t *scales, int lane)
 {
     tc_fence_before();
     __syncwarp();
-    if (lane == 0) mbar_arrive_cluster(bar);
+    if (lane == 0) {
+        mbar_arrive_cluster(bar);
+        mbar_arrive(scales);
+    }
 }
 
 // Bytes of a stage: a CTA's rows are half of the launch's largest tile.
@@ -277,11 +283,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp8(const __grid_constant__ Map
     uint64_t *empty = full + kStages;   // MMAs of a stage finished (each CTA)
     uint64_t *aempty = empty + kStages; // an accumulator was read out (leader)
     uint64_t *ready = aempty + 2;       // a stage's scales are there
-    uint64_t *drain = ready + kScales;
+    uint64_t *sfree = ready + kScales;  // ... were read by every sum warp
+    uint64_t *drain = sfree + kScales;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     int *ring_slot = reinterpret_cast<int *>(tmem_slot + 2);
-    volatile int *progress = reinterpret_cast<volatile int *>(tmem_slot + 3);  // stages whose MMAs are done
     int32_t *off = reinterpret_cast<int32_t *>(tmem_slot + 4);
     int32_t *start = off + kMaxExperts + 1;
 
@@ -296,10 +302,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp8(const __grid_constant__ Map
             mbar_init(&empty[s], 1);
         }
         for (int a = 0; a < 2; ++a) mbar_init(&aempty[a], 2 * kSumWarps);
-        for (int s = 0; s < kScales; ++s) mbar_init(&ready[s], 1);
+        for (int s = 0; s < kScales; ++s) {
+            mbar_init(&ready[s], 1);
+            mbar_init(&sfree[s], kSumWarps);
+        }
         mbar_init(drain, 1);
         *abort_flag = 0;
-        *progress = 0;
         fence_barrier_init();
         tma_prefetch_map(&maps.weight);
         tma_prefetch_map(&maps.out);
@@ -428,14 +436,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp8(const __grid_constant__ Map
                     }
                     if (ok) named_bar_arrive(1 + (it & 1), 32 * kSumWarps + 32);
                     else named_bar_sync(1 + (it & 1), 32 * kSumWarps + 32);  // an aborted run's sums go on to the end, in step
-                    if (lane == 0) *progress = it + 1;
                 }
             } else {
                 // ---------------------------------------------------- scales
                 const int wide_blocks = (args.cols + 127) / 128;
                 const int64_t plane = static_cast<int64_t>(wide_blocks) * blocks, wstep = kGrad ? wide_blocks : 1;
                 // what is loaded next: tile, block, and what is known of the tile
-                int t = first, b = 0, n = 0, ring = 0, rows = 0;
+                int t = first, b = 0, n = 0, rows = 0;
                 const float *rs = nullptr, *ws = nullptr;
                 bool second = false;
                 const bool quads = args.scale_stride % 4 == 0, wquads = !kGrad && blocks % 4 == 0;
@@ -467,20 +474,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp8(const __grid_constant__ Map
                     if ((b += f.n) == blocks) b = 0, t += stride, ++n;
                 };
                 int made = 0;
-                // stage `made` goes where stage made - kScales was, whose sums were read out before the MMAs of stage
-                // made - kAhead began: those are done
                 auto make = [&](const Four &f) {
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         if (!ok || j >= f.n) break;
-                        if (made >= kAhead) ok = __all_sync(0xffffffffu, reached(progress, made - kAhead + 1, tmo, abort_flag));
+                        // where stage made - kScales was, whose scales every sum warp has read
+                        const int round = made / kScales, slot = made - round * kScales;
+                        if (round > 0) ok = __all_sync(0xffffffffu, wait_slowly(&sfree[slot], (round - 1) & 1, tmo, abort_flag));
                         if (!ok) break;
-                        float *to = scales + ring * 256 + lane;
+                        float *to = scales + slot * 256 + lane;
 #pragma unroll
                         for (int i = 0; i < 4; ++i) to[32 * i] = f.row[i][j] * f.col[0][j], to[128 + 32 * i] = f.row[i][j] * f.col[1][j];
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(&ready[ring]);
-                        if (++ring == kScales) ring = 0;
+                        if (lane == 0) mbar_arrive(&ready[slot]);
                         ++made;
                     }
                 };
@@ -526,7 +532,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp8(const __grid_constant__ Map
                 tc_fence_after();
                 if (b == 0) live = infos[n % kInfos].w > 32 * q && infos[n % kInfos].y + kWidth * part < args.cols;
                 const uint64_t s2 = twice(my_scales[ring * 256]);
-                if (++ring == kScales) ring = 0;
                 if (live) {
                     const uint32_t from = mine + buf * kBC;
                     uint32_t v[2][16];
@@ -535,13 +540,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp8(const __grid_constant__ Map
                     for (int j = 0; j < kWidth / 16; ++j) {
                         tmem_wait_ld();
                         if (j + 1 < kWidth / 16) tmem_ld16(from + 16 * (j + 1), v[(j + 1) & 1]);
-                        else release(cluster_addr(&aempty[buf], 0), lane);
+                        else release(cluster_addr(&aempty[buf], 0), &sfree[ring], lane);
 #pragma unroll
                         for (int u = 0; u < 8; ++u) fma2(acc[8 * j + u], v[j & 1][2 * u], v[j & 1][2 * u + 1], s2);
                     }
                 } else {
-                    release(cluster_addr(&aempty[buf], 0), lane);
+                    release(cluster_addr(&aempty[buf], 0), &sfree[ring], lane);
                 }
+                if (++ring == kScales) ring = 0;
             }
             if (*abort_flag) ok = false;
             if (ok && live) {
