@@ -445,7 +445,10 @@ typedef struct {
  *   transposed 0: out [T][N] = A . W[e]^T (+ bias[e]), rows of length K;
  *   transposed 1: out [T][K] = A . W[e], rows of length N (a multiple of 16): the input gradient, no bias.
  * offsets, bias [E][N] (bf16, or NULL) and zero_rest as for bsl_grouped_forward; offsets NULL: W has E = 1
- * and owns all rows.  T >= 0. */
+ * and owns all rows.  T >= 0.
+ * A block's sum of products of codes is multiplied by the product of its two scales, which is rounded to fp32.
+ * So two blocks whose largest magnitudes multiply to more than 6.8e43 (2^128 448^2) give infinities, and NaN under
+ * a sum of zero; below 2.4e-33 (2^-126 448^2) the product is a multiple of 2^-149, and below 1.4e-40 zero. */
 BSL_API bsl_status bsl_fp8_product(const uint8_t *codes, const float *scales, int32_t T, const int32_t *offsets,
                                    const bsl_fp8 *W, int32_t transposed, const void *bias, void *out, int32_t zero_rest,
                                    void *stream);

@@ -1268,7 +1268,7 @@ def _fp8_product(A, Wq: Fp8Tensor, dims: int, transposed: bool, offsets, bias, o
 
 
 def forward_fp8(X, Wq: Fp8Tensor, bias: torch.Tensor | None = None, out: torch.Tensor | None = None) -> torch.Tensor:
-    """Y = Q(X) Q(W)^T (+ bias), bf16 [M, N], 8-bit products with fp32 sums and scales.  X is bf16
+    """Y = Q(X) Q(W)^T (+ bias), bf16 [M, N], 8-bit products with fp32 sums, scales and products of two scales.  X is bf16
     [M, K] (quantised on the way as by :func:`quantize_fp8`) or an Fp8Tensor with scales by row,
     ``Wq`` a weight [N, K] in tiles, N a multiple of 8."""
     return _fp8_product(X, Wq, 2, False, None, bias, out)
