@@ -473,7 +473,8 @@ BSL_API bsl_status bsl_fp8_get_status(const bsl_fp8 *W, int32_t *status_host, vo
  * descending order, ties to the lowest expert (-0 equals 0; a NaN comes after everything), and their weights:
  * with the scores s_i = exp(l_i) / sum_j exp(l_j) (score 0) or 1 / (1 + exp(-l_i)) (score 1), and S the sum
  * of the chosen scores, factor * s or (renormalize not 0) factor * s / S.  A logit of -inf has the score 0,
- * also in a row that holds nothing else; then the row's weights are 0.  Softmax rows with a NaN or +inf give NaN.
+ * also in a row that holds nothing else; then the row's weights are 0.  So are the weights s / S of sigmoids of a row
+ * whose largest logit is below -700.  Softmax rows with a NaN or +inf give NaN.
  * 1 <= k <= E <= BSL_GROUPED_MAX_EXPERTS, k <= BSL_ROUTE_MAX_K. */
 #define BSL_ROUTE_MAX_K 32
 

@@ -1454,7 +1454,8 @@ def route(logits: torch.Tensor, k: int, score: str = "softmax", renormalize: boo
         Y = grouped_forward(rows, Wg, r.offsets)
         out = torch.zeros_like(X).index_add_(0, r.order // k, Y * r.weights.flatten()[r.order, None].to(Y.dtype))
 
-    Logits of -inf weigh 0, in a row of nothing else too.  The weights' gradient flows to the logits."""
+    Logits of -inf weigh 0, in a row of nothing else too (renormalised sigmoids: nothing above -700).  The
+    weights' gradient flows to the logits."""
     if getattr(logits, "requires_grad", False) and torch.is_grad_enabled():
         return Routing(*RouteFunction.apply(logits, k, score, bool(renormalize), float(factor), sort))
     return _route(logits, k, score, bool(renormalize), float(factor), sort)

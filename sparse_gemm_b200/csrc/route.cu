@@ -9,6 +9,9 @@
 // maximum over the warp (of the logit's bits, ordered as numbers) and a minimum
 // over the experts that have it, so that ties go to the lowest one.  Choices go
 // by the logits, whose order the scores share, so rounded scores decide nothing.
+// Sigmoids that are divided by their sum are taken over exp(m), m the largest chosen
+// logit or 0, exp(l - m) / (1 + exp(l)): far below 0, where the sigmoids themselves are
+// no fp32 numbers, their quotients still are.
 //
 // Sorting is by counting: each CTA counts the experts of its run of tokens, and a
 // second kernel adds up the counts of the runs before its own and places its
@@ -69,6 +72,15 @@ __device__ __forceinline__ float warp_sum(float v)
 
 __device__ __forceinline__ float sigmoid_of(float l) { return 1.f / (1.f + expf(-l)); }
 
+// A row whose largest chosen logit is below this has sigmoids under 10^-304, and weights of zero.
+constexpr float kNothing = -700.f;
+
+// The same over exp(base), base = min(the largest chosen logit, 0); l is chosen.
+__device__ __forceinline__ float sigmoid_over(float l, float base)
+{
+    return l > 0.f ? sigmoid_of(l) : expf(l - base) / (1.f + expf(l));
+}
+
 // A token's choices: lane j < k returns expert j and its weight.
 template <int NE>
 __device__ __forceinline__ void choose(const RouteArgs &a, int64_t row, int lane, int &expert, float &weight)
@@ -107,8 +119,12 @@ __device__ __forceinline__ void choose(const RouteArgs &a, int64_t row, int lane
     }
     float s = 0.f, total = 1.f;
     if (a.sigmoid) {
-        if (lane < a.k) s = sigmoid_of(mine);
-        if (a.renormalize) total = warp_sum(s);
+        if (a.renormalize) {
+            if (lane < a.k && !(top < kNothing)) s = sigmoid_over(mine, fminf(top, 0.f));
+            total = warp_sum(s);
+        } else if (lane < a.k) {
+            s = sigmoid_of(mine);
+        }
     } else {
         float all = 0.f;
 #pragma unroll
@@ -120,7 +136,7 @@ __device__ __forceinline__ void choose(const RouteArgs &a, int64_t row, int lane
         if (all != all) total = all;  // a NaN or an infinity anywhere in the row
         if (top == -INFINITY) s = 0.f, total = 1.f;  // nothing is left: weights of zero
     }
-    if (total == 0.f) total = 1.f;  // (sigmoids of -inf)
+    if (total == 0.f) total = 1.f;  // (sigmoids that are nothing)
     weight = a.factor * (s / total);
 }
 
@@ -271,7 +287,8 @@ __global__ void __launch_bounds__(512) k_sort(const RouteArgs a)
 // dl of a token, from D_i = the sum of dw_j over the choices j of expert i, and G = sum_i D_i s_i:
 //   softmax, weights s:          factor s_i (D_i - G)
 //   softmax, weights s / S:      factor s_i / S (D_i - G / S) for the chosen, S = the sum of their scores
-//   sigmoid:                     factor s_i (1 - s_i) D_i, or factor s_i (1 - s_i) (D_i - G / S) / S for the chosen
+//   sigmoid:                     factor s_i (1 - s_i) D_i, or factor s_i (1 - s_i) (D_i - G / S) / S for the chosen,
+//                                whose scores may all be over the same number
 // Nothing is read by a choice's index, so one out of range does no harm.
 template <int NE>
 __global__ void __launch_bounds__(256) k_route_backward(const RouteArgs a)
@@ -302,9 +319,20 @@ __global__ void __launch_bounds__(256) k_route_backward(const RouteArgs a)
     }
     float slope[NE];  // of a score by its own logit, over the score's share
     if (a.sigmoid) {
+        float top = 0.f;  // divided by their sum: over exp(base), as in the forward
+        if (a.renormalize) {
+            top = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < NE; ++i)
+                if (in[i]) top = fmaxf(top, l[i]);
+#pragma unroll
+            for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+        }
+        const float base = fminf(top, 0.f);
 #pragma unroll
         for (int i = 0; i < NE; ++i) {
-            const float e = expf(-fabsf(l[i])), one = 1.f / (1.f + e);
+            const float small = expf(-fabsf(l[i])), one = 1.f / (1.f + small);
+            const float e = top < kNothing ? 0.f : base < 0.f && in[i] ? expf(l[i] - base) : small;
             s[i] = l[i] >= 0.f ? one : e * one;
             slope[i] = e * one * one;
             if (l[i] != l[i]) s[i] = slope[i] = l[i];
