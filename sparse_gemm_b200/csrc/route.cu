@@ -356,7 +356,7 @@ __global__ void __launch_bounds__(256) k_route_backward(const RouteArgs a)
     float G = 0.f, S = 0.f;
 #pragma unroll
     for (int i = 0; i < NE; ++i) {
-        G += D[i] * s[i];
+        G += in[i] ? D[i] * s[i] : 0.f;  // (a NaN that was not chosen is nobody's)
         S += in[i] ? s[i] : 0.f;
     }
     G = warp_sum(G);

@@ -107,3 +107,21 @@ def test_a_masked_choice_beside_a_low_one():
     assert np.allclose(r.weights.cpu().numpy(), [[want, 1 - want, 0, 0]], rtol=1e-6)
     d = sg.route_backward(torch.tensor([[1.0, 0, 5, 7]], device="cuda"), l, r.experts, score="sigmoid").cpu().numpy()
     assert np.allclose(d, [[want * (1 - want), 0, -want * (1 - want), 0]], rtol=1e-5)
+
+
+@pytest.mark.parametrize("renormalize", [False, True])
+@pytest.mark.parametrize("E,k", [(6, 2), (40, 8), (300, 32)])
+def test_a_nan_that_was_not_chosen(E, k, renormalize):
+    """It changes no sigmoid weight, and no gradient but its own, which is zero."""
+    rng = np.random.default_rng(E)
+    l = torch.from_numpy(rng.standard_normal((20, E)).astype(np.float32)).cuda()
+    g = torch.from_numpy(rng.standard_normal((20, k)).astype(np.float32)).cuda()
+    how = dict(score="sigmoid", renormalize=renormalize)
+    r = sg.route(l, k, **how)
+    want = sg.route_backward(g, l, r.experts, **how)
+    last = l.argmin(1, keepdim=True)
+    bad = l.scatter(1, last, float("nan"))
+    got = sg.route(bad, k, **how)
+    assert torch.equal(got.experts, r.experts) and torch.equal(got.weights, r.weights)
+    d = sg.route_backward(g, bad, got.experts, **how)
+    assert torch.equal(d, want) and not d.gather(1, last).any()
