@@ -1298,9 +1298,20 @@ def fp8_status(Wq: Fp8Tensor) -> int:
     return int(out.value)
 
 
+def _bias_grad_of(dY: torch.Tensor, offsets) -> torch.Tensor:
+    """The sums of dY's rows, by expert or (without offsets) all of them."""
+    if offsets is not None:
+        return grouped_bias_grad(dY, offsets)
+    rows = dY.shape[0]
+    if rows == 0:
+        return dY.new_zeros(dY.shape[1])
+    return grouped_bias_grad(dY, torch.arange(0, rows + 1, rows, dtype=torch.int32, device=dY.device))[0]
+
+
 class Fp8LinearFunction(torch.autograd.Function):
     """Autograd wrapper of the 8-bit layer over a frozen weight: forward as :func:`forward_fp8` (or
-    :func:`grouped_forward_fp8`, with offsets), backward the input's gradient, quantised by row too."""
+    :func:`grouped_forward_fp8`, with offsets), backward the input's gradient, quantised by row too,
+    and the bias's, the sums of an expert's rows as they are."""
 
     @staticmethod
     def forward(ctx, X, Wq, offsets=None, bias=None):
@@ -1311,11 +1322,14 @@ class Fp8LinearFunction(torch.autograd.Function):
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dY):
-        dX = None
+        offsets = ctx.saved_tensors[0] if ctx.saved_tensors else None
+        dY = _readable(dY)
+        dX = db = None
         if ctx.needs_input_grad[0]:
-            offsets = ctx.saved_tensors[0] if ctx.saved_tensors else None
-            dX = _fp8_product(_readable(dY), ctx.Wq, len(ctx.Wq.shape), True, offsets, None, None)
-        return dX, None, None, None
+            dX = _fp8_product(dY, ctx.Wq, len(ctx.Wq.shape), True, offsets, None, None)
+        if ctx.needs_input_grad[3]:
+            db = _bias_grad_of(dY, offsets)
+        return dX, None, None, db
 
 
 class Fp8Linear(torch.nn.Module):

@@ -1,0 +1,87 @@
+"""Autograd of the 8-bit layer: the bias's gradient, weights that change between forward and backward, ranks of the weight
+and the offsets."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import experts
+from tests._experts import check, normal, offsets_of
+from tests.test_gpu_fp8 import weights
+
+pytestmark = pytest.mark.gpu
+
+if torch.cuda.is_available():
+    import sparse_gemm_b200 as sg
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from sparse_gemm_b200 import build
+    build.build()
+
+
+@pytest.mark.parametrize("rows,N", [([1], 24), ([700], 144), ([5, 0, 70, 33], 144), ([3, 0, 300], 136)])
+@pytest.mark.parametrize("with_input", [False, True])
+def test_gradient_of_a_trained_bias(rows, N, with_input):
+    """Column sums of the upstream gradient, over an expert's rows; with and without the input's gradient beside it (which
+    wants output features in sixteens)."""
+    if with_input and N % 16:
+        N = 144
+    rng = np.random.default_rng(sum(rows) + N)
+    front = 0 if len(rows) == 1 else 2
+    off, o = offsets_of(rows, front)
+    T, E = sum(rows) + 2 * front, len(rows)
+    Wq, _ = weights(rng, *((N, 272) if E == 1 else (E, N, 272)))
+    X, _ = normal(rng, (T, 272))
+    bias, _ = normal(rng, (N,) if E == 1 else (E, N))
+    X.requires_grad_(with_input)
+    bias.requires_grad_(True)
+    Y = sg.Fp8LinearFunction.apply(X, Wq, None if E == 1 else off, bias)
+    g, gf = normal(rng, (T, N))
+    Y.backward(g)
+    ref, S = experts.grouped_bias_grad(gf, o)
+    check(bias.grad.view(E, N), ref, S, max(rows), "bias")
+    if with_input:
+        call = sg.backward_input_fp8(g, Wq) if E == 1 else sg.grouped_backward_input_fp8(g, Wq, off)
+        assert torch.equal(X.grad, call)
+    else:
+        assert X.grad is None
+    # differences: the sum of Y times g is linear in the bias
+    step = torch.zeros_like(bias)
+    step.view(-1)[5] = 1.0
+    with torch.no_grad():
+        more = sg.Fp8LinearFunction.apply(X, Wq, None if E == 1 else off, (bias * 0 + step))
+        none = sg.Fp8LinearFunction.apply(X, Wq, None if E == 1 else off, (bias * 0))
+    diff = ((more.double() - none.double()) * g.double()).sum()
+    size = ((more.double().abs() + none.double().abs()) * g.double().abs() * (more != none)).sum()
+    assert (diff - bias.grad.view(-1)[5].double()).abs() <= 2.0 ** -8 * (size + bias.grad.view(-1)[5].double().abs())
+
+
+def test_gradient_of_a_trained_bias_of_broadcast_and_no_rows():
+    rng = np.random.default_rng(1)
+    Wq, _ = weights(rng, 144, 272)
+    bias = torch.zeros(144, dtype=torch.bfloat16, device="cuda", requires_grad=True)
+    X, _ = normal(rng, (9, 272))
+    sg.Fp8LinearFunction.apply(X, Wq, None, bias).sum().backward()
+    assert (bias.grad == 9).all()
+    bias.grad = None
+    sg.Fp8LinearFunction.apply(X[:0], Wq, None, bias).sum().backward()
+    assert not bias.grad.any()
+
+
+def test_a_trained_bias_in_a_captured_backward():
+    rng = np.random.default_rng(2)
+    Wq, _ = weights(rng, 144, 272)
+    Wq.status
+    X, _ = normal(rng, (70, 272))
+    bias, _ = normal(rng, (144,))
+    bias.requires_grad_(True)
+    g, _ = normal(rng, (70, 144))
+    want, = torch.autograd.grad(sg.Fp8LinearFunction.apply(X, Wq, None, bias), bias, g)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got, = torch.autograd.grad(sg.Fp8LinearFunction.apply(X, Wq, None, bias), bias, g)
+    got.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
