@@ -1316,6 +1316,7 @@ class Fp8LinearFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, X, Wq, offsets=None, bias=None):
         ctx.Wq = Wq
+        ctx.has_bias = bias is not None
         ctx.save_for_backward(*(() if offsets is None else (offsets,)))
         return _fp8_product(_readable(X), Wq, len(Wq.shape), False, offsets, bias, None)
 
@@ -1327,7 +1328,7 @@ class Fp8LinearFunction(torch.autograd.Function):
         dX = db = None
         if ctx.needs_input_grad[0]:
             dX = _fp8_product(dY, ctx.Wq, len(ctx.Wq.shape), True, offsets, None, None)
-        if ctx.needs_input_grad[3]:
+        if ctx.has_bias and ctx.needs_input_grad[3]:
             db = _bias_grad_of(dY, offsets)
         return dX, None, None, db
 

@@ -69,6 +69,20 @@ def test_gradient_of_a_trained_bias_of_broadcast_and_no_rows():
     assert not bias.grad.any()
 
 
+def test_arguments_that_are_left_out():
+    rng = np.random.default_rng(5)
+    Wq, _ = weights(rng, 2, 144, 272)
+    one = sg.Fp8Tensor(Wq.codes[0], Wq.scales[0])
+    off, _ = offsets_of([4, 5])
+    X, _ = normal(rng, (9, 272))
+    X.requires_grad_(True)
+    g, _ = normal(rng, (9, 144))
+    for args, want in (((one,), lambda: sg.backward_input_fp8(g, one)), ((one, None), lambda: sg.backward_input_fp8(g, one)),
+                       ((Wq, off), lambda: sg.grouped_backward_input_fp8(g, Wq, off))):
+        got, = torch.autograd.grad(sg.Fp8LinearFunction.apply(X, *args), X, g)
+        assert torch.equal(got, want())
+
+
 def test_a_trained_bias_in_a_captured_backward():
     rng = np.random.default_rng(2)
     Wq, _ = weights(rng, 144, 272)
