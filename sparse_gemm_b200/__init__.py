@@ -1211,6 +1211,8 @@ def quantize_fp8(X: torch.Tensor, block_rows: int = 1, out: Fp8Tensor | None = N
                          f"blocks of {block_rows} on {X.device}")
     else:
         _refuse_overlap(out, X)
+        for t in (out.codes, out.scales):   # autograd sees that they changed
+            torch.autograd.graph.increment_version(t)
     planes, rows = (1, X.numel() // K) if block_rows == 1 else (math.prod(shape[:-2]), R)
     _check(library().bsl_fp8_quantize(X.data_ptr(), planes, rows, K, block_rows, out._codes_ptr, out._scales_ptr,
                                       _stream(X)), "bsl_fp8_quantize")
@@ -1311,19 +1313,22 @@ def _bias_grad_of(dY: torch.Tensor, offsets) -> torch.Tensor:
 class Fp8LinearFunction(torch.autograd.Function):
     """Autograd wrapper of the 8-bit layer over a frozen weight: forward as :func:`forward_fp8` (or
     :func:`grouped_forward_fp8`, with offsets), backward the input's gradient, quantised by row too,
-    and the bias's, the sums of an expert's rows as they are."""
+    and the bias's, the sums of an expert's rows as they are.  A weight that changed between the two is
+    refused, as any tensor that was saved for a backward pass."""
 
     @staticmethod
     def forward(ctx, X, Wq, offsets=None, bias=None):
+        Y = _fp8_product(_readable(X), Wq, len(Wq.shape), False, offsets, bias, None)
         ctx.Wq = Wq
         ctx.has_bias = bias is not None
-        ctx.save_for_backward(*(() if offsets is None else (offsets,)))
-        return _fp8_product(_readable(X), Wq, len(Wq.shape), False, offsets, bias, None)
+        # the weight too, so that one that changed in between is refused (inference tensors have no versions)
+        ctx.save_for_backward(offsets, *(t for t in (Wq.codes, Wq.scales) if not t.is_inference()))
+        return Y
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dY):
-        offsets = ctx.saved_tensors[0] if ctx.saved_tensors else None
+        offsets = ctx.saved_tensors[0]
         dY = _readable(dY)
         dX = db = None
         if ctx.needs_input_grad[0]:

@@ -99,3 +99,49 @@ def test_a_trained_bias_in_a_captured_backward():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("grouped", [False, True])
+def test_a_weight_that_changed_before_the_backward_is_refused(grouped):
+    rng = np.random.default_rng(3)
+    shape = (2, 144, 272) if grouped else (144, 272)
+    W, _ = normal(rng, shape)
+    other, _ = normal(rng, shape)
+    off, _ = offsets_of([4, 5])
+    make = sg.GroupedFp8Linear if grouped else sg.Fp8Linear
+    args = (off,) if grouped else ()
+    x, _ = normal(rng, (9, 272))
+    x.requires_grad_(True)
+    g, _ = normal(rng, (9, 144))
+    for change in (lambda m: sg.quantize_fp8(other, block_rows=128, out=m.weight8), lambda m: m.load_state_dict(make.from_dense(other).state_dict()),
+                   lambda m: m.scales.add_(1), lambda m: m.codes.zero_()):
+        layer = make.from_dense(W)
+        y = layer(x, *args)
+        change(layer)
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            y.backward(g)
+        layer(x, *args).backward(g)   # the changed weight, once it is the forward's too
+        assert torch.isfinite(x.grad.float()).all()
+        x.grad = None
+
+
+def test_weights_of_inference_mode_and_two_backwards():
+    """Inference tensors have no versions and are used as they are; an unchanged weight may be gone through twice."""
+    rng = np.random.default_rng(4)
+    W, _ = normal(rng, (144, 272))
+    with torch.inference_mode():
+        Wi = sg.quantize_fp8(W, block_rows=128)
+    Wq = sg.quantize_fp8(W, block_rows=128)
+    x, _ = normal(rng, (9, 272))
+    x.requires_grad_(True)
+    g, _ = normal(rng, (9, 144))
+    want = sg.backward_input_fp8(g, Wq)
+    for w in (Wi, Wq):
+        y = sg.Fp8LinearFunction.apply(x, w)
+        for _ in range(2):
+            got, = torch.autograd.grad(y, x, g, retain_graph=True)
+            assert torch.equal(got, want)
+    with torch.inference_mode():
+        sg.quantize_fp8(W, block_rows=128, out=Wi)
+        sg.quantize_fp8(W, block_rows=128, out=Wq)
+        assert torch.equal(sg.Fp8LinearFunction.apply(x, Wq), y)
