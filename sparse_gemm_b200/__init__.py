@@ -1318,7 +1318,7 @@ class Fp8LinearFunction(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, X, Wq, offsets=None, bias=None):
-        Y = _fp8_product(_readable(X), Wq, len(Wq.shape), False, offsets, bias, None)
+        Y = _fp8_product(_readable(X), Wq, 2 if offsets is None else 3, False, offsets, bias, None)
         ctx.Wq = Wq
         ctx.has_bias = bias is not None
         # the weight too, so that one that changed in between is refused (inference tensors have no versions)

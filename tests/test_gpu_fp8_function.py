@@ -145,3 +145,17 @@ def test_weights_of_inference_mode_and_two_backwards():
         sg.quantize_fp8(W, block_rows=128, out=Wi)
         sg.quantize_fp8(W, block_rows=128, out=Wq)
         assert torch.equal(sg.Fp8LinearFunction.apply(x, Wq), y)
+
+
+def test_offsets_go_with_weights_of_experts_only():
+    """A weight [N, K] with offsets, which would be left aside, and weights [E, N, K] without are refused."""
+    rng = np.random.default_rng(6)
+    Wq, _ = weights(rng, 2, 144, 272)
+    one = sg.Fp8Tensor(Wq.codes[0], Wq.scales[0])
+    off, _ = offsets_of([4, 5])
+    X, _ = normal(rng, (9, 272))
+    for bad in (lambda: sg.Fp8LinearFunction.apply(X, one, off), lambda: sg.Fp8LinearFunction.apply(X, Wq),
+                lambda: sg.GroupedFp8Linear(one)(X, off), lambda: sg.Fp8Linear(Wq)(X), lambda: sg.GroupedFp8Linear(Wq)(X, None)):
+        with pytest.raises(ValueError, match="Wq must be an Fp8Tensor"):
+            bad()
+    assert torch.equal(sg.GroupedFp8Linear(Wq)(X, off), sg.grouped_forward_fp8(X, Wq, off))
