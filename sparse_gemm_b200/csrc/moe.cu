@@ -173,17 +173,22 @@ __device__ __forceinline__ void load_vec(Vec<F8> &x, const __nv_bfloat16 *row, i
 
 // Four e4m3 codes to two registers of two bf16, codes 0, 2 and codes 1, 3: the bits s e e e e m m m go to the sign and
 // to the lowest exponent and highest mantissa bits, which is 2^-120 of the value, subnormal codes included, and one
-// exact product brings it in.  The NaN codes come out as 480 and are looked for apart: they, and no other, have bit 7
+// exact product brings it to 2^-9 of the value, 0.875 at most: a block's sum over tokens of up to 10^36 stays finite.  The
+// sums of all blocks get the 2^9 back at the end (code_unit; in the scales it took 177 us for 171: 32 tokens, six of 64
+// experts of 2048 x 1408).  The NaN codes come out as 480 and are looked for apart: they, and no other, have bit 7
 // of their byte set in what is returned.
 __device__ __forceinline__ uint32_t decode4(uint32_t w, uint32_t &even, uint32_t &odd)
 {
     const uint32_t m = w & 0x7F7F7F7Fu;
     even = (w * 256 & 0x80008000u) | (m & 0x007F007Fu) * 16;
     odd = (w & 0x80008000u) | (m >> 4 & 0x07F007F0u);
-    asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(even) : "r"(0x7B807B80u));
-    asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(odd) : "r"(0x7B807B80u));
+    asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(even) : "r"(0x77007700u));
+    asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(odd) : "r"(0x77007700u));
     return m + 0x01010101u;
 }
+
+template <bool F8>
+constexpr float code_unit() { return F8 ? 512.f : 1.f; }
 
 // A step's products, added to acc: NT groups of tokens, `live` of them there.  8 bits: the sum of the block times the
 // rows' scales; the codes of a word are taken as 0, 2 and 1, 3, and so are the tokens' elements.
@@ -334,6 +339,7 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_of(NT)) k_moe_up(const MoeAr
             const int r = i / 8, f = i % 8;
             float gate = 0.f, up = 0.f;
             for (int j = mine * team; j < (mine + 1) * team; ++j) gate += part[j][r][f], up += part[j][r][f + 8];  // in order
+            gate *= code_unit<F8>(), up *= code_unit<F8>();
             // (__expf is off by some 2^-20, the rounding of h by up to 2^-8)
             const float h = gate / (1.f + __expf(-gate)) * up * plan.share[group.slot + r];
             a.h[static_cast<int64_t>(group.slot + r) * a.I + i0 + f] = __float2bfloat16(h);
@@ -478,7 +484,7 @@ __global__ void __launch_bounds__(kWarps * 32, down_ctas(F8, NT)) k_moe_down(con
 #pragma unroll
         for (int j = 0; j < kWarps; ++j) y += sums[(j * a.T + r) * kStride + f];
         if (parts > 1) sums[r * kStride + f] = y;  // (nobody else reads or writes this one)
-        else if (n0 + f < a.H) a.Y[static_cast<int64_t>(r) * a.H + n0 + f] = __float2bfloat16(y);
+        else if (n0 + f < a.H) a.Y[static_cast<int64_t>(r) * a.H + n0 + f] = __float2bfloat16(y * code_unit<F8>());
     }
     if (parts == 1) return;
     cluster_sync_all();
@@ -490,7 +496,7 @@ __global__ void __launch_bounds__(kWarps * 32, down_ctas(F8, NT)) k_moe_down(con
             asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(other) : "r"(cluster_addr(sums + r * kStride + f, p)) : "memory");
             y += other;
         }
-        if (n0 + f < a.H) a.Y[static_cast<int64_t>(r) * a.H + n0 + f] = __float2bfloat16(y);
+        if (n0 + f < a.H) a.Y[static_cast<int64_t>(r) * a.H + n0 + f] = __float2bfloat16(y * code_unit<F8>());
     }
     cluster_sync_all();  // until the others have read this CTA's sums
 }
