@@ -125,3 +125,19 @@ def test_a_nan_that_was_not_chosen(E, k, renormalize):
     assert torch.equal(got.experts, r.experts) and torch.equal(got.weights, r.weights)
     d = sg.route_backward(g, bad, got.experts, **how)
     assert torch.equal(d, want) and not d.gather(1, last).any()
+
+
+@pytest.mark.parametrize("how", [dict(), dict(renormalize=False, factor=2.5), dict(score="sigmoid")])
+def test_gradient_without_sorting(how):
+    """route(sort=False) has no offsets and no order, and the same gradient."""
+    rng = np.random.default_rng(7)
+    l = torch.from_numpy(rng.standard_normal((300, 40)).astype(np.float32)).cuda()
+    g = torch.from_numpy(rng.standard_normal((300, 4)).astype(np.float32)).cuda()
+    grads = []
+    for sort in (False, True):
+        t = l.clone().requires_grad_(True)
+        r = sg.route(t, 4, sort=sort, **how)
+        assert (r.offsets is None) == (r.order is None) == (not sort) and r.weights.requires_grad
+        r.weights.backward(g)
+        grads.append(t.grad)
+    assert torch.equal(*grads) and torch.equal(grads[0], sg.route_backward(g, l, r.experts, **how))
