@@ -33,10 +33,12 @@
 // is one sum in a fixed order.
 //
 // What bounds it with many rows is the turn of an accumulator, two of which fill
-// TMEM: MMAs 690 clocks (the four of a stage, beside copies and TMEM reads), 190
-// until the sums see them, 600 until they have read it out (their FMAs take 280 of
-// it), 180 until the next MMAs; half of that a stage.  Measured at 8192 x 4096 x 14336:
-// 500 us (1920 TFLOP/s), 598 with the rows' conversion (17) in long runs, which power holds back; MMAs and copies
+// TMEM: a stage takes 905 clocks (issue to issue, by clock() in a copy of this kernel), half a
+// turn, and a tile's end 3260 more, while the sums write it, so 1010 a stage of 32-stage
+// tiles.  With clocks at three points, which slow it to 1110 a stage, a turn is 1310 from the issue until
+// the sums see the block, 680 until they have read it out (their FMAs take 280 of it) and 235
+// until the next issue.  Measured at 8192 x 4096 x 14336: 502 us for single calls (1920 TFLOP/s), 566 in a
+// row of them at 1556 MHz, which power holds back, 595 with the rows' conversion (17); MMAs and copies
 // alone 305.  Steps and what they took: output by plain stores, which all SMs issue at
 // the same time, 562, by copies from shared memory 545; without a split of the
 // registers by setmaxnreg 502.  Eight sum warps with twice the columns took 530, and
