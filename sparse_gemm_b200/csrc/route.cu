@@ -355,19 +355,20 @@ __global__ void __launch_bounds__(256) k_route_backward(const RouteArgs a)
     }
     float G = 0.f, S = 0.f;
 #pragma unroll
-    for (int i = 0; i < NE; ++i) {
-        G += in[i] ? D[i] * s[i] : 0.f;  // (a NaN that was not chosen is nobody's)
-        S += in[i] ? s[i] : 0.f;
-    }
-    G = warp_sum(G);
+    for (int i = 0; i < NE; ++i) S += in[i] ? s[i] : 0.f;
     S = warp_sum(S);
     if (S == 0.f) S = 1.f;
+    // divided by their sum: G / S, by the quotients, of which an only choice's is one, so that its difference is zero
+#pragma unroll
+    for (int i = 0; i < NE; ++i)
+        if (in[i]) G += D[i] * (a.renormalize ? s[i] / S : s[i]);  // (a NaN that was not chosen is nobody's)
+    G = warp_sum(G);
 #pragma unroll
     for (int i = 0; i < NE; ++i) {
         const int e = 32 * i + lane;
         if (e >= a.E) continue;
         float d;
-        if (a.renormalize) d = in[i] ? slope[i] / S * (D[i] - G / S) : 0.f;
+        if (a.renormalize) d = in[i] ? slope[i] / S * (D[i] - G) : 0.f;
         else if (a.sigmoid) d = in[i] ? slope[i] * D[i] : 0.f;
         else d = slope[i] * (D[i] - G);
         d *= a.factor;

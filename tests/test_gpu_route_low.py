@@ -141,3 +141,17 @@ def test_gradient_without_sorting(how):
         r.weights.backward(g)
         grads.append(t.grad)
     assert torch.equal(*grads) and torch.equal(grads[0], sg.route_backward(g, l, r.experts, **how))
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E", [1, 2, 33, 256, 1024])
+def test_an_only_choice_that_is_divided_by_itself(E, score):
+    """Its weight is the factor, whatever the logits, and their gradient is zero, not a rounding."""
+    rng = np.random.default_rng(E)
+    for half in (False, True):
+        l = torch.from_numpy((rng.standard_normal((500, E)) * 3 - 2).astype(np.float32)).cuda()
+        l = l.to(torch.bfloat16) if half else l
+        g = torch.from_numpy(rng.standard_normal((500, 1)).astype(np.float32)).cuda()
+        r = sg.route(l, 1, score=score, factor=0.7)
+        assert (r.weights == np.float32(0.7)).all()
+        assert not sg.route_backward(g, l, r.experts, score=score, factor=0.7).any()
